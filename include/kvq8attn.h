@@ -90,6 +90,25 @@ typedef struct {
     int32_t capacity;
 } kvf16_cache;
 
+/* Element types of the calls that take more than one. */
+enum kvq8_dtype { KVQ8_F32 = 0, KVQ8_F16 = 1, KVQ8_BF16 = 2 };
+
+/* A paged Q8_0 cache: codes [n_pages][n_kv_heads][page_size][head_dim], scales
+ * [n_pages][n_kv_heads][page_size][head_dim / 32] (fp16 bits), so a page holds page_size
+ * consecutive rows of every KV head.  head_dim 128 or 256; page_size a power of two, 16 .. 1024.
+ * Token slot s is row s % page_size of page s / page_size.  A request's page table lists its pages
+ * in order of position.  Slot and element offsets are 64-bit. */
+typedef struct {
+    const int8_t* k_codes;
+    const uint16_t* k_scales;
+    const int8_t* v_codes;
+    const uint16_t* v_scales;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t n_pages;
+} kvq8_paged_cache;
+
 /*
  * kvq8_quantize -- append n_tok tokens of K (or V) values to one plane pair.
  *   x      : fp32 [n_tok][n_kv_heads][head_dim]
@@ -406,6 +425,153 @@ int attn_prompt_q8(const uint16_t* q, int n_q, int n_q_heads, const kvq8_cache* 
 #define KVQ8_NOALLOC_SCRATCH_BYTES (8u * 1024u * 1024u)
 int attn_verify_q8_noalloc(const float* q, int n_rows, int n_q_heads, const kvq8_cache* kv, int kv_len,
                            int q_pos0, float softmax_scale, float* out, int n_split, kvq8_stream_t stream);
+
+/*
+ * ---- Serving a batch over a paged cache --------------------------------------------------------
+ * One step for n_seqs requests of different lengths, all lengths on the device:
+ *   kvq8_paged_tables (pages and slots of the new tokens), kvq8_paged_append (their K and V into the
+ *   pages), attn_verify_paged_q8 (every request's window over its pages), logits_adjust (penalties,
+ *   biases and grammars on the window's logits), argmax_rows_top_prob; token_counts keeps what the
+ *   penalties read.
+ * The new tokens of all requests are the rows of one batch: request b owns rows row_starts[b] ..
+ * row_starts[b + 1] - 1 (int32, device, n_seqs + 1 entries, ascending), its window of T rows.  No call
+ * synchronises or reads a length on the host, so a step can be captured into a graph and replayed
+ * as the lengths change.  n_seqs is at most 4096.
+ */
+
+/*
+ * kvq8_paged_tables -- block tables and slots from request lengths.
+ *   lens, n_new : int32 [n_seqs]: tokens each request holds after the step, and how many of them are
+ *                 new (0 <= n_new <= lens); lens = 0 ends a request
+ *   held        : int32 [n_seqs]: pages each request holds now
+ *   page_table  : int32 [n_seqs][max_pages], updated: entries [held, need) of a request that grows to
+ *                 need = ceil(lens / page_size) pages are filled; other entries are left alone
+ *   free_ring   : int32 [n_pages], updated: the free pages, ring_state = int32 {head, count}; entry
+ *                 (head + i) % n_pages, i < count, is the i-th free page
+ *   held_out, ring_out : held and ring_state after the step; may be the inputs themselves
+ *   row_starts  : int32 [n_seqs + 1]: exclusive sums of n_new (output)
+ *   slots, positions : int64 / int32 [n_rows]: cache slot and position of every new token, in request
+ *                 order; -1 in the rows behind the last
+ *   status      : int32 [1]: 0; 1 = too few free pages; 2 = malformed (a length below 0, n_new > lens,
+ *                 lens > max_pages * page_size, held outside [0, max_pages], more than n_rows new
+ *                 tokens, a ring_state outside its range, or more pages held and free than n_pages)
+ * Pages are taken from the ring's head and given back behind its tail in order of request, then of
+ * position; a page given back in a call is not taken in the same call.  All or nothing: with a
+ * nonzero status held_out and ring_out repeat the inputs, page_table and free_ring are unchanged,
+ * every slot is -1 and every row start 0, so the step's other calls then do nothing.
+ * Page ids are passed through as they stand in the ring; the calls that use them check their range.
+ * Errors: INVALID_ARG, UNSUPPORTED (n_seqs > 4096, page_size, n_pages or n_rows > 2^30), MISALIGNED
+ * (4 bytes; slots 8).  One launch.
+ */
+int kvq8_paged_tables(const int32_t* lens, const int32_t* n_new, const int32_t* held, int n_seqs, int page_size,
+                      int32_t* page_table, int max_pages, int32_t* free_ring, int n_pages,
+                      const int32_t* ring_state, int32_t* held_out, int32_t* ring_out, int32_t* row_starts,
+                      int64_t* slots, int32_t* positions, int n_rows, int32_t* status, kvq8_stream_t stream);
+
+/*
+ * kvq8_paged_append -- quantise n_tok tokens of K and V into the cache at their slots, one launch.
+ *   k, v   : [n_tok][n_kv_heads][head_dim] of `dtype` (KVQ8_F32, KVQ8_F16, KVQ8_BF16), device;
+ *            k_stride / v_stride elements between tokens (>= n_kv_heads * head_dim; a multiple of
+ *            16 bytes), the heads of a token contiguous
+ *   slots  : int64 [n_tok], device; a token whose slot lies outside [0, n_pages * page_size) is
+ *            skipped.  No two tokens of a call may have the same slot: its contents would be a
+ *            mixture of theirs.
+ * The bytes are those of kvq8_append for the same values (in fp32).  The planes are written through.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size), MISALIGNED (16 bytes; slots 8).
+ */
+int kvq8_paged_append(const void* k, const void* v, int dtype, int n_tok, int64_t k_stride, int64_t v_stride,
+                      const kvq8_paged_cache* kv, const int64_t* slots, kvq8_stream_t stream);
+
+/*
+ * kvq8_paged_read -- the values code * scale of n_tok slots, rounded once to `dtype`, one launch.
+ *   k, v : [token][head][head_dim] of `dtype`; k_strides / v_strides (host, 2 entries): elements
+ *          between tokens and between heads, each >= head_dim and a multiple of 16 bytes.  Strides
+ *          {head_dim, capacity * head_dim} write the planes of a kvf16_cache, over which
+ *          attn_prompt_f16 then runs: a prompt chunk behind a paged context.
+ *   slots : int64 [n_tok], device, repeats allowed; a slot outside the cache gives zeros.
+ * Errors: as for kvq8_paged_append.
+ */
+int kvq8_paged_read(const kvq8_paged_cache* kv, const int64_t* slots, int n_tok, int dtype, void* k, void* v,
+                    const int64_t* k_strides, const int64_t* v_strides, kvq8_stream_t stream);
+
+/* Bytes of workspace attn_verify_paged_q8 needs on the current device (0: unsupported shape). */
+size_t attn_verify_paged_q8_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim, int max_rows);
+
+/*
+ * attn_verify_paged_q8 -- verify attention of every request's window over the paged cache: chains
+ * and trees of drafted tokens, and plain decoding (windows of one row).
+ *   q        : fp16 or bf16 (`dtype`) [n_rows][n_q_heads][head_dim], q_stride elements between rows
+ *              (a multiple of 16 bytes); out: the same type, [n_rows][n_q_heads][head_dim], contiguous
+ *   page_table : int32 [n_seqs][max_pages]; lens: int32 [n_seqs], tokens of each request in the cache,
+ *              the window's own included
+ *   max_rows : the longest window of the batch, 1 .. 64
+ *   window_mask : uint64 [n_rows] or null.  A row sees every key before the window (n < lens - T), and
+ *              the window key lens - T + j exactly when bit j < T of its word is set; null: j <= its
+ *              place in the window.  A row that sees no key gets zeros.
+ *   workspace : attn_verify_paged_q8_workspace_bytes(...) bytes; calls that may overlap need one each
+ * Rows of no request (behind row_starts[n_seqs]) and the rows of a malformed request (T > max_rows,
+ * T > lens, lens > max_pages * page_size, rows outside [0, n_rows)) are left as they were.  Keys on a
+ * page id outside [0, n_pages) are left out, as if masked.  Masked and unused cache rows may hold any
+ * codes, but their scales must be finite where they stand before lens.
+ * K, V and p enter the tensor cores in fp16 (code * scale rounded once), q in fp16 times a power of
+ * two per row; scores, softmax statistics and sums are fp32.  Values must stay inside the fp16 range.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, n_q_heads / n_kv_heads > 64, max_rows > 64,
+ * n_seqs > 4096, n_rows > 2^24), WORKSPACE, MISALIGNED.
+ */
+int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows, int n_q_heads,
+                         const kvq8_paged_cache* kv, const int32_t* page_table, int max_pages, const int32_t* lens,
+                         const int32_t* row_starts, int n_seqs, int max_rows, const uint64_t* window_mask,
+                         float softmax_scale, void* out, void* workspace, size_t workspace_bytes,
+                         kvq8_stream_t stream);
+
+/*
+ * logits_adjust -- penalties for repeated tokens, biases and grammar masks on a window's logits.
+ *   logits  : [n_rows][vocab] of `dtype`, logits_stride elements between rows
+ *   out     : fp32 [n_rows][vocab], out_stride elements between rows; may be `logits` itself (fp32,
+ *             equal strides)
+ *   penalties : fp32 [n_seqs][3] repetition, frequency, presence, or null (none; then counts and
+ *             window_tokens must be null)
+ *   counts  : uint32 [n_states][vocab] as token_counts keeps them, or null; state_of: int32 [n_seqs],
+ *             the counts row of each request (null: b; outside [0, n_states): nothing counted)
+ *   window_tokens : int32 [n_rows] or null: the drafted tokens; row r also counts those of its own
+ *             path, the tokens of window places j whose bit is set in window_mask[r] (uint64 [n_rows];
+ *             null: j <= its place)
+ *   bias_starts : int32 [n_seqs + 1] or null: request b adds bias_values[i] to bias_tokens[i] for i in
+ *             [bias_starts[b], bias_starts[b + 1]) (n_bias entries in all); of several entries of one
+ *             token the last holds
+ *   grammar : uint32 [n_grammar][ceil(vocab / 32)] or null, bit v % 32 of word v / 32 = value v is
+ *             allowed; grammar_of: int32 [n_rows], the mask of each row (null: r; outside
+ *             [0, n_grammar): everything is allowed)
+ * With c = times v was generated, seen = c > 0 or v in the prompt, in fp32 and in this order:
+ *   seen: x = x > 0 ? x / repetition : x * repetition;  x -= frequency * c + (c > 0 ? presence : 0);
+ *   x += bias;  not allowed: x = -inf (whatever x was).
+ * Tokens outside [0, vocab) are ignored.  Rows of no request, and of a request with more than 64 rows
+ * where window_tokens is given, are left as they were.
+ * Errors: INVALID_ARG, UNSUPPORTED (n_seqs > 4096, vocab > 2^30, n_rows > 262140), MISALIGNED (element
+ * size; window_mask 8).  One launch.
+ */
+int logits_adjust(const void* logits, int dtype, int64_t logits_stride, int n_rows, int vocab,
+                  const int32_t* row_starts, int n_seqs, const float* penalties, const uint32_t* counts,
+                  int n_states, const int32_t* state_of, const int32_t* window_tokens, const uint64_t* window_mask,
+                  const int32_t* bias_starts, const int32_t* bias_tokens, const float* bias_values, int n_bias,
+                  const uint32_t* grammar, int n_grammar, const int32_t* grammar_of, float* out, int64_t out_stride,
+                  kvq8_stream_t stream);
+
+/*
+ * token_counts -- count tokens into counts rows: bit 31 of a value's word = it stands in the prompt,
+ * bits 0 .. 30 = times generated.
+ *   tokens  : int32 [n_tokens]; list i is [token_starts[i], token_starts[i + 1]) (int32 [n_lists + 1]),
+ *             its first prompt_lens[i] tokens (int32 [n_lists]; null: none) the prompt, the rest generated
+ *   state_of : int32 [n_lists], the counts row of each list (null: i; outside [0, n_states): skipped);
+ *             several lists may have the same row
+ *   clear   : nonzero: the lists' rows start from zero, else the tokens are added to what they hold
+ * Tokens outside [0, vocab) and lists outside [0, n_tokens] are ignored.  Integer sums: the result does
+ * not depend on the order of execution.  Errors: INVALID_ARG, UNSUPPORTED (n_lists > 4096, sizes above
+ * 2^30), MISALIGNED (4 bytes).
+ */
+int token_counts(const int32_t* tokens, const int32_t* token_starts, int n_lists, int n_tokens,
+                 const int32_t* prompt_lens, const int32_t* state_of, int clear, uint32_t* counts, int n_states,
+                 int vocab, kvq8_stream_t stream);
 
 /*
  * kvq8_selftest_convert -- a self-test hook: runs the code -> fp16 conversions that the verify

@@ -34,7 +34,8 @@ EXPORTED = ("kvq8_quantize", "kvq8_append", "attn_verify_q8_workspace_bytes", "a
             "attn_prompt_k8v4", "attn_prompt_f16_workspace_bytes", "attn_prompt_f16", "attn_combine",
             "attn_prompt_q8_workspace_bytes", "attn_prompt_q8", "attn_verify_q8_noalloc", "kvq8_device_error", "kvq8_status_str",
             "argmax_rows_top_prob_workspace_bytes", "argmax_rows_top_prob", "kvq8_selftest_convert",
-            "kvq8_selftest_wait_timeout")
+            "kvq8_selftest_wait_timeout", "kvq8_paged_tables", "kvq8_paged_append", "kvq8_paged_read",
+            "attn_verify_paged_q8_workspace_bytes", "attn_verify_paged_q8", "logits_adjust", "token_counts")
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
 
@@ -59,6 +60,13 @@ class kvq8_cache(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32)]
+
+
+class kvq8_paged_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -133,6 +141,22 @@ def load_library():
         lib.attn_prompt_q8.restype = i32
         lib.attn_verify_q8_noalloc.argtypes = [vp, i32, i32, cp, i32, i32, f32, vp, i32, vp]
         lib.attn_verify_q8_noalloc.restype = i32
+        cpg, i64 = ctypes.POINTER(kvq8_paged_cache), ctypes.c_int64
+        lib.kvq8_paged_tables.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+        lib.kvq8_paged_tables.restype = i32
+        lib.kvq8_paged_append.argtypes = [vp, vp, i32, i32, i64, i64, cpg, vp, vp]
+        lib.kvq8_paged_append.restype = i32
+        lib.kvq8_paged_read.argtypes = [cpg, vp, i32, i32, vp, vp, ctypes.POINTER(i64), ctypes.POINTER(i64), vp]
+        lib.kvq8_paged_read.restype = i32
+        lib.attn_verify_paged_q8_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.attn_verify_paged_q8_workspace_bytes.restype = sz
+        lib.attn_verify_paged_q8.argtypes = [vp, i32, i64, i32, i32, cpg, vp, i32, vp, vp, i32, i32, vp, f32, vp, vp, sz, vp]
+        lib.attn_verify_paged_q8.restype = i32
+        lib.logits_adjust.argtypes = [vp, i32, i64, i32, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, i32,
+                                      vp, vp, i64, vp]
+        lib.logits_adjust.restype = i32
+        lib.token_counts.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, i32, i32, vp]
+        lib.token_counts.restype = i32
         lib.kvq8_device_error.argtypes = [i32]
         lib.kvq8_device_error.restype = i32
         lib.kvq8_status_str.argtypes = [i32]
@@ -642,3 +666,229 @@ def attn_verify_q8_noalloc(q: torch.Tensor, cache: KVCacheQ8, kv_len: int, q_pos
                                                int(n_split), _stream(stream))
     _check("attn_verify_q8_noalloc", st)
     return out
+
+
+# ---------------------------------------------------------------- serving a batch over a paged cache
+
+_DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _addr(t, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
+    """The address of a contiguous tensor of this type and shape on this device.  These calls serve steps of a few
+    microseconds, so the good case is tested with the fewest calls into torch."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device} "
+                     f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
+
+
+def _maybe(t, name: str, dtype: torch.dtype, shape: tuple, device: int):
+    return None if t is None else _addr(t, name, dtype, shape, device)
+
+
+def _launch_on(device: int, stream) -> int:
+    """The raw stream to launch on, after checking that the tensors live on the current device."""
+    if device < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if torch.cuda.current_device() != device:
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if hasattr(stream, "device") and stream.device.index != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _scratch(nbytes: int, device, stream):
+    """A workspace from the allocator for one call: taken on the stream that uses it."""
+    if stream is None or not hasattr(stream, "cuda_stream"):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+class KVPagedCacheQ8:
+    """Caller-owned paged Q8_0 K/V planes on one device (kvq8_paged_cache of include/kvq8attn.h): codes
+    int8 [n_pages][n_kv_heads][page_size][head_dim], scales fp16 [n_pages][n_kv_heads][page_size][head_dim/32]."""
+
+    def __init__(self, n_kv_heads: int, head_dim: int, page_size: int, n_pages: int, device="cuda"):
+        rows = (n_pages, n_kv_heads, page_size)
+        self._set(torch.zeros(rows + (head_dim,), dtype=torch.int8, device=device),
+                  torch.zeros(rows + (head_dim // 32,), dtype=torch.float16, device=device),
+                  torch.zeros(rows + (head_dim,), dtype=torch.int8, device=device),
+                  torch.zeros(rows + (head_dim // 32,), dtype=torch.float16, device=device))
+
+    @classmethod
+    def from_planes(cls, k_codes, k_scales, v_codes, v_scales):
+        c = cls.__new__(cls)
+        c._set(k_codes, k_scales, v_codes, v_scales)
+        return c
+
+    def _set(self, k_codes, k_scales, v_codes, v_scales):
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
+        shape = tuple(k_codes.shape)
+        self.device, self._index = k_codes.device, k_codes.get_device()
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _addr(t, name, torch.int8, shape, self._index)
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _addr(t, name, torch.float16, shape[:3] + (self.head_dim // 32,), self._index)
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self._struct = kvq8_paged_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+                                        self.n_kv_heads, self.head_dim, self.page_size, self.n_pages)
+
+    def struct(self) -> kvq8_paged_cache:
+        return self._struct
+
+
+def kvq8_paged_tables(lens: torch.Tensor, n_new: torch.Tensor, held: torch.Tensor, page_table: torch.Tensor,
+                      free_ring: torch.Tensor, ring_state: torch.Tensor, page_size: int, row_starts: torch.Tensor,
+                      slots: torch.Tensor, positions: torch.Tensor, status: torch.Tensor,
+                      held_out: torch.Tensor | None = None, ring_out: torch.Tensor | None = None, stream=None) -> None:
+    """Pages and slots of a step's new tokens from the requests' lengths: int32 lens, n_new, held [n], page_table
+    [n][max_pages] and free_ring [n_pages] (both updated), ring_state [2]; outputs row_starts int32 [n + 1], slots
+    int64 [n_rows], positions int32 [n_rows], status int32 [1].  held and ring_state are updated in place unless
+    held_out / ring_out are given."""
+    n, dev, i32 = lens.shape[0], lens.get_device(), torch.int32
+    if page_table.dim() != 2 or free_ring.dim() != 1 or slots.dim() != 1:
+        raise ValueError("page_table must be [n][max_pages], free_ring [n_pages] and slots [n_rows]")
+    mp, n_pages, n_rows = page_table.shape[1], free_ring.shape[0], slots.shape[0]
+    st = (_lib or load_library()).kvq8_paged_tables(
+        _addr(lens, "lens", i32, (n,), dev), _addr(n_new, "n_new", i32, (n,), dev), _addr(held, "held", i32, (n,), dev),
+        n, int(page_size), _addr(page_table, "page_table", i32, (n, mp), dev), mp,
+        _addr(free_ring, "free_ring", i32, (n_pages,), dev), n_pages, _addr(ring_state, "ring_state", i32, (2,), dev),
+        _addr(held if held_out is None else held_out, "held_out", i32, (n,), dev),
+        _addr(ring_state if ring_out is None else ring_out, "ring_out", i32, (2,), dev),
+        _addr(row_starts, "row_starts", i32, (n + 1,), dev), _addr(slots, "slots", torch.int64, (n_rows,), dev),
+        _addr(positions, "positions", i32, (n_rows,), dev), n_rows, _addr(status, "status", i32, (1,), dev),
+        _launch_on(dev, stream))
+    _check("kvq8_paged_tables", st)
+
+
+def _token_stride(t: torch.Tensor, name: str, cache: KVPagedCacheQ8) -> int:
+    if t.dim() != 3 or t.shape[1:] != (cache.n_kv_heads, cache.head_dim) or t.get_device() != cache._index:
+        raise ValueError(f"{name} must be [n_tok][{cache.n_kv_heads}][{cache.head_dim}] on {cache.device}")
+    if t.stride(2) != 1 or (t.stride(1) != cache.head_dim and cache.n_kv_heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else cache.n_kv_heads * cache.head_dim
+
+
+def kvq8_paged_append(k: torch.Tensor, v: torch.Tensor, cache: KVPagedCacheQ8, slots: torch.Tensor, stream=None) -> None:
+    """Quantise K and V values [n_tok][n_kv_heads][head_dim] (fp32, fp16 or bf16; tokens may be strided) into the
+    cache at int64 slots [n_tok], which are distinct; slots outside the cache are skipped."""
+    if k.dtype is not v.dtype or k.dtype not in _DTYPE or k.shape != v.shape:
+        raise ValueError("k and v must have one shape and one type (float32, float16 or bfloat16)")
+    ks, vs = _token_stride(k, "k", cache), _token_stride(v, "v", cache)
+    st = (_lib or load_library()).kvq8_paged_append(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], k.shape[0], ks, vs,
+                                          cache._struct, _addr(slots, "slots", torch.int64, (k.shape[0],), cache._index),
+                                          _launch_on(cache._index, stream))
+    _check("kvq8_paged_append", st)
+
+
+def kvq8_paged_read(cache: KVPagedCacheQ8, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
+    """Write the values of int64 slots [n_tok] into k and v [n_tok][n_kv_heads][head_dim] (fp32, fp16 or bf16; tokens
+    and heads may be strided, so a KVCacheF16's planes can be given as k.transpose(0, 1)[:n_tok])."""
+    n = slots.shape[0]
+    if k.dtype is not v.dtype or k.dtype not in _DTYPE:
+        raise ValueError("k and v must have one type (float32, float16 or bfloat16)")
+    strides = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t.shape != (n, cache.n_kv_heads, cache.head_dim) or t.stride(2) != 1 or t.get_device() != cache._index:
+            raise ValueError(f"{name} must be [{n}][{cache.n_kv_heads}][{cache.head_dim}] with contiguous dims on {cache.device}")
+        strides.append((ctypes.c_int64 * 2)(t.stride(0) if n > 1 else cache.head_dim,
+                                            t.stride(1) if cache.n_kv_heads > 1 else cache.head_dim))
+    st = (_lib or load_library()).kvq8_paged_read(cache._struct, _addr(slots, "slots", torch.int64, (n,), cache._index), n,
+                                        _DTYPE[k.dtype], k.data_ptr(), v.data_ptr(), strides[0], strides[1],
+                                        _launch_on(cache._index, stream))
+    _check("kvq8_paged_read", st)
+
+
+def attn_verify_paged_q8_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int, max_rows: int) -> int:
+    return int((_lib or load_library()).attn_verify_paged_q8_workspace_bytes(n_q_heads, n_kv_heads, head_dim, max_rows))
+
+
+def attn_verify_paged_q8(q: torch.Tensor, cache: KVPagedCacheQ8, page_table: torch.Tensor, lens: torch.Tensor,
+                         row_starts: torch.Tensor, max_rows: int, softmax_scale: float,
+                         window_mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Verify attention of a batch's windows: fp16 or bf16 q [n_rows][Hq][hd] (rows may be strided), page_table int32
+    [n][max_pages], lens int32 [n], row_starts int32 [n + 1], window_mask int64 [n_rows] (bit j of a row's word = it
+    sees window key j) or None for chains.  Returns out, of q's type; rows of no request are left as they were."""
+    dev = cache._index
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16) or q.get_device() != dev or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be float16 or bfloat16 [n_rows][n_q_heads][{cache.head_dim}] on {cache.device}")
+    n_rows, hq, hd = q.shape
+    if q.stride(2) != 1 or (q.stride(1) != hd and hq > 1):
+        raise ValueError("q: the heads of a row must be contiguous")
+    n, mp = page_table.shape
+    if out is None:
+        out = torch.empty((n_rows, hq, hd), dtype=q.dtype, device=q.device) if stream is None else \
+            _scratch(n_rows * hq * hd * 2, q.device, stream).view(q.dtype).view(n_rows, hq, hd)
+    lib = (_lib or load_library())
+    if workspace is None:
+        workspace = _scratch(max(lib.attn_verify_paged_q8_workspace_bytes(hq, cache.n_kv_heads, hd, int(max_rows)), 16), q.device,
+                             stream)
+    st = lib.attn_verify_paged_q8(
+        q.data_ptr(), _DTYPE[q.dtype], q.stride(0) if n_rows > 1 else hq * hd, n_rows, hq, cache._struct,
+        _addr(page_table, "page_table", torch.int32, (n, mp), dev), mp, _addr(lens, "lens", torch.int32, (n,), dev),
+        _addr(row_starts, "row_starts", torch.int32, (n + 1,), dev), n, int(max_rows),
+        _maybe(window_mask, "window_mask", torch.int64, (n_rows,), dev), float(softmax_scale),
+        _addr(out, "out", q.dtype, (n_rows, hq, hd), dev), workspace.data_ptr(), workspace.nbytes, _launch_on(dev, stream))
+    _check("attn_verify_paged_q8", st)
+    return out
+
+
+def logits_adjust(logits: torch.Tensor, row_starts: torch.Tensor, penalties: torch.Tensor | None = None,
+                  counts: torch.Tensor | None = None, state_of: torch.Tensor | None = None,
+                  window_tokens: torch.Tensor | None = None, window_mask: torch.Tensor | None = None,
+                  bias_starts: torch.Tensor | None = None, bias_tokens: torch.Tensor | None = None,
+                  bias_values: torch.Tensor | None = None, grammar: torch.Tensor | None = None,
+                  grammar_of: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Logits [n_rows][V] (fp32, fp16 or bf16; rows may be strided) bent by the requests' penalties fp32 [n][3]
+    (repetition, frequency, presence) over counts int32 [n_states][V] and the drafted window_tokens int32 [n_rows],
+    by biases and by grammar masks int32 [n_grammar][ceil(V/32)]; see include/kvq8attn.h.  Returns fp32 out [n_rows][V]
+    (out=logits works in place for fp32); rows of no request are left as they were."""
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+    if logits.dim() != 2 or logits.dtype not in _DTYPE or logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("logits must be [n_rows][V] of float32, float16 or bfloat16 with contiguous rows")
+    rows, vocab = logits.shape
+    n = row_starts.shape[0] - 1
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=f32, device=logits.device) if stream is None else \
+            _scratch(rows * vocab * 4, logits.device, stream).view(f32).view(rows, vocab)
+    if out.dtype is not f32 or out.shape != logits.shape or out.get_device() != dev or (out.stride(1) != 1 and vocab > 1):
+        raise ValueError(f"out must be float32 [{rows}][{vocab}] with contiguous rows on {logits.device}")
+    n_states = 0 if counts is None else counts.shape[0]
+    n_bias = 0 if bias_tokens is None else bias_tokens.shape[0]
+    n_grammar = 0 if grammar is None else grammar.shape[0]
+    st = (_lib or load_library()).logits_adjust(
+        logits.data_ptr(), _DTYPE[logits.dtype], logits.stride(0) if rows > 1 else vocab, rows, vocab,
+        _addr(row_starts, "row_starts", i32, (n + 1,), dev), n, _maybe(penalties, "penalties", f32, (n, 3), dev),
+        _maybe(counts, "counts", i32, (n_states, vocab), dev), n_states,
+        _maybe(state_of, "state_of", i32, (n,), dev), _maybe(window_tokens, "window_tokens", i32, (rows,), dev),
+        _maybe(window_mask, "window_mask", torch.int64, (rows,), dev),
+        _maybe(bias_starts, "bias_starts", i32, (n + 1,), dev),
+        _maybe(bias_tokens, "bias_tokens", i32, (n_bias,), dev),
+        _maybe(bias_values, "bias_values", f32, (n_bias,), dev), n_bias,
+        _maybe(grammar, "grammar", i32, (n_grammar, (vocab + 31) // 32), dev), n_grammar,
+        _maybe(grammar_of, "grammar_of", i32, (rows,), dev), out.data_ptr(), out.stride(0) if rows > 1 else vocab,
+        _launch_on(dev, stream))
+    _check("logits_adjust", st)
+    return out
+
+
+def token_counts(tokens: torch.Tensor, token_starts: torch.Tensor, counts: torch.Tensor,
+                 prompt_lens: torch.Tensor | None = None, state_of: torch.Tensor | None = None, clear: bool = False,
+                 stream=None) -> torch.Tensor:
+    """Count int32 tokens [n_tokens], list i = [token_starts[i], token_starts[i + 1]), into counts int32 [n_states][V]
+    (bit 31: in the prompt; bits 0-30: times generated); clear: the lists' rows start from zero.  Returns counts."""
+    dev, i32 = counts.get_device(), torch.int32
+    n = token_starts.shape[0] - 1
+    if counts.dim() != 2 or tokens.dim() != 1:
+        raise ValueError("counts must be [n_states][V] and tokens [n_tokens]")
+    st = (_lib or load_library()).token_counts(
+        _addr(tokens, "tokens", i32, tuple(tokens.shape), dev), _addr(token_starts, "token_starts", i32, (n + 1,), dev), n,
+        tokens.shape[0], _maybe(prompt_lens, "prompt_lens", i32, (n,), dev),
+        _maybe(state_of, "state_of", i32, (n,), dev), 1 if clear else 0,
+        _addr(counts, "counts", i32, tuple(counts.shape), dev), counts.shape[0], counts.shape[1], _launch_on(dev, stream))
+    _check("token_counts", st)
+    return counts
