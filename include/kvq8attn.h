@@ -516,7 +516,8 @@ size_t attn_verify_paged_q8_workspace_bytes(int n_q_heads, int n_kv_heads, int h
  * K, V and p enter the tensor cores in fp16 (code * scale rounded once), q in fp16 times a power of
  * two per row; scores, softmax statistics and sums are fp32.  Values must stay inside the fp16 range.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, n_q_heads / n_kv_heads > 64, max_rows > 64,
- * n_seqs > 4096, n_rows > 2^24), WORKSPACE, MISALIGNED.
+ * n_seqs > 4096, n_rows > 2^24), WORKSPACE, MISALIGNED (16 bytes; the code planes 32: a block is one
+ * load; int32 arrays 4, window_mask 8).  Two launches.
  */
 int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows, int n_q_heads,
                          const kvq8_paged_cache* kv, const int32_t* page_table, int max_pages, const int32_t* lens,

@@ -76,11 +76,12 @@ VERIFY = dict(q=A, dtype=1, q_stride=1024, n_rows=6, n_q_heads=8, kv=_cache(), p
 @pytest.mark.parametrize("but,status", [
     *[({"kv": _cache(**c)}, s) for c, s in CACHES], *[({k: None}, INVALID) for k in ("q", "out", "page_table", "lens", "row_starts", "kv")],
     ({"dtype": 0}, INVALID), ({"dtype": 9}, INVALID), ({"n_rows": -1}, INVALID), ({"n_seqs": -1}, INVALID), ({"max_pages": 0}, INVALID),
+    ({"kv": _cache(k_codes=A + 16)}, MISALIGNED), ({"kv": _cache(v_codes=A + 16)}, MISALIGNED),
     ({"n_q_heads": 0}, INVALID), ({"max_rows": 0}, INVALID), ({"q_stride": 1023}, INVALID),
     *[({"scale": x}, INVALID) for x in (0.0, -1.0, float("inf"), float("nan"))],
     ({"n_q_heads": 7, "q_stride": 4096}, UNSUPPORTED), ({"n_q_heads": 130, "q_stride": 1 << 20}, UNSUPPORTED), ({"max_rows": 65}, UNSUPPORTED),
     ({"n_seqs": 4097}, UNSUPPORTED), ({"n_rows": 2 ** 24 + 1}, UNSUPPORTED), ({"workspace": None}, WORKSPACE),
-    ({"workspace_bytes": 15}, WORKSPACE), ({"q": A + 8}, MISALIGNED), ({"out": A + 2}, MISALIGNED), ({"workspace": A + 8}, MISALIGNED),
+    ({"workspace_bytes": 152 * 2 * 12 * 128 * 4}, WORKSPACE), ({"q": A + 8}, MISALIGNED), ({"out": A + 2}, MISALIGNED), ({"workspace": A + 8}, MISALIGNED),
     ({"q_stride": 1028}, MISALIGNED), ({"lens": A + 1}, MISALIGNED), ({"page_table": A + 2}, MISALIGNED),
     ({"row_starts": A + 2}, MISALIGNED), ({"window_mask": A + 4}, MISALIGNED), ({"n_rows": 0, "q": None}, OK), ({"n_seqs": 0, "q": None}, OK)])
 def test_verify(but, status):
