@@ -4,28 +4,42 @@
 // key ctx + j where bit j of its mask is set (chains: j <= t):
 //   o = sum_n p_n v_n / sum_n p_n,  p_n = exp(scale * q . k_n),  k and v = code * scale of their block.
 //
-// The T x group rows (row t, head hh of one KV head: t * group + hh) are the M = 128 rows of a tcgen05 tile, so a
-// key tile is read and dequantised once for all of them:
-//   S = Q K^T : A = Q from tensor memory (fp16 pairs), B = K^ [keys][dims] in shared memory (K-major)
-//   O += P V^ : A = P from tensor memory, B = V^ [keys][dims] (MN-major), fp32 accumulation in tensor memory
-// Work: the (request, KV head, 128-row chunk) items, each ceil(len / BN) key tiles, laid end to end and cut into one
-// equal share per SM.  Every CTA works its share out by itself from the lengths on the device (one scan over the
-// requests), so nothing waits for the host and a captured call follows new lengths.  A share holds at most one item
-// that it did not begin and one that it does not end: those leave a partial (o, m, l) in the CTA's two workspace
-// slots, joined by the second kernel; items wholly inside a share are written at once.
+// The T x group rows of a window and KV head (t * group + hh) are few and the keys many, so the products are taken
+// transposed: keys, then dims, are the M = 128 rows of the tcgen05 tiles, the window's rows their N columns.
+//   S^T [128 keys x N]  = K^ [keys x dims] Q^T  : A = K^ in tensor memory, B = Q in shared memory (K-major)
+//   O^T [dims x N]     += V^ [keys x dims]^T P^T : A = V^ (MN-major), B = P [keys x rows] (MN-major), shared memory
+// A tile costs the tensor cores 2 HD / 16 instructions of N columns (about 44 cycles each up to N = 64) where rows as
+// M = 128 cost the full tile whatever the window.
 //
-// Warps of a CTA (each wait between them is an mbarrier wait with an iteration limit):
-//   0-3   softmax: one row per thread, running maximum and sum in registers (fp32), P back to tensor memory
-//   4     issues the MMAs (one thread), owns tensor memory
-//   5-12  dequantise: codes and scales from global memory straight into registers, two tiles ahead, then fp16
-//         (code * scale, rounded once) into three-deep K^ and V^ rings in shared memory.  A thread takes whole
-//         32-value blocks (one 32-byte load and one scale); lanes 0-7 hold eight consecutive keys of the same block,
-//         whose swizzled 16-byte stores fall into different banks.
-// Rows behind len and keys on page ids outside the pool are not read: they enter as zeros and are masked.
+// Work: the (request, KV head) items, each ceil(len / 128) key tiles, laid end to end and cut into one equal share per
+// team of C CTAs, C = the row chunks of the batch's longest window; CTA k of a team takes the k-th part of each item's
+// rows, so the team's CTAs read the same tiles at the same time and all but the first find them in L2.  Every CTA works
+// its share out by itself from the lengths on the device (one scan over the requests), so nothing waits for the host
+// and a captured call follows new lengths.  A share holds at most one item that it did not begin and one that it does
+// not end: those leave a partial (o, m, l) in the CTA's two workspace slots, joined by the second kernel; items wholly
+// inside a share are written at once.
+//
+// Warps of a CTA (every wait is an mbarrier wait with an iteration limit; a role that ran out of patience flags the
+// error and goes on without waiting, so every loop ends and every named barrier is met):
+//   0-3   softmax, one key per thread: p = 2^(s - ref) against a reference maximum per row kept in shared memory.
+//         The references follow only jumps of more than 2^8, found by one vote per tile.
+//         The row sums of the fp16 weights, as the product uses them, by mma.sync against ones (fp32).
+//   4     issues S^T = K^ Q^T; 5 issues O^T += V^T P^T (one thread each)
+//   6, 7  fetch the codes and scales of K and V into a ring of 64-key slots, most of shared memory, by tensor copies of
+//         up to a page (codes, 128-byte swizzle) and bulk copies (scales).  A load takes about 2 us under load, so an
+//         SM's share of the memory's rate is some 90 KB in flight.  Loads held in registers had 40 KB in flight; 16-byte
+//         asynchronous copies stopped at about 16 KB a warp.
+//   8-11  K: one key per thread, codes to fp16 (code * scale, rounded once) into tensor memory
+//   12-15 V: blocks of 8 keys x 4 per step into a 128-byte-swizzled tile in shared memory, 64 keys at a time
+// Keys on page ids outside the pool are not fetched.  Those and the rows behind len in a page enter V^ as zeros, and
+// their scores are masked whatever they are.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 #include "tc.cuh"
+#include "tmap.cuh"
 
 namespace kvq8 {
 
@@ -33,37 +47,54 @@ unsigned int* device_error_flag();
 
 namespace {
 
-constexpr int kRows = 128;                  // rows of a tile
-constexpr int kIssueWarp = 4, kDeqWarp0 = 5, kDeqWarps = 8;
-constexpr int kVerifyThreads = (kDeqWarp0 + kDeqWarps) * 32;
-constexpr int kStages = 3;                  // K^ and V^ tiles in shared memory
+constexpr int BN = 128;                     // keys of a tile
+constexpr int kQkWarp = 4, kPvWarp = 5, kFetchWarp0 = 6, kKWarp0 = 8, kVWarp0 = 12;
+constexpr int kVerifyThreads = 512;
+constexpr int kSoftThreads = 128;
 constexpr uint32_t kPollLimit = 1u << 24;
-constexpr float kLazy = 8.0f;               // the running maximum follows only jumps of more than 2^8
-constexpr float kLift = 6.0f;               // p is 2^6 larger than 2^(s - m): at most 2^14, and fp16 keeps it to 2^-30
+constexpr float kLazy = 8.0f;               // the references follow only jumps of more than 2^8
+constexpr float kLift = 6.0f;               // p is 2^6 larger than 2^(s - ref): at most 2^14, and fp16 keeps it to 2^-30
+constexpr float kNoRef = -1e30f;            // the reference of a row that has seen no key yet
 constexpr uint32_t kTmemCols = 512;
 
-__host__ __device__ constexpr int keys_per_tile(int hd) { return hd == 128 ? 128 : 64; }
-
-// Barriers, a ring of kStages each: K^ written, V^ written, S complete (and K^ free), P written, PV complete (and V^
-// free).  Tile j uses entry j % kStages; its next use needs tile j + kStages, which needs every wait on this one.
-enum { kBarK = 0, kBarV = kStages, kBarS = 2 * kStages, kBarP = 3 * kStages, kBarO = 4 * kStages, kBarQ = 5 * kStages,
-       kBarCount = 5 * kStages + 1 };
-
-template <int HD>
+// Shapes: NMAX rows of a chunk, 32 or 64; NK tiles of K^ in tensor memory, NV of V^ and two of weights in shared memory;
+// the fetch ring takes what is left of that.  Up to 32 rows the two weight tiles are the halves of one 64-row atom.
+template <int HD, int NMAX>
 struct VL {
-    static constexpr int BN = keys_per_tile(HD);
-    static constexpr int kTile = BN * HD * 2;              // bytes of one fp16 tile
-    static constexpr int kSmK = 0, kSmV = kStages * kTile, kSmBar = 2 * kStages * kTile;
-    static constexpr int kSmTmem = kSmBar + kBarCount * 8, kSmScan = (kSmTmem + 4 + 15) / 16 * 16;
-    static constexpr int kSmBytes = kSmScan + 64 + (kVerifyThreads / 32) * 8;
-    static constexpr uint32_t kTmQ = 0, kTmO = HD / 2, kTmS = kTmO + HD;
-    static constexpr uint32_t kIdescS = tc::idesc_f16_f32(kRows, BN, false), kIdescO = tc::idesc_f16_f32(kRows, HD, true);
-    // a dequantising warp covers 8 keys x 4 blocks at a time; passes per plane and tile
-    static constexpr int kUnits = BN * HD / 32 / 32 / kDeqWarps;
-    static_assert(kUnits == 2, "two passes");
-    static constexpr int kPages = HD == 256 ? 1 : 2;       // distinct keys of a thread per tile
-    static_assert(kTmS + 2 * BN <= kTmemCols, "tensor memory");
-    static_assert(kSmBytes <= 227 * 1024, "shared memory");
+    static constexpr bool kSmall = NMAX <= 32;
+    static constexpr int NK = 2, NV = HD == 256 ? 1 : 2;
+    static constexpr int kTile = BN * HD * 2;
+    static constexpr int kPNext = kSmall ? 64 : BN * 128;  // from one weight tile to the other
+    static constexpr int kSmPBytes = kSmall ? BN * 128 : 2 * BN * 128;
+    static constexpr int kSmV = 0, kSmQ = NV * kTile, kSmP = kSmQ + HD / 64 * NMAX * 128, kSmTab = kSmP + kSmPBytes;
+    // tables: per row reference, lifted negative reference, factor of the last raise, output row and window mask (two
+    // segments each); maxima, the tile's row sums and row sums per softmax
+    // warp
+    static constexpr int kTabRef = 0, kTabNeg = kTabRef + 4 * NMAX, kTabAlpha = kTabNeg + 4 * NMAX,
+                         kTabRow = kTabAlpha + 4 * NMAX, kTabMax = kTabRow + 8 * NMAX,
+                         kTabTile = kTabMax + 16 * NMAX, kTabSum = kTabTile + 16 * NMAX, kTabMask = kTabSum + 16 * NMAX,
+                         kTabMisc = kTabMask + 16 * NMAX;
+    static constexpr int kSmScan = kSmTab + kTabMisc + 32, kSmTmem = kSmScan + 48 + (kVerifyThreads / 32) * 8;
+    static constexpr int kSmBar = kSmTmem + 16;
+    // fetch slots: 64 keys of codes, [128-byte half of the head][key][128 bytes] with the 16-byte chunks of key n at
+    // chunk ^ n % 8; their scales apart
+    static constexpr int kCodes = 64 * HD, kScales = 64 * HD / 16, kMaxSlots = 16;
+    static constexpr int kSmSlots = (kSmBar + (2 * kMaxSlots + 19) * 8 + 1023) / 1024 * 1024;
+    static constexpr int kFit = (227 * 1024 - kSmSlots) / (kCodes + kScales), R = kFit < kMaxSlots ? kFit : kMaxSlots;
+    // K and V have rings of their own (slots 0 .. RK - 1 and the rest), and a K slot always serves the same half of a tile:
+    // every wait is then for the use just before or the one after it, by roles that saw that one, as parities need
+    static constexpr int RK = (R + 1) / 2 / 2 * 2, RV = R - RK;
+    static_assert(RK >= 2 && RV >= 2, "a tile of each");
+    static constexpr int kSmScales = kSmSlots + R * kCodes, kSmBytes = kSmScales + R * kScales;
+    // barriers: fetch slot full / free; 64-key halves of V^ written / used (two of each tile); then pairs by tile: K^
+    // written, scores ready, weights ready, product done; then queries ready
+    static constexpr int kFull = 0, kFree = R, kV = 2 * R, kVFree = kV + 4, kK = kVFree + 4, kS = kK + 2, kP = kS + 2, kO = kP + 2,
+                         kQ = kO + 2;
+    static constexpr int kMt = HD / 128;                   // 128-dim tiles of O^T
+    static constexpr uint32_t kTmO = 0, kTmS = kMt * NMAX, kTmK = kTmS + 2 * NMAX;
+    static_assert(kTmK + NK * HD / 2 <= kTmemCols, "tensor memory");
+    static_assert(R >= 4 && kSmBytes <= 227 * 1024, "shared memory");
+    static_assert(kSmQ % 1024 == 0 && kSmP % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
 };
 
 struct PagedVerifyParams {
@@ -78,33 +109,33 @@ struct PagedVerifyParams {
     const int32_t* lens;
     const int32_t* row_starts;
     const uint64_t* mask;
-    float* part_o;     // [grid][2][part_rows][HD]
-    float2* part_ml;   // [grid][2][part_rows] (m in log2 units, l)
-    int4* joins;       // [grid]: the item that CTA c begins and does not end (first q row, KV head, rows, last CTA)
+    float* part_o;     // [grid][2][chunk][HD]
+    float2* part_ml;   // [grid][2][chunk] (m in log2 units, l)
+    int4* joins;       // [grid]: the item that CTA c begins and does not end (first q row, KV head, rows, last team)
     unsigned int* error;
-    int n_rows, n_q_heads, n_kv_heads, group, n_pages, page_shift, max_pages, n_seqs, max_rows, part_rows;
-    float scale_log2;
+    int n_rows, n_q_heads, n_kv_heads, group, n_pages, page_shift, max_pages, n_seqs, max_rows, chunk, team;
+    float scale_log2, per_group;  // per_group = 1 / group
+    // code planes as (head_dim bytes, rows of n_pages * n_kv_heads * page_size), boxes of 128 bytes x `box` keys
+    CUtensorMap tmap_k, tmap_v;
+    int box;
 };
 
 // ---------------------------------------------------------------- the shares
 
-// A request as the kernel sees it; items = 0 where there is nothing to do or its numbers make no sense.
+// A request as the kernel sees it; tiles = 0 where there is nothing to do or its numbers make no sense.
 struct Request {
-    int len, rows, row0, tiles, items;
+    int len, rows, row0, tiles;
 };
 
-template <int BN>
 __device__ __forceinline__ Request request_of(const PagedVerifyParams& p, int b) {
     Request q;
     q.row0 = __ldg(p.row_starts + b);
     const int end = __ldg(p.row_starts + b + 1);
     q.len = __ldg(p.lens + b);
-    q.tiles = q.items = q.rows = 0;
-    if (q.row0 < 0 || end > p.n_rows || end <= q.row0) return q;
     q.rows = end - q.row0;
-    if (q.rows > p.max_rows || q.rows > q.len || (int64_t)q.len > ((int64_t)p.max_pages << p.page_shift)) return q;
-    q.tiles = (int)(((int64_t)q.len + BN - 1) / BN);
-    q.items = p.n_kv_heads * ((q.rows * p.group + kRows - 1) / kRows);
+    const bool good = q.row0 >= 0 && end <= p.n_rows && end > q.row0 && q.rows <= p.max_rows && q.rows <= q.len &&
+                      (int64_t)q.len <= ((int64_t)p.max_pages << p.page_shift);
+    q.tiles = good ? (int)(((unsigned)q.len + BN - 1) / BN) : 0;
     return q;
 }
 
@@ -118,34 +149,56 @@ struct Segment {
 
 // A CTA's share, segment by segment.  Each role walks it on its own.
 struct Walk {
-    int b, item, t;
+    int b, kvh, t;
     long long left;
     Request q;
 
-    template <int BN>
     __device__ __forceinline__ bool next(const PagedVerifyParams& p, Segment& s) {
-        if (left <= 0) return false;
-        while (item >= q.items) {
-            item = 0;
-            if (++b >= p.n_seqs) return false;
-            q = request_of<BN>(p, b);
+#pragma unroll 1
+        while (left > 0) {
+#pragma unroll 1
+            while (kvh == p.n_kv_heads || q.tiles == 0) {
+                kvh = 0;
+                if (++b >= p.n_seqs) return false;
+                q = request_of(p, b);
+            }
+            s.b = b;
+            s.kvh = kvh;
+            // the team's equal parts of the rows, so that no CTA pays for a tile of a few rows
+            const int rows = q.rows * p.group;
+            s.r0 = 0;
+            s.n = rows;
+            if (p.team > 1) {
+                const int per = (rows + p.team - 1) / p.team;
+                s.r0 = (int)(blockIdx.x % p.team) * per;
+                s.n = min(per, rows - s.r0);
+            }
+            s.t0 = t;
+            s.t1 = (int)min((long long)q.tiles, t + left);
+            s.q = q;
+            left -= s.t1 - s.t0;
+            t = s.t1;
+            if (t == q.tiles) {
+                t = 0;
+                ++kvh;
+            }
+            if (s.n > 0) return true;  // fewer rows than CTAs in the team: some have none
         }
-        const int chunks = q.items / p.n_kv_heads;
-        s.b = b;
-        s.kvh = item / chunks;
-        s.r0 = (item - s.kvh * chunks) * kRows;
-        s.n = min(kRows, q.rows * p.group - s.r0);
-        s.t0 = t;
-        s.t1 = (int)min((long long)q.tiles, t + left);
-        s.q = q;
-        left -= s.t1 - s.t0;
-        t = s.t1;
-        if (t == q.tiles) {
-            t = 0;
-            ++item;
-        }
-        return true;
+        return false;
     }
+};
+
+// The window row of row rr of an item, rr / group: rr is below 2^12 and group at most 64, so rr + 1/2 is further from a
+// multiple of group than the product's rounding.
+__device__ __forceinline__ int window_row(const PagedVerifyParams& p, int rr) { return (int)(((float)rr + 0.5f) * p.per_group); }
+
+__device__ __noinline__ long long divide(long long a, long long b) { return a / b; }
+
+// Shares of u units: every team below `shares` gets base of them, the first `rest` one more.
+struct Shares {
+    long long base, rest;
+    int shares;
+    __device__ __forceinline__ long long begin(int c) const { return c < shares ? c * base + min((long long)c, rest) : base * shares + rest; }
 };
 
 // Exclusive sum over the block of one value per thread, and the total; all threads call it.
@@ -171,69 +224,52 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* s_w
 
 // ---------------------------------------------------------------- dequantising
 
-struct Block {           // one 32-value block: its codes and its scale
-    uint32_t w[8];
-    uint32_t scale;
-};
-
-__device__ __forceinline__ void load_block(Block& x, const int8_t* codes, const uint16_t* scales, int64_t block, bool on) {
-    if (on) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]), "=r"(x.w[6]), "=r"(x.w[7])
-                     : "l"(codes + block * 32));
-        x.scale = __ldg(scales + block);
-    } else {
+// Sixteen codes as eight fp16 pairs, code * scale rounded once.
+__device__ __forceinline__ void values16(uint4 codes, __half2 scale, uint32_t* h) {
+    const uint32_t w[4] = {codes.x ^ 0x80808080u, codes.y ^ 0x80808080u, codes.z ^ 0x80808080u, codes.w ^ 0x80808080u};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x.w[i] = 0u;
-        x.scale = 0u;
+    for (int e = 0; e < 4; ++e) {
+        h[2 * e] = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4140>(w[e])), scale));
+        h[2 * e + 1] = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4342>(w[e])), scale));
     }
 }
 
-// The block as fp16, code * scale rounded once, at [key n][block] of a 128-byte-swizzled tile: 64-dim atoms of BN
-// rows of 128 bytes, the 16-byte chunks of row n stored at chunk ^ (n % 8).
-template <int BN>
-__device__ __forceinline__ void store_block(const Block& x, uint8_t* tile, int n, int block) {
-    const __half2 sc = __half2half2(__ushort_as_half((unsigned short)x.scale));
-    uint8_t* row = tile + (block >> 1) * (BN * 128) + (n >> 3) * 1024 + (n & 7) * 128;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t w = x.w[2 * k + e] ^ 0x80808080u;
-            h[2 * e] = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4140>(w)), sc));
-            h[2 * e + 1] = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4342>(w)), sc));
-        }
-        *reinterpret_cast<uint4*>(row + (((4 * (block & 1) + k) ^ (n & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+// Chunk c (16 codes) of key n of a fetch slot.
+__device__ __forceinline__ int code_at(int n, int c) { return (c >> 3) * 8192 + n * 128 + (((c ^ n) & 7) << 4); }
+
+// One box of a plane's tensor map into shared memory, completion counted in bytes.  x is 0 or 128: copies start on
+// 16-byte boundaries.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
+        : "memory");
 }
 
-// ---------------------------------------------------------------- queries and output
+// ---------------------------------------------------------------- queries
 
-// Sixteen-byte pieces of a query row as fp16 pairs.  fp16 rows go in as they are; bf16 rows times a power of two that
-// brings their largest element into [2^7, 2^8), undone in the score's scale.
+// Queries as fp16 pairs.  fp16 rows go in as they are; bf16 rows of a chunk times one power of two that brings the
+// chunk's largest element into [2^14, 2^15), undone in the scores' scale.  A row 2^k below the largest keeps its
+// precision to 2^(39 - k) below its own largest, and its scores are as much smaller.
 template <typename T>
 struct Query;
 template <>
 struct Query<__half> {
-    static __device__ __forceinline__ float lift(const uint4*, int) { return 1.0f; }
-    static __device__ __forceinline__ float drop(float) { return 1.0f; }
+    static constexpr bool kLifted = false;
+    static __device__ __forceinline__ uint32_t top(uint4) { return 0u; }
     static __device__ __forceinline__ uint32_t pair(uint32_t w, float) { return w; }
     static __device__ __forceinline__ uint32_t out(float a, float b) { return h2_as_u32(__floats2half2_rn(a, b)); }
+    static __device__ __forceinline__ uint16_t one(float a) { return __half_as_ushort(__float2half_rn(a)); }
 };
 template <>
 struct Query<__nv_bfloat16> {
-    static __device__ __forceinline__ float lift(const uint4* row, int pieces) {
-        uint32_t top = 0;
-        for (int c = 0; c < pieces; ++c) {
-            const uint4 v = __ldg(row + c);
-            for (uint32_t w : {v.x, v.y, v.z, v.w}) top = max(top, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
-        }
-        const int e = (int)(top >> 7);                      // biased exponent
-        if (e == 0 || e == 255) return 1.0f;                // zeros and subnormals; not finite
-        return __uint_as_float((uint32_t)min(127 + 127 + 7 - e, 254) << 23);
+    static constexpr bool kLifted = true;
+    // the largest magnitude's bits (NaN and infinity above all)
+    static __device__ __forceinline__ uint32_t top(uint4 v) {
+        uint32_t t = 0;
+        for (uint32_t w : {v.x, v.y, v.z, v.w}) t = max(t, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+        return t;
     }
-    static __device__ __forceinline__ float drop(float lifted) { return 1.0f / lifted; }  // a power of two: exact
     static __device__ __forceinline__ uint32_t pair(uint32_t w, float lifted) {
         return h2_as_u32(__floats2half2_rn(__uint_as_float(w << 16) * lifted, __uint_as_float(w & 0xffff0000u) * lifted));
     }
@@ -241,40 +277,75 @@ struct Query<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+    static __device__ __forceinline__ uint16_t one(float a) { return __bfloat16_as_ushort(__float2bfloat16_rn(a)); }
 };
 
-// Bit c = a row with window mask m sees key key0 + c: keys before ctx, then its mask's bits.
-__device__ __forceinline__ uint64_t seen64(long long key0, int ctx, uint64_t m) {
-    const long long before = ctx - key0;  // keys of this group before the window
-    if (before >= 64) return ~0ull;
-    if (before > 0) return ((1ull << before) - 1) | (m << before);
-    return before > -64 ? m >> -before : 0ull;
+// The power of two that brings a bf16 magnitude (its bits) into [2^14, 2^15); 1 for zeros, subnormals and what is
+// not finite.
+__device__ __forceinline__ float lift_of(uint32_t top) {
+    const int e = (int)(top >> 7);
+    if (e == 0 || e == 255) return 1.0f;
+    return __uint_as_float((uint32_t)min(127 + 127 + 14 - e, 254) << 23);
 }
 
-template <typename T, int HD>
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+    return one;
+}
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n bar.red.or.pred b, 1, 128, a;\n selp.u32 %0, 1, 0, b;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
+}
+
+// Maximum over a warp of floats, by their order-preserving integers.
+__device__ __forceinline__ float warp_max(float x) {
+    int i = __float_as_int(x);
+    i ^= (i >> 31) & 0x7fffffff;
+    i = __reduce_max_sync(0xffffffffu, i);
+    return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+template <typename T, int HD, int NMAX>
 __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const __grid_constant__ PagedVerifyParams p) {
-    using L = VL<HD>;
-    constexpr int BN = L::BN;
+    using L = VL<HD, NMAX>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = smem_u32(smem), bar = sbase + L::kSmBar;
     auto B = [&](int id) { return bar + 8u * (uint32_t)id; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSmTmem);
-    long long* s_start = reinterpret_cast<long long*>(smem + L::kSmScan);  // the request of the first unit, units into it
-    long long* s_warp = s_start + 8;
+    Shares* s_cut = reinterpret_cast<Shares*>(smem + L::kSmScan);
+    int* s_start = reinterpret_cast<int*>(smem + L::kSmScan + 32);  // request, KV head and tile of the first unit
+    long long* s_warp = reinterpret_cast<long long*>(smem + L::kSmScan + 48);
 
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(B(kBarK + s), kDeqWarps);
-            tc::mbar_init(B(kBarV + s), kDeqWarps);
-            tc::mbar_init(B(kBarS + s), 1);
-            tc::mbar_init(B(kBarP + s), 4);
-            tc::mbar_init(B(kBarO + s), 1);
+#pragma unroll 1
+        for (int s = 0; s < L::R; ++s) {
+            tc::mbar_init(B(L::kFull + s), 1);
+            tc::mbar_init(B(L::kFree + s), s < L::RK ? 2 : 4);  // the warps that read it
         }
-        tc::mbar_init(B(kBarQ), 4);
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+            tc::mbar_init(B(L::kV + s), 4);
+            tc::mbar_init(B(L::kVFree + s), 1);
+        }
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(B(L::kK + s), 4);
+            tc::mbar_init(B(L::kS + s), 1);
+            tc::mbar_init(B(L::kP + s), 4);
+            tc::mbar_init(B(L::kO + s), 1);
+        }
+        tc::mbar_init(B(L::kQ), 4);
         tc::mbar_init_fence();
     }
-    if (warp == kIssueWarp) tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    if (warp == kQkWarp) tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -282,22 +353,31 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     const int per = (p.n_seqs + kVerifyThreads - 1) / kVerifyThreads;
     const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
     long long mine = 0, units;
+#pragma unroll 1
     for (int b = b_lo; b < b_hi; ++b) {
-        const Request q = request_of<BN>(p, b);
-        mine += (long long)q.tiles * q.items;
+        const Request q = request_of(p, b);
+        mine += (long long)q.tiles * p.n_kv_heads;
     }
     const long long before = block_exclusive(mine, s_warp, units);
     // no more shares than units: every share of an item that was cut has tiles of it, and so a partial
-    const long long shares = units < gridDim.x ? units : (long long)gridDim.x, me = blockIdx.x;
-    const long long u0 = me < shares ? me * units / shares : units, u1 = me < shares ? (me + 1) * units / shares : units;
+    const int me = blockIdx.x / p.team;
+    if (tid == 0) {
+        s_cut->shares = (int)min(units, (long long)(gridDim.x / p.team));
+        s_cut->base = s_cut->shares ? divide(units, s_cut->shares) : 0;
+        s_cut->rest = units - s_cut->base * s_cut->shares;
+    }
+    __syncthreads();
+    const long long u0 = s_cut->begin(me), u1 = s_cut->begin(me + 1);
     if (u0 < u1 && before <= u0 && u0 < before + mine) {
         long long at = before;
+#pragma unroll 1
         for (int b = b_lo; b < b_hi; ++b) {
-            const Request q = request_of<BN>(p, b);
-            const long long here = (long long)q.tiles * q.items;
+            const Request q = request_of(p, b);
+            const long long here = (long long)q.tiles * p.n_kv_heads;
             if (u0 < at + here) {
                 s_start[0] = b;
-                s_start[1] = u0 - at;
+                s_start[1] = (int)divide(u0 - at, q.tiles);
+                s_start[2] = (int)(u0 - at - (long long)s_start[1] * q.tiles);
                 break;
             }
             at += here;
@@ -310,322 +390,537 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     Walk walk;
     walk.left = u1 - u0;
     walk.b = p.n_seqs;
-    walk.item = walk.t = 0;
-    walk.q.items = 0;
+    walk.kvh = walk.t = 0;
+    walk.q.tiles = 0;
     if (u0 < u1) {
-        walk.b = (int)s_start[0];
-        walk.q = request_of<BN>(p, walk.b);
-        walk.item = (int)(s_start[1] / walk.q.tiles);
-        walk.t = (int)(s_start[1] - (long long)walk.item * walk.q.tiles);
+        walk.b = s_start[0];
+        walk.kvh = s_start[1];
+        walk.t = s_start[2];
+        walk.q = request_of(p, walk.b);
     }
     Segment seg;
     bool ok = true;
+    // After a time-out the role runs on without waiting.  (Loops in this kernel are kept rolled: the roles' code together
+    // should stay in the instruction caches, and stalls for instructions were a quarter of all before.)
+    auto wait = [&](int id, int phase) {
+        if (!ok) return;
+        const uint32_t at = B(id), parity = (uint32_t)phase & 1u;
+#pragma unroll 1
+        for (uint32_t i = 0; i < kPollLimit; ++i)
+            if (tc::mbar_try_wait(at, parity)) return;
+        ok = false;
+    };
 
-    if (warp == kIssueWarp) {
-        if (lane == 0) {
-            const uint64_t kdesc0 = tc::smem_desc_sw128(sbase + L::kSmK, 16, 1024);
-            const uint64_t vdesc0 = tc::smem_desc_sw128(sbase + L::kSmV, BN * 128, 1024);
-            int st = 0, s_ph = 0, q_ph = 0, sb = 0;  // ring entry and phase of tile j; S buffer j % 2
-            auto pv = [&](int st1, int ph1, int sb1, bool first) {
-                if (!tc::mbar_wait(B(kBarP + st1), ph1, kPollLimit) || !tc::mbar_wait(B(kBarV + st1), ph1, kPollLimit)) return false;
+    if (warp == kQkWarp) {
+        const uint32_t one = elect_one();
+        const uint64_t qd = tc::smem_desc_sw128(sbase + L::kSmQ, 16, 1024);
+        int j = 0, segs = 0;
+#pragma unroll 1
+        while (walk.next(p, seg)) {
+            wait(L::kQ, segs++);
+            const uint32_t idesc = tc::idesc_f16_f32_ab(BN, (seg.n + 15) & ~15, false, false);
+#pragma unroll 1
+            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
+                wait(L::kK + j % L::NK, j / L::NK);
+                if (j >= 2) wait(L::kP + (j & 1), (j - 2) >> 1);  // the scores of tile j - 2 have been read
                 tc::fence_after_sync();
-                const uint64_t vd = vdesc0 + (uint64_t)((st1 * L::kTile) >> 4);
-#pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
-                    tc::mma_ts(tmem + L::kTmO, tmem + L::kTmS + sb1 * BN + k * 8, vd + (uint64_t)((k * 2048) >> 4), L::kIdescO,
-                               (!first || k > 0) ? 1u : 0u);
-                tc::mma_commit(B(kBarO + st1));
-                return true;
-            };
-            while (ok && walk.next<BN>(p, seg)) {
-                if (!tc::mbar_wait(B(kBarQ), q_ph, kPollLimit)) { ok = false; break; }
-                q_ph ^= 1;
-                tc::fence_after_sync();
-                int st1 = 0, ph1 = 0, sb1 = 0;
-                for (int t = seg.t0; t < seg.t1; ++t) {
-                    if (!tc::mbar_wait(B(kBarK + st), s_ph, kPollLimit)) { ok = false; break; }
-                    tc::fence_after_sync();
-                    const uint64_t kd = kdesc0 + (uint64_t)((st * L::kTile) >> 4);
-                    // S overwrites the columns that held P of tile j - 2, whose PV was issued before (issue order holds)
+                if (one) {
+                    const uint32_t d = tmem + L::kTmS + (j & 1) * NMAX, k0 = tmem + L::kTmK + (j % L::NK) * (HD / 2);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k)
-                        tc::mma_ts(tmem + L::kTmS + sb * BN, tmem + L::kTmQ + k * 8,
-                                   kd + (uint64_t)((((k >> 2) * (BN * 128)) + (k & 3) * 32) >> 4), L::kIdescS, k > 0 ? 1u : 0u);
-                    tc::mma_commit(B(kBarS + st));
-                    if (t > seg.t0 && !pv(st1, ph1, sb1, t - 1 == seg.t0)) { ok = false; break; }
-                    st1 = st, ph1 = s_ph, sb1 = sb;
-                    sb ^= 1;
-                    if (++st == kStages) st = 0, s_ph ^= 1;
+                        tc::mma_ts(d, k0 + 8 * k, qd + (uint64_t)(((k >> 2) * (NMAX * 128) + (k & 3) * 32) >> 4), idesc,
+                                   k > 0 ? 1u : 0u);
+                    tc::mma_commit(B(L::kS + (j & 1)));
                 }
-                if (ok && !pv(st1, ph1, sb1, seg.t1 - 1 == seg.t0)) ok = false;
-            }
-            if (!ok) atomicOr(p.error, 1u);
-        }
-        __syncwarp();
-    } else if (warp < 4) {
-        const int r = warp * 32 + lane;
-        const uint32_t rows_tm = tmem + ((uint32_t)(warp * 32) << 16);
-        int st = 0, ph = 0, sb = 0;
-        while (ok && walk.next<BN>(p, seg)) {
-            const bool busy = warp * 32 < seg.n, valid = r < seg.n;  // a warp without rows only keeps the barriers going
-            const int rr = seg.r0 + (valid ? r : 0), t_row = rr / p.group;
-            const int head = seg.kvh * p.group + rr - t_row * p.group, row = seg.q.row0 + t_row;
-            const int ctx = seg.q.len - seg.q.rows;
-            uint64_t m64 = 0;
-            float cs = p.scale_log2;
-            if (busy) {
-                if (valid) {
-                    m64 = p.mask ? __ldg(p.mask + row) : (2ull << t_row) - 1;
-                    if (seg.q.rows < 64) m64 &= (1ull << seg.q.rows) - 1;
-                }
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (int64_t)row * p.q_stride +
-                                                                  (int64_t)head * HD);
-                const float lifted = Query<T>::lift(src, HD / 8);
-                cs *= Query<T>::drop(lifted);
-#pragma unroll 1
-                for (int c = 0; c < HD / 64; ++c) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint4 v = __ldg(src + c * 8 + k);
-                        w[4 * k] = Query<T>::pair(v.x, lifted);
-                        w[4 * k + 1] = Query<T>::pair(v.y, lifted);
-                        w[4 * k + 2] = Query<T>::pair(v.z, lifted);
-                        w[4 * k + 3] = Query<T>::pair(v.w, lifted);
-                    }
-                    tc::tmem_st32(rows_tm + L::kTmQ + 32 * c, w);
-                }
-                tc::tmem_wait_st();
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(B(kBarQ));
-
-            float m = -INFINITY, l = 0.0f;
-            const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
-            // page ids of the tile's 16-key groups, one per lane, loaded a tile ahead
-            auto page_of = [&](int t) {
-                const long long key = (long long)t * BN + 16 * lane;
-                return lane < BN / 16 && t < seg.t1 && key < seg.q.len ? __ldg(pages + (key >> p.page_shift)) : 0;
-            };
-            int page = busy ? page_of(seg.t0) : 0;
-            int o_st = 0, o_ph = 0;
-            for (int t = seg.t0; t < seg.t1; ++t) {
-                if (!__all_sync(0xffffffffu, tc::mbar_wait(B(kBarS + st), ph, kPollLimit))) { ok = false; break; }
-                tc::fence_after_sync();
-                if (busy) {
-                    const uint32_t bad = __ballot_sync(0xffffffffu, page < 0 || page >= p.n_pages);
-                    page = page_of(t + 1);
-                    const uint32_t scol = rows_tm + L::kTmS + sb * BN;
-                    const long long key0 = (long long)t * BN;
-                    const bool whole = key0 + BN <= ctx && !bad;
-                    auto load = [&](int h, float (&x)[64]) {  // scores of keys 64 h .. 64 h + 63 of the tile
-                        uint32_t a[32], b[32];
-                        tc::tmem_ld32(scol + 64 * h, a);
-                        tc::tmem_ld32(scol + 64 * h + 32, b);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(a[c]), x[32 + c] = __uint_as_float(b[c]);
-                        if (!whole) {
-                            uint64_t see = seen64(key0 + 64 * h, ctx, m64);
-#pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                if (bad >> (4 * h + g) & 1) see &= ~(0xffffull << (16 * g));
-                            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                if (!(lo >> c & 1)) x[c] = -INFINITY;
-                                if (!(hi >> c & 1)) x[32 + c] = -INFINITY;
-                            }
-                        }
-                    };
-                    float x[64], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int h = 0; h < BN / 64; ++h) {
-                        load(h, x);
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
-                    }
-                    const float m_new = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * cs);
-                    const bool raise = m_new > m + kLazy || (m == -INFINITY && m_new != -INFINITY);
-                    if (__any_sync(0xffffffffu, raise)) {
-                        float a = 1.0f;
-                        if (raise) {
-                            a = m == -INFINITY ? 0.0f : ex2_approx(m - m_new);
-                            m = m_new;
-                            l *= a;
-                        }
-                        if (t > seg.t0) {  // every earlier PV has landed before its rows are scaled
-                            if (!__all_sync(0xffffffffu, tc::mbar_wait(B(kBarO + o_st), o_ph, kPollLimit))) { ok = false; break; }
-                            tc::fence_after_sync();
-#pragma unroll 1
-                            for (int c = 0; c < HD / 32; ++c) {
-                                uint32_t o[32];
-                                tc::tmem_ld32(rows_tm + L::kTmO + 32 * c, o);
-                                tc::tmem_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
-                                tc::tmem_st32(rows_tm + L::kTmO + 32 * c, o);
-                            }
-                        }
-                    }
-                    const bool live = m != -INFINITY;
-                    const float off = live ? kLift - m : 0.0f;
-#pragma unroll 1
-                    for (int h = 0; h < BN / 64; ++h) {
-                        if (BN > 64) load(h, x);
-                        uint32_t pk[32];
-                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float a = live ? ex2_approx(fmaf(x[2 * c], cs, off)) : 0.0f;
-                            const float b = live ? ex2_approx(fmaf(x[2 * c + 1], cs, off)) : 0.0f;
-                            sum[2 * (c & 1)] += a;
-                            sum[2 * (c & 1) + 1] += b;
-                            pk[c] = h2_as_u32(__floats2half2_rn(a, b));
-                        }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                        // P of half h goes over columns 32 h .. 32 h + 31, whose scores have been read
-                        tc::tmem_st32(scol + 32 * h, pk);
-                    }
-                    tc::tmem_wait_st();
-                }
-                tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(B(kBarP + st));
-                o_st = st, o_ph = ph;
-                sb ^= 1;
-                if (++st == kStages) st = 0, ph ^= 1;
             }
-            if (!ok) break;
-            if (!__all_sync(0xffffffffu, tc::mbar_wait(B(kBarO + o_st), o_ph, kPollLimit))) { ok = false; break; }
-            tc::fence_after_sync();
-            if (busy) {
-                const bool whole = seg.begins() && seg.ends();
-                const int slot = 2 * blockIdx.x + (seg.begins() ? 1 : 0);
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ((int64_t)row * p.n_q_heads + head) * HD);
-                float4* part = reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * p.part_rows + (valid ? r : 0)) * HD);
-#pragma unroll 1
-                for (int c = 0; c < HD / 32; ++c) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(rows_tm + L::kTmO + 32 * c, o);
-                    tc::tmem_wait_ld();
-                    if (!valid) continue;
-                    auto f = [&](int k) { return __uint_as_float(o[k]); };
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t y[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                y[e] = l > 0.0f ? Query<T>::out(f(8 * k + 2 * e) * inv, f(8 * k + 2 * e + 1) * inv) : 0u;
-                            dst[4 * c + k] = make_uint4(y[0], y[1], y[2], y[3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) part[8 * c + k] = make_float4(f(4 * k), f(4 * k + 1), f(4 * k + 2), f(4 * k + 3));
-                    }
-                }
-                if (valid && !whole) p.part_ml[(int64_t)slot * p.part_rows + r] = make_float2(m, l);
-            }
-            tc::fence_before_sync();
         }
         if (!ok) atomicOr(p.error, 1u);
-    } else {
-        // blocks of this thread in a tile: hd256, blocks jj and 4 + jj of key 8 w + nn; hd128, block jj of keys
-        // 8 w + nn and 64 + 8 w + nn
-        const int w = warp - kDeqWarp0, nn = lane & 7, jj = lane >> 3;
-        int st = 0, ph = 0;
-        Block kx[2][2], vx[2][2];
-        // the tile whose page ids are being fetched: a tile ahead of the loads
-        int page[L::kPages], off[L::kPages];
-        int t = 0;
+    } else if (warp == kPvWarp) {
+        const uint32_t one = elect_one();
+        const uint64_t vd0 = tc::smem_desc_sw128(sbase + L::kSmV, BN * 128, 1024);
+        const uint64_t pd0 = tc::smem_desc_sw128(sbase + L::kSmP, BN * 128, 1024);
+        int j = 0;
+#pragma unroll 1
+        while (walk.next(p, seg)) {
+            const uint32_t idesc = tc::idesc_f16_f32_ab(128, (seg.n + 15) & ~15, true, true);
+#pragma unroll 1
+            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
+                wait(L::kP + (j & 1), j >> 1);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int v = 2 * (j % L::NV) + half;
+                    wait(L::kV + v, j / L::NV);
+                    tc::fence_after_sync();
+                    if (one) {
+                        const uint64_t vd = vd0 + (uint64_t)(((j % L::NV) * L::kTile + half * 8192) >> 4);
+                        const uint64_t pd = pd0 + (uint64_t)(((j & 1) * L::kPNext + half * 8192) >> 4);
+                        const uint32_t more = t > seg.t0 || half ? 1u : 0u;
+#pragma unroll
+                        for (int m = 0; m < L::kMt; ++m)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_ss(tmem + L::kTmO + m * NMAX, vd + (uint64_t)((m * 2 * BN * 128 + k * 2048) >> 4),
+                                           pd + (uint64_t)((k * 2048) >> 4), idesc, k > 0 ? 1u : more);
+                        tc::mma_commit(B(L::kVFree + v));
+                        if (half) tc::mma_commit(B(L::kO + (j & 1)));
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (!ok) atomicOr(p.error, 1u);
+    } else if (warp < 4) {
+        float* ref = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabRef);
+        float* neg = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabNeg);
+        float* alpha = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabAlpha);
+        int* out_row = reinterpret_cast<int*>(smem + L::kSmTab + L::kTabRow);
+        float* warp_top = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabMax);
+        float* tile_sums = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabTile) + warp * NMAX;
+        float* sums = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabSum);  // [warp][row]
+        uint64_t* masks = reinterpret_cast<uint64_t*>(smem + L::kSmTab + L::kTabMask);
+        int* misc = reinterpret_cast<int*>(smem + L::kSmTab + L::kTabMisc);  // largest query of each warp
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        float cs = 0.0f, cs_next = 0.0f;
+
+        // Queries of a segment into shared memory ([64-dim atom][row][128 bytes], 16-byte chunks at chunk ^ row % 8)
+        // and its rows' tables; rows up to the next 16 are zeros.  Called once every product with the queries before
+        // has been read.
+        auto stage = [&](const Segment& s, int parity) {
+            const int n16 = (s.n + 15) & ~15, pieces = n16 * (HD / 8);
+            auto piece = [&](int i) {  // 16 bytes of row i / (HD / 8)
+                const int r = i / (HD / 8), c = i - r * (HD / 8), rr = s.r0 + r, t = window_row(p, rr);
+                if (r >= s.n) return make_uint4(0u, 0u, 0u, 0u);
+                const int64_t at = (int64_t)(s.q.row0 + t) * p.q_stride + (int64_t)(s.kvh * p.group + rr - t * p.group) * HD;
+                return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at) + c);
+            };
+            // a thread's pieces at once where registers allow (one round trip to memory), else in two batches
+            constexpr int kPer = NMAX * (HD / 8) / kSoftThreads, kBatch = kPer <= 8 ? kPer : kPer / 2;
+            uint4 v[kBatch];
+            auto fetch = [&](int b0) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int at = tid + (b0 + i) * kSoftThreads;
+                    v[i] = at < pieces ? piece(at) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            float lifted = 1.0f;
+            if (Query<T>::kLifted) {
+                uint32_t top = 0;
+#pragma unroll 1
+                for (int b0 = 0; b0 < kPer; b0 += kBatch) {
+                    fetch(b0);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) top = max(top, Query<T>::top(v[i]));
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (lane == 0) misc[warp] = (int)top;
+                soft_sync();
+                lifted = lift_of((uint32_t)max(max(misc[0], misc[1]), max(misc[2], misc[3])));
+            }
+            cs_next = p.scale_log2 / lifted;
+#pragma unroll 1
+            for (int b0 = 0; b0 < kPer; b0 += kBatch) {
+                if (!Query<T>::kLifted || kPer > kBatch) fetch(b0);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int at = tid + (b0 + i) * kSoftThreads, r = at / (HD / 8), c = at - r * (HD / 8);
+                    if (at < pieces)
+                        *reinterpret_cast<uint4*>(smem + L::kSmQ + (c >> 3) * (NMAX * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(Query<T>::pair(v[i].x, lifted), Query<T>::pair(v[i].y, lifted),
+                                       Query<T>::pair(v[i].z, lifted), Query<T>::pair(v[i].w, lifted));
+                }
+            }
+            if (tid < n16) {
+                const int rr = s.r0 + tid, t = window_row(p, rr), row = s.q.row0 + t;
+                uint64_t m = 0;
+                if (tid < s.n) {
+                    m = p.mask ? __ldg(p.mask + row) : (2ull << t) - 1;
+                    if (s.q.rows < 64) m &= (1ull << s.q.rows) - 1;
+                }
+                masks[parity * NMAX + tid] = m;
+                out_row[parity * NMAX + tid] = tid < s.n ? row * p.n_q_heads + s.kvh * p.group + rr - t * p.group : -1;
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(B(L::kQ));
+        };
+
+        Segment next_seg;
+        bool more = walk.next(p, next_seg);
+        int j = 0, segs = 0, n16 = 0;
+#pragma unroll 1
+        while (true) {
+            // a segment's queries go in before the one before's output is read: its first scores overlap that
+            const int parity = segs & 1;
+            if (more) stage(next_seg, parity);
+            if (segs > 0) {
+                soft_sync();
+                wait(L::kO + ((j - 1) & 1), (j - 1) >> 1);
+                const bool whole = seg.begins() && seg.ends();
+                const int slot = 2 * blockIdx.x + (seg.begins() ? 1 : 0);
+                if (tid < n16) {
+                    const float l = (sums[tid] + sums[NMAX + tid]) + (sums[2 * NMAX + tid] + sums[3 * NMAX + tid]);
+                    alpha[tid] = l > 0.0f ? 1.0f / l : 0.0f;
+                    if (!whole && tid < seg.n)
+                        p.part_ml[(int64_t)slot * p.chunk + tid] = make_float2(ref[tid] == kNoRef ? -INFINITY : ref[tid], l);
+                }
+                soft_sync();
+                tc::fence_after_sync();
+                const int* rows = out_row + (parity ^ 1) * NMAX;
+#pragma unroll 1
+                for (int m = 0; m < L::kMt; ++m) {
+                    const int dim = m * 128 + tid;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < n16; c0 += 16) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(tmem + lanes + L::kTmO + m * NMAX + c0, o);
+                        tc::tmem_wait_ld();
+                        if (whole) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const int row = rows[c0 + c];
+                                const float inv = alpha[c0 + c];
+                                if (row >= 0)
+                                    static_cast<uint16_t*>(p.out)[(int64_t)row * HD + dim] =
+                                        inv > 0.0f ? Query<T>::one(__uint_as_float(o[c]) * inv) : (uint16_t)0;
+                            }
+                        } else {
+                            float* dst = p.part_o + ((int64_t)slot * p.chunk + c0) * HD + dim;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (c0 + c < seg.n) dst[c * HD] = __uint_as_float(o[c]);
+                        }
+                    }
+                }
+                tc::fence_before_sync();
+                soft_sync();  // references and output rows have been read
+            }
+            if (!more) break;
+            seg = next_seg;
+            cs = cs_next;
+            n16 = (seg.n + 15) & ~15;
+            const int ctx = seg.q.len - seg.q.rows;
+            if (tid < n16) {
+                ref[tid] = kNoRef;
+                neg[tid] = kLift - kNoRef;
+                sums[tid] = sums[NMAX + tid] = sums[2 * NMAX + tid] = sums[3 * NMAX + tid] = 0.0f;
+            }
+            soft_sync();
+            const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
+            auto page_of = [&](int t) {  // this thread's key's page, loaded a tile ahead
+                const long long key = (long long)t * BN + tid;
+                return t < seg.t1 && key < seg.q.len ? __ldg(pages + (key >> p.page_shift)) : 0;
+            };
+            int page = page_of(seg.t0);
+#pragma unroll 1
+            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
+                const bool bad = page < 0 || page >= p.n_pages;
+                page = page_of(t + 1);
+                const long long key = (long long)t * BN + tid;
+                // what rows see of this key: all of them, none, or those with its bit in their masks
+                const int bit = (int)min(key - ctx, (long long)64);
+                const bool none = bad || key >= seg.q.len;
+                wait(L::kS + (j & 1), j >> 1);
+                tc::fence_after_sync();
+                const uint32_t scol = tmem + lanes + L::kTmS + (j & 1) * NMAX;
+                const bool masked = __any_sync(0xffffffffu, none || bit >= 0);
+                auto mask = [&](int c0, float (&x)[16], const uint32_t (&w)[16]) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(w[c]);
+                    if (masked) {
+                        const uint64_t* m = masks + parity * NMAX + c0;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (none || (bit >= 0 && !(m[c] >> (bit & 63) & 1))) x[c] = -INFINITY;
+                    }
+                };
+                if (j >= 2) wait(L::kO + (j & 1), (j - 2) >> 1);  // the weights of tile j - 2 have been used
+                uint8_t* prow = smem + L::kSmP + (L::kSmall ? 0 : (j & 1) * L::kPNext) + tid * 128;
+                const int swz = ((L::kSmall ? (j & 1) * 4 : 0) ^ (tid & 7)) << 4;
+#pragma unroll 1
+                for (int pass = t == seg.t0 ? 0 : 1; pass < 3; ++pass) {
+                    if (pass != 1) {
+                        // References to the tile's maxima where those are more than 2^8 above; sums and O^T follow.
+                        soft_sync();  // every thread has read the old references
+#pragma unroll 1
+                        for (int c0 = 0; c0 < n16; c0 += 16) {
+                            float x[16];
+                            uint32_t w[16];
+                            tc::tmem_ld16(scol + c0, w);
+                            tc::tmem_wait_ld();
+                            mask(c0, x, w);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float m = warp_max(x[c]);
+                                if (lane == c) warp_top[warp * NMAX + c0 + c] = m;
+                            }
+                            __syncwarp();
+                        }
+                        soft_sync();
+                        if (tid < n16) {
+                            const float m = cs * fmaxf(fmaxf(warp_top[tid], warp_top[NMAX + tid]),
+                                                       fmaxf(warp_top[2 * NMAX + tid], warp_top[3 * NMAX + tid]));
+                            const float old = ref[tid];
+                            float a = 1.0f;
+                            if (m > old + kLazy) {
+                                a = old == kNoRef ? 0.0f : ex2_approx(old - m);
+                                ref[tid] = m;
+                                neg[tid] = kLift - m;
+                            }
+                            alpha[tid] = a;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) sums[g * NMAX + tid] *= a;
+                        }
+                        if (t > seg.t0) wait(L::kO + ((j - 1) & 1), (j - 1) >> 1);  // every earlier product has landed
+                        soft_sync();
+                        if (t > seg.t0) {
+                            tc::fence_after_sync();
+#pragma unroll 1
+                            for (int m = 0; m < L::kMt; ++m)
+#pragma unroll 1
+                                for (int c0 = 0; c0 < n16; c0 += 16) {
+                                    uint32_t o[16];
+                                    tc::tmem_ld16(tmem + lanes + L::kTmO + m * NMAX + c0, o);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c0 + c]);
+                                    tc::tmem_st16(tmem + lanes + L::kTmO + m * NMAX + c0, o);
+                                }
+                            tc::tmem_wait_st();
+                        }
+                    }
+                    // Weights of this key, 16 rows at a time, the next scores on their way meanwhile; does a score pass
+                    // its reference by more than 2^8?  And the sums of the rounded weights over the warp's 32 keys: each
+                    // exchange halves the rows a lane holds, and a pair of lanes ends with the sum of one row.
+                    // (mma.sync against ones shares the tensor cores with the products: 1.6 us a tile at 96 rows.)
+                    float over = -INFINITY;
+                    uint32_t w[16];
+                    tc::tmem_ld16(scol, w);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < n16; c0 += 16) {
+                        float x[16];
+                        tc::tmem_wait_ld16(w);
+                        mask(c0, x, w);
+                        if (c0 + 16 < n16) tc::tmem_ld16(scol + c0 + 16, w);
+                        uint32_t h[8];
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 r = *reinterpret_cast<const float4*>(neg + c0 + c);
+                            const float e0 = fmaf(x[c], cs, r.x), e1 = fmaf(x[c + 1], cs, r.y), e2 = fmaf(x[c + 2], cs, r.z),
+                                        e3 = fmaf(x[c + 3], cs, r.w);
+                            over = fmaxf(over, fmaxf(fmaxf(e0, e1), fmaxf(e2, e3)));
+                            h[c / 2] = h2_as_u32(__floats2half2_rn(ex2_approx(e0), ex2_approx(e1)));
+                            h[c / 2 + 1] = h2_as_u32(__floats2half2_rn(ex2_approx(e2), ex2_approx(e3)));
+                        }
+                        *reinterpret_cast<uint4*>(prow + (swz ^ (c0 << 1))) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(prow + (swz ^ (c0 << 1) ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float2 f = __half22float2(u32_as_h2(h[c]));
+                            x[2 * c] = f.x, x[2 * c + 1] = f.y;
+                        }
+#pragma unroll
+                        for (int n = 8; n >= 1; n >>= 1) {
+                            const bool up = lane & (2 * n);
+#pragma unroll
+                            for (int i = 0; i < n; ++i) {
+                                const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+                                x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * n);
+                            }
+                        }
+                        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+                        if (!(lane & 1)) tile_sums[c0 + (lane >> 1)] = x[0];
+                    }
+                    if (!soft_any(over > kLazy + kLift)) break;
+                }
+                tc::fence_proxy_async_smem();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(B(L::kP + (j & 1)));
+#pragma unroll
+                for (int c = 0; c < NMAX; c += 32)
+                    if (c + lane < n16) sums[warp * NMAX + c + lane] += tile_sums[c + lane];
+            }
+            ++segs;
+            more = walk.next(p, next_seg);
+        }
+        if (!ok) atomicOr(p.error, 1u);
+    } else if (warp < kKWarp0) {
+        // codes and scales of one plane, K from warp 6 and V from warp 7, 64 keys at a time: lane g fetches group g of
+        // `box` keys, which lie in one page
+        const bool is_v = warp > kFetchWarp0;
+        const CUtensorMap* map = is_v ? &p.tmap_v : &p.tmap_k;
+        const uint16_t* scales = is_v ? p.vs : p.ks;
+        const int groups = BN / p.box, per_half = groups / 2;
+        const int first = is_v ? L::RK : 0, ring = is_v ? L::RV : L::RK;
+        int slot = first, turn = 0;
+        int t = 0, page = -1, issued = 0;
         bool have = false;
-        auto ahead = [&]() {
+        auto ahead = [&]() {  // the page ids of the next tile, fetched a tile before its copies
             if (!have || ++t >= seg.t1) {
-                have = walk.next<BN>(p, seg);
+                have = walk.next(p, seg);
                 t = seg.t0;
                 if (!have) return;
             }
-            const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
-#pragma unroll
-            for (int i = 0; i < L::kPages; ++i) {
-                const long long key = (long long)t * BN + 64 * i + 8 * w + nn;
-                off[i] = (int)key & ((1 << p.page_shift) - 1);
-                page[i] = key < seg.q.len ? __ldg(pages + (key >> p.page_shift)) : -1;
-            }
-        };
-        auto block_at = [&](int u, int kvh, bool& on) {  // block index of pass u in the planes
-            const int i = L::kPages == 1 ? 0 : u;
-            on = page[i] >= 0 && page[i] < p.n_pages;
-            const int64_t row = (((int64_t)page[i] * p.n_kv_heads + kvh) << p.page_shift) + off[i];
-            return row * (HD / 32) + (HD == 256 ? 4 * u + jj : jj);
-        };
-        auto key_of = [&](int u) { return HD == 256 ? 8 * w + nn : 64 * u + 8 * w + nn; };
-        auto blk_of = [&](int u) { return HD == 256 ? 4 * u + jj : jj; };
-        bool full[2];
-        auto load_tile = [&](Block (&k)[2], Block (&v)[2], bool& f) {
-            f = have;
-            if (!have) return;
-            bool on[2];
-            int64_t at[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) at[u] = block_at(u, seg.kvh, on[u]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) load_block(k[u], p.kc, p.ks, at[u], on[u]);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) load_block(v[u], p.vc, p.vs, at[u], on[u]);
-            ahead();
-        };
-        bool reused = false;  // the ring has gone round once
-        auto put_tile = [&](const Block (&k)[2], const Block (&v)[2]) {
-            if (reused && !__all_sync(0xffffffffu, tc::mbar_wait(B(kBarS + st), ph ^ 1, kPollLimit))) return false;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) store_block<BN>(k[u], smem + L::kSmK + st * L::kTile, key_of(u), blk_of(u));
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(B(kBarK + st));
-            if (reused && !__all_sync(0xffffffffu, tc::mbar_wait(B(kBarO + st), ph ^ 1, kPollLimit))) return false;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) store_block<BN>(v[u], smem + L::kSmV + st * L::kTile, key_of(u), blk_of(u));
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(B(kBarV + st));
-            if (++st == kStages) st = 0, ph ^= 1, reused = true;
-            return true;
+            const long long key = (long long)t * BN + p.box * lane;
+            page = lane < groups && key < seg.q.len ? __ldg(p.table + (int64_t)seg.b * p.max_pages + (key >> p.page_shift)) : -1;
         };
         ahead();
-        load_tile(kx[0], vx[0], full[0]);
-        load_tile(kx[1], vx[1], full[1]);
-        while (true) {
-            if (!full[0]) break;
-            if (!put_tile(kx[0], vx[0])) { ok = false; break; }
-            load_tile(kx[0], vx[0], full[0]);
-            if (!full[1]) break;
-            if (!put_tile(kx[1], vx[1])) { ok = false; break; }
-            load_tile(kx[1], vx[1], full[1]);
+#pragma unroll 1
+        while (have) {
+            const bool on = page >= 0 && page < p.n_pages;
+            const int off = (int)(((uint32_t)t * BN + (uint32_t)(p.box * lane)) & ((1u << p.page_shift) - 1));
+            const int64_t row = on ? (((int64_t)page * p.n_kv_heads + seg.kvh) << p.page_shift) + off : 0;
+            ahead();
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (turn > 0) wait(L::kFree + slot, turn - 1);
+                const bool mine = on && lane / per_half == half;
+                const int n = __popc(__ballot_sync(0xffffffffu, mine));
+                if (lane == 0) tc::mbar_arrive_expect_tx(B(L::kFull + slot), (uint32_t)(n * p.box * (HD + HD / 16)));
+                __syncwarp();
+                if (mine) {
+                    const int g = lane - half * per_half;
+                    const uint32_t dst = sbase + L::kSmSlots + slot * L::kCodes + g * p.box * 128;
+#pragma unroll
+                    for (int x = 0; x < HD / 128; ++x) tma_load_2d(dst + x * 8192, map, 128 * x, (int)row, B(L::kFull + slot));
+                    tc::bulk_g2s(sbase + L::kSmScales + slot * L::kScales + g * p.box * (HD / 16), scales + row * (HD / 32),
+                                 p.box * (HD / 16), B(L::kFull + slot));
+                }
+                __syncwarp();
+                ++issued;
+                if (++slot == first + ring) slot = first, ++turn;
+            }
         }
-        if (!ok && lane == 0) atomicOr(p.error, 1u);
+        // the block is not left while a copy into its memory is in flight
+#pragma unroll 1
+        for (int i = max(0, issued - ring); i < issued; ++i)
+            if (!tc::mbar_wait(B(L::kFull + first + i % ring), (uint32_t)(i / ring) & 1u, kPollLimit)) ok = false;
+        if (!ok) atomicOr(p.error, 1u);
+    } else if (warp < kVWarp0) {
+        // K^: thread = key = tensor-memory lane
+        const int w = warp - kKWarp0, half = w >> 1, n = (w & 1) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        int slot = half, turn = 0, j = 0;
+#pragma unroll 1
+        while (walk.next(p, seg)) {
+#pragma unroll 1
+            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
+                wait(L::kFull + slot, turn);
+                if (j >= L::NK) wait(L::kS + ((j - L::NK) & 1), (j - L::NK) >> 1);  // K^ of tile j - NK has been used
+                tc::fence_after_sync();
+                __syncwarp();
+                const uint8_t* src = smem + L::kSmSlots + slot * L::kCodes;
+                const uint16_t* sc = reinterpret_cast<const uint16_t*>(smem + L::kSmScales + slot * L::kScales) + n * (HD / 32);
+                const uint32_t to = tmem + lanes + L::kTmK + (j % L::NK) * (HD / 2);
+                const uint4 c0 = *reinterpret_cast<const uint4*>(src + code_at(n, 0)), c1 = *reinterpret_cast<const uint4*>(src + code_at(n, 1));
+                uint4 a = c0, b = c1;
+#pragma unroll 1
+                for (int k = 0; k < HD / 32; ++k) {
+                    const __half2 scale = __half2half2(__ushort_as_half(sc[k]));
+                    uint32_t h[16];
+                    values16(a, scale, h);
+                    values16(b, scale, h + 8);
+                    const int next = k + 1 < HD / 32 ? k + 1 : k;
+                    a = *reinterpret_cast<const uint4*>(src + code_at(n, 2 * next));
+                    b = *reinterpret_cast<const uint4*>(src + code_at(n, 2 * next + 1));
+                    tc::tmem_st16(to + 16 * k, h);
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(B(L::kFree + slot));
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(B(L::kK + j % L::NK));
+                slot += 2;
+                if (slot >= L::RK) slot -= L::RK, ++turn;
+            }
+        }
+        if (!ok) atomicOr(p.error, 1u);
+    } else {
+        // V^: lanes 0-7 hold eight consecutive keys of one block, so that their 16-byte loads and swizzled stores fall
+        // into different banks.  Scales of keys that are not there become zero, and so do their values.
+        const int w = warp - kVWarp0, nn = lane & 7, jj = lane >> 3;
+        int slot = L::RK, turn = 0, j = 0;
+#pragma unroll 1
+        while (walk.next(p, seg)) {
+            const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
+            auto page_of = [&](int t) {  // of the tile's 16-key group `lane`, loaded a tile ahead
+                const long long key = (long long)t * BN + 16 * lane;
+                return lane < 8 && t < seg.t1 && key < seg.q.len ? __ldg(pages + (key >> p.page_shift)) : 0;
+            };
+            int page = page_of(seg.t0);
+#pragma unroll 1
+            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
+                const uint32_t bad = __ballot_sync(0xffffffffu, page < 0 || page >= p.n_pages);
+                page = page_of(t + 1);
+                const int keys = (int)min((long long)seg.q.len - (long long)t * BN, (long long)BN);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const int v = 2 * (j % L::NV) + half;
+                    wait(L::kFull + slot, turn);
+                    if (j >= L::NV) wait(L::kVFree + v, j / L::NV - 1);  // the half of tile j - NV has been used
+                    __syncwarp();
+                    const uint8_t* src = smem + L::kSmSlots + slot * L::kCodes;
+                    const uint16_t* sc = reinterpret_cast<const uint16_t*>(smem + L::kSmScales + slot * L::kScales);
+                    uint8_t* tile = smem + L::kSmV + (j % L::NV) * L::kTile + half * 8192;
+                    const bool there0 = !(bad >> (4 * half + w) & 1);  // this warp's 16 keys are one group
+                    const int n0 = w * 16 + nn;
+                    uint4 a = *reinterpret_cast<const uint4*>(src + code_at(n0, 2 * jj)), b = *reinterpret_cast<const uint4*>(src + code_at(n0, 2 * jj + 1));
+#pragma unroll 1
+                    for (int i = 0; i < 2 * (HD / 128); ++i) {
+                        const int n = n0 + 8 * (i & 1), k = 4 * (i >> 1) + jj;  // key of the slot, block
+                        const bool there = there0 && 64 * half + n < keys;
+                        const __half2 scale = __half2half2(__ushort_as_half(there ? sc[n * (HD / 32) + k] : (uint16_t)0));
+                        uint32_t h[16];
+                        values16(a, scale, h);
+                        values16(b, scale, h + 8);
+                        const int i1 = i + 1 < 2 * (HD / 128) ? i + 1 : i, n1 = n0 + 8 * (i1 & 1), k1 = 4 * (i1 >> 1) + jj;
+                        a = *reinterpret_cast<const uint4*>(src + code_at(n1, 2 * k1));
+                        b = *reinterpret_cast<const uint4*>(src + code_at(n1, 2 * k1 + 1));
+                        // [64-dim atom][key][128 bytes], 16-byte chunks at chunk ^ key % 8
+                        uint8_t* row = tile + (k >> 1) * (BN * 128) + (n >> 3) * 1024 + nn * 128;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            *reinterpret_cast<uint4*>(row + (((4 * (k & 1) + c) ^ nn) << 4)) =
+                                make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive(B(L::kFree + slot));
+                        tc::mbar_arrive(B(L::kV + v));
+                    }
+                    if (++slot == L::R) slot = L::RK, ++turn;
+                }
+            }
+        }
+        if (!ok) atomicOr(p.error, 1u);
     }
 
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kIssueWarp) tc::tmem_dealloc(tmem, kTmemCols);
+    if (warp == kQkWarp) tc::tmem_dealloc(tmem, kTmemCols);
     if (tid == 0) {
         // the last segment, if its item goes on in later CTAs: they are joined under this CTA's number
         int4 join = make_int4(0, 0, 0, -1);
         if (u0 < u1) {
             walk.left = u1 - u0;
-            walk.b = (int)s_start[0];
-            walk.q = request_of<BN>(p, walk.b);
-            walk.item = (int)(s_start[1] / walk.q.tiles);
-            walk.t = (int)(s_start[1] - (long long)walk.item * walk.q.tiles);
-            while (walk.next<BN>(p, seg)) {}
-            if (seg.begins() && !seg.ends()) {
+            walk.b = s_start[0];
+            walk.kvh = s_start[1];
+            walk.t = s_start[2];
+            walk.q = request_of(p, walk.b);
+            bool any = false;
+#pragma unroll 1
+            while (walk.next(p, seg)) any = true;
+            // (a last item without rows for this CTA is not in `seg`: then t, left behind by it, is not the segment's end)
+            if (any && seg.begins() && !seg.ends() && walk.t == seg.t1 && walk.b == seg.b && walk.kvh == seg.kvh) {
                 const long long last = u1 - seg.t1 + seg.q.tiles - 1;  // the item's last unit
-                join = make_int4(seg.q.row0, seg.kvh, seg.r0 | seg.n << 16, (int)(((last + 1) * shares - 1) / units));
+                const long long longer = s_cut->rest * (s_cut->base + 1);
+                const long long team = last < longer ? divide(last, s_cut->base + 1) : s_cut->rest + divide(last - longer, s_cut->base);
+                join = make_int4(seg.q.row0, seg.kvh, seg.r0 | seg.n << 16, (int)team);
             }
         }
         p.joins[blockIdx.x] = join;
@@ -637,7 +932,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
 constexpr int kJoinThreads = 256;
 
 // The rows of every item that was cut, one after another over the blocks: o = sum_c 2^(m_c - m) o_c / sum_c
-// 2^(m_c - m) l_c over its parts, slot 1 of the CTA that began it and slot 0 of the later ones.
+// 2^(m_c - m) l_c over its parts, slot 1 of the CTA that began it and slot 0 of the same place in the later teams.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedVerifyParams p, int n_ctas) {
     constexpr int kCols = HD / 4, kGroups = kJoinThreads / kCols;
@@ -675,8 +970,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             else
                 hi = mid;
         }
-        const int c0 = lo, r = task - s_first[c0], parts = s_join[c0].w - c0 + 1;
-        auto slot = [&](int i) { return (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * p.part_rows + r; };
+        const int c0 = lo, r = task - s_first[c0], parts = s_join[c0].w - c0 / p.team + 1;
+        auto slot = [&](int i) { return (int64_t)(2 * (c0 + i * p.team) + (i == 0 ? 1 : 0)) * p.chunk + r; };
         float m = -INFINITY;
         for (int i = tid; i < parts; i += kJoinThreads) m = fmaxf(m, p.part_ml[slot(i)].x);
 #pragma unroll
@@ -729,15 +1024,22 @@ int sm_count() {
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct VerifyPlan {
-    int part_rows;
+    int chunk, team;  // most rows of a CTA, CTAs that share an item's rows
+    bool small;
     size_t ml_off, join_off, bytes;
 };
 
+// Up to 32 rows a window and KV head the kernel with the deeper fetch ring runs; above it teams of CTAs with up to 64.
+constexpr int chunk_of(bool small) { return small ? 32 : 64; }
+
 VerifyPlan verify_plan(int ctas, int group, int hd, int max_rows) {
     VerifyPlan v;
-    v.part_rows = max_rows * group < kRows ? max_rows * group : kRows;
-    v.ml_off = up256((size_t)ctas * 2 * v.part_rows * hd * sizeof(float));
-    v.join_off = v.ml_off + up256((size_t)ctas * 2 * v.part_rows * sizeof(float2));
+    const int rows = max_rows * group;
+    v.small = rows <= 32;
+    v.team = (rows + chunk_of(v.small) - 1) / chunk_of(v.small);
+    v.chunk = (rows + v.team - 1) / v.team;
+    v.ml_off = up256((size_t)ctas * 2 * v.chunk * hd * sizeof(float));
+    v.join_off = v.ml_off + up256((size_t)ctas * 2 * v.chunk * sizeof(float2));
     v.bytes = v.join_off + (size_t)ctas * sizeof(int4);
     return v;
 }
@@ -759,11 +1061,24 @@ int launch_dependent(Kernel* kernel, int grid, int threads, int smem, cudaStream
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
 }
 
-template <typename T, int HD>
+// The code plane as rows of head_dim bytes; a box is 128 bytes of `box` consecutive keys of a page.
+bool encode_codes(CUtensorMap* map, const int8_t* codes, const kvq8_paged_cache* kv, int box) {
+    const EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)kv->head_dim, (cuuint64_t)kv->n_pages * kv->n_kv_heads * kv->page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)kv->head_dim};
+    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(codes), dims, strides, boxes, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int HD, bool SMALL>
 int launch_verify(const PagedVerifyParams& p, int ctas, cudaStream_t s) {
+    constexpr int N = chunk_of(SMALL);
     static SmemOptIn opt;
-    if (opt.ensure(paged_verify_kernel<T, HD>, VL<HD>::kSmBytes) != KVQ8_OK) return KVQ8_ERR_CUDA;
-    const int rc = launch_dependent(paged_verify_kernel<T, HD>, ctas, kVerifyThreads, VL<HD>::kSmBytes, s, p);
+    if (opt.ensure(paged_verify_kernel<T, HD, N>, VL<HD, N>::kSmBytes) != KVQ8_OK) return KVQ8_ERR_CUDA;
+    const int rc = launch_dependent(paged_verify_kernel<T, HD, N>, ctas, kVerifyThreads, VL<HD, N>::kSmBytes, s, p);
     if (rc != KVQ8_OK) return rc;
     return launch_dependent(paged_join_kernel<T, HD>, 4 * ctas, kJoinThreads, 0, s, p, ctas);
 }
@@ -789,8 +1104,8 @@ extern "C" int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, 
     if ((dtype != KVQ8_F16 && dtype != KVQ8_BF16) || n_rows < 0 || n_seqs < 0 || max_pages < 1) return KVQ8_ERR_INVALID_ARG;
     if (n_q_heads < 1 || max_rows < 1 || !(softmax_scale > 0.0f) || softmax_scale == INFINITY) return KVQ8_ERR_INVALID_ARG;
     if (n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 64 || max_rows > kMaxWindowRows || n_seqs > kMaxSeqs ||
-        n_rows > (1 << 24))
-        return KVQ8_ERR_UNSUPPORTED;
+        n_rows > (1 << 24) || (int64_t)kv->n_pages * kv->n_kv_heads * kv->page_size > 0x7fffffffLL)
+        return KVQ8_ERR_UNSUPPORTED;  // the last: rows of a plane are tensor-map coordinates
     if (n_rows == 0 || n_seqs == 0) return KVQ8_OK;
     if (!q || !out || !page_table || !lens || !row_starts || q_stride < (int64_t)n_q_heads * kv->head_dim)
         return KVQ8_ERR_INVALID_ARG;
@@ -800,18 +1115,24 @@ extern "C" int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, 
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (q_stride * 2) % 16 || !aligned_to(page_table, 4) ||
         !aligned_to(lens, 4) || !aligned_to(row_starts, 4) || !aligned_to(window_mask, 8))
         return KVQ8_ERR_MISALIGNED;
-    if (!aligned_to(kv->k_codes, 32) || !aligned_to(kv->v_codes, 32)) return KVQ8_ERR_MISALIGNED;  // whole blocks per load
     unsigned int* error = device_error_flag();
     if (!error) return KVQ8_ERR_CUDA;
     char* ws = static_cast<char*>(workspace);
-    const PagedVerifyParams p = {q, out, q_stride, kv->k_codes, kv->k_scales, kv->v_codes, kv->v_scales, page_table, lens,
+    PagedVerifyParams p = {q, out, q_stride, kv->k_codes, kv->k_scales, kv->v_codes, kv->v_scales, page_table, lens,
                                  row_starts, window_mask, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + v.ml_off),
                                  reinterpret_cast<int4*>(ws + v.join_off), error, n_rows, n_q_heads, kv->n_kv_heads, group,
-                                 kv->n_pages, log2_of(kv->page_size), max_pages, n_seqs, max_rows, v.part_rows,
-                                 softmax_scale * kLog2e};
+                                 kv->n_pages, log2_of(kv->page_size), max_pages, n_seqs, max_rows, v.chunk, v.team,
+                                 softmax_scale * kLog2e, 1.0f / (float)group};
+    p.box = kv->page_size < 64 ? kv->page_size : 64;
+    if (!encode_codes(&p.tmap_k, kv->k_codes, kv, p.box) || !encode_codes(&p.tmap_v, kv->v_codes, kv, p.box)) return KVQ8_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    const bool hd128 = kv->head_dim == 128;
-    if (dtype == KVQ8_F16)
-        return hd128 ? launch_verify<__half, 128>(p, ctas, s) : launch_verify<__half, 256>(p, ctas, s);
-    return hd128 ? launch_verify<__nv_bfloat16, 128>(p, ctas, s) : launch_verify<__nv_bfloat16, 256>(p, ctas, s);
+    auto run = [&](auto hd, auto small) {
+        constexpr int HD = decltype(hd)::value;
+        constexpr bool SMALL = decltype(small)::value;
+        return dtype == KVQ8_F16 ? launch_verify<__half, HD, SMALL>(p, ctas, s) : launch_verify<__nv_bfloat16, HD, SMALL>(p, ctas, s);
+    };
+    using std::integral_constant;
+    if (kv->head_dim == 128)
+        return v.small ? run(integral_constant<int, 128>(), std::true_type()) : run(integral_constant<int, 128>(), std::false_type());
+    return v.small ? run(integral_constant<int, 256>(), std::true_type()) : run(integral_constant<int, 256>(), std::false_type());
 }
