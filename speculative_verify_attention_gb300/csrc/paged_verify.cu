@@ -23,14 +23,17 @@
 // error and goes on without waiting, so every loop ends and every named barrier is met):
 //   0-3   softmax, one key per thread: p = 2^(s - ref) against a reference maximum per row kept in shared memory.
 //         The references follow only jumps of more than 2^8, found by one vote per tile.
-//         The row sums of the fp16 weights, as the product uses them, by mma.sync against ones (fp32).
-//   4     issues S^T = K^ Q^T; 5 issues O^T += V^T P^T (one thread each)
-//   6, 7  fetch the codes and scales of K and V into a ring of 64-key slots, most of shared memory, by tensor copies of
-//         up to a page (codes, 128-byte swizzle) and bulk copies (scales).  A load takes about 2 us under load, so an
-//         SM's share of the memory's rate is some 90 KB in flight.  Loads held in registers had 40 KB in flight; 16-byte
-//         asynchronous copies stopped at about 16 KB a warp.
+//   4     issues S^T = K^ Q^T
+//   5     issues O^T += V^T P^T and, as one more 128-row tile with ones for V, the row sums of the fp16 weights: fp32 sums
+//         of what the product uses.  (Exchanges between the lanes cost the softmax warps as much as the softmax, and
+//         mma.sync waits behind the products.)
 //   8-11  K: one key per thread, codes to fp16 (code * scale, rounded once) into tensor memory
-//   12-15 V: blocks of 8 keys x 4 per step into a 128-byte-swizzled tile in shared memory, 64 keys at a time
+//   12-19 V: units of 8 keys x 4 blocks into a 128-byte-swizzled tile in shared memory, 64 keys at a time
+//   20-23 fetch K (20, 21) and V (22, 23) into rings of 64-key slots, most of shared memory: codes by tensor copies of up
+//         to a page (128-byte swizzle), scales by asynchronous copies.  A load takes about 2 us under load: an SM's share
+//         of the memory's rate is some 90 KB in flight.  (Loads held in the converters' registers had 40 KB in flight,
+//         copies issued by the converters took as many instructions as the conversion, and one warp a plane was bound
+//         by its issue: 60-100 ns a copy.)
 // Keys on page ids outside the pool are not fetched.  Those and the rows behind len in a page enter V^ as zeros, and
 // their scores are masked whatever they are.
 #include <cuda_bf16.h>
@@ -48,8 +51,8 @@ unsigned int* device_error_flag();
 namespace {
 
 constexpr int BN = 128;                     // keys of a tile
-constexpr int kQkWarp = 4, kPvWarp = 5, kFetchWarp0 = 6, kKWarp0 = 8, kVWarp0 = 12;
-constexpr int kVerifyThreads = 512;
+constexpr int kQkWarp = 4, kPvWarp = 5, kKWarp0 = 8, kVWarp0 = 12, kFetchWarp0 = 20;
+constexpr int kVerifyThreads = 768;
 constexpr int kSoftThreads = 128;
 constexpr uint32_t kPollLimit = 1u << 24;
 constexpr float kLazy = 8.0f;               // the references follow only jumps of more than 2^8
@@ -58,42 +61,40 @@ constexpr float kNoRef = -1e30f;            // the reference of a row that has s
 constexpr uint32_t kTmemCols = 512;
 
 // Shapes: NMAX rows of a chunk, 32 or 64; NK tiles of K^ in tensor memory, NV of V^ and two of weights in shared memory;
-// the fetch ring takes what is left of that.  Up to 32 rows the two weight tiles are the halves of one 64-row atom.
+// the fetch rings take what is left of that.  Up to 32 rows the two weight tiles are the halves of one 64-row atom.
 template <int HD, int NMAX>
 struct VL {
     static constexpr bool kSmall = NMAX <= 32;
-    static constexpr int NK = 2, NV = HD == 256 ? 1 : 2;
+    static constexpr int NK = HD == 256 && !kSmall ? 1 : 2, NV = HD == 256 ? 1 : 2;
     static constexpr int kTile = BN * HD * 2;
     static constexpr int kPNext = kSmall ? 64 : BN * 128;  // from one weight tile to the other
-    static constexpr int kSmPBytes = kSmall ? BN * 128 : 2 * BN * 128;
-    static constexpr int kSmV = 0, kSmQ = NV * kTile, kSmP = kSmQ + HD / 64 * NMAX * 128, kSmTab = kSmP + kSmPBytes;
+    static constexpr int kSmV = 0, kSmQ = NV * kTile, kSmP = kSmQ + HD / 64 * NMAX * 128;
+    static constexpr int kSmTab = kSmP + (kSmall ? 1 : 2) * BN * 128;
     // tables: per row reference, lifted negative reference, factor of the last raise, output row and window mask (two
-    // segments each); maxima, the tile's row sums and row sums per softmax
-    // warp
+    // segments each); maxima per softmax warp
     static constexpr int kTabRef = 0, kTabNeg = kTabRef + 4 * NMAX, kTabAlpha = kTabNeg + 4 * NMAX,
-                         kTabRow = kTabAlpha + 4 * NMAX, kTabMax = kTabRow + 8 * NMAX,
-                         kTabTile = kTabMax + 16 * NMAX, kTabSum = kTabTile + 16 * NMAX, kTabMask = kTabSum + 16 * NMAX,
+                         kTabRow = kTabAlpha + 4 * NMAX, kTabMax = kTabRow + 8 * NMAX, kTabMask = kTabMax + 16 * NMAX,
                          kTabMisc = kTabMask + 16 * NMAX;
     static constexpr int kSmScan = kSmTab + kTabMisc + 32, kSmTmem = kSmScan + 48 + (kVerifyThreads / 32) * 8;
     static constexpr int kSmBar = kSmTmem + 16;
     // fetch slots: 64 keys of codes, [128-byte half of the head][key][128 bytes] with the 16-byte chunks of key n at
     // chunk ^ n % 8; their scales apart
     static constexpr int kCodes = 64 * HD, kScales = 64 * HD / 16, kMaxSlots = 16;
-    static constexpr int kSmSlots = (kSmBar + (2 * kMaxSlots + 19) * 8 + 1023) / 1024 * 1024;
+    static constexpr int kSmSlots = (kSmBar + (2 * kMaxSlots + 17) * 8 + 1023) / 1024 * 1024;
     static constexpr int kFit = (227 * 1024 - kSmSlots) / (kCodes + kScales), R = kFit < kMaxSlots ? kFit : kMaxSlots;
     // K and V have rings of their own (slots 0 .. RK - 1 and the rest), and a K slot always serves the same half of a tile:
     // every wait is then for the use just before or the one after it, by roles that saw that one, as parities need
     static constexpr int RK = (R + 1) / 2 / 2 * 2, RV = R - RK;
-    static_assert(RK >= 2 && RV >= 2, "a tile of each");
     static constexpr int kSmScales = kSmSlots + R * kCodes, kSmBytes = kSmScales + R * kScales;
     // barriers: fetch slot full / free; 64-key halves of V^ written / used (two of each tile); then pairs by tile: K^
     // written, scores ready, weights ready, product done; then queries ready
     static constexpr int kFull = 0, kFree = R, kV = 2 * R, kVFree = kV + 4, kK = kVFree + 4, kS = kK + 2, kP = kS + 2, kO = kP + 2,
                          kQ = kO + 2;
-    static constexpr int kMt = HD / 128;                   // 128-dim tiles of O^T
-    static constexpr uint32_t kTmO = 0, kTmS = kMt * NMAX, kTmK = kTmS + 2 * NMAX;
-    static_assert(kTmK + NK * HD / 2 <= kTmemCols, "tensor memory");
-    static_assert(R >= 4 && kSmBytes <= 227 * 1024, "shared memory");
+    static constexpr int kMt = HD / 128;  // 128-dim tiles of O^T; one more of as many columns holds the row sums
+    static constexpr uint32_t kTmO = 0, kTmSum = kMt * NMAX, kTmS = kTmSum + NMAX, kTmK = kTmS + 2 * NMAX,
+                              kTmOnes = kTmK + NK * HD / 2;
+    static_assert(kTmOnes + 16 <= kTmemCols, "tensor memory");
+    static_assert(RK >= 2 && RV >= 2 && kSmBytes <= 227 * 1024, "shared memory: a tile of each at least");
     static_assert(kSmQ % 1024 == 0 && kSmP % 1024 == 0, "swizzled tiles stay 1024-byte aligned");
 };
 
@@ -153,7 +154,8 @@ struct Walk {
     long long left;
     Request q;
 
-    __device__ __forceinline__ bool next(const PagedVerifyParams& p, Segment& s) {
+    // (one copy of the code for all roles: it runs once a segment)
+    __device__ __noinline__ bool next(const PagedVerifyParams& p, Segment& s) {
 #pragma unroll 1
         while (left > 0) {
 #pragma unroll 1
@@ -234,9 +236,6 @@ __device__ __forceinline__ void values16(uint4 codes, __half2 scale, uint32_t* h
     }
 }
 
-// Chunk c (16 codes) of key n of a fetch slot.
-__device__ __forceinline__ int code_at(int n, int c) { return (c >> 3) * 8192 + n * 128 + (((c ^ n) & 7) << 4); }
-
 // One box of a plane's tensor map into shared memory, completion counted in bytes.  x is 0 or 128: copies start on
 // 16-byte boundaries.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
@@ -288,6 +287,25 @@ __device__ __forceinline__ float lift_of(uint32_t top) {
     return __uint_as_float((uint32_t)min(127 + 127 + 14 - e, 254) << 23);
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned short lds16(uint32_t at) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
@@ -327,12 +345,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     if (tid == 0) {
 #pragma unroll 1
         for (int s = 0; s < L::R; ++s) {
-            tc::mbar_init(B(L::kFull + s), 1);
-            tc::mbar_init(B(L::kFree + s), s < L::RK ? 2 : 4);  // the warps that read it
+            tc::mbar_init(B(L::kFull + s), 66);                  // two fetching warps: their bytes and each lane's copies
+            tc::mbar_init(B(L::kFree + s), s < L::RK ? 2 : 8);  // the warps that read it
         }
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
-            tc::mbar_init(B(L::kV + s), 4);
+            tc::mbar_init(B(L::kV + s), 8);
             tc::mbar_init(B(L::kVFree + s), 1);
         }
 #pragma unroll 1
@@ -387,6 +405,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (warp < 4) {
+        uint32_t ones[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ones[i] = 0x3C003C00u;
+        tc::tmem_st16(tmem + ((uint32_t)(warp * 32) << 16) + L::kTmOnes, ones);
+        tc::tmem_wait_st();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
     Walk walk;
     walk.left = u1 - u0;
     walk.b = p.n_seqs;
@@ -444,6 +472,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
 #pragma unroll 1
         while (walk.next(p, seg)) {
             const uint32_t idesc = tc::idesc_f16_f32_ab(128, (seg.n + 15) & ~15, true, true);
+            const uint32_t idesc_sum = tc::idesc_f16_f32_ab(128, (seg.n + 15) & ~15, false, true);
 #pragma unroll 1
             for (int t = seg.t0; t < seg.t1; ++t, ++j) {
                 wait(L::kP + (j & 1), j >> 1);
@@ -463,6 +492,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
                                 tc::mma_ss(tmem + L::kTmO + m * NMAX, vd + (uint64_t)((m * 2 * BN * 128 + k * 2048) >> 4),
                                            pd + (uint64_t)((k * 2048) >> 4), idesc, k > 0 ? 1u : more);
                         tc::mma_commit(B(L::kVFree + v));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_ts(tmem + L::kTmSum, tmem + L::kTmOnes, pd + (uint64_t)((k * 2048) >> 4), idesc_sum, k > 0 ? 1u : more);
                         if (half) tc::mma_commit(B(L::kO + (j & 1)));
                     }
                     __syncwarp();
@@ -476,8 +508,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
         float* alpha = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabAlpha);
         int* out_row = reinterpret_cast<int*>(smem + L::kSmTab + L::kTabRow);
         float* warp_top = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabMax);
-        float* tile_sums = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabTile) + warp * NMAX;
-        float* sums = reinterpret_cast<float*>(smem + L::kSmTab + L::kTabSum);  // [warp][row]
         uint64_t* masks = reinterpret_cast<uint64_t*>(smem + L::kSmTab + L::kTabMask);
         int* misc = reinterpret_cast<int*>(smem + L::kSmTab + L::kTabMisc);  // largest query of each warp
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -488,58 +518,44 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
         // has been read.
         auto stage = [&](const Segment& s, int parity) {
             const int n16 = (s.n + 15) & ~15, pieces = n16 * (HD / 8);
-            auto piece = [&](int i) {  // 16 bytes of row i / (HD / 8)
-                const int r = i / (HD / 8), c = i - r * (HD / 8), rr = s.r0 + r, t = window_row(p, rr);
-                if (r >= s.n) return make_uint4(0u, 0u, 0u, 0u);
-                const int64_t at = (int64_t)(s.q.row0 + t) * p.q_stride + (int64_t)(s.kvh * p.group + rr - t * p.group) * HD;
-                return __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + at) + c);
+            const int rr = s.r0 + tid, my_t = window_row(p, rr), my_row = s.q.row0 + my_t;
+            uint64_t my_mask = 0;
+            if (tid < s.n) my_mask = p.mask ? __ldg(p.mask + my_row) : (2ull << my_t) - 1;
+            auto at = [&](int i) {  // where piece i (16 bytes of row i / (HD / 8)) lies
+                const int r = i / (HD / 8), c = i - r * (HD / 8);
+                return L::kSmQ + (c >> 3) * (NMAX * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
             };
-            // a thread's pieces at once where registers allow (one round trip to memory), else in two batches
-            constexpr int kPer = NMAX * (HD / 8) / kSoftThreads, kBatch = kPer <= 8 ? kPer : kPer / 2;
-            uint4 v[kBatch];
-            auto fetch = [&](int b0) {
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int at = tid + (b0 + i) * kSoftThreads;
-                    v[i] = at < pieces ? piece(at) : make_uint4(0u, 0u, 0u, 0u);
-                }
-            };
+            // all pieces at once: one round trip to memory
+#pragma unroll 4
+            for (int i = tid; i < pieces; i += kSoftThreads) {
+                const int r = i / (HD / 8), c = i - r * (HD / 8), q_rr = s.r0 + r, t = window_row(p, q_rr);
+                const int64_t off = r < s.n ? (int64_t)(s.q.row0 + t) * p.q_stride + (int64_t)(s.kvh * p.group + q_rr - t * p.group) * HD + c * 8 : 0;
+                cp_async_16(sbase + at(i), static_cast<const uint16_t*>(p.q) + off, r < s.n ? 16 : 0);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
             float lifted = 1.0f;
-            if (Query<T>::kLifted) {
+            if (Query<T>::kLifted) {  // a thread reads and rewrites the pieces that it fetched
                 uint32_t top = 0;
-#pragma unroll 1
-                for (int b0 = 0; b0 < kPer; b0 += kBatch) {
-                    fetch(b0);
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) top = max(top, Query<T>::top(v[i]));
-                }
+#pragma unroll 2
+                for (int i = tid; i < pieces; i += kSoftThreads) top = max(top, Query<T>::top(*reinterpret_cast<const uint4*>(smem + at(i))));
                 top = __reduce_max_sync(0xffffffffu, top);
                 if (lane == 0) misc[warp] = (int)top;
                 soft_sync();
                 lifted = lift_of((uint32_t)max(max(misc[0], misc[1]), max(misc[2], misc[3])));
+#pragma unroll 2
+                for (int i = tid; i < pieces; i += kSoftThreads) {
+                    uint4* q16 = reinterpret_cast<uint4*>(smem + at(i));
+                    const uint4 v = *q16;
+                    *q16 = make_uint4(Query<T>::pair(v.x, lifted), Query<T>::pair(v.y, lifted), Query<T>::pair(v.z, lifted),
+                                      Query<T>::pair(v.w, lifted));
+                }
             }
             cs_next = p.scale_log2 / lifted;
-#pragma unroll 1
-            for (int b0 = 0; b0 < kPer; b0 += kBatch) {
-                if (!Query<T>::kLifted || kPer > kBatch) fetch(b0);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int at = tid + (b0 + i) * kSoftThreads, r = at / (HD / 8), c = at - r * (HD / 8);
-                    if (at < pieces)
-                        *reinterpret_cast<uint4*>(smem + L::kSmQ + (c >> 3) * (NMAX * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(Query<T>::pair(v[i].x, lifted), Query<T>::pair(v[i].y, lifted),
-                                       Query<T>::pair(v[i].z, lifted), Query<T>::pair(v[i].w, lifted));
-                }
-            }
             if (tid < n16) {
-                const int rr = s.r0 + tid, t = window_row(p, rr), row = s.q.row0 + t;
-                uint64_t m = 0;
-                if (tid < s.n) {
-                    m = p.mask ? __ldg(p.mask + row) : (2ull << t) - 1;
-                    if (s.q.rows < 64) m &= (1ull << s.q.rows) - 1;
-                }
-                masks[parity * NMAX + tid] = m;
-                out_row[parity * NMAX + tid] = tid < s.n ? row * p.n_q_heads + s.kvh * p.group + rr - t * p.group : -1;
+                if (s.q.rows < 64) my_mask &= (1ull << s.q.rows) - 1;
+                masks[parity * NMAX + tid] = my_mask;
+                out_row[parity * NMAX + tid] = tid < s.n ? my_row * p.n_q_heads + s.kvh * p.group + rr - my_t * p.group : -1;
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -555,24 +571,30 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
             const int parity = segs & 1;
             if (more) stage(next_seg, parity);
             if (segs > 0) {
-                soft_sync();
                 wait(L::kO + ((j - 1) & 1), (j - 1) >> 1);
+                tc::fence_after_sync();
                 const bool whole = seg.begins() && seg.ends();
                 const int slot = 2 * blockIdx.x + (seg.begins() ? 1 : 0);
-                if (tid < n16) {
-                    const float l = (sums[tid] + sums[NMAX + tid]) + (sums[2 * NMAX + tid] + sums[3 * NMAX + tid]);
-                    alpha[tid] = l > 0.0f ? 1.0f / l : 0.0f;
-                    if (!whole && tid < seg.n)
-                        p.part_ml[(int64_t)slot * p.chunk + tid] = make_float2(ref[tid] == kNoRef ? -INFINITY : ref[tid], l);
-                }
-                soft_sync();
-                tc::fence_after_sync();
                 const int* rows = out_row + (parity ^ 1) * NMAX;
 #pragma unroll 1
-                for (int m = 0; m < L::kMt; ++m) {
-                    const int dim = m * 128 + tid;
+                for (int c0 = 0; c0 < n16; c0 += 16) {
+                    float inv[16];  // every lane of the sums' tile holds them
+                    {
+                        uint32_t l[16];
+                        tc::tmem_ld16(tmem + lanes + L::kTmSum + c0, l);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const float sum = __uint_as_float(l[c]);
+                            inv[c] = sum > 0.0f ? 1.0f / sum : 0.0f;
+                            if (!whole && tid == c0 + c && tid < seg.n)
+                                p.part_ml[(int64_t)slot * p.chunk + tid] = make_float2(ref[tid] == kNoRef ? -INFINITY : ref[tid], sum);
+                        }
+                    }
+                    __syncwarp();
 #pragma unroll 1
-                    for (int c0 = 0; c0 < n16; c0 += 16) {
+                    for (int m = 0; m < L::kMt; ++m) {
+                        const int dim = m * 128 + tid;
                         uint32_t o[16];
                         tc::tmem_ld16(tmem + lanes + L::kTmO + m * NMAX + c0, o);
                         tc::tmem_wait_ld();
@@ -580,10 +602,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 const int row = rows[c0 + c];
-                                const float inv = alpha[c0 + c];
                                 if (row >= 0)
                                     static_cast<uint16_t*>(p.out)[(int64_t)row * HD + dim] =
-                                        inv > 0.0f ? Query<T>::one(__uint_as_float(o[c]) * inv) : (uint16_t)0;
+                                        inv[c] != 0.0f ? Query<T>::one(__uint_as_float(o[c]) * inv[c]) : (uint16_t)0;
                             }
                         } else {
                             float* dst = p.part_o + ((int64_t)slot * p.chunk + c0) * HD + dim;
@@ -604,7 +625,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
             if (tid < n16) {
                 ref[tid] = kNoRef;
                 neg[tid] = kLift - kNoRef;
-                sums[tid] = sums[NMAX + tid] = sums[2 * NMAX + tid] = sums[3 * NMAX + tid] = 0.0f;
             }
             soft_sync();
             const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
@@ -669,15 +689,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
                                 neg[tid] = kLift - m;
                             }
                             alpha[tid] = a;
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) sums[g * NMAX + tid] *= a;
                         }
                         if (t > seg.t0) wait(L::kO + ((j - 1) & 1), (j - 1) >> 1);  // every earlier product has landed
                         soft_sync();
                         if (t > seg.t0) {
                             tc::fence_after_sync();
 #pragma unroll 1
-                            for (int m = 0; m < L::kMt; ++m)
+                            for (int m = 0; m <= L::kMt; ++m)  // the last holds the row sums
 #pragma unroll 1
                                 for (int c0 = 0; c0 < n16; c0 += 16) {
                                     uint32_t o[16];
@@ -691,9 +709,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
                         }
                     }
                     // Weights of this key, 16 rows at a time, the next scores on their way meanwhile; does a score pass
-                    // its reference by more than 2^8?  And the sums of the rounded weights over the warp's 32 keys: each
-                    // exchange halves the rows a lane holds, and a pair of lanes ends with the sum of one row.
-                    // (mma.sync against ones shares the tensor cores with the products: 1.6 us a tile at 96 rows.)
+                    // its reference by more than 2^8?
                     float over = -INFINITY;
                     uint32_t w[16];
                     tc::tmem_ld16(scol, w);
@@ -715,22 +731,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
                         }
                         *reinterpret_cast<uint4*>(prow + (swz ^ (c0 << 1))) = make_uint4(h[0], h[1], h[2], h[3]);
                         *reinterpret_cast<uint4*>(prow + (swz ^ (c0 << 1) ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float2 f = __half22float2(u32_as_h2(h[c]));
-                            x[2 * c] = f.x, x[2 * c + 1] = f.y;
-                        }
-#pragma unroll
-                        for (int n = 8; n >= 1; n >>= 1) {
-                            const bool up = lane & (2 * n);
-#pragma unroll
-                            for (int i = 0; i < n; ++i) {
-                                const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
-                                x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * n);
-                            }
-                        }
-                        x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-                        if (!(lane & 1)) tile_sums[c0 + (lane >> 1)] = x[0];
                     }
                     if (!soft_any(over > kLazy + kLift)) break;
                 }
@@ -738,55 +738,75 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(B(L::kP + (j & 1)));
-#pragma unroll
-                for (int c = 0; c < NMAX; c += 32)
-                    if (c + lane < n16) sums[warp * NMAX + c + lane] += tile_sums[c + lane];
             }
             ++segs;
             more = walk.next(p, next_seg);
         }
         if (!ok) atomicOr(p.error, 1u);
-    } else if (warp < kKWarp0) {
-        // codes and scales of one plane, K from warp 6 and V from warp 7, 64 keys at a time: lane g fetches group g of
-        // `box` keys, which lie in one page
-        const bool is_v = warp > kFetchWarp0;
+    } else if (warp >= kFetchWarp0) {
+        // Two warps a plane; each fetches 32 of a slot's 64 keys: scales a key per lane, codes in boxes of `box` keys, which
+        // lie in one page (a box of 64 keys: the first warp its lower 128 bytes, the second the upper).  The pages are
+        // looked up a tile ahead.
+        const int f = warp - kFetchWarp0, part = f & 1;
+        const bool is_v = f >= 2;
         const CUtensorMap* map = is_v ? &p.tmap_v : &p.tmap_k;
         const uint16_t* scales = is_v ? p.vs : p.ks;
-        const int groups = BN / p.box, per_half = groups / 2;
         const int first = is_v ? L::RK : 0, ring = is_v ? L::RV : L::RK;
-        int slot = first, turn = 0;
-        int t = 0, page = -1, issued = 0;
+        int slot = first, turn = 0, issued = 0, t = 0, page = -1;
         bool have = false;
-        auto ahead = [&]() {  // the page ids of the next tile, fetched a tile before its copies
+        // lane l < 4 stands for 16 keys of half l / 2, the part's first or second (the slot's first, in a box of 64)
+        const bool whole_slot = p.box == 64;
+        auto key_of = [&](int tile) { return (long long)tile * BN + 64 * (lane >> 1) + (whole_slot ? 0 : 32 * part + 16 * (lane & 1)); };
+        auto ahead = [&]() {
             if (!have || ++t >= seg.t1) {
                 have = walk.next(p, seg);
                 t = seg.t0;
                 if (!have) return;
             }
-            const long long key = (long long)t * BN + p.box * lane;
-            page = lane < groups && key < seg.q.len ? __ldg(p.table + (int64_t)seg.b * p.max_pages + (key >> p.page_shift)) : -1;
+            page = lane < 4 && key_of(t) < seg.q.len ? __ldg(p.table + (int64_t)seg.b * p.max_pages + (key_of(t) >> p.page_shift)) : -1;
         };
         ahead();
 #pragma unroll 1
         while (have) {
             const bool on = page >= 0 && page < p.n_pages;
-            const int off = (int)(((uint32_t)t * BN + (uint32_t)(p.box * lane)) & ((1u << p.page_shift) - 1));
-            const int64_t row = on ? (((int64_t)page * p.n_kv_heads + seg.kvh) << p.page_shift) + off : 0;
+            const int off = (int)(key_of(t) & ((1 << p.page_shift) - 1));
+            const int row = on ? (((page * p.n_kv_heads) + seg.kvh) << p.page_shift) + off : -1;
             ahead();
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 if (turn > 0) wait(L::kFree + slot, turn - 1);
-                const bool mine = on && lane / per_half == half;
-                const int n = __popc(__ballot_sync(0xffffffffu, mine));
-                if (lane == 0) tc::mbar_arrive_expect_tx(B(L::kFull + slot), (uint32_t)(n * p.box * (HD + HD / 16)));
-                __syncwarp();
-                if (mine) {
-                    const int g = lane - half * per_half;
-                    const uint32_t dst = sbase + L::kSmSlots + slot * L::kCodes + g * p.box * 128;
+                const uint32_t full = B(L::kFull + slot), dst = sbase + L::kSmSlots + slot * L::kCodes + part * 4096;
+                const int r0 = __shfl_sync(0xffffffffu, row, 2 * half), r1 = __shfl_sync(0xffffffffu, row, 2 * half + 1);
+                // scales of key 32 part + lane
+                const int r = whole_slot || lane < 16 ? r0 : r1;
+                if (r >= 0) {
+                    const uint16_t* sc = scales + ((int64_t)r + (whole_slot ? 32 * part + lane : lane & 15)) * (HD / 32);
+                    const uint32_t to = sbase + L::kSmScales + slot * L::kScales + (32 * part + lane) * (HD / 16);
+                    if (HD == 256)
+                        cp_async_16(to, sc, 16);
+                    else
+                        cp_async_8(to, sc, 8);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+                if (elect_one()) {
+                    if (p.box == 16) {
+                        tc::mbar_arrive_expect_tx(full, (uint32_t)((r0 >= 0) + (r1 >= 0)) * 16 * HD);
 #pragma unroll
-                    for (int x = 0; x < HD / 128; ++x) tma_load_2d(dst + x * 8192, map, 128 * x, (int)row, B(L::kFull + slot));
-                    tc::bulk_g2s(sbase + L::kSmScales + slot * L::kScales + g * p.box * (HD / 16), scales + row * (HD / 32),
-                                 p.box * (HD / 16), B(L::kFull + slot));
+                        for (int x = 0; x < HD / 128; ++x) {
+                            if (r0 >= 0) tma_load_2d(dst + x * 8192, map, 128 * x, r0, full);
+                            if (r1 >= 0) tma_load_2d(dst + x * 8192 + 2048, map, 128 * x, r1, full);
+                        }
+                    } else if (p.box == 32) {
+                        tc::mbar_arrive_expect_tx(full, r0 >= 0 ? 32 * HD : 0);
+#pragma unroll
+                        for (int x = 0; x < HD / 128; ++x)
+                            if (r0 >= 0) tma_load_2d(dst + x * 8192, map, 128 * x, r0, full);
+                    } else {
+                        const int x = HD == 256 ? part : 0;
+                        const bool mine = r0 >= 0 && (HD == 256 || part == 0);
+                        tc::mbar_arrive_expect_tx(full, mine ? 64 * 128 : 0);
+                        if (mine) tma_load_2d(dst - part * 4096 + x * 8192, map, 128 * x, r0, full);
+                    }
                 }
                 __syncwarp();
                 ++issued;
@@ -795,96 +815,54 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
         }
         // the block is not left while a copy into its memory is in flight
 #pragma unroll 1
-        for (int i = max(0, issued - ring); i < issued; ++i)
-            if (!tc::mbar_wait(B(L::kFull + first + i % ring), (uint32_t)(i / ring) & 1u, kPollLimit)) ok = false;
-        if (!ok) atomicOr(p.error, 1u);
-    } else if (warp < kVWarp0) {
-        // K^: thread = key = tensor-memory lane
-        const int w = warp - kKWarp0, half = w >> 1, n = (w & 1) * 32 + lane;
-        const uint32_t lanes = (uint32_t)(w * 32) << 16;
-        int slot = half, turn = 0, j = 0;
-#pragma unroll 1
-        while (walk.next(p, seg)) {
-#pragma unroll 1
-            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
-                wait(L::kFull + slot, turn);
-                if (j >= L::NK) wait(L::kS + ((j - L::NK) & 1), (j - L::NK) >> 1);  // K^ of tile j - NK has been used
-                tc::fence_after_sync();
-                __syncwarp();
-                const uint8_t* src = smem + L::kSmSlots + slot * L::kCodes;
-                const uint16_t* sc = reinterpret_cast<const uint16_t*>(smem + L::kSmScales + slot * L::kScales) + n * (HD / 32);
-                const uint32_t to = tmem + lanes + L::kTmK + (j % L::NK) * (HD / 2);
-                const uint4 c0 = *reinterpret_cast<const uint4*>(src + code_at(n, 0)), c1 = *reinterpret_cast<const uint4*>(src + code_at(n, 1));
-                uint4 a = c0, b = c1;
-#pragma unroll 1
-                for (int k = 0; k < HD / 32; ++k) {
-                    const __half2 scale = __half2half2(__ushort_as_half(sc[k]));
-                    uint32_t h[16];
-                    values16(a, scale, h);
-                    values16(b, scale, h + 8);
-                    const int next = k + 1 < HD / 32 ? k + 1 : k;
-                    a = *reinterpret_cast<const uint4*>(src + code_at(n, 2 * next));
-                    b = *reinterpret_cast<const uint4*>(src + code_at(n, 2 * next + 1));
-                    tc::tmem_st16(to + 16 * k, h);
-                }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(B(L::kFree + slot));
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(B(L::kK + j % L::NK));
-                slot += 2;
-                if (slot >= L::RK) slot -= L::RK, ++turn;
-            }
+        for (int i = max(0, issued - ring); i < issued; ++i) {
+            if (!ok) atomicOr(p.error, 1u);
+            ok = true;
+            wait(L::kFull + first + i % ring, i / ring);
         }
         if (!ok) atomicOr(p.error, 1u);
-    } else {
-        // V^: lanes 0-7 hold eight consecutive keys of one block, so that their 16-byte loads and swizzled stores fall
-        // into different banks.  Scales of keys that are not there become zero, and so do their values.
+    } else if (warp >= kVWarp0) {
+        // V^: lanes 0-7 hold the eight keys of one block, so that their 16-byte loads and swizzled stores fall into
+        // different banks.  Scales of keys that are not there become zero, and so do their values.
+        constexpr int U = HD / 128;
         const int w = warp - kVWarp0, nn = lane & 7, jj = lane >> 3;
+        const uint32_t src0 = sbase + L::kSmSlots + (8 * w + nn) * 128 + ((nn ^ (2 * jj)) << 4);
+        const uint32_t scale0 = sbase + L::kSmScales + (8 * w + nn) * (HD / 16) + jj * 2;
+        // [64-dim atom][key][128 bytes], 16-byte chunks at chunk ^ key % 8; block jj of a unit: chunks 4 (jj % 2) ..
+        const uint32_t dst0 = sbase + L::kSmV + (jj >> 1) * (BN * 128) + w * 1024 + nn * 128 + (((4 * (jj & 1)) ^ nn) << 4);
         int slot = L::RK, turn = 0, j = 0;
 #pragma unroll 1
         while (walk.next(p, seg)) {
             const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
-            auto page_of = [&](int t) {  // of the tile's 16-key group `lane`, loaded a tile ahead
-                const long long key = (long long)t * BN + 16 * lane;
-                return lane < 8 && t < seg.t1 && key < seg.q.len ? __ldg(pages + (key >> p.page_shift)) : 0;
+            const int len = seg.q.len, t1 = seg.t1;
+            auto page_of = [&](int t) {  // lane g < 2: of this warp's keys of half g, loaded a tile ahead
+                const long long key = (long long)t * BN + 64 * lane + 8 * w;
+                return lane < 2 && t < t1 && key < len ? __ldg(pages + (key >> p.page_shift)) : 0;
             };
             int page = page_of(seg.t0);
 #pragma unroll 1
-            for (int t = seg.t0; t < seg.t1; ++t, ++j) {
+            for (int t = seg.t0; t < t1; ++t, ++j) {
                 const uint32_t bad = __ballot_sync(0xffffffffu, page < 0 || page >= p.n_pages);
                 page = page_of(t + 1);
-                const int keys = (int)min((long long)seg.q.len - (long long)t * BN, (long long)BN);
+                const long long key = (long long)t * BN + 8 * w + nn;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     const int v = 2 * (j % L::NV) + half;
                     wait(L::kFull + slot, turn);
                     if (j >= L::NV) wait(L::kVFree + v, j / L::NV - 1);  // the half of tile j - NV has been used
                     __syncwarp();
-                    const uint8_t* src = smem + L::kSmSlots + slot * L::kCodes;
-                    const uint16_t* sc = reinterpret_cast<const uint16_t*>(smem + L::kSmScales + slot * L::kScales);
-                    uint8_t* tile = smem + L::kSmV + (j % L::NV) * L::kTile + half * 8192;
-                    const bool there0 = !(bad >> (4 * half + w) & 1);  // this warp's 16 keys are one group
-                    const int n0 = w * 16 + nn;
-                    uint4 a = *reinterpret_cast<const uint4*>(src + code_at(n0, 2 * jj)), b = *reinterpret_cast<const uint4*>(src + code_at(n0, 2 * jj + 1));
-#pragma unroll 1
-                    for (int i = 0; i < 2 * (HD / 128); ++i) {
-                        const int n = n0 + 8 * (i & 1), k = 4 * (i >> 1) + jj;  // key of the slot, block
-                        const bool there = there0 && 64 * half + n < keys;
-                        const __half2 scale = __half2half2(__ushort_as_half(there ? sc[n * (HD / 32) + k] : (uint16_t)0));
+                    const bool there = !(bad >> half & 1) && key + 64 * half < len;
+                    const uint32_t dst = dst0 + (j % L::NV) * L::kTile + half * 8192, src = src0 + slot * L::kCodes;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const uint16_t sc = lds16(scale0 + slot * L::kScales + 8 * u);
+                        const __half2 scale = __half2half2(__ushort_as_half(there ? sc : (uint16_t)0));
                         uint32_t h[16];
-                        values16(a, scale, h);
-                        values16(b, scale, h + 8);
-                        const int i1 = i + 1 < 2 * (HD / 128) ? i + 1 : i, n1 = n0 + 8 * (i1 & 1), k1 = 4 * (i1 >> 1) + jj;
-                        a = *reinterpret_cast<const uint4*>(src + code_at(n1, 2 * k1));
-                        b = *reinterpret_cast<const uint4*>(src + code_at(n1, 2 * k1 + 1));
-                        // [64-dim atom][key][128 bytes], 16-byte chunks at chunk ^ key % 8
-                        uint8_t* row = tile + (k >> 1) * (BN * 128) + (n >> 3) * 1024 + nn * 128;
+                        values16(lds128(src + u * 8192), scale, h);
+                        values16(lds128((src + u * 8192) ^ 16), scale, h + 8);
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            *reinterpret_cast<uint4*>(row + (((4 * (k & 1) + c) ^ nn) << 4)) =
-                                make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+                            sts128((dst + u * (2 * BN * 128)) ^ (c << 4), make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]));
                     }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
@@ -894,6 +872,47 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
                     }
                     if (++slot == L::R) slot = L::RK, ++turn;
                 }
+            }
+        }
+        if (!ok) atomicOr(p.error, 1u);
+    } else if (warp >= kKWarp0) {
+        // K^: thread = key = tensor-memory lane
+        const int w = warp - kKWarp0, half = w >> 1, n = (w & 1) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(w * 32) << 16;
+        const uint32_t src0 = sbase + L::kSmSlots + n * 128 + ((n & 7) << 4), scale0 = sbase + L::kSmScales + n * (HD / 16);
+        int slot = half, turn = 0, j = 0;
+#pragma unroll 1
+        while (walk.next(p, seg)) {
+            const int t1 = seg.t1;
+#pragma unroll 1
+            for (int t = seg.t0; t < t1; ++t, ++j) {
+                wait(L::kFull + slot, turn);
+                if (j >= L::NK) wait(L::kS + ((j - L::NK) & 1), (j - L::NK) >> 1);  // K^ of tile j - NK has been used
+                tc::fence_after_sync();
+                __syncwarp();
+                const uint32_t to = tmem + lanes + L::kTmK + (j % L::NK) * (HD / 2);
+#pragma unroll 1
+                for (int u = 0; u < HD / 128; ++u) {  // four blocks
+                    const uint32_t src = src0 + slot * L::kCodes + u * 8192;
+                    const uint2 sc = lds64(scale0 + slot * L::kScales + 8 * u);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const __half2 s2 = u32_as_h2(k ? sc.y : sc.x);
+                        uint32_t h[32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            values16(lds128(src ^ ((4 * k + c) << 4)), c < 2 ? __low2half2(s2) : __high2half2(s2), h + 8 * c);
+                        tc::tmem_st32(to + 64 * u + 32 * k, h);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(B(L::kFree + slot));
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(B(L::kK + j % L::NK));
+                slot += 2;
+                if (slot >= L::RK) slot -= L::RK, ++turn;
             }
         }
         if (!ok) atomicOr(p.error, 1u);
