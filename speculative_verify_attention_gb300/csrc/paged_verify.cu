@@ -38,8 +38,6 @@
 // their scores are masked whatever they are.
 #include <cuda_bf16.h>
 
-#include <type_traits>
-
 #include "paged.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
@@ -75,7 +73,7 @@ struct VL {
     static constexpr int kTabRef = 0, kTabNeg = kTabRef + 4 * NMAX, kTabAlpha = kTabNeg + 4 * NMAX,
                          kTabRow = kTabAlpha + 4 * NMAX, kTabMax = kTabRow + 8 * NMAX, kTabMask = kTabMax + 16 * NMAX,
                          kTabMisc = kTabMask + 16 * NMAX;
-    static constexpr int kSmScan = kSmTab + kTabMisc + 32, kSmTmem = kSmScan + 48 + (kVerifyThreads / 32) * 8;
+    static constexpr int kSmScan = kSmTab + kTabMisc + 32, kSmTmem = kSmScan + 64 + (kVerifyThreads / 32) * 8;
     static constexpr int kSmBar = kSmTmem + 16;
     // fetch slots: 64 keys of codes, [128-byte half of the head][key][128 bytes] with the 16-byte chunks of key n at
     // chunk ^ n % 8; their scales apart
@@ -128,6 +126,7 @@ struct Request {
     int len, rows, row0, tiles;
 };
 
+template <int KEYS>
 __device__ __forceinline__ Request request_of(const PagedVerifyParams& p, int b) {
     Request q;
     q.row0 = __ldg(p.row_starts + b);
@@ -136,7 +135,7 @@ __device__ __forceinline__ Request request_of(const PagedVerifyParams& p, int b)
     q.rows = end - q.row0;
     const bool good = q.row0 >= 0 && end <= p.n_rows && end > q.row0 && q.rows <= p.max_rows && q.rows <= q.len &&
                       (int64_t)q.len <= ((int64_t)p.max_pages << p.page_shift);
-    q.tiles = good ? (int)(((unsigned)q.len + BN - 1) / BN) : 0;
+    q.tiles = good ? (int)(((unsigned)q.len + KEYS - 1) / KEYS) : 0;
     return q;
 }
 
@@ -148,7 +147,8 @@ struct Segment {
     __device__ __forceinline__ bool ends() const { return t1 == q.tiles; }
 };
 
-// A CTA's share, segment by segment.  Each role walks it on its own.
+// A CTA's share, segment by segment, in tiles of KEYS keys.
+template <int KEYS>
 struct Walk {
     int b, kvh, t;
     long long left;
@@ -162,7 +162,7 @@ struct Walk {
             while (kvh == p.n_kv_heads || q.tiles == 0) {
                 kvh = 0;
                 if (++b >= p.n_seqs) return false;
-                q = request_of(p, b);
+                q = request_of<KEYS>(p, b);
             }
             s.b = b;
             s.kvh = kvh;
@@ -203,7 +203,8 @@ struct Shares {
     __device__ __forceinline__ long long begin(int c) const { return c < shares ? c * base + min((long long)c, rest) : base * shares + rest; }
 };
 
-// Exclusive sum over the block of one value per thread, and the total; all threads call it.
+// Exclusive sum over a block of THREADS of one value per thread, and the total; all threads call it.
+template <int THREADS>
 __device__ __forceinline__ long long block_exclusive(long long v, long long* s_warp, long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long inc = v;
@@ -217,11 +218,94 @@ __device__ __forceinline__ long long block_exclusive(long long v, long long* s_w
     long long before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kVerifyThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += s_warp[w];
         total += s_warp[w];
     }
     return before + inc - v;
+}
+
+// A CTA's place: its share [u0, u1) of all units, how they were cut, and where it starts.
+struct Place {
+    Shares cut;
+    long long units, u0, u1;
+    int b, kvh, t;
+};
+
+// Every thread of the block calls it; `place` and `s_warp` (THREADS / 32 words) are in shared memory, and `place` is whole
+// after the block's next barrier.
+template <int KEYS, int THREADS>
+__device__ __forceinline__ void find_place(const PagedVerifyParams& p, Place* place, long long* s_warp) {
+    const int tid = threadIdx.x;
+    const int per = (p.n_seqs + THREADS - 1) / THREADS;
+    const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
+    long long mine = 0, units;
+#pragma unroll 1
+    for (int b = b_lo; b < b_hi; ++b) mine += (long long)request_of<KEYS>(p, b).tiles * p.n_kv_heads;
+    const long long before = block_exclusive<THREADS>(mine, s_warp, units);
+    if (tid == 0) {
+        // no more shares than units: every share of an item that was cut has tiles of it, and so a partial
+        Shares cut;
+        cut.shares = (int)min(units, (long long)(gridDim.x / p.team));
+        cut.base = cut.shares ? divide(units, cut.shares) : 0;
+        cut.rest = units - cut.base * cut.shares;
+        place->cut = cut;
+        place->units = units;
+        place->u0 = cut.begin(blockIdx.x / p.team);
+        place->u1 = cut.begin(blockIdx.x / p.team + 1);
+    }
+    __syncthreads();
+    const long long u0 = place->u0;
+    if (u0 < place->u1 && before <= u0 && u0 < before + mine) {
+        long long at = before;
+#pragma unroll 1
+        for (int b = b_lo; b < b_hi; ++b) {
+            const Request q = request_of<KEYS>(p, b);
+            const long long here = (long long)q.tiles * p.n_kv_heads;
+            if (u0 < at + here) {
+                place->b = b;
+                place->kvh = (int)divide(u0 - at, q.tiles);
+                place->t = (int)(u0 - at - (long long)place->kvh * q.tiles);
+                break;
+            }
+            at += here;
+        }
+    }
+}
+
+template <int KEYS>
+__device__ __forceinline__ Walk<KEYS> walk_from(const PagedVerifyParams& p, const Place& place) {
+    Walk<KEYS> w;
+    w.left = place.u1 - place.u0;
+    w.b = p.n_seqs;
+    w.kvh = w.t = 0;
+    w.q.tiles = 0;
+    if (w.left > 0) {
+        w.b = place.b;
+        w.kvh = place.kvh;
+        w.t = place.t;
+        w.q = request_of<KEYS>(p, w.b);
+    }
+    return w;
+}
+
+// What one thread leaves for the joining kernel: the item that this CTA begins and does not end, under its number.
+template <int KEYS>
+__device__ __forceinline__ void leave_join(const PagedVerifyParams& p, const Place& place) {
+    int4 join = make_int4(0, 0, 0, -1);
+    Walk<KEYS> walk = walk_from<KEYS>(p, place);
+    Segment seg;
+    bool any = false;
+#pragma unroll 1
+    while (walk.next(p, seg)) any = true;
+    if (any && seg.begins() && !seg.ends()) {
+        const long long last = place.u1 - seg.t1 + seg.q.tiles - 1;  // the item's last unit
+        const long long longer = place.cut.rest * (place.cut.base + 1);
+        const long long team = last < longer ? divide(last, place.cut.base + 1)
+                                             : place.cut.rest + divide(last - longer, place.cut.base);
+        join = make_int4(seg.q.row0, seg.kvh, seg.r0 | seg.n << 16, (int)team);
+    }
+    p.joins[blockIdx.x] = join;
 }
 
 // ---------------------------------------------------------------- dequantising
@@ -338,9 +422,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     const uint32_t sbase = smem_u32(smem), bar = sbase + L::kSmBar;
     auto B = [&](int id) { return bar + 8u * (uint32_t)id; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSmTmem);
-    Shares* s_cut = reinterpret_cast<Shares*>(smem + L::kSmScan);
-    int* s_start = reinterpret_cast<int*>(smem + L::kSmScan + 32);  // request, KV head and tile of the first unit
-    long long* s_warp = reinterpret_cast<long long*>(smem + L::kSmScan + 48);
+    Place* place = reinterpret_cast<Place*>(smem + L::kSmScan);
+    long long* s_warp = reinterpret_cast<long long*>(smem + L::kSmScan + 64);
 
     if (tid == 0) {
 #pragma unroll 1
@@ -367,40 +450,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // this CTA's share of the units
-    const int per = (p.n_seqs + kVerifyThreads - 1) / kVerifyThreads;
-    const int b_lo = min(tid * per, p.n_seqs), b_hi = min(b_lo + per, p.n_seqs);
-    long long mine = 0, units;
-#pragma unroll 1
-    for (int b = b_lo; b < b_hi; ++b) {
-        const Request q = request_of(p, b);
-        mine += (long long)q.tiles * p.n_kv_heads;
-    }
-    const long long before = block_exclusive(mine, s_warp, units);
-    // no more shares than units: every share of an item that was cut has tiles of it, and so a partial
-    const int me = blockIdx.x / p.team;
-    if (tid == 0) {
-        s_cut->shares = (int)min(units, (long long)(gridDim.x / p.team));
-        s_cut->base = s_cut->shares ? divide(units, s_cut->shares) : 0;
-        s_cut->rest = units - s_cut->base * s_cut->shares;
-    }
-    __syncthreads();
-    const long long u0 = s_cut->begin(me), u1 = s_cut->begin(me + 1);
-    if (u0 < u1 && before <= u0 && u0 < before + mine) {
-        long long at = before;
-#pragma unroll 1
-        for (int b = b_lo; b < b_hi; ++b) {
-            const Request q = request_of(p, b);
-            const long long here = (long long)q.tiles * p.n_kv_heads;
-            if (u0 < at + here) {
-                s_start[0] = b;
-                s_start[1] = (int)divide(u0 - at, q.tiles);
-                s_start[2] = (int)(u0 - at - (long long)s_start[1] * q.tiles);
-                break;
-            }
-            at += here;
-        }
-    }
+    find_place<BN, kVerifyThreads>(p, place, s_warp);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -415,17 +465,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    Walk walk;
-    walk.left = u1 - u0;
-    walk.b = p.n_seqs;
-    walk.kvh = walk.t = 0;
-    walk.q.tiles = 0;
-    if (u0 < u1) {
-        walk.b = s_start[0];
-        walk.kvh = s_start[1];
-        walk.t = s_start[2];
-        walk.q = request_of(p, walk.b);
-    }
+    Walk<BN> walk = walk_from<BN>(p, *place);
     Segment seg;
     bool ok = true;
     // After a time-out the role runs on without waiting.  (Loops in this kernel are kept rolled: the roles' code together
@@ -922,28 +962,330 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
     __syncthreads();
     tc::fence_after_sync();
     if (warp == kQkWarp) tc::tmem_dealloc(tmem, kTmemCols);
-    if (tid == 0) {
-        // the last segment, if its item goes on in later CTAs: they are joined under this CTA's number
-        int4 join = make_int4(0, 0, 0, -1);
-        if (u0 < u1) {
-            walk.left = u1 - u0;
-            walk.b = s_start[0];
-            walk.kvh = s_start[1];
-            walk.t = s_start[2];
-            walk.q = request_of(p, walk.b);
-            bool any = false;
+    if (tid == 0) leave_join<BN>(p, *place);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Up to 8 rows a window and KV head (16 at head_dim 128): the tensor-core tiles above would be mostly empty and their
+// hand-offs and per-tile instructions would bound the scan, so here a warp does everything for its own 16 keys at a time,
+// on mma.sync and without shared memory: loads straight into registers in fragment order, S^T = K^ Q^T, softmax, and
+// O^T += V^T P^T with O^T in registers.  All warps run the same short loop and never wait for one another until the
+// segment's end, where their (o, m, l) are joined through shared memory.
+//   K : lane (g, c) = (lane / 4, lane % 4) holds the 32-value block c of keys g and g + 8: word s of a block feeds k-step s
+//       (the contraction runs over the dims in the order block 0's, 1's, 2's, 3's word s), Q is laid out alike;
+//   V : lane (g, c) holds dims 16 g .. 16 g + 15 of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: two keys' bytes interleaved are the
+//       fp16 pairs of the transposed operand;
+//   P^T comes from the scores' fragments by an 8 x 8 transpose.
+// The next 16 keys' codes are requested as soon as a register is free, and 32 keys' further ahead into L2.
+template <int HD, int NT>
+struct FL {
+    static constexpr int kWarps = 6, kCtas = 2;             // per SM: 168 registers a thread
+    static constexpr int N = 8 * NT, H = HD / 128;           // rows; 128-dim halves
+    static constexpr int kSmO = 0, kSmMl = kWarps * N * HD * 4, kSmBytes = kSmMl + kWarps * N * 8;
+};
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void load32(uint32_t (&w)[8], const int8_t* at) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(at));
+}
+__device__ __forceinline__ uint4 load16(const int8_t* at) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+}
+__device__ __forceinline__ void prefetch_l2(const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
+
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(FL<HD, NT>::kWarps * 32, FL<HD, NT>::kCtas) paged_verify_few_kernel(const __grid_constant__ PagedVerifyParams p) {
+    using L = FL<HD, NT>;
+    constexpr int W = L::kWarps, H = L::H, N = L::N, KEYS = 16;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ Place place;
+    __shared__ long long s_warp[W];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    float* s_o = reinterpret_cast<float*>(smem + L::kSmO);        // [warp][row][dim]
+    float2* s_ml = reinterpret_cast<float2*>(smem + L::kSmMl);    // [warp][row]
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    find_place<KEYS, W * 32>(p, &place, s_warp);
+    __syncthreads();
+    Walk<KEYS> walk = walk_from<KEYS>(p, place);
+    Segment next;
 #pragma unroll 1
-            while (walk.next(p, seg)) any = true;
-            // (a last item without rows for this CTA is not in `seg`: then t, left behind by it, is not the segment's end)
-            if (any && seg.begins() && !seg.ends() && walk.t == seg.t1 && walk.b == seg.b && walk.kvh == seg.kvh) {
-                const long long last = u1 - seg.t1 + seg.q.tiles - 1;  // the item's last unit
-                const long long longer = s_cut->rest * (s_cut->base + 1);
-                const long long team = last < longer ? divide(last, s_cut->base + 1) : s_cut->rest + divide(last - longer, s_cut->base);
-                join = make_int4(seg.q.row0, seg.kvh, seg.r0 | seg.n << 16, (int)team);
+    while (walk.next(p, next)) {
+        const Segment seg = next;
+        const int len = seg.q.len, ctx = len - seg.q.rows, t1 = seg.t1;
+        // queries: row 8 n + g, dims 32 c + 4 s .. + 3 of each half, as k-step s of the B operand
+        uint32_t q[NT][H][16];
+        float cs = p.scale_log2;
+        {
+            uint32_t top = 0;
+            uint4 raw[NT][H][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int r = 8 * n + g, t = window_row(p, r);
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) + (int64_t)(seg.q.row0 + t) * p.q_stride +
+                                      (int64_t)(seg.kvh * p.group + r - t * p.group) * HD + 32 * c;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        raw[n][h][i] = r < seg.n ? __ldg(reinterpret_cast<const uint4*>(src + 128 * h) + i) : make_uint4(0u, 0u, 0u, 0u);
+                        top = max(top, Query<T>::top(raw[n][h][i]));
+                    }
+            }
+            float lifted = 1.0f;
+            if (Query<T>::kLifted) lifted = lift_of(__reduce_max_sync(0xffffffffu, top));
+            cs = p.scale_log2 / lifted;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 v = raw[n][h][i];
+                        q[n][h][4 * i] = Query<T>::pair(v.x, lifted);
+                        q[n][h][4 * i + 1] = Query<T>::pair(v.y, lifted);
+                        q[n][h][4 * i + 2] = Query<T>::pair(v.z, lifted);
+                        q[n][h][4 * i + 3] = Query<T>::pair(v.w, lifted);
+                    }
+        }
+        float o[H * 8][NT][4], neg[NT][2], l[NT][2];
+#pragma unroll
+        for (int m = 0; m < H * 8; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) neg[n][0] = neg[n][1] = kLift - kNoRef, l[n][0] = l[n][1] = 0.0f;
+
+        // the cache row of a 16-key group (one page holds it), -1 where there is none
+        const int32_t* pages = p.table + (int64_t)seg.b * p.max_pages;
+        auto page_at = [&](int t) { return t < t1 ? __ldg(pages + (((long long)t * KEYS) >> p.page_shift)) : -1; };
+        auto row_at = [&](int t, int page) {
+            const int off = (int)(((unsigned)t * KEYS) & ((1u << p.page_shift) - 1));
+            return page >= 0 && page < p.n_pages ? (((int64_t)page * p.n_kv_heads + seg.kvh) << p.page_shift) + off : (int64_t)-1;
+        };
+        uint32_t kw[2][H][8], kd[2][H];
+        uint4 vw[4][H];
+        uint32_t vd[4][H];
+        auto load_k = [&](int64_t row, int keys) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool on = row >= 0 && g + 8 * i < keys;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    if (on) {
+                        load32(kw[i][h], p.kc + (row + g + 8 * i) * HD + 128 * h + 32 * c);
+                        kd[i][h] = __ldg(p.ks + (row + g + 8 * i) * (HD / 32) + 4 * h + c);
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) kw[i][h][s] = 0u;
+                        kd[i][h] = 0u;
+                    }
+                }
+            }
+        };
+        auto load_v = [&](int64_t row, int keys) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = 2 * c + (i & 1) + 8 * (i >> 1);
+                const bool on = row >= 0 && key < keys;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    if (on) {
+                        vw[i][h] = load16(p.vc + (row + key) * HD + 128 * h + 16 * g);
+                        vd[i][h] = __ldg(p.vs + (row + key) * (HD / 32) + 4 * h + (g >> 1));
+                    } else {
+                        vw[i][h] = make_uint4(0u, 0u, 0u, 0u);
+                        vd[i][h] = 0u;
+                    }
+                }
+            }
+        };
+        int t = seg.t0 + warp;
+        int64_t row = row_at(t, page_at(t)), row1 = row_at(t + W, page_at(t + W));
+        int page2 = page_at(t + 2 * W);
+        auto keys_of = [&](int t) { return (int)min((long long)len - (long long)t * KEYS, (long long)KEYS); };
+        if (t < t1) {
+            load_k(row, keys_of(t));
+            load_v(row, keys_of(t));
+        }
+#pragma unroll 1
+        for (; t < t1; t += W) {
+            // the group after the next into L2: 16 rows of codes are consecutive, and so are their scales
+            const int64_t row2 = row_at(t + 2 * W, page2);
+            page2 = page_at(t + 3 * W);
+            if (row2 >= 0) {
+                const int8_t* codes = lane < 16 ? p.kc : p.vc;
+#pragma unroll
+                for (int h = 0; h < H; ++h) prefetch_l2(codes + row2 * HD + ((lane & 15) + 16 * h) * 128);
+                if (lane < 2 * H) prefetch_l2((lane < H ? p.ks : p.vs) + row2 * (HD / 32) + (lane % H) * 64);
+            }
+            float sc[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const __half2 d0 = __half2half2(__ushort_as_half((unsigned short)kd[0][h])), d1 = __half2half2(__ushort_as_half((unsigned short)kd[1][h]));
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t w0 = kw[0][h][s] ^ 0x80808080u, w1 = kw[1][h][s] ^ 0x80808080u;
+                    const uint32_t a0 = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4140>(w0)), d0));
+                    const uint32_t a1 = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4140>(w1)), d1));
+                    const uint32_t a2 = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4342>(w0)), d0));
+                    const uint32_t a3 = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4342>(w1)), d1));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16_16816(sc[n], a0, a1, a2, a3, q[n][h][2 * s], q[n][h][2 * s + 1]);
+                }
+            }
+            const int keys = row >= 0 ? keys_of(t) : 0, keys1 = t + W < t1 ? keys_of(t + W) : 0;
+            load_k(keys1 ? row1 : (int64_t)-1, keys1);
+            // masks: keys that are not there, and in the window those without their bit
+            const long long key0 = (long long)t * KEYS;
+            if (keys < KEYS || key0 + KEYS > ctx) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * n + 2 * c + e, wt = window_row(p, r);
+                        uint64_t m = 0;
+                        if (r < seg.n) m = p.mask ? __ldg(p.mask + seg.q.row0 + wt) : (2ull << wt) - 1;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int key = g + 8 * i;
+                            const long long at = key0 + key - ctx;  // place in the window
+                            if (key >= keys || (at >= 0 && !(m >> (at & 63) & 1))) sc[n][2 * i + e] = -INFINITY;
+                        }
+                    }
+            }
+            float x[NT][4];
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+                float over = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[n][i] = fmaf(sc[n][i], cs, neg[n][i & 1]);
+                        over = fmaxf(over, x[n][i]);
+                    }
+                if (pass || !__any_sync(0xffffffffu, over > kLazy + kLift)) break;
+                // references to the maxima where a score passed one by more than 2^8; sums and O^T follow
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float a[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(sc[n][e], sc[n][2 + e]) * cs;
+#pragma unroll
+                        for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+                        const float ref = kLift - neg[n][e];
+                        a[e] = 1.0f;
+                        if (m > ref + kLazy) {
+                            a[e] = neg[n][e] == kLift - kNoRef ? 0.0f : ex2_approx(ref - m);
+                            neg[n][e] = kLift - m;
+                        }
+                        l[n][e] *= a[e];
+                    }
+#pragma unroll
+                    for (int m = 0; m < H * 8; ++m) o[m][n][0] *= a[0], o[m][n][1] *= a[1], o[m][n][2] *= a[0], o[m][n][3] *= a[1];
+                }
+            }
+            uint32_t b0[NT], b1[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const __half2 h0 = __floats2half2_rn(ex2_approx(x[n][0]), ex2_approx(x[n][1]));
+                const __half2 h1 = __floats2half2_rn(ex2_approx(x[n][2]), ex2_approx(x[n][3]));
+                const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+                l[n][0] += f0.x + f1.x;
+                l[n][1] += f0.y + f1.y;
+                b0[n] = transpose8(h2_as_u32(h0));
+                b1[n] = transpose8(h2_as_u32(h1));
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const __half2 d01 = __halves2half2(__ushort_as_half((unsigned short)vd[0][h]), __ushort_as_half((unsigned short)vd[1][h]));
+                const __half2 d23 = __halves2half2(__ushort_as_half((unsigned short)vd[2][h]), __ushort_as_half((unsigned short)vd[3][h]));
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t w0 = (s == 0 ? vw[0][h].x : s == 1 ? vw[0][h].y : s == 2 ? vw[0][h].z : vw[0][h].w) ^ 0x80808080u;
+                    const uint32_t w1 = (s == 0 ? vw[1][h].x : s == 1 ? vw[1][h].y : s == 2 ? vw[1][h].z : vw[1][h].w) ^ 0x80808080u;
+                    const uint32_t w2 = (s == 0 ? vw[2][h].x : s == 1 ? vw[2][h].y : s == 2 ? vw[2][h].z : vw[2][h].w) ^ 0x80808080u;
+                    const uint32_t w3 = (s == 0 ? vw[3][h].x : s == 1 ? vw[3][h].y : s == 2 ? vw[3][h].z : vw[3][h].w) ^ 0x80808080u;
+                    const uint32_t lo01 = prmt2<0x5140>(w0, w1), hi01 = prmt2<0x7362>(w0, w1);
+                    const uint32_t lo23 = prmt2<0x5140>(w2, w3), hi23 = prmt2<0x7362>(w2, w3);
+                    auto half2_of = [&](uint32_t x, __half2 d, bool upper) {
+                        return h2_as_u32(__hmul2(u32_as_h2(upper ? biased_bytes_to_half2<0x4342>(x) : biased_bytes_to_half2<0x4140>(x)), d));
+                    };
+                    const uint32_t a0 = half2_of(lo01, d01, false), a1 = half2_of(lo01, d01, true);
+                    const uint32_t a2 = half2_of(lo23, d23, false), a3 = half2_of(lo23, d23, true);
+                    const uint32_t e0 = half2_of(hi01, d01, false), e1 = half2_of(hi01, d01, true);
+                    const uint32_t e2 = half2_of(hi23, d23, false), e3 = half2_of(hi23, d23, true);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16_16816(o[8 * h + 2 * s][n], a0, a1, a2, a3, b0[n], b1[n]);
+                        mma_f16_16816(o[8 * h + 2 * s + 1][n], e0, e1, e2, e3, b0[n], b1[n]);
+                    }
+                }
+            }
+            load_v(keys1 ? row1 : (int64_t)-1, keys1);
+            row = row1;
+            row1 = row2;
+        }
+
+        // the warps' parts: (reference, sum) and O of each row; o[m] holds dims 16 g + 2 (m % 8) and the next of half m / 8
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+                const int r = 8 * n + 2 * c + e;
+                if (g == 0) s_ml[warp * N + r] = make_float2(neg[n][e] == kLift - kNoRef ? -INFINITY : kLift - neg[n][e], l[n][e]);
+#pragma unroll
+                for (int m = 0; m < H * 8; ++m)
+                    *reinterpret_cast<float2*>(s_o + (warp * N + r) * HD + 128 * (m >> 3) + 16 * g + 2 * (m & 7)) = make_float2(o[m][n][e], o[m][n][2 + e]);
+            }
+        __syncthreads();
+        const bool whole = seg.begins() && seg.ends();
+        const int slot = 2 * blockIdx.x + (seg.begins() ? 1 : 0);
+#pragma unroll 1
+        for (int i = tid; i < seg.n * (HD / 4); i += W * 32) {
+            const int r = i / (HD / 4), d = i - r * (HD / 4);
+            float m = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) m = fmaxf(m, s_ml[w * N + r].x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float2 ml = s_ml[w * N + r];
+                const float a = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+                const float4 v = reinterpret_cast<const float4*>(s_o + (w * N + r) * HD)[d];
+                sum += a * ml.y;
+                acc.x += a * v.x, acc.y += a * v.y, acc.z += a * v.z, acc.w += a * v.w;
+            }
+            if (whole) {
+                const int t = window_row(p, r);
+                const int64_t out_row = (int64_t)(seg.q.row0 + t) * p.n_q_heads + seg.kvh * p.group + r - t * p.group;
+                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + out_row * HD)[d] =
+                    sum > 0.0f ? make_uint2(Query<T>::out(acc.x * inv, acc.y * inv), Query<T>::out(acc.z * inv, acc.w * inv)) : make_uint2(0u, 0u);
+            } else {
+                reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * p.chunk + r) * HD)[d] = acc;
+                if (d == 0) p.part_ml[(int64_t)slot * p.chunk + r] = make_float2(m, sum);
             }
         }
-        p.joins[blockIdx.x] = join;
+        __syncthreads();  // before the next segment's parts
     }
+    if (tid == 0) leave_join<KEYS>(p, place);
 }
 
 // ---------------------------------------------------------------- joining the partials
@@ -1037,29 +1379,30 @@ int sm_count() {
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
         sms = 152;
-    return sms < 1024 ? sms : 1024;
+    return sms < 512 ? sms : 512;  // the joining kernel lists at most 1024 CTAs
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+enum { kFew = 0, kSome = 1, kMany = 2 };
+
 struct VerifyPlan {
-    int chunk, team;  // most rows of a CTA, CTAs that share an item's rows
-    bool small;
+    int route, ctas, chunk, team;  // CTAs; most rows of one; CTAs that share an item's rows
     size_t ml_off, join_off, bytes;
 };
 
-// Up to 32 rows a window and KV head the kernel with the deeper fetch ring runs; above it teams of CTAs with up to 64.
-constexpr int chunk_of(bool small) { return small ? 32 : 64; }
-
-VerifyPlan verify_plan(int ctas, int group, int hd, int max_rows) {
+// By the rows of the batch's longest window and KV head: up to 8 (16 at head_dim 128) the kernel in which each warp scans
+// for itself; up to 32 the tensor-core tiles with the deeper fetch ring; above that teams of CTAs with up to 64 rows each.
+VerifyPlan verify_plan(int sms, int group, int hd, int max_rows) {
     VerifyPlan v;
     const int rows = max_rows * group;
-    v.small = rows <= 32;
-    v.team = (rows + chunk_of(v.small) - 1) / chunk_of(v.small);
+    v.route = rows <= (hd == 128 ? 16 : 8) ? kFew : rows <= 32 ? kSome : kMany;
+    v.ctas = v.route == kFew ? 2 * sms : sms;
+    v.team = v.route == kMany ? (rows + 63) / 64 : 1;
     v.chunk = (rows + v.team - 1) / v.team;
-    v.ml_off = up256((size_t)ctas * 2 * v.chunk * hd * sizeof(float));
-    v.join_off = v.ml_off + up256((size_t)ctas * 2 * v.chunk * sizeof(float2));
-    v.bytes = v.join_off + (size_t)ctas * sizeof(int4);
+    v.ml_off = up256((size_t)v.ctas * 2 * v.chunk * hd * sizeof(float));
+    v.join_off = v.ml_off + up256((size_t)v.ctas * 2 * v.chunk * sizeof(float2));
+    v.bytes = v.join_off + (size_t)v.ctas * sizeof(int4);
     return v;
 }
 
@@ -1092,14 +1435,30 @@ bool encode_codes(CUtensorMap* map, const int8_t* codes, const kvq8_paged_cache*
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int HD, bool SMALL>
-int launch_verify(const PagedVerifyParams& p, int ctas, cudaStream_t s) {
-    constexpr int N = chunk_of(SMALL);
+template <typename T, int HD, int N>
+int launch_tiles(const PagedVerifyParams& p, const VerifyPlan& v, cudaStream_t s) {
     static SmemOptIn opt;
     if (opt.ensure(paged_verify_kernel<T, HD, N>, VL<HD, N>::kSmBytes) != KVQ8_OK) return KVQ8_ERR_CUDA;
-    const int rc = launch_dependent(paged_verify_kernel<T, HD, N>, ctas, kVerifyThreads, VL<HD, N>::kSmBytes, s, p);
+    return launch_dependent(paged_verify_kernel<T, HD, N>, v.ctas, kVerifyThreads, VL<HD, N>::kSmBytes, s, p);
+}
+
+template <typename T, int HD, int NT>
+int launch_few(const PagedVerifyParams& p, const VerifyPlan& v, cudaStream_t s) {
+    using L = FL<HD, NT>;
+    static SmemOptIn opt;
+    if (opt.ensure(paged_verify_few_kernel<T, HD, NT>, L::kSmBytes) != KVQ8_OK) return KVQ8_ERR_CUDA;
+    return launch_dependent(paged_verify_few_kernel<T, HD, NT>, v.ctas, L::kWarps * 32, L::kSmBytes, s, p);
+}
+
+template <typename T, int HD>
+int launch_verify(const PagedVerifyParams& p, const VerifyPlan& v, cudaStream_t s) {
+    int rc;
+    if (v.route == kFew)
+        rc = HD == 128 && v.chunk > 8 ? launch_few<T, 128, 2>(p, v, s) : launch_few<T, HD, 1>(p, v, s);
+    else
+        rc = v.route == kSome ? launch_tiles<T, HD, 32>(p, v, s) : launch_tiles<T, HD, 64>(p, v, s);
     if (rc != KVQ8_OK) return rc;
-    return launch_dependent(paged_join_kernel<T, HD>, 4 * ctas, kJoinThreads, 0, s, p, ctas);
+    return launch_dependent(paged_join_kernel<T, HD>, 4 * sm_count(), kJoinThreads, 0, s, p, v.ctas);
 }
 
 }  // namespace
@@ -1128,12 +1487,13 @@ extern "C" int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, 
     if (n_rows == 0 || n_seqs == 0) return KVQ8_OK;
     if (!q || !out || !page_table || !lens || !row_starts || q_stride < (int64_t)n_q_heads * kv->head_dim)
         return KVQ8_ERR_INVALID_ARG;
-    const int ctas = sm_count(), group = n_q_heads / kv->n_kv_heads;
-    const VerifyPlan v = verify_plan(ctas, group, kv->head_dim, max_rows);
+    const int group = n_q_heads / kv->n_kv_heads;
+    const VerifyPlan v = verify_plan(sm_count(), group, kv->head_dim, max_rows);
     if (!workspace || workspace_bytes < v.bytes) return KVQ8_ERR_WORKSPACE;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (q_stride * 2) % 16 || !aligned_to(page_table, 4) ||
         !aligned_to(lens, 4) || !aligned_to(row_starts, 4) || !aligned_to(window_mask, 8))
         return KVQ8_ERR_MISALIGNED;
+    if (!aligned_to(kv->k_codes, 32) || !aligned_to(kv->v_codes, 32)) return KVQ8_ERR_MISALIGNED;  // whole blocks per load
     unsigned int* error = device_error_flag();
     if (!error) return KVQ8_ERR_CUDA;
     char* ws = static_cast<char*>(workspace);
@@ -1145,13 +1505,7 @@ extern "C" int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, 
     p.box = kv->page_size < 64 ? kv->page_size : 64;
     if (!encode_codes(&p.tmap_k, kv->k_codes, kv, p.box) || !encode_codes(&p.tmap_v, kv->v_codes, kv, p.box)) return KVQ8_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    auto run = [&](auto hd, auto small) {
-        constexpr int HD = decltype(hd)::value;
-        constexpr bool SMALL = decltype(small)::value;
-        return dtype == KVQ8_F16 ? launch_verify<__half, HD, SMALL>(p, ctas, s) : launch_verify<__nv_bfloat16, HD, SMALL>(p, ctas, s);
-    };
-    using std::integral_constant;
     if (kv->head_dim == 128)
-        return v.small ? run(integral_constant<int, 128>(), std::true_type()) : run(integral_constant<int, 128>(), std::false_type());
-    return v.small ? run(integral_constant<int, 256>(), std::true_type()) : run(integral_constant<int, 256>(), std::false_type());
+        return dtype == KVQ8_F16 ? launch_verify<__half, 128>(p, v, s) : launch_verify<__nv_bfloat16, 128>(p, v, s);
+    return dtype == KVQ8_F16 ? launch_verify<__half, 256>(p, v, s) : launch_verify<__nv_bfloat16, 256>(p, v, s);
 }
