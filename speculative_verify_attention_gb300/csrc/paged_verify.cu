@@ -980,7 +980,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_kernel(const _
 // The next 16 keys' codes are requested as soon as a register is free, and 32 keys' further ahead into L2.
 template <int HD, int NT>
 struct FL {
-    static constexpr int kWarps = 6, kCtas = 2;             // per SM: 168 registers a thread
+    // Warps of a CTA and CTAs of an SM.  At head_dim 128 two CTAs of 6 warps have 168 registers a thread; at 256 that
+    // spills, and one CTA of 8 warps has 255.  Measured both ways: 64 requests of 8192 tokens at head_dim 128 151 us
+    // against 171 us, 20 requests of 16000 tokens at head_dim 256 42 us against 33 us.
+    static constexpr int kWarps = HD == 256 ? 8 : 6, kCtas = HD == 256 ? 1 : 2;
     static constexpr int N = 8 * NT, H = HD / 128;           // rows; 128-dim halves
     static constexpr int kSmO = 0, kSmMl = kWarps * N * HD * 4, kSmBytes = kSmMl + kWarps * N * 8;
 };
@@ -991,11 +994,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ void load32(uint32_t (&w)[8], const int8_t* at) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(at));
-}
 __device__ __forceinline__ uint4 load16(const int8_t* at) {
     uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
@@ -1397,30 +1395,13 @@ VerifyPlan verify_plan(int sms, int group, int hd, int max_rows) {
     VerifyPlan v;
     const int rows = max_rows * group;
     v.route = rows <= (hd == 128 ? 16 : 8) ? kFew : rows <= 32 ? kSome : kMany;
-    v.ctas = v.route == kFew ? 2 * sms : sms;
+    v.ctas = v.route == kFew ? (hd == 128 ? FL<128, 1>::kCtas : FL<256, 1>::kCtas) * sms : sms;
     v.team = v.route == kMany ? (rows + 63) / 64 : 1;
     v.chunk = (rows + v.team - 1) / v.team;
     v.ml_off = up256((size_t)v.ctas * 2 * v.chunk * hd * sizeof(float));
     v.join_off = v.ml_off + up256((size_t)v.ctas * 2 * v.chunk * sizeof(float2));
     v.bytes = v.join_off + (size_t)v.ctas * sizeof(int4);
     return v;
-}
-
-// Launched as programmatic dependents: their set-up overlaps the end of the kernel before, and they wait for all of
-// its writes before they read or write anything (griddepcontrol.wait).
-template <typename Kernel, typename... Args>
-int launch_dependent(Kernel* kernel, int grid, int threads, int smem, cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
 }
 
 // The code plane as rows of head_dim bytes; a box is 128 bytes of `box` consecutive keys of a page.
