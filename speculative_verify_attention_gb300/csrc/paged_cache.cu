@@ -1,12 +1,12 @@
 // paged_cache.cu -- K and V tokens into the pages of a Q8_0 cache by slot (kvq8_paged_append), and back out of them
 // as values (kvq8_paged_read).
 //
-// Append is the block quantiser of kvq8_append (q8_0_block: scale max|x| / 127 of 32 values, codes x / scale rounded
-// half away from zero) over fp32, fp16 or bf16 tokens, the cache row taken from the token's slot.  Read is its
-// inverse, code * scale rounded once to the type asked for.  Both are bandwidth-bound: one read and one write of
-// each value.
-#include <cuda_bf16.h>
-
+// Append is the block quantiser of kvq8_append (scale max|x| / 127 of 32 values, codes x / scale rounded half away from
+// zero) over fp32, fp16 or bf16 tokens, the cache row taken from the token's slot.  Read is its inverse, code * scale
+// rounded once to the type asked for.  Both read and write each value once, and are near enough to the memory's rate
+// for instructions a value to count: neither has a conversion instruction a value.  16401 tokens of 8 x 128 fp32 into the
+// cache and as many slots back as fp16 (238 MB) 53 us in two launches, 4.5 TB/s; with four values a lane and
+// conversion instructions 79 us, with twice the tokens a thread 57 us.
 #include "paged.cuh"
 #include "q8_0.cuh"
 
@@ -14,26 +14,10 @@ namespace kvq8 {
 namespace {
 
 constexpr int kPagedThreads = 256;
-constexpr int kPagedTok = 4;
-
+// Tokens of a thread: their loads are in flight together (64 bytes of input in append, 32 of codes in read).
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__half>(const __half* p) {
-    const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 a = __half22float2(u32_as_h2(r.x)), b = __half22float2(u32_as_h2(r.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 r = __ldg(reinterpret_cast<const uint2*>(p));  // a bf16 is the upper half of its fp32
-    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                       __uint_as_float(r.y & 0xffff0000u));
-}
+constexpr int kAppendTok = sizeof(T) == 4 ? 2 : 4;
+constexpr int kReadTok = 4;
 
 struct PagedIO {
     const void* x[2];         // append: K and V tokens; read: unused
@@ -47,38 +31,41 @@ struct PagedIO {
     int n_tok, n_kv_heads, head_dim, page_shift;
 };
 
-// Block (tx, ty): tx consecutive float4 columns of a token row (a multiple of 32, so a warp stays in one row) for
-// ty * kPagedTok tokens; grid z is the plane.  Lanes of tokens past the end or with a slot outside the cache
-// quantise zeros (every lane takes part in the block's shuffle maximum) and store nothing.
+// Block (tx, ty): tx consecutive groups of eight values of a token's row for ty x kAppendTok tokens; grid z is the
+// plane.  The four lanes of a 32-value block are in one row (rows hold whole blocks, so a row's groups are a multiple
+// of 16, and tx is one too).  Lanes past the row's or the tokens' end, or with a slot outside the cache, quantise zeros
+// (every lane takes part in the shuffles) and store nothing.
 template <typename T>
-__global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const PagedIO p) {
+__global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const __grid_constant__ PagedIO p) {
+    constexpr int TOK = kAppendTok<T>;
     const int z = blockIdx.z;
     const T* x = static_cast<const T*>(p.x[z]);
-    const int f4_head = p.head_dim / 4;
+    const int g_head = p.head_dim / 8;
     const int j = blockIdx.y * blockDim.x + threadIdx.x;
-    const bool col_ok = j < p.n_kv_heads * f4_head;
-    const int h = j / f4_head, i = j - h * f4_head;
-    const int tok0 = (blockIdx.x * blockDim.y + threadIdx.y) * kPagedTok;
-    float4 v[kPagedTok];
-    int64_t slot[kPagedTok];
+    const bool col_ok = j < p.n_kv_heads * g_head;
+    const int h = j / g_head, i = j - h * g_head;
+    const int tok0 = (blockIdx.x * blockDim.y + threadIdx.y) * TOK;
+    Eight<T> v[TOK];
+    int64_t slot[TOK];
 #pragma unroll
-    for (int t = 0; t < kPagedTok; ++t) {
-        v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int t = 0; t < TOK; ++t) {
+        v[t].clear();
         slot[t] = -1;
         if (col_ok && tok0 + t < p.n_tok) {
             slot[t] = __ldg(p.slots + tok0 + t);
-            v[t] = load4<T>(x + (int64_t)(tok0 + t) * p.tok_stride[z] + (int64_t)j * 4);
+            v[t].load(x + (int64_t)(tok0 + t) * p.tok_stride[z] + (int64_t)j * 8);
         }
     }
-    const int nb = p.head_dim / kQBlock;
 #pragma unroll
-    for (int t = 0; t < kPagedTok; ++t) {
+    for (int t = 0; t < TOK; ++t) {
+        float f[8];
+        v[t].floats(f);
         uint16_t scale_bits;
-        const uint32_t packed = q8_0_block(v[t], &scale_bits);
+        const uint2 packed = q8_0_block8(f, &scale_bits);
         if (slot[t] >= 0 && slot[t] < p.n_slots) {
             const int64_t row = paged_row(slot[t], h, p.n_kv_heads, p.page_shift);
-            *reinterpret_cast<uint32_t*>(p.codes[z] + row * p.head_dim + i * 4) = packed;
-            if ((i & 7) == 0) p.scales[z][row * nb + (i >> 3)] = scale_bits;
+            *reinterpret_cast<uint2*>(p.codes[z] + row * p.head_dim + i * 8) = packed;
+            if ((i & 3) == 0) p.scales[z][row * (p.head_dim / kQBlock) + (i >> 2)] = scale_bits;
         }
     }
 }
@@ -110,21 +97,20 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* dst, const 
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// The same block shape over groups of eight values: 8 code bytes and their scale in, eight values out.  A slot
-// outside the cache gives zeros.
+// The same block shape: eight code bytes and their scale in, eight values out.  A slot outside the cache gives zeros.
 template <typename T>
-__global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const PagedIO p) {
+__global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const __grid_constant__ PagedIO p) {
     const int z = blockIdx.z;
     T* y = static_cast<T*>(p.y[z]);
     const int g_head = p.head_dim / 8;
     const int j = blockIdx.y * blockDim.x + threadIdx.x;
     if (j >= p.n_kv_heads * g_head) return;
     const int h = j / g_head, i = j - h * g_head;
-    const int tok0 = (blockIdx.x * blockDim.y + threadIdx.y) * kPagedTok;
-    uint2 c[kPagedTok];
-    uint16_t sc[kPagedTok];
+    const int tok0 = (blockIdx.x * blockDim.y + threadIdx.y) * kReadTok;
+    uint2 c[kReadTok];
+    uint16_t sc[kReadTok];
 #pragma unroll
-    for (int t = 0; t < kPagedTok; ++t) {
+    for (int t = 0; t < kReadTok; ++t) {
         c[t] = make_uint2(0u, 0u);
         sc[t] = 0;
         if (tok0 + t < p.n_tok) {
@@ -137,29 +123,35 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const PagedIO
         }
     }
 #pragma unroll
-    for (int t = 0; t < kPagedTok; ++t) {
+    for (int t = 0; t < kReadTok; ++t) {
         if (tok0 + t >= p.n_tok) break;
         const float d = half_bits_to_float(sc[t]);
+        const uint32_t lo = c[t].x ^ 0x80808080u, hi = c[t].y ^ 0x80808080u;  // code + 128
         float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = (float)(int8_t)(c[t].x >> (8 * k)) * d;  // exact in fp32: 8 by 11 bits
-            v[4 + k] = (float)(int8_t)(c[t].y >> (8 * k)) * d;
+        for (int k = 0; k < 4; ++k) {  // 2^23 + (code + 128) by its bits; the product is exact in fp32, 8 by 11 bits
+            v[k] = (__uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7440 + k)) - 8388736.0f) * d;
+            v[4 + k] = (__uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7440 + k)) - 8388736.0f) * d;
         }
         store8<T>(y + (int64_t)(tok0 + t) * p.tok_stride[z] + (int64_t)h * p.head_stride[z] + i * 8, v);
     }
 }
 
-// Columns a block covers (a multiple of 32, at most 256) and its token rows.
+// Groups of a row that a block covers and its token rows, whole warps in all: a row's groups are a multiple of 16 (half
+// a warp), so an odd multiple takes an even count of rows, or is rounded up where one row fills the block.
 dim3 paged_block(int cols) {
-    const int tx = cols < kPagedThreads ? cols / 32 * 32 : kPagedThreads;
-    return dim3((unsigned)tx, (unsigned)(kPagedThreads / tx));
+    int tx = cols < kPagedThreads ? cols : kPagedThreads, ty = kPagedThreads / tx;
+    if (tx % 32) {
+        if (ty == 1) tx = (tx + 31) / 32 * 32;
+        if (ty > 1) ty &= ~1;
+    }
+    return dim3((unsigned)tx, (unsigned)ty);
 }
 
 template <typename Kernel>
-int launch_paged(Kernel* kernel, const PagedIO& p, int cols, cudaStream_t stream) {
+int launch_paged(Kernel* kernel, const PagedIO& p, int cols, int tok, cudaStream_t stream) {
     const dim3 block = paged_block(cols);
-    const int64_t per = (int64_t)block.y * kPagedTok;
+    const int64_t per = (int64_t)block.y * tok;
     const int64_t gx = (p.n_tok + per - 1) / per;
     const dim3 grid((unsigned)gx, (unsigned)((cols + block.x - 1) / block.x), 2u);
     kernel<<<grid, block, 0, stream>>>(p);
@@ -202,11 +194,11 @@ extern "C" int kvq8_paged_append(const void* k, const void* v, int dtype, int n_
     p.x[1] = v;
     p.tok_stride[0] = k_stride;
     p.tok_stride[1] = v_stride;
-    const int cols = (int)(row / 4);
+    const int cols = (int)(row / 8);
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == KVQ8_F32) return launch_paged(paged_append_kernel<float>, p, cols, s);
-    if (dtype == KVQ8_F16) return launch_paged(paged_append_kernel<__half>, p, cols, s);
-    return launch_paged(paged_append_kernel<__nv_bfloat16>, p, cols, s);
+    if (dtype == KVQ8_F32) return launch_paged(paged_append_kernel<float>, p, cols, kAppendTok<float>, s);
+    if (dtype == KVQ8_F16) return launch_paged(paged_append_kernel<__half>, p, cols, kAppendTok<__half>, s);
+    return launch_paged(paged_append_kernel<__nv_bfloat16>, p, cols, kAppendTok<__nv_bfloat16>, s);
 }
 
 extern "C" int kvq8_paged_read(const kvq8_paged_cache* kv, const int64_t* slots, int n_tok, int dtype, void* k, void* v,
@@ -231,8 +223,7 @@ extern "C" int kvq8_paged_read(const kvq8_paged_cache* kv, const int64_t* slots,
     if (!aligned16(k) || !aligned16(v) || !aligned_to(slots, 8)) return KVQ8_ERR_MISALIGNED;
     const int cols = kv->n_kv_heads * (kv->head_dim / 8);
     cudaStream_t s = (cudaStream_t)stream;
-    const int padded = cols < 32 ? 32 : cols;  // hd128 with one head has 16 groups a row
-    if (dtype == KVQ8_F32) return launch_paged(paged_read_kernel<float>, p, padded, s);
-    if (dtype == KVQ8_F16) return launch_paged(paged_read_kernel<__half>, p, padded, s);
-    return launch_paged(paged_read_kernel<__nv_bfloat16>, p, padded, s);
+    if (dtype == KVQ8_F32) return launch_paged(paged_read_kernel<float>, p, cols, kReadTok, s);
+    if (dtype == KVQ8_F16) return launch_paged(paged_read_kernel<__half>, p, cols, kReadTok, s);
+    return launch_paged(paged_read_kernel<__nv_bfloat16>, p, cols, kReadTok, s);
 }

@@ -82,6 +82,48 @@ __device__ __forceinline__ uint32_t q8_0_block(float4 v, uint16_t* scale_bits) {
     return packed;
 }
 
+// The same block held by 4 consecutive lanes, 8 values per lane in block order, for kernels that are bound by issue:
+// two shuffles a lane instead of three a half lane, and no conversion instruction a value.  With r as above and M =
+// 1.5 * 2^23, t = fl(x r + M) is M plus the nearest integer n of x r (the spacing of floats at M is 1), so n is the low
+// byte of t's bits, and fl(x r - n) is within 2^-25 of x r - n.  x r differs from fl(x / d) by less than 2^-15, so
+// where |x r - n| <= 1/2 - 2^-12 the code is n, as above; other lanes, and those with a value that is not finite
+// (max.NaN keeps it), take the IEEE division.
+__device__ __forceinline__ uint2 q8_0_block8(const float (&x)[8], uint16_t* scale_bits) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float d = scale_of<127>(amax);
+    *scale_bits = __half_as_ushort(__float2half_rn(d));
+    constexpr float kMagic = 12582912.0f;
+    float r, far = 0.0f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    uint32_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float t = __fmaf_rn(x[e], r, kMagic);
+        const float off = fabsf(__fmaf_rn(x[e], r, -__fsub_rn(t, kMagic)));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(off));
+        c[e] = __float_as_uint(t);
+    }
+    if (!(far <= 0.5f - 0x1p-12f)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = (uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x[e], d)), -127.0f), 127.0f);
+    }
+    if (d == 0.0f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = 0u;
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t lo = __byte_perm(c[4 * e], c[4 * e + 1], 0x0040), hi = __byte_perm(c[4 * e + 2], c[4 * e + 3], 0x0040);
+        w[e] = __byte_perm(lo, hi, 0x5410);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
 }  // namespace kvq8
 
 namespace kvq8 {
