@@ -6,17 +6,18 @@
 //   x = seen ? (x > 0 ? x / repetition : x * repetition) : x
 //   x = x - (frequency * c + presence * [c > 0]);  x = x + bias(v);  x = allowed(v) ? x : -inf
 // all in fp32, whatever the type of the logits.
-#include <cuda_bf16.h>
+#include <float.h>
 
 #include "paged.cuh"
 
 namespace kvq8 {
 namespace {
 
-constexpr int kAdjThreads = 256;
+constexpr int kAdjThreads = 128;
 constexpr int kAdjPer = 8;                          // values of one row per thread
 constexpr int kAdjChunk = kAdjThreads * kAdjPer;    // vocabulary values per block
-constexpr int kAdjRows = kAdjThreads / kMaxWindowRows;  // rows per block: a thread for every (row, window token)
+constexpr int kAdjDepth = 2;                        // rows whose logits are in flight
+constexpr int kAdjRows = 12;                        // rows of a request that a block takes, about
 constexpr uint32_t kInPrompt = 0x80000000u;
 
 struct AdjustParams {
@@ -37,205 +38,200 @@ struct AdjustParams {
     int n_rows, vocab, n_seqs, n_states, n_bias, n_grammar;
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-// Eight consecutive values, 16-byte aligned (two loads for fp32).
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __half* p, float (&x)[8]) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(u32_as_h2(w[k]));
-        x[2 * k] = f.x, x[2 * k + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[2 * k] = __uint_as_float(w[k] << 16), x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+// A seen value under the repetition penalty.  x / b by b's rounded reciprocal r and one corrected step, as in scale_of of
+// the quantiser: within one unit of the last place (mostly the IEEE quotient) in four operations instead of a called
+// division, which bound the kernel where a few percent of the vocabulary was seen (every warp then has such a value).
+// An infinite x has no remainder (NaN, which the maximum drops).
+__device__ __forceinline__ float repeated(float x, float b, float r) {
+    const float q0 = x * r;
+    const float q = fmaf(fmaxf(fmaf(-q0, b, x), -FLT_MAX), r, q0);
+    return x > 0.0f ? q : x * b;
 }
 
-struct Penalty {
-    float repetition, frequency, presence;
-    bool on;
-};
-
-__device__ __forceinline__ float bend(float x, uint32_t word, int extra, const Penalty& q, float bias, bool allowed) {
+// The rare value: one that the row's window tokens raise the count of, or any where b or r is not a normal number.
+__device__ __noinline__ float bend(float x, uint32_t word, int extra, float b, float frequency, float presence, float bias) {
     const int c = (int)(word & ~kInPrompt) + extra;
-    if (q.on) {
-        if (c > 0 || (word & kInPrompt)) x = x > 0.0f ? x / q.repetition : x * q.repetition;
-        x -= q.frequency * (float)c + (c > 0 ? q.presence : 0.0f);
-    }
-    x += bias;
-    return allowed ? x : -INFINITY;
+    if (c > 0 || word) x = x > 0.0f ? x / b : x * b;
+    return x + (bias - (c > 0 ? frequency * (float)c + presence : 0.0f));
 }
 
-// Block (chunk of the vocabulary, group of kAdjRows rows).  The rows' logits are requested before anything else.
-// Counts and the bias table of a request are loaded once for its rows of the group.  A row's window tokens change
-// few of its values: the thread of (row, window token j) computes that value from the raw logit before any is
-// written (the output may be the input) and writes it after the row's plain values.
+// Block (chunk of the vocabulary, request, share of its rows): a thread owns the same eight values of every row, so the
+// penalties and biases of those are worked out once and stay in its registers, and it knows which of the window's
+// tokens are among them (`mine`, one bit a token).  Then the rows stream past, kAdjDepth rows' logits in flight.  No
+// thread reads what another writes, so the output may be the input.
+// Bound by issue: about 180 instructions for a warp's 256 values where every warp has a seen one.  12 requests of 16 to
+// 32 rows over 248320 bf16 logits (451 MB) 98 us, 4.6 TB/s; the same with a division called per seen value 182 us, with
+// four rows in flight and 6 blocks of an SM (80 registers) 108 us, with 32 rows a block (fewer prologues, a longer tail)
+// 121 us, with 8 rows 100 us.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kAdjThreads) logits_adjust_kernel(const AdjustParams p) {
-    __shared__ int s_bias[kAdjChunk];  // last entry of the request's list for each value of the chunk, or -1
-    __shared__ int s_seq[kAdjRows];
-    const int tid = threadIdx.x;
-    const int r0 = blockIdx.y * kAdjRows, v0 = blockIdx.x * kAdjChunk;
-    const T* in = static_cast<const T*>(p.logits);
-    auto at = [&](int i) { return VEC ? v0 + tid * kAdjPer + i : v0 + i * kAdjThreads + tid; };
+__global__ void __launch_bounds__(kAdjThreads, !VEC ? 4 : sizeof(T) == 4 ? 6 : 8) logits_adjust_kernel(const __grid_constant__ AdjustParams p) {
+    // (place + 1) << 32 | value of the last entry of the request's list for each value of the chunk, or 0
+    __shared__ __align__(16) unsigned long long s_bias[kAdjChunk];
+    __shared__ uint32_t s_mine[2][kAdjThreads];             // window tokens among a thread's values
+    __shared__ int s_token[kMaxWindowRows];
+    const int tid = threadIdx.x, b = blockIdx.y;
+    const int v0 = blockIdx.x * kAdjChunk;
+    // what depends on the request alone, asked for together
+    const int first = __ldg(p.row_starts + b), last = __ldg(p.row_starts + b + 1);
+    const bool on = p.penalties != nullptr;
+    float repetition = 1.0f, frequency = 0.0f, presence = 0.0f;
+    if (on) repetition = __ldg(p.penalties + 3 * b), frequency = __ldg(p.penalties + 3 * b + 1), presence = __ldg(p.penalties + 3 * b + 2);
+    int state = -1, b0 = 0, b1 = 0;
+    if (p.counts) state = p.state_of ? __ldg(p.state_of + b) : b;
+    if (p.bias_starts) b0 = __ldg(p.bias_starts + b), b1 = __ldg(p.bias_starts + b + 1);
+    const int rows = last - first;
+    if (first < 0 || last > p.n_rows || rows <= (int)blockIdx.z || (p.tokens && rows > kMaxWindowRows)) return;
+    if (b0 < 0 || b1 > p.n_bias) b0 = b1 = 0;
+    const bool counted = state >= 0 && state < p.n_states, windows = on && p.tokens;
+    const bool odd = !(fabsf(repetition) > 0x1p-100f && fabsf(repetition) < 0x1p100f);
 
-    float x[kAdjRows][kAdjPer];
-#pragma unroll
-    for (int k = 0; k < kAdjRows; ++k) {
-        const bool row_ok = r0 + k < p.n_rows;
-        const T* src = in + (int64_t)(r0 + k) * p.in_stride;
+    auto at = [&](int i) { return VEC ? v0 + tid * kAdjPer + i : v0 + i * kAdjThreads + tid; };
+    const bool mine_ok = at(0) < p.vocab;  // of VEC all eight values, of the others the first at least
+    const int lane = tid & 31, step = gridDim.z, n_rows = (rows - (int)blockIdx.z + step - 1) / step;
+    // The block's n-th row is z + n step.  Its grammar: lane n % 32 holds the index of it, 32 rows at a time.
+    auto grammar_at = [&](int n) {
+        if (!p.grammar || n >= n_rows) return -1;
+        const int r = first + (int)blockIdx.z + n * step, g = p.grammar_of ? __ldg(p.grammar_of + r) : r;
+        return g < p.n_grammar ? g : -1;
+    };
+    int grammars = grammar_at(lane);
+    const int64_t in_step = (int64_t)step * p.in_stride, out_step = (int64_t)step * p.out_stride;
+    const T* src = static_cast<const T*>(p.logits) + (int64_t)(first + (int)blockIdx.z) * p.in_stride;
+    float* dst = p.out + (int64_t)(first + (int)blockIdx.z) * p.out_stride;
+    const int64_t n_words = (p.vocab + 31) / 32;
+    Eight<T> x[kAdjDepth];
+    uint32_t allowed[kAdjDepth];  // bit i (VEC: from bit at(0) % 32 on): value i of the row is allowed
+    auto load = [&](int k, int n) {  // row n into place k; called for n = 0, 1, 2, ...
+        if (n >= n_rows) return;
         if (VEC) {
-            if (row_ok && at(0) < p.vocab) load8(src + at(0), x[k]);
+            if (mine_ok) x[k].load_whole(src + at(0));
         } else {
 #pragma unroll
-            for (int i = 0; i < kAdjPer; ++i) x[k][i] = row_ok && at(i) < p.vocab ? to_f32(src[at(i)]) : 0.0f;
+            for (int i = 0; i < kAdjPer; ++i) x[k].put(i, at(i) < p.vocab ? src[at(i)] : T(0.0f));
         }
-    }
-    if (tid < kAdjRows) s_seq[tid] = -1;
-    __syncthreads();
-    for (int b = tid; b < p.n_seqs; b += kAdjThreads) {
-        const int a = p.row_starts[b], e = p.row_starts[b + 1];
-        if (a < 0 || e > p.n_rows || (p.tokens && e - a > kMaxWindowRows)) continue;
-#pragma unroll
-        for (int k = 0; k < kAdjRows; ++k)
-            if (a <= r0 + k && r0 + k < e) s_seq[k] = b;
-    }
-    __syncthreads();
-
-    for (int k0 = 0; k0 < kAdjRows;) {  // rows k0 .. k1 - 1 belong to one request
-        const int b = s_seq[k0];
-        int k1 = k0 + 1;
-        while (k1 < kAdjRows && s_seq[k1] == b) ++k1;
-        if (b < 0) {
-            k0 = k1;
-            continue;
-        }
-        const int first = p.row_starts[b], rows = p.row_starts[b + 1] - first;
-        Penalty q = {1.0f, 0.0f, 0.0f, p.penalties != nullptr};
-        if (q.on) q.repetition = p.penalties[3 * b], q.frequency = p.penalties[3 * b + 1], q.presence = p.penalties[3 * b + 2];
-        int state = p.counts ? (p.state_of ? p.state_of[b] : b) : -1;
-        if (state < 0 || state >= p.n_states) state = -1;
-        const uint32_t* counts = p.counts + (int64_t)max(state, 0) * p.vocab;
-        uint32_t word[kAdjPer];
-#pragma unroll
-        for (int i = 0; i < kAdjPer; ++i) word[i] = 0u;
-        if (q.on && state >= 0) {
+        src += in_step;
+        if ((n & 31) == 0 && n) grammars = grammar_at(n + lane);
+        const int g = __shfl_sync(0xffffffffu, grammars, n & 31);
+        allowed[k] = ~0u;
+        if (g >= 0) {
+            const uint32_t* words = p.grammar + g * n_words;
             if (VEC) {
-                if (at(0) < p.vocab) {
-                    const uint4 a = __ldg(reinterpret_cast<const uint4*>(counts + at(0)));
-                    const uint4 c = __ldg(reinterpret_cast<const uint4*>(counts + at(0)) + 1);
-                    word[0] = a.x, word[1] = a.y, word[2] = a.z, word[3] = a.w;
-                    word[4] = c.x, word[5] = c.y, word[6] = c.z, word[7] = c.w;
+                if (mine_ok) allowed[k] = __ldg(words + (at(0) >> 5));
+            } else {
+                allowed[k] = 0u;
+#pragma unroll
+                for (int i = 0; i < kAdjPer; ++i)
+                    if (at(i) < p.vocab) allowed[k] |= (__ldg(words + (at(i) >> 5)) >> (at(i) & 31) & 1u) << i;
+            }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kAdjDepth; ++k) load(k, k);
+    const uint32_t* counts = p.counts + (int64_t)max(state, 0) * p.vocab;
+    uint32_t word[kAdjPer];
+#pragma unroll
+    for (int i = 0; i < kAdjPer; ++i) word[i] = 0u;
+    if (counted) {
+        if (VEC) {
+            if (at(0) < p.vocab) load32(word, counts + at(0));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kAdjPer; ++i)
+                if (at(i) < p.vocab) word[i] = __ldg(counts + at(i));
+        }
+    }
+
+    uint64_t mine = 0;
+    float bias[kAdjPer];
+#pragma unroll
+    for (int i = 0; i < kAdjPer; ++i) bias[i] = 0.0f;
+    if (windows || b1 > b0 || odd) {
+        s_mine[0][tid] = s_mine[1][tid] = 0u;
+#pragma unroll
+        for (int i = 0; i < kAdjPer / 2; ++i) reinterpret_cast<uint4*>(s_bias)[i * kAdjThreads + tid] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        for (int j = tid; windows && j < rows; j += kAdjThreads) {
+            const int v = __ldg(p.tokens + first + j);
+            s_token[j] = v;
+            if (v >= v0 && v < min(v0 + kAdjChunk, p.vocab))
+                atomicOr(&s_mine[j >> 5][VEC ? (v - v0) / kAdjPer : (v - v0) % kAdjThreads], 1u << (j & 31));
+        }
+        for (int i = tid; i < b1 - b0; i += kAdjThreads) {
+            const int v = __ldg(p.bias_tokens + b0 + i);
+            const uint32_t value = __float_as_uint(__ldg(p.bias_values + b0 + i));
+            if (v >= v0 && v < v0 + kAdjChunk) atomicMax(&s_bias[v - v0], (unsigned long long)(i + 1) << 32 | value);
+        }
+        __syncthreads();
+        mine = (uint64_t)s_mine[1][tid] << 32 | s_mine[0][tid];
+#pragma unroll
+        for (int i = 0; i < kAdjPer; ++i) bias[i] = __uint_as_float((uint32_t)s_bias[at(i) - v0]);
+    }
+    // c and the mark of a value, as its penalty and a bit
+    const float inverse = 1.0f / repetition;
+    uint32_t seen = 0;
+    bool touched = false;
+    float shift[kAdjPer];  // - (frequency c + presence) + bias
+#pragma unroll
+    for (int i = 0; i < kAdjPer; ++i) {
+        const int c = (int)(word[i] & ~kInPrompt);
+        shift[i] = bias[i] - (c > 0 ? frequency * (float)c + presence : 0.0f);
+        if (word[i]) seen |= 1u << i;
+        touched |= word[i] || bias[i] != 0.0f;
+    }
+
+    for (int n0 = 0; n0 < n_rows; n0 += kAdjDepth) {
+#pragma unroll
+        for (int k = 0; k < kAdjDepth; ++k) {
+            if (n0 + k >= n_rows) break;
+            float y[8];
+            x[k].floats(y);
+            const uint32_t bits = VEC ? allowed[k] >> (at(0) & 31) : allowed[k];
+            load(k, n0 + k + kAdjDepth);
+            uint64_t sees = 0;
+            if (mine) {
+                const int r = (int)blockIdx.z + (n0 + k) * step;
+                sees = mine & (p.mask ? __ldg(p.mask + first + r) : (2ull << r) - 1);
+            }
+            if (sees || (odd && touched)) {
+#pragma unroll
+                for (int i = 0; i < kAdjPer; ++i) {
+                    int extra = 0;
+#pragma unroll 1
+                    for (uint64_t rest = sees; rest; rest &= rest - 1) extra += s_token[__ffsll((long long)rest) - 1] == at(i);
+                    const uint32_t w = counted && at(i) < p.vocab ? __ldg(counts + at(i)) : 0u;
+                    const float bias = __uint_as_float((uint32_t)s_bias[at(i) - v0]);
+                    y[i] = bend(y[i], w, extra, repetition, frequency, presence, bias);
                 }
+            } else if (touched) {
+#pragma unroll
+                for (int i = 0; i < kAdjPer; ++i) {
+                    if (seen >> i & 1) y[i] = repeated(y[i], repetition, inverse);
+                    y[i] += shift[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAdjPer; ++i)
+                if (!(bits >> i & 1)) y[i] = -INFINITY;
+            if (VEC) {
+                if (mine_ok)
+                    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + at(0)), "f"(y[0]), "f"(y[1]),
+                                 "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                                 : "memory");
             } else {
 #pragma unroll
                 for (int i = 0; i < kAdjPer; ++i)
-                    if (at(i) < p.vocab) word[i] = __ldg(counts + at(i));
+                    if (at(i) < p.vocab) dst[at(i)] = y[i];
             }
+            dst += out_step;
         }
-        int n_bias = 0, bias0 = 0;
-        if (p.bias_starts) {
-            bias0 = p.bias_starts[b];
-            const int e = p.bias_starts[b + 1];
-            if (bias0 >= 0 && e <= p.n_bias && e > bias0) n_bias = e - bias0;
-        }
-        float bias[kAdjPer];
-#pragma unroll
-        for (int i = 0; i < kAdjPer; ++i) bias[i] = 0.0f;
-        if (n_bias) {
-            __syncthreads();  // an earlier request's table has been read
-#pragma unroll
-            for (int i = 0; i < kAdjPer; ++i) s_bias[i * kAdjThreads + tid] = -1;
-            __syncthreads();
-            for (int i = tid; i < n_bias; i += kAdjThreads) {
-                const int v = __ldg(p.bias_tokens + bias0 + i);
-                if (v >= v0 && v < v0 + kAdjChunk) atomicMax(&s_bias[v - v0], i);
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kAdjPer; ++i) {
-                const int e = s_bias[at(i) - v0];
-                if (e >= 0) bias[i] = __ldg(p.bias_values + bias0 + e);
-            }
-        }
-        // this thread's window token: (row kw, token j)
-        const int kw = tid / kMaxWindowRows, j = tid % kMaxWindowRows;
-        int special = -1;
-        float special_x = 0.0f;
-        if (q.on && p.tokens && kw >= k0 && kw < k1 && j < rows) {
-            const int r = r0 + kw;
-            const uint64_t all = rows >= 64 ? ~0ull : (1ull << rows) - 1;
-            uint64_t m = p.mask ? p.mask[r] : (2ull << (r - first)) - 1;
-            m &= all;
-            const int v = p.tokens[first + j];
-            if ((m >> j & 1) && v >= v0 && v < min(v0 + kAdjChunk, p.vocab)) {
-                int extra = 0, lowest = -1;
-                for (uint64_t rest = m; rest; rest &= rest - 1) {
-                    const int i = __ffsll((long long)rest) - 1;
-                    if (p.tokens[first + i] == v) {
-                        if (lowest < 0) lowest = i;
-                        ++extra;
-                    }
-                }
-                if (lowest == j) {
-                    float bv = 0.0f;
-                    if (n_bias && s_bias[v - v0] >= 0) bv = p.bias_values[bias0 + s_bias[v - v0]];
-                    bool allowed = true;
-                    const int g = p.grammar ? (p.grammar_of ? p.grammar_of[r] : r) : -1;
-                    if (g >= 0 && g < p.n_grammar)
-                        allowed = p.grammar[(int64_t)g * ((p.vocab + 31) / 32) + (v >> 5)] >> (v & 31) & 1;
-                    special = v;
-                    special_x = bend(to_f32(in[(int64_t)r * p.in_stride + v]), state >= 0 ? counts[v] : 0u, extra, q, bv, allowed);
-                }
-            }
-        }
-        __syncthreads();  // every special value has read its logit
-#pragma unroll
-        for (int k = 0; k < kAdjRows; ++k) {
-            if (k < k0 || k >= k1) continue;
-            const int r = r0 + k;
-            const int g = p.grammar ? (p.grammar_of ? p.grammar_of[r] : r) : -1;
-            const bool masked = g >= 0 && g < p.n_grammar;
-            const uint32_t* words = p.grammar + (int64_t)max(g, 0) * ((p.vocab + 31) / 32);
-            float* dst = p.out + (int64_t)r * p.out_stride;
-            if (VEC) {
-                if (at(0) < p.vocab) {
-                    const uint32_t bits = masked ? __ldg(words + (at(0) >> 5)) >> (at(0) & 31) : 0xffu;
-                    float y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = bend(x[k][i], word[i], 0, q, bias[i], bits >> i & 1);
-                    reinterpret_cast<float4*>(dst + at(0))[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    reinterpret_cast<float4*>(dst + at(0))[1] = make_float4(y[4], y[5], y[6], y[7]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < kAdjPer; ++i) {
-                    if (at(i) >= p.vocab) break;
-                    const bool allowed = !masked || (__ldg(words + (at(i) >> 5)) >> (at(i) & 31) & 1);
-                    dst[at(i)] = bend(x[k][i], word[i], 0, q, bias[i], allowed);
-                }
-            }
-        }
-        __syncthreads();  // the plain values are written
-        if (special >= 0) p.out[(int64_t)(r0 + kw) * p.out_stride + special] = special_x;
-        k0 = k1;
     }
 }
 
 template <typename T>
 int launch_adjust(const AdjustParams& p, bool vec, cudaStream_t s) {
-    const dim3 grid((unsigned)((p.vocab + kAdjChunk - 1) / kAdjChunk), (unsigned)((p.n_rows + kAdjRows - 1) / kAdjRows));
+    // about kAdjRows rows a block, by the mean of the requests' rows
+    const int shares = (p.n_rows + p.n_seqs * kAdjRows - 1) / (p.n_seqs * kAdjRows);
+    const dim3 grid((unsigned)((p.vocab + kAdjChunk - 1) / kAdjChunk), (unsigned)p.n_seqs, (unsigned)(shares < 65535 ? shares : 65535));
     if (vec)
         logits_adjust_kernel<T, true><<<grid, kAdjThreads, 0, s>>>(p);
     else
@@ -244,6 +240,9 @@ int launch_adjust(const AdjustParams& p, bool vec, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------- counts
+
+constexpr int kCountThreads = 256;
+constexpr int kCountPer = 4;  // tokens of a thread in flight
 
 struct CountParams {
     const int32_t* tokens;
@@ -259,27 +258,44 @@ __device__ __forceinline__ int list_state(const CountParams& p, int list) {
     return st >= 0 && st < p.n_states ? st : -1;
 }
 
-__global__ void __launch_bounds__(256) counts_clear_kernel(const CountParams p) {
+// Rows are cleared 16 bytes a thread; a row need not start or end on 16 bytes.
+__global__ void __launch_bounds__(kCountThreads) counts_clear_kernel(const CountParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int st = list_state(p, blockIdx.y);
     if (st < 0) return;
-    for (int v = blockIdx.x * 256 + threadIdx.x; v < p.vocab; v += gridDim.x * 256) p.counts[(int64_t)st * p.vocab + v] = 0u;
+    uint32_t* row = p.counts + (int64_t)st * p.vocab;
+    const int head = min((int)(-(reinterpret_cast<intptr_t>(row) >> 2) & 3), p.vocab), body = (p.vocab - head) / 4;
+    const int i0 = blockIdx.x * kCountThreads + threadIdx.x;
+    if (i0 < head) row[i0] = 0u;
+    if (i0 < p.vocab - head - 4 * body) row[head + 4 * body + i0] = 0u;
+    for (int i = i0; i < body; i += gridDim.x * kCountThreads) reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-__global__ void __launch_bounds__(256) counts_add_kernel(const CountParams p) {
+// A thread's first tokens are on their way before the wait for the cleared rows.  The adds commute, so their order does
+// not change the counts.
+__global__ void __launch_bounds__(kCountThreads) counts_add_kernel(const CountParams p) {
     const int list = blockIdx.y;
     const int st = list_state(p, list);
     const int a = p.starts[list], e = p.starts[list + 1];
-    if (st < 0 || a < 0 || e > p.n_tokens) return;
+    const bool on = st >= 0 && a >= 0 && e <= p.n_tokens;
     const int prompt = a + (p.prompt_lens ? max(p.prompt_lens[list], 0) : 0);
+    const int step = gridDim.x * kCountThreads, i0 = a + blockIdx.x * kCountThreads + threadIdx.x;
+    int tok[kCountPer];
+#pragma unroll
+    for (int k = 0; k < kCountPer; ++k) tok[k] = on && i0 + k * step < e ? __ldg(p.tokens + i0 + k * step) : -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!on) return;
     uint32_t* row = p.counts + (int64_t)st * p.vocab;
-    for (int i = a + blockIdx.x * 256 + threadIdx.x; i < e; i += gridDim.x * 256) {
-        const int v = p.tokens[i];
-        if (v < 0 || v >= p.vocab) continue;
+    auto add = [&](int i, int v) {
+        if (v < 0 || v >= p.vocab) return;
         if (i < prompt)
             atomicOr(row + v, kInPrompt);
         else
             atomicAdd(row + v, 1u);
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kCountPer; ++k) add(i0 + k * step, tok[k]);
+    for (int64_t i = i0 + (int64_t)kCountPer * step; i < e; i += step) add((int)i, p.tokens[i]);
 }
 
 }  // namespace
@@ -303,7 +319,7 @@ extern "C" int logits_adjust(const void* logits, int dtype, int64_t logits_strid
     if (grammar && n_grammar < 1) return KVQ8_ERR_INVALID_ARG;
     // in place: only where an element's input and output are the same bytes
     if (static_cast<const void*>(out) == logits && (dtype != KVQ8_F32 || logits_stride != out_stride)) return KVQ8_ERR_INVALID_ARG;
-    if (n_seqs > kMaxSeqs || vocab > (1 << 30) || n_rows > kAdjRows * 65535) return KVQ8_ERR_UNSUPPORTED;
+    if (n_seqs > kMaxSeqs || vocab > (1 << 30) || n_rows > 262140) return KVQ8_ERR_UNSUPPORTED;
     if (!aligned_to(logits, (size_t)esz) || !aligned_to(window_mask, 8)) return KVQ8_ERR_MISALIGNED;
     for (const void* q : {(const void*)row_starts, (const void*)penalties, (const void*)counts, (const void*)state_of,
                           (const void*)window_tokens, (const void*)bias_starts, (const void*)bias_tokens,
@@ -312,9 +328,9 @@ extern "C" int logits_adjust(const void* logits, int dtype, int64_t logits_strid
     AdjustParams p = {logits, out, logits_stride, out_stride, row_starts, penalties, counts, state_of, window_tokens,
                       window_mask, n_bias > 0 ? bias_starts : nullptr, bias_tokens, bias_values, grammar, grammar_of,
                       n_rows, vocab, n_seqs, n_states, n_bias, n_grammar};
-    // eight-value accesses where every row starts on 16 bytes (logits, counts, output) and rows hold whole groups
-    const bool vec = vocab % 8 == 0 && aligned16(logits) && aligned16(out) && (logits_stride * esz) % 16 == 0 &&
-                     out_stride % 4 == 0 && (!counts || aligned16(counts));
+    // eight values an access (16 bytes of logits of 16 bits, else 32) where every row starts on that and holds whole groups
+    const bool vec = vocab % 8 == 0 && aligned_to(logits, (size_t)(8 * esz)) && logits_stride % 8 == 0 && aligned_to(out, 32) &&
+                     out_stride % 8 == 0 && aligned_to(counts, 32);
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == KVQ8_F32) return launch_adjust<float>(p, vec, s);
     if (dtype == KVQ8_F16) return launch_adjust<__half>(p, vec, s);
@@ -335,13 +351,15 @@ extern "C" int token_counts(const int32_t* tokens, const int32_t* token_starts, 
     const CountParams p = {tokens, token_starts, prompt_lens, state_of, counts, n_tokens, n_states, vocab, n_lists};
     cudaStream_t s = (cudaStream_t)stream;
     if (clear) {
-        const int gx = (vocab + 2047) / 2048;
-        counts_clear_kernel<<<dim3((unsigned)(gx < 128 ? gx : 128), (unsigned)n_lists), 256, 0, s>>>(p);
+        const int gx = (vocab / 4 + 4 * kCountThreads - 1) / (4 * kCountThreads) + 1;
+        counts_clear_kernel<<<dim3((unsigned)(gx < 128 ? gx : 128), (unsigned)n_lists), kCountThreads, 0, s>>>(p);
         const int rc = launch_status();
         if (rc != KVQ8_OK) return rc;
     }
     if (n_tokens == 0) return KVQ8_OK;
-    const int gx = (n_tokens / n_lists + 1023) / 1024 + 1;
-    counts_add_kernel<<<dim3((unsigned)(gx < 64 ? gx : 64), (unsigned)n_lists), 256, 0, s>>>(p);
+    const int per = kCountThreads * kCountPer, gx = (n_tokens / n_lists + per - 1) / per + 1;
+    const dim3 grid((unsigned)(gx < 64 ? gx : 64), (unsigned)n_lists);
+    if (clear) return launch_dependent(counts_add_kernel, grid, kCountThreads, 0, s, p);
+    counts_add_kernel<<<grid, kCountThreads, 0, s>>>(p);
     return launch_status();
 }
