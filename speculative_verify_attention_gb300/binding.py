@@ -827,6 +827,8 @@ def attn_verify_paged_q8(q: torch.Tensor, cache: KVPagedCacheQ8, page_table: tor
     if workspace is None:
         workspace = _scratch(max(lib.attn_verify_paged_q8_workspace_bytes(hq, cache.n_kv_heads, hd, int(max_rows)), 16), q.device,
                              stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {cache.device}")
     st = lib.attn_verify_paged_q8(
         q.data_ptr(), _DTYPE[q.dtype], q.stride(0) if n_rows > 1 else hq * hd, n_rows, hq, cache._struct,
         _addr(page_table, "page_table", torch.int32, (n, mp), dev), mp, _addr(lens, "lens", torch.int32, (n,), dev),
