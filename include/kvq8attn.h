@@ -513,11 +513,12 @@ size_t attn_verify_paged_q8_workspace_bytes(int n_q_heads, int n_kv_heads, int h
  * T > lens, lens > max_pages * page_size, rows outside [0, n_rows)) are left as they were.  Keys on a
  * page id outside [0, n_pages) are left out, as if masked.  Masked and unused cache rows may hold any
  * codes, but their scales must be finite where they stand before lens.
- * K, V and p enter the tensor cores in fp16 (code * scale rounded once), q in fp16 times a power of
- * two per row; scores, softmax statistics and sums are fp32.  Values must stay inside the fp16 range.
+ * K, V and p enter the tensor cores in fp16 (code * scale rounded once), bf16 q as fp16 times a power
+ * of two (one for the rows that a thread block holds); scores, softmax statistics and sums are fp32.
+ * Values of the cache must stay inside the fp16 range.  The same call gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, n_q_heads / n_kv_heads > 64, max_rows > 64,
- * n_seqs > 4096, n_rows > 2^24), WORKSPACE, MISALIGNED (16 bytes; the code planes 32: a block is one
- * load; int32 arrays 4, window_mask 8).  Two launches.
+ * n_seqs > 4096, n_rows > 2^24, n_pages * n_kv_heads * page_size > 2^31 - 1), WORKSPACE, MISALIGNED
+ * (16 bytes; the code planes 32: a block is one load; int32 arrays 4, window_mask 8).  Two launches.
  */
 int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows, int n_q_heads,
                          const kvq8_paged_cache* kv, const int32_t* page_table, int max_pages, const int32_t* lens,
@@ -543,9 +544,10 @@ int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows,
  *   grammar : uint32 [n_grammar][ceil(vocab / 32)] or null, bit v % 32 of word v / 32 = value v is
  *             allowed; grammar_of: int32 [n_rows], the mask of each row (null: r; outside
  *             [0, n_grammar): everything is allowed)
- * With c = times v was generated, seen = c > 0 or v in the prompt, in fp32 and in this order:
- *   seen: x = x > 0 ? x / repetition : x * repetition;  x -= frequency * c + (c > 0 ? presence : 0);
- *   x += bias;  not allowed: x = -inf (whatever x was).
+ * With c = times v was generated, seen = c > 0 or v in the prompt, in fp32 and in this order (each
+ * operation rounded once, the quotient within one unit of its last place):
+ *   seen: x = x > 0 ? x / repetition : x * repetition;
+ *   x += bias - (frequency * c + (c > 0 ? presence : 0));  not allowed: x = -inf (whatever x was).
  * Tokens outside [0, vocab) are ignored.  Rows of no request, and of a request with more than 64 rows
  * where window_tokens is given, are left as they were.
  * Errors: INVALID_ARG, UNSUPPORTED (n_seqs > 4096, vocab > 2^30, n_rows > 262140), MISALIGNED (element

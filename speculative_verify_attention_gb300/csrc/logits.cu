@@ -4,7 +4,7 @@
 // Row r of request b, value v, with c the times v was generated (counts, plus the window tokens that row r sees)
 // and "seen" whether v was generated or stands in the prompt (bit 31 of its count):
 //   x = seen ? (x > 0 ? x / repetition : x * repetition) : x
-//   x = x - (frequency * c + presence * [c > 0]);  x = x + bias(v);  x = allowed(v) ? x : -inf
+//   x = x + (bias(v) - (frequency * c + presence * [c > 0]));  x = allowed(v) ? x : -inf
 // all in fp32, whatever the type of the logits.
 #include <float.h>
 
@@ -62,9 +62,10 @@ __device__ __noinline__ float bend(float x, uint32_t word, int extra, float b, f
 // Bound by issue: about 180 instructions for a warp's 256 values where every warp has a seen one.  12 requests of 16 to
 // 32 rows over 248320 bf16 logits (451 MB) 98 us, 4.6 TB/s; the same with a division called per seen value 182 us, with
 // four rows in flight and 6 blocks of an SM (80 registers) 108 us, with 32 rows a block (fewer prologues, a longer tail)
-// 121 us, with 8 rows 100 us.
+// 121 us, with 8 rows 100 us.  Rows of an odd length go by single values: 106299 of them 74 us, and 100 us with 4 blocks of
+// an SM instead of 8.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kAdjThreads, !VEC ? 4 : sizeof(T) == 4 ? 6 : 8) logits_adjust_kernel(const __grid_constant__ AdjustParams p) {
+__global__ void __launch_bounds__(kAdjThreads, VEC && sizeof(T) == 4 ? 6 : 8) logits_adjust_kernel(const __grid_constant__ AdjustParams p) {
     // (place + 1) << 32 | value of the last entry of the request's list for each value of the chunk, or 0
     __shared__ __align__(16) unsigned long long s_bias[kAdjChunk];
     __shared__ uint32_t s_mine[2][kAdjThreads];             // window tokens among a thread's values

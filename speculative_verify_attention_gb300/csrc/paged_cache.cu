@@ -5,15 +5,15 @@
 // zero) over fp32, fp16 or bf16 tokens, the cache row taken from the token's slot.  Read is its inverse, code * scale
 // rounded once to the type asked for.  Both read and write each value once, and are near enough to the memory's rate
 // for instructions a value to count: neither has a conversion instruction a value.  16401 tokens of 8 x 128 fp32 into the
-// cache and as many slots back as fp16 (238 MB) 53 us in two launches, 4.5 TB/s; with four values a lane and
-// conversion instructions 79 us, with twice the tokens a thread 57 us.
+// cache and as many slots back as fp16 (238 MB) 52 us in two launches, 4.6 TB/s; with four values a lane and
+// conversion instructions 79 us, with twice the tokens a thread 57 us, with blocks of 256 threads 53 us.
 #include "paged.cuh"
 #include "q8_0.cuh"
 
 namespace kvq8 {
 namespace {
 
-constexpr int kPagedThreads = 256;
+constexpr int kPagedThreads = 128;
 // Tokens of a thread: their loads are in flight together (64 bytes of input in append, 32 of codes in read).
 template <typename T>
 constexpr int kAppendTok = sizeof(T) == 4 ? 2 : 4;

@@ -77,6 +77,8 @@ VERIFY = dict(q=A, dtype=1, q_stride=1024, n_rows=6, n_q_heads=8, kv=_cache(), p
     *[({"kv": _cache(**c)}, s) for c, s in CACHES], *[({k: None}, INVALID) for k in ("q", "out", "page_table", "lens", "row_starts", "kv")],
     ({"dtype": 0}, INVALID), ({"dtype": 9}, INVALID), ({"n_rows": -1}, INVALID), ({"n_seqs": -1}, INVALID), ({"max_pages": 0}, INVALID),
     ({"kv": _cache(k_codes=A + 16)}, MISALIGNED), ({"kv": _cache(v_codes=A + 16)}, MISALIGNED),
+    ({"kv": _cache(n_pages=2 ** 30, page_size=16, n_kv_heads=1)}, UNSUPPORTED),
+    ({"kv": _cache(n_pages=2 ** 16, page_size=1024, n_kv_heads=32)}, UNSUPPORTED),
     ({"n_q_heads": 0}, INVALID), ({"max_rows": 0}, INVALID), ({"q_stride": 1023}, INVALID),
     *[({"scale": x}, INVALID) for x in (0.0, -1.0, float("inf"), float("nan"))],
     ({"n_q_heads": 7, "q_stride": 4096}, UNSUPPORTED), ({"n_q_heads": 130, "q_stride": 1 << 20}, UNSUPPORTED), ({"max_rows": 65}, UNSUPPORTED),
