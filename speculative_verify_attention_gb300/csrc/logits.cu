@@ -80,9 +80,10 @@ __global__ void __launch_bounds__(kAdjThreads, VEC && sizeof(T) == 4 ? 6 : 8) lo
     int state = -1, b0 = 0, b1 = 0;
     if (p.counts) state = p.state_of ? __ldg(p.state_of + b) : b;
     if (p.bias_starts) b0 = __ldg(p.bias_starts + b), b1 = __ldg(p.bias_starts + b + 1);
+    if (first < 0 || last < first || last > p.n_rows) return;
     const int rows = last - first;
-    if (first < 0 || last > p.n_rows || rows <= (int)blockIdx.z || (p.tokens && rows > kMaxWindowRows)) return;
-    if (b0 < 0 || b1 > p.n_bias) b0 = b1 = 0;
+    if (rows <= (int)blockIdx.z || (p.tokens && rows > kMaxWindowRows)) return;
+    if (b0 < 0 || b1 < b0 || b1 > p.n_bias) b0 = b1 = 0;
     const bool counted = state >= 0 && state < p.n_states, windows = on && p.tokens;
     const bool odd = !(fabsf(repetition) > 0x1p-100f && fabsf(repetition) < 0x1p100f);
 
@@ -278,8 +279,8 @@ __global__ void __launch_bounds__(kCountThreads) counts_add_kernel(const CountPa
     const int list = blockIdx.y;
     const int st = list_state(p, list);
     const int a = p.starts[list], e = p.starts[list + 1];
-    const bool on = st >= 0 && a >= 0 && e <= p.n_tokens;
-    const int prompt = a + (p.prompt_lens ? max(p.prompt_lens[list], 0) : 0);
+    const bool on = st >= 0 && a >= 0 && a <= e && e <= p.n_tokens;
+    const int prompt = p.prompt_lens ? max(p.prompt_lens[list], 0) : 0;
     const int step = gridDim.x * kCountThreads, i0 = a + blockIdx.x * kCountThreads + threadIdx.x;
     int tok[kCountPer];
 #pragma unroll
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(kCountThreads) counts_add_kernel(const CountPa
     uint32_t* row = p.counts + (int64_t)st * p.vocab;
     auto add = [&](int i, int v) {
         if (v < 0 || v >= p.vocab) return;
-        if (i < prompt)
+        if (i - a < prompt)
             atomicOr(row + v, kInPrompt);
         else
             atomicAdd(row + v, 1u);
