@@ -97,7 +97,8 @@ enum kvq8_dtype { KVQ8_F32 = 0, KVQ8_F16 = 1, KVQ8_BF16 = 2 };
  * [n_pages][n_kv_heads][page_size][head_dim / 32] (fp16 bits), so a page holds page_size
  * consecutive rows of every KV head.  head_dim 128 or 256; page_size a power of two, 16 .. 1024.
  * Token slot s is row s % page_size of page s / page_size.  A request's page table lists its pages
- * in order of position.  Slot and element offsets are 64-bit. */
+ * in order of position.  Slots and element offsets are 64-bit; n_pages * n_kv_heads * page_size, the
+ * rows of a plane, is at most 2^31 - 1 (UNSUPPORTED otherwise). */
 typedef struct {
     const int8_t* k_codes;
     const uint16_t* k_scales;
@@ -517,8 +518,7 @@ size_t attn_verify_paged_q8_workspace_bytes(int n_q_heads, int n_kv_heads, int h
  * of two (one for the rows that a thread block holds); scores, softmax statistics and sums are fp32.
  * Values of the cache must stay inside the fp16 range.  The same call gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, n_q_heads / n_kv_heads > 64, max_rows > 64,
- * n_seqs > 4096, n_rows > 2^24, n_pages * n_kv_heads * page_size > 2^31 - 1), WORKSPACE, MISALIGNED
- * (16 bytes; the code planes 32: a block is one load; int32 arrays 4, window_mask 8).  Two launches.
+ * n_seqs > 4096, n_rows > 2^24, a cache of too many rows), WORKSPACE, MISALIGNED (16 bytes; the code planes 32: a block is one load; int32 arrays 4, window_mask 8).  Two launches.
  */
 int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows, int n_q_heads,
                          const kvq8_paged_cache* kv, const int32_t* page_table, int max_pages, const int32_t* lens,

@@ -14,11 +14,11 @@ constexpr int kMaxWindowRows = 64;    // rows of one request's window: one bit e
 
 // A slot is page * page_size + offset.  Planes: codes [n_pages][n_kv_heads][page_size][head_dim], scales
 // [n_pages][n_kv_heads][page_size][head_dim / 32], so a page holds page_size consecutive rows of each head.
-// The row index below times head_dim (or head_dim / 32) is the element offset; it is 64-bit throughout.
-__device__ __forceinline__ int64_t paged_row(int64_t slot, int head, int n_kv_heads, int page_shift) {
-    const int64_t page = slot >> page_shift;
-    const int off = (int)(slot & ((1 << page_shift) - 1));
-    return ((page * n_kv_heads + head) << page_shift) + off;
+// Rows are counted in 32 bits (2^31 of them are more than the device's memory); the row times head_dim (or head_dim / 32) is
+// the element offset, in 64 bits.
+__device__ __forceinline__ uint32_t paged_row(uint32_t slot, int head, int n_kv_heads, int page_shift) {
+    const uint32_t page = slot >> page_shift, off = slot & ((1u << page_shift) - 1);
+    return ((page * (uint32_t)n_kv_heads + (uint32_t)head) << page_shift) + off;
 }
 
 inline int log2_of(int v) {
@@ -34,7 +34,7 @@ inline int check_paged(const kvq8_paged_cache* kv) {
     if (!kv->k_codes || !kv->k_scales || !kv->v_codes || !kv->v_scales) return KVQ8_ERR_INVALID_ARG;
     if (kv->head_dim != 128 && kv->head_dim != 256) return KVQ8_ERR_UNSUPPORTED;
     if (kv->page_size < 16 || kv->page_size > 1024 || (kv->page_size & (kv->page_size - 1))) return KVQ8_ERR_UNSUPPORTED;
-    if (kv->n_kv_heads > 4096) return KVQ8_ERR_UNSUPPORTED;
+    if (kv->n_kv_heads > 4096 || (int64_t)kv->n_pages * kv->n_kv_heads * kv->page_size > 0x7fffffffLL) return KVQ8_ERR_UNSUPPORTED;
     if (!aligned16(kv->k_codes) || !aligned16(kv->k_scales) || !aligned16(kv->v_codes) || !aligned16(kv->v_scales))
         return KVQ8_ERR_MISALIGNED;
     return KVQ8_OK;

@@ -63,31 +63,33 @@ __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const __gri
         uint16_t scale_bits;
         const uint2 packed = q8_0_block8(f, &scale_bits);
         if (slot[t] >= 0 && slot[t] < p.n_slots) {
-            const int64_t row = paged_row(slot[t], h, p.n_kv_heads, p.page_shift);
-            *reinterpret_cast<uint2*>(p.codes[z] + row * p.head_dim + i * 8) = packed;
-            if ((i & 3) == 0) p.scales[z][row * (p.head_dim / kQBlock) + (i >> 2)] = scale_bits;
+            const uint64_t row = paged_row((uint32_t)slot[t], h, p.n_kv_heads, p.page_shift);
+            *reinterpret_cast<uint2*>(p.codes[z] + row * (uint32_t)p.head_dim + i * 8) = packed;
+            if ((i & 3) == 0) p.scales[z][row * (uint32_t)(p.head_dim / kQBlock) + (i >> 2)] = scale_bits;
         }
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<float>(float* dst, const float (&v)[8]) {
+// Eight codes times their scale.  fp32 and bf16: 2^23 + (code + 128) by its bits, and a product that is exact in fp32 (8 by 11
+// bits); fp16: its product rounds the exact one once as well, subnormals included.
+__device__ __forceinline__ void values8(uint2 c, uint16_t scale, float (&v)[8]) {
+    const float d = half_bits_to_float(scale);
+    const uint32_t lo = c.x ^ 0x80808080u, hi = c.y ^ 0x80808080u;  // code + 128
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[k] = (__uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7440 + k)) - 8388736.0f) * d;
+        v[4 + k] = (__uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7440 + k)) - 8388736.0f) * d;
+    }
+}
+__device__ __forceinline__ void store_values(float* dst, uint2 c, uint16_t scale) {
+    float v[8];
+    values8(c, scale, v);
     reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-template <>
-__device__ __forceinline__ void store8<__half>(__half* dst, const float (&v)[8]) {
-    uint4 o;
-    o.x = h2_as_u32(__floats2half2_rn(v[0], v[1]));
-    o.y = h2_as_u32(__floats2half2_rn(v[2], v[3]));
-    o.z = h2_as_u32(__floats2half2_rn(v[4], v[5]));
-    o.w = h2_as_u32(__floats2half2_rn(v[6], v[7]));
-    *reinterpret_cast<uint4*>(dst) = o;
-}
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* dst, const float (&v)[8]) {
+__device__ __forceinline__ void store_values(__nv_bfloat16* dst, uint2 c, uint16_t scale) {
+    float v[8];
+    values8(c, scale, v);
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -95,6 +97,16 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* dst, const 
         o[k] = *reinterpret_cast<const uint32_t*>(&b);
     }
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void store_values(__half* dst, uint2 c, uint16_t scale) {
+    const __half2 d = __half2half2(__ushort_as_half(scale));
+    const uint32_t lo = c.x ^ 0x80808080u, hi = c.y ^ 0x80808080u;
+    uint4 o;
+    o.x = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4140>(lo)), d));
+    o.y = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4342>(lo)), d));
+    o.z = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4140>(hi)), d));
+    o.w = h2_as_u32(__hmul2(u32_as_h2(biased_bytes_to_half2<0x4342>(hi)), d));
+    *reinterpret_cast<uint4*>(dst) = o;
 }
 
 // The same block shape: eight code bytes and their scale in, eight values out.  A slot outside the cache gives zeros.
@@ -116,24 +128,16 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const __grid_
         if (tok0 + t < p.n_tok) {
             const int64_t slot = __ldg(p.slots + tok0 + t);
             if (slot >= 0 && slot < p.n_slots) {
-                const int64_t row = paged_row(slot, h, p.n_kv_heads, p.page_shift);
-                c[t] = *reinterpret_cast<const uint2*>(p.codes[z] + row * p.head_dim + i * 8);
-                sc[t] = p.scales[z][row * (p.head_dim / kQBlock) + (i >> 2)];
+                const uint64_t row = paged_row((uint32_t)slot, h, p.n_kv_heads, p.page_shift);
+                c[t] = *reinterpret_cast<const uint2*>(p.codes[z] + row * (uint32_t)p.head_dim + i * 8);
+                sc[t] = p.scales[z][row * (uint32_t)(p.head_dim / kQBlock) + (i >> 2)];
             }
         }
     }
 #pragma unroll
     for (int t = 0; t < kReadTok; ++t) {
         if (tok0 + t >= p.n_tok) break;
-        const float d = half_bits_to_float(sc[t]);
-        const uint32_t lo = c[t].x ^ 0x80808080u, hi = c[t].y ^ 0x80808080u;  // code + 128
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 2^23 + (code + 128) by its bits; the product is exact in fp32, 8 by 11 bits
-            v[k] = (__uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7440 + k)) - 8388736.0f) * d;
-            v[4 + k] = (__uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7440 + k)) - 8388736.0f) * d;
-        }
-        store8<T>(y + (int64_t)(tok0 + t) * p.tok_stride[z] + (int64_t)h * p.head_stride[z] + i * 8, v);
+        store_values(y + (int64_t)(tok0 + t) * p.tok_stride[z] + (int64_t)h * p.head_stride[z] + i * 8, c[t], sc[t]);
     }
 }
 

@@ -555,8 +555,8 @@ extern "C" int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, 
     if ((dtype != KVQ8_F16 && dtype != KVQ8_BF16) || n_rows < 0 || n_seqs < 0 || max_pages < 1) return KVQ8_ERR_INVALID_ARG;
     if (n_q_heads < 1 || max_rows < 1 || !(softmax_scale > 0.0f) || softmax_scale == INFINITY) return KVQ8_ERR_INVALID_ARG;
     if (n_q_heads % kv->n_kv_heads || n_q_heads / kv->n_kv_heads > 64 || max_rows > kMaxWindowRows || n_seqs > kMaxSeqs ||
-        n_rows > (1 << 24) || (int64_t)kv->n_pages * kv->n_kv_heads * kv->page_size > 0x7fffffffLL)
-        return KVQ8_ERR_UNSUPPORTED;  // the last: rows of a plane are counted in 32 bits
+        n_rows > (1 << 24))
+        return KVQ8_ERR_UNSUPPORTED;
     if (n_rows == 0 || n_seqs == 0) return KVQ8_OK;
     if (!q || !out || !page_table || !lens || !row_starts || q_stride < (int64_t)n_q_heads * kv->head_dim)
         return KVQ8_ERR_INVALID_ARG;
