@@ -40,14 +40,17 @@ struct RL {
     static constexpr int kTabInv = 0, kTabAlpha = 4 * NMAX, kTabRow = 12 * NMAX, kTabMisc = 20 * NMAX, kTabScan = kTabMisc + 48,
                          kTabTmem = kTabScan + 64 + (kVerifyThreads / 32 + 1) / 2 * 16, kTabBar = kTabTmem + 16;
     static constexpr int kMaxSlots = 8, kTabBytes = kTabBar + (2 * kMaxSlots + 11) * 8;
-    static constexpr int kFit = (227 * 1024 - kSmRing - kTabBytes) / kSlot / H * H, R = kFit < kMaxSlots ? kFit : kMaxSlots;
+    static constexpr int kFit = (227 * 1024 - kSmRing - kTabBytes) / kSlot;
+    // K and V have rings of their own, of two tiles, V's of one where there is no room: K^ of tile j + 1 is wanted while the
+    // softmax of tile j runs, V^ of tile j only after it.
+    static constexpr int RK = 2 * H, RV = kFit >= 4 * H ? 2 * H : H, R = RK + RV;
+    static_assert(kFit >= 3 * H && R <= kMaxSlots, "a tile of V^ and two of K^ at least");
     static constexpr int kSmTab = kSmRing + R * kSlot, kSmBytes = kSmTab + kTabBytes;
     // Two tiles of scores in tensor memory: one of each group, or two of the one, which then has two of weights too.
     // barriers: ring slot full / free; a tile of scores ready / read; weights ready; product done; queries ready
     static constexpr int kFull = 0, kFree = R, kS = 2 * R, kSFree = kS + 2, kP = kSFree + 2, kO = kP + 2, kQ = kO + 2, kRaise = kQ + 1, kR = kQ + 2;
     static constexpr uint32_t kTmO = 0, kTmS = kMt * NMAX;
     static_assert(kGroups * kBuf == 2 && kTmS + 128 <= kTmemCols, "tensor memory");
-    static_assert(R >= 2 * H, "the ring holds a tile: the scores of tile j + 1 are issued before the product of tile j");
     static_assert(kSmBytes <= 227 * 1024 && kSmP % 1024 == 0 && kSmRing % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 };
 
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
     if (tid == 0) {
 #pragma unroll 1
         for (int s = 0; s < R; ++s) {
-            tc::mbar_init(B(L::kFull + s), 8);
+            tc::mbar_init(B(L::kFull + s), 4);
             tc::mbar_init(B(L::kFree + s), 1);
         }
 #pragma unroll 1
@@ -143,17 +146,45 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
     auto pp = [](int j) { return L::kBuf > 1 ? j >> 1 : j; };
 
     if (warp == kMmaWarp) {
+        // All products, issued by one lane.  It is the chain that every tile goes through, so the descriptors are constants: a
+        // tile's place in the rings is its number's parity (or fixed), and the code is there once for each.
         const uint32_t one = elect_one();
-        int raises = 0;
         const uint64_t qd = tc::smem_desc_sw128(sbase + L::kSmQ, 16, 1024);
         const uint64_t pd = tc::smem_desc_sw128(sbase + L::kSmP, 16, 1024);
         const uint64_t kd0 = tc::smem_desc_sw128(sbase + L::kSmRing, 16, 1024);
-        const uint64_t vd0 = tc::smem_desc_sw128(sbase + L::kSmRing, L::kVKeys * 128, 1024);
+        const uint64_t vd0 = tc::smem_desc_sw128(sbase + L::kSmRing + L::RK * L::kSlot, L::kVKeys * 128, 1024);
         const uint32_t idesc_s = tc::idesc_f16_f32_ab(128, BN, false, false);
+        int raises = 0;
+        // S of a group and tile j, whose parity is ODD
+        auto scores = [&](auto odd, int g, int j, bool both) {
+            constexpr int ODD = decltype(odd)::value;
+            const int b = kGroups > 1 ? g : ODD;  // the group's tile of scores
+            if (j >= L::kBuf) wait(L::kSFree + b, j / L::kBuf - 1);
+            if (g == 0 || both) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    constexpr int kFirst = ODD * H;
+                    if (g == 0) wait(L::kFull + kFirst + h, j >> 1);
+                    tc::fence_after_sync();
+                    if (one) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma_ss(tmem + L::kTmS + b * 64, qd + (uint64_t)(((h * 2 + (k >> 2)) * NMAX * 128 + g * 64 * 128 + (k & 3) * 32) >> 4),
+                                       kd0 + (uint64_t)(((kFirst + h) * L::kSlot + (k >> 2) * 64 * 128 + (k & 3) * 32) >> 4), idesc_s,
+                                       h > 0 || k > 0 ? 1u : 0u);
+                        if (g == 1 || !both) tc::mma_commit(B(L::kFree + kFirst + h));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (one) tc::mma_commit(B(L::kS + b));
+            __syncwarp();
+        };
         // O^T (+)= V^T P^T of tile j
-        auto product = [&](int j, uint32_t idesc, int n16, uint32_t more) {
-            wait(L::kP + pb(j), pp(j));
-            if (kGroups > 1 && more && raised_b[j & 1]) {  // its rows' columns in the lanes of the warps that it lacks
+        auto product = [&](auto odd, int j, uint32_t idesc, int n16, uint32_t more) {
+            constexpr int ODD = decltype(odd)::value, kBufP = L::kBuf > 1 ? ODD : 0, kFirst = L::RV > H ? ODD * H : 0;
+            wait(L::kP + kBufP, pp(j));
+            if (kGroups > 1 && more && raised_b[ODD]) {  // its rows' columns in the lanes of the warps that it lacks
                 wait(L::kO + pb(j - 1), pp(j - 1));
                 tc::fence_after_sync();
                 rescale(j, 128, n16);
@@ -161,25 +192,25 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                 tc::fence_before_sync();
                 __syncwarp();
             }
-#pragma unroll 1
+#pragma unroll
             for (int h = 0; h < H; ++h) {
-                const int n = j * 2 * H + H + h, slot = n % R;
-                wait(L::kFull + slot, n / R);
+                wait(L::kFull + L::RK + kFirst + h, L::RV > H ? j >> 1 : j);
                 tc::fence_after_sync();
                 if (one) {
-                    const uint64_t vd = vd0 + (uint64_t)((slot * L::kSlot) >> 4), ph = pd + (uint64_t)((pb(j) * NMAX * 128 + h * L::kVKeys * 2) >> 4);
 #pragma unroll
                     for (int m = 0; m < L::kMt; ++m)
 #pragma unroll
                         for (int k = 0; k < L::kVKeys / 16; ++k)
-                            tc::mma_ss(tmem + L::kTmO + m * NMAX, vd + (uint64_t)((m * 2 * L::kVKeys * 128 + k * 2048) >> 4),
-                                       ph + (uint64_t)((k * 32) >> 4), idesc, h > 0 || k > 0 ? 1u : more);
-                    tc::mma_commit(B(L::kFree + slot));
-                    if (h == H - 1) tc::mma_commit(B(L::kO + pb(j)));
+                            tc::mma_ss(tmem + L::kTmO + m * NMAX, vd0 + (uint64_t)(((kFirst + h) * L::kSlot + m * 2 * L::kVKeys * 128 + k * 2048) >> 4),
+                                       pd + (uint64_t)((kBufP * NMAX * 128 + h * L::kVKeys * 2 + k * 32) >> 4), idesc, h > 0 || k > 0 ? 1u : more);
+                    tc::mma_commit(B(L::kFree + L::RK + kFirst + h));
+                    if (h == H - 1) tc::mma_commit(B(L::kO + kBufP));
                 }
                 __syncwarp();
             }
         };
+        constexpr std::integral_constant<int, 0> even{};
+        constexpr std::integral_constant<int, 1> odd{};
         int j = 0, segs = 0;
 #pragma unroll 1
         while (walk.next(p, seg)) {
@@ -189,36 +220,24 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
             const bool both = kGroups > 1 && seg.n > 128;
             const int t0 = seg.t0, t1 = seg.t1;
 #pragma unroll 1
-            for (int t = t0; t < t1; ++t, ++j) {
-#pragma unroll 1
-                for (int g = 0; g < kGroups; ++g) {
-                    const int b = kGroups > 1 ? g : j & 1;  // the group's tile of scores
-                    if (j >= L::kBuf) wait(L::kSFree + b, j / L::kBuf - 1);
-                    if (g == 0 || both) {
-#pragma unroll 1
-                        for (int h = 0; h < H; ++h) {
-                            const int n = j * 2 * H + h, slot = n % R;
-                            if (g == 0) wait(L::kFull + slot, n / R);
-                            tc::fence_after_sync();
-                            if (one) {
-                                const uint64_t kd = kd0 + (uint64_t)((slot * L::kSlot) >> 4);
-                                const uint64_t qh = qd + (uint64_t)((h * 2 * NMAX * 128 + g * 64 * 128) >> 4);
+            for (int t = t0; t <= t1; ++t) {
+                // the scores of tile t, number j, then the product of the tile before
+                const uint32_t more = t - 1 > t0 ? 1u : 0u;
+                if (j & 1) {
+                    if (t < t1) {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    tc::mma_ss(tmem + L::kTmS + b * 64, qh + (uint64_t)(((k >> 2) * NMAX * 128 + (k & 3) * 32) >> 4),
-                                               kd + (uint64_t)(((k >> 2) * 64 * 128 + (k & 3) * 32) >> 4), idesc_s,
-                                               h > 0 || k > 0 ? 1u : 0u);
-                                if (g == 1 || !both) tc::mma_commit(B(L::kFree + slot));
-                            }
-                            __syncwarp();
-                        }
+                        for (int g = 0; g < kGroups; ++g) scores(odd, g, j, both);
                     }
-                    if (one) tc::mma_commit(B(L::kS + b));
-                    __syncwarp();
+                    if (t > t0) product(even, j - 1, idesc_o, n16, more);
+                } else {
+                    if (t < t1) {
+#pragma unroll
+                        for (int g = 0; g < kGroups; ++g) scores(even, g, j, both);
+                    }
+                    if (t > t0) product(odd, j - 1, idesc_o, n16, more);
                 }
-                if (t > t0) product(j - 1, idesc_o, n16, t - 1 > t0 ? 1u : 0u);
+                if (t < t1) ++j;
             }
-            product(j - 1, idesc_o, n16, t1 - 1 > t0 ? 1u : 0u);
         }
         if (kGroups > 1 && lane < 2) {
             raised_b[2] = 0;
@@ -384,29 +403,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                     const int b = kGroups > 1 ? g : j & 1;
                     wait(L::kS + b, j / L::kBuf);
                     tc::fence_after_sync();
-                    // The scores, 32 keys at a time (64 in registers would spill), those of unseen keys -inf.
-                    const bool all = __all_sync(0xffffffffu, sees == ~0ull);
-                    auto scores = [&](int half, uint32_t (&s)[32]) {
-                        tc::tmem_ld32(tmem + lanes + L::kTmS + b * 64 + 32 * half, s);
-                        tc::tmem_wait_ld32(s);
-                        if (!all) {
-                            const uint32_t see = half ? (uint32_t)(sees >> 32) : (uint32_t)sees;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!(see >> c & 1)) s[c] = 0xff800000u;
-                        }
-                    };
+                    // The scores in registers, so that their place is free for the next tile's at once; those of unseen keys -inf.
+                    uint32_t x[64];
+                    if (live) tc::tmem_ld64(tmem + lanes + L::kTmS + b * 64, x);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(B(L::kSFree + b));
                     bool raise = false;
                     float top = 0.0f;
                     if (live) {
-                        float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t s[32];
-                            scores(half, s);
+                        if (!__all_sync(0xffffffffu, sees == ~0ull)) {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) most[c & 3] = fmaxf(most[c & 3], __uint_as_float(s[c]));
+                            for (int c = 0; c < 64; ++c)
+                                if (!((c < 32 ? (uint32_t)sees : (uint32_t)(sees >> 32)) >> (c & 31) & 1)) x[c] = 0xff800000u;
                         }
+                        float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) most[c & 3] = fmaxf(most[c & 3], __uint_as_float(x[c]));
                         top = cs * fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
                         raise = mine && top > ref + kLazy;
                     }
@@ -423,27 +436,18 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                         if (owner) alpha[(j & 1) * NMAX + row] = a;
                     }
                     if (kGroups > 1 && warp == 6 && lane == 0) raised_b[j & 1] = raised;
-                    uint32_t weights[32];
                     if (live) {
+                        float part[2] = {0.0f, 0.0f};
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t s[32];
-                            scores(half, s);
-                            float part[2] = {0.0f, 0.0f};
-#pragma unroll
-                            for (int c = 0; c < 32; c += 2) {
-                                const float e0 = ex2_approx(fmaf(__uint_as_float(s[c]), cs, neg));
-                                const float e1 = ex2_approx(fmaf(__uint_as_float(s[c + 1]), cs, neg));
-                                part[0] += e0;
-                                part[1] += e1;
-                                weights[16 * half + c / 2] = h2_as_u32(__floats2half2_rn(e0, e1));
-                            }
-                            l += part[0] + part[1];
+                        for (int c = 0; c < 64; c += 2) {
+                            const float e0 = ex2_approx(fmaf(__uint_as_float(x[c]), cs, neg));
+                            const float e1 = ex2_approx(fmaf(__uint_as_float(x[c + 1]), cs, neg));
+                            part[0] += e0;
+                            part[1] += e1;
+                            x[c / 2] = h2_as_u32(__floats2half2_rn(e0, e1));
                         }
+                        l += part[0] + part[1];
                     }
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(B(L::kSFree + b));
                     if (j >= L::kBuf) wait(L::kO + pb(j), pp(j) - 1);  // the weights before in this place have been used
                     if (raised && t > t0) {
                         wait(L::kO + pb(j - 1), pp(j - 1));  // every product so far has landed
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
                             sts128(sbase + L::kSmP + pb(j) * NMAX * 128 + row * 128 + ((c ^ (row & 7)) << 4),
-                                   make_uint4(weights[4 * c], weights[4 * c + 1], weights[4 * c + 2], weights[4 * c + 3]));
+                                   make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
                     }
                     tc::fence_proxy_async_smem();
                     tc::fence_before_sync();
@@ -482,16 +486,22 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
         }
         if (!wait.ok) atomicOr(p.error, 1u);
     } else {
-        // A thread converts one 32-value block of each half tile: lanes 0-7 the same block of eight keys, so that their
-        // swizzled 16-byte stores fall into different banks.  A tile's codes are loaded while the one before is converted,
-        // and the one after it is asked into L2.
-        const int w = warp - kConvWarp0, nn = lane & 7, jj = lane >> 3;
-        constexpr bool kWide = HD == 256;
-        const int v_key = kWide ? 8 * (w & 3) + nn : 8 * w + nn, v_block = kWide ? 4 * (w >> 2) + jj : jj;
-        const uint32_t k_dst = sbase + L::kSmRing + (jj >> 1) * (64 * 128) + (8 * w + nn) * 128 + (((4 * (jj & 1)) ^ nn) << 4);
-        const uint32_t v_dst = sbase + L::kSmRing + (v_block >> 1) * (L::kVKeys * 128) + v_key * 128 + (((4 * (jj & 1)) ^ nn) << 4);
-        uint32_t codes[2][H][8];
-        uint32_t scale[2][H];
+        // Four warps a plane, each at its own pace.  A thread converts two 32-value blocks of each half tile: lanes 0-7 the same
+        // block of eight keys, so that their swizzled 16-byte stores fall into different banks.  A tile's codes are loaded while
+        // the one before is converted, and the one after it is asked into L2.
+        const int w = (warp - kConvWarp0) & 3, nn = lane & 7, jj = lane >> 3;
+        const bool is_v = warp >= kConvWarp0 + 4;
+        const int8_t* plane = is_v ? p.vc : p.kc;
+        const uint16_t* scales = is_v ? p.vs : p.ks;
+        // half s of a tile is its keys 32 s .. (V at head_dim 256), or its dims 128 s ..; block i of the thread in it the other
+        // way round: its keys are 32 x + 8 w + nn, its blocks 4 y + jj
+        const bool by_keys = is_v && H == 2;
+        const int first = is_v ? L::RK : 0, ring = is_v ? L::RV : L::RK;
+        const uint32_t next = by_keys ? 8192 : 4096;  // from block 0 to block 1
+        const uint32_t dst = sbase + L::kSmRing + first * L::kSlot + (jj >> 1) * (by_keys ? 4096 : 8192) + (8 * w + nn) * 128 + (((4 * (jj & 1)) ^ nn) << 4);
+        uint32_t codes[H][2][8], scale[H][2];
+        uint32_t row[2];
+        bool there[2] = {false, false};
         int t = 0, t1 = 0, len = 0, kvh = 0;
         const int32_t* pages = p.table;
         int page[kAhead + 2];  // lane x < 4: page of keys 16 x .. of the tile and of the next ones
@@ -499,6 +509,13 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
         auto page_of = [&](int u) {
             const long long key = (long long)u * BN + 16 * lane;
             return lane < 4 && u < t1 && key < len ? __ldg(pages + (key >> p.page_shift)) : -1;
+        };
+        // The cache row of key `key` of tile u, whose page is among `ids`.
+        auto row_of = [&](int ids, int u, int key, uint32_t& row) {
+            const int id = __shfl_sync(0xffffffffu, ids, key >> 4);
+            const uint32_t off = ((uint32_t)u * BN + key) & ((1u << p.page_shift) - 1);
+            row = (((uint32_t)id * p.n_kv_heads + kvh) << p.page_shift) + off;
+            return id >= 0 && id < p.n_pages && (long long)u * BN + key < len;
         };
         auto ahead = [&]() {
             if (have && ++t < t1) {
@@ -513,73 +530,64 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                 for (int x = 0; x <= kAhead; ++x) page[x] = page_of(t + x);
             }
             page[kAhead + 1] = page_of(t + kAhead + 1);
-        };
-        // The cache row of key `key` of tile u, whose page is among `ids`.  (Rows are counted in 32 bits: 2^31 of them are
-        // more than the device's memory.)
-        auto row_of = [&](int ids, int u, int key, uint32_t& row) {
-            const int id = __shfl_sync(0xffffffffu, ids, key >> 4);
-            const uint32_t off = ((uint32_t)u * BN + key) & ((1u << p.page_shift) - 1);
-            row = (((uint32_t)id * p.n_kv_heads + kvh) << p.page_shift) + off;
-            return id >= 0 && id < p.n_pages && (long long)u * BN + key < len;
-        };
-        // What is not there gets scale 0, and any codes.
-        auto load = [&](int part) {  // the halves of K or V of the tile at t
-            uint32_t row = 0;
-            bool there = false;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                if (part || h == 0) there = row_of(page[0], t, part ? h * L::kVKeys + v_key : 8 * w + nn, row);
-                const int block = part ? v_block : 4 * h + jj;
-                scale[part][h] = 0;
-                if (there) {
-                    load32(codes[part][h], (part ? p.vc : p.kc) + (uint64_t)row * HD + 32 * block);
-                    load_u16(scale[part][h], (part ? p.vs : p.ks) + (uint64_t)row * (HD / 32) + block);
-                }
+            for (int x = 0; x < 2; ++x) there[x] = row_of(page[0], t, 32 * x + 8 * w + nn, row[x]);
+            // a 128-byte line of codes of the tile after next per thread, and the scales
+            uint32_t line;
+            if (row_of(page[kAhead], t + kAhead, 16 * w + (lane >> 1), line) && (H == 2 || !(lane & 1))) {
+                prefetch_l2(plane + (uint64_t)line * HD + 128 * (lane & 1));
+                if ((lane & 15) == 0) prefetch_l2(scales + (uint64_t)line * (HD / 32));
             }
         };
-        auto prefetch = [&]() {  // the tile after the one at t: a 128-byte line of codes per thread, and the scales
-            uint32_t row;
-            if (!row_of(page[kAhead], t + kAhead, 8 * w + (lane >> 2), row) || (!kWide && (lane & 1))) return;
-            prefetch_l2((lane & 2 ? p.vc : p.kc) + (uint64_t)row * HD + 128 * (lane & 1));
-            if (lane < 4 && !(lane & 1)) prefetch_l2((lane & 2 ? p.vs : p.ks) + (uint64_t)row * (HD / 32));
+        // What is not there gets scale 0, and any codes.
+        auto load = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int x = by_keys ? s : i, block = 4 * (by_keys ? i : s) + jj;
+                const uint64_t r = x ? row[1] : row[0];
+                scale[s][i] = 0;
+                if (x ? there[1] : there[0]) {
+                    load32(codes[s][i], plane + r * HD + 32 * block);
+                    load_u16(scale[s][i], scales + r * (HD / 32) + block);
+                }
+            }
         };
 #pragma unroll
         for (int i = 0; i < 2 * H; ++i)
 #pragma unroll
-            for (int x = 0; x < 8; ++x) codes[i / H][i % H][x] = 0u;
+            for (int x = 0; x < 8; ++x) codes[i >> 1][i & 1][x] = 0u;
         int slot = 0, turn = 0;
         ahead();
         if (have) {
-            load(0);
-            load(1);
-            prefetch();
+#pragma unroll
+            for (int s = 0; s < H; ++s) load(s);
         }
 #pragma unroll 1
         while (have) {
             ahead();
-            if (have) prefetch();
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
+            for (int s = 0; s < H; ++s) {
+                // the slot's state is asked for before the conversion and looked at after it
+                const bool is_free = turn == 0 || tc::mbar_try_wait(B(L::kFree + first + slot), (turn - 1) & 1);
+                uint32_t v[2][16];
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    // the slot's state is asked for before the conversion and looked at after it
-                    const bool is_free = turn == 0 || tc::mbar_try_wait(B(L::kFree + slot + h), (turn - 1) & 1);
-                    uint32_t v[16];
-                    const __half2 d = __half2half2(__ushort_as_half((unsigned short)scale[part][h]));
-                    uint32_t(&c)[8] = codes[part][h];
-                    values16(make_uint4(c[0], c[1], c[2], c[3]), d, v);
-                    values16(make_uint4(c[4], c[5], c[6], c[7]), d, v + 8);
-                    if (!is_free) wait(L::kFree + slot + h, turn - 1);
-                    const uint32_t to = (part ? v_dst : k_dst) + (slot + h) * L::kSlot;
-#pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) sts128(to ^ (c4 << 4), make_uint4(v[4 * c4], v[4 * c4 + 1], v[4 * c4 + 2], v[4 * c4 + 3]));
+                for (int i = 0; i < 2; ++i) {
+                    const __half2 d = __half2half2(__ushort_as_half((unsigned short)scale[s][i]));
+                    uint32_t(&c)[8] = codes[s][i];
+                    values16(make_uint4(c[0], c[1], c[2], c[3]), d, v[i]);
+                    values16(make_uint4(c[4], c[5], c[6], c[7]), d, v[i] + 8);
                 }
+                if (have) load(s);
+                if (!is_free) wait(L::kFree + first + slot, turn - 1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        sts128((dst + slot * L::kSlot + i * next) ^ (c << 4), make_uint4(v[i][4 * c], v[i][4 * c + 1], v[i][4 * c + 2], v[i][4 * c + 3]));
                 tc::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane < H) tc::mbar_arrive(B(L::kFull + slot + lane));
-                slot += H;
-                if (slot == R) slot = 0, ++turn;
-                if (have) load(part);
+                if (lane == 0) tc::mbar_arrive(B(L::kFull + first + slot));
+                if (++slot == ring) slot = 0, ++turn;
             }
         }
         if (!wait.ok) atomicOr(p.error, 1u);
