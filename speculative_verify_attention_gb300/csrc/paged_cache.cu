@@ -5,8 +5,8 @@
 // zero) over fp32, fp16 or bf16 tokens, the cache row taken from the token's slot.  Read is its inverse, code * scale
 // rounded once to the type asked for.  Both read and write each value once, and are near enough to the memory's rate
 // for instructions a value to count: neither has a conversion instruction a value.  16401 tokens of 8 x 128 fp32 into the
-// cache and as many slots back as fp16 (238 MB) 52 us in two launches, 4.6 TB/s; with four values a lane and
-// conversion instructions 79 us, with twice the tokens a thread 57 us, with blocks of 256 threads 53 us.
+// cache and as many slots back as fp16 (238 MB) 48 us in two launches, 4.9 TB/s; with four values a lane and
+// conversion instructions 79 us, with twice the tokens a thread 57 us, with fp16 values rounded from fp32 products 52 us.
 #include "paged.cuh"
 #include "q8_0.cuh"
 

@@ -476,11 +476,13 @@ struct VerifyPlan {
     size_t ml_off, join_off, bytes;
 };
 
-// More key tiles (of 64) than this an SM, by the tables' capacity, and windows of up to 64 rows go to the streaming kernel:
-// it has a deep ring of fetches but takes longer to start.  Measured with 24 query and 4 KV heads of 256 dims, 24 rows:
-// 8 requests of 20676 tokens (68 tiles an SM) 75 us streaming, 112 us by rows; of 8192 (27) 50 and 56; of 4096 (13) 42 and
-// 33; one request of 2048 (1) 25 and 16.
-constexpr int kStreamTiles = 20;
+// With more key tiles (of 64) than this an SM, by the tables' capacity, windows of up to 64 rows go to the streaming kernel: it
+// has a deep ring of fetches but takes longer to start, and its time grows with the rows.  Measured with 24 query and 4 KV
+// heads of 256 dims, streaming and by rows, us:
+//   24 rows: one request of 2048 tokens (1 tile an SM) 25 and 16, 8 of 2048 (7) 39 and 27, 8 of 20676 (68) 74 and 88,
+//            16 of 20676 (136) 106 and 145
+//   48 rows: 30 and 17, 48 and 28, 87 and 89, 125 and 149;  60 rows: 35 and 17, 47 and 29, 92 and 91, 133 and 150
+inline int stream_tiles(int rows) { return rows <= 32 ? 32 : 64; }
 
 // The lengths are on the device, so all of this is by the longest window and the capacity.
 VerifyPlan verify_plan(int sms, int group, int hd, int max_rows) {
@@ -522,7 +524,7 @@ int launch_verify(PagedVerifyParams& p, const VerifyPlan& v, const kvq8_paged_ca
         rc = HD == 128 && v.chunk > 8 ? launch_few<T, 128, 2>(p, v, s) : launch_few<T, HD, 1>(p, v, s);
     } else {
         const int64_t tiles = (int64_t)p.n_seqs * p.n_kv_heads * ((((int64_t)p.max_pages << p.page_shift) + 63) / 64);
-        if (v.chunk <= 64 && v.team == 1 && tiles > (int64_t)kStreamTiles * v.ctas) {
+        if (v.chunk <= 64 && v.team == 1 && tiles > (int64_t)stream_tiles(v.chunk) * v.ctas) {
             p.box = kv->page_size < 64 ? kv->page_size : 64;
             if (!encode_codes(&p.tmap_k, kv->k_codes, kv, p.box) || !encode_codes(&p.tmap_v, kv->v_codes, kv, p.box)) return KVQ8_ERR_CUDA;
             rc = launch_verify_stream(p, dtype, HD, v.chunk, v.ctas, s);

@@ -11,13 +11,16 @@
 //   0-3   softmax of rows 0 .. 127; 6, 7: of rows 128 .. 191.  References follow only jumps of more than 2^8, by one vote a
 //         group and tile; the group then rescales its columns of O^T.
 //   4     issues all products; 5: sleeps, and rescales the second group's columns in its lanes when that raises (4 too)
-//   8-15  convert: a 32-value block a thread, loaded into registers a tile ahead and asked into L2 a tile earlier, times its
-//         scale and rounded once to fp16, into a ring of 16 KB half tiles (128-byte swizzle)
-// Measured: 16 requests of 20676 tokens (24 / 4 heads of 256 dims, 32-row trees, 144 rows a KV head on average) 254 us, of
-// which 45 us do not depend on the length; without the conversion and its loads 214, with one product of 16 a half of the
-// scores 230: no one part bounds it but the chain through them (scores, softmax, weights, product) with one tile of
-// scores a group.  Issuing whatever product is ready instead of one order: 277 us.  Two tiles of weights and a shorter
-// ring: 381 us.  Scores held in 64 registers from the maximum to the weights, or 17 warps: spills, 318 us.
+//   8-15  convert K (8-11) and V: a 32-value block at a time, loaded into registers a tile ahead and asked into L2 a tile
+//         earlier, times its scale and rounded once to fp16, into a ring of 16 KB half tiles (128-byte swizzle)
+// Measured: 16 requests of 20676 tokens (24 / 4 heads of 256 dims, 32-row trees, 144 rows a KV head on average) 204 us, of
+// which 45 us do not depend on the length; without loads 198, without conversion as well 190, with an eighth of the scores'
+// products 180, of O^T's 194, without any of these and the exponentials 138: what is left is the hand-offs from one role to the
+// next, which one tile of scores a group puts in a row.
+// Steps: one ring for K and V, and scores in tensor memory until the weights are made 254 us; rings of their own 236; the issuing
+// warp's descriptors as constants instead of worked out from the tile's number 204.  Slower: issuing from a single
+// thread's loop 260 (its operands are no longer uniform), from two warps 257, whatever is ready first 277, O^T before the
+// scores 265; two tiles of weights and a shorter ring 381; loads two tiles ahead 233.
 #include "paged_verify.cuh"
 
 namespace kvq8 {
