@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(FL<HD, NT>::kWarps * 32, FL<HD, NT>::kCtas) pa
             if (whole) {
                 const int t = window_row(p, r);
                 const int64_t out_row = (int64_t)(seg.q.row0 + t) * p.n_q_heads + seg.kvh * p.group + r - t * p.group;
-                const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+                const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // (NaN stays one)
                 reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + out_row * HD)[d] =
-                    sum > 0.0f ? make_uint2(Query<T>::out(acc.x * inv, acc.y * inv), Query<T>::out(acc.z * inv, acc.w * inv)) : make_uint2(0u, 0u);
+                    sum != 0.0f ? make_uint2(Query<T>::out(acc.x * inv, acc.y * inv), Query<T>::out(acc.z * inv, acc.w * inv)) : make_uint2(0u, 0u);
             } else {
                 reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * p.chunk + r) * HD)[d] = acc;
                 if (d == 0) p.part_ml[(int64_t)slot * p.chunk + r] = make_float2(m, sum);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
                 const bool on = i + u * di < parts;
                 const int64_t at = slot(on ? i + u * di : i);
                 ml[u] = p.part_ml[at];
-                if (!on) ml[u].x = -INFINITY;
+                if (!on) ml[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) o[u][v] = reinterpret_cast<const float4*>(p.part_o)[at * (HD / 4) + 32 * v + lane];
             }
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             for (int v = 0; v < V; ++v) acc[v].x *= a, acc[v].y *= a, acc[v].z *= a, acc[v].w *= a;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (ml[u].x == -INFINITY) continue;  // a part that saw no key, or none (its o may be anything)
+                if (ml[u].x == -INFINITY && ml[u].y == 0.0f) continue;  // a part that saw no key, or none (its o may be anything)
                 const float w = ex2_approx(ml[u].x - m);
                 l += w * ml[u].y;
 #pragma unroll
@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         const int head = s_join[c0].y * p.group + rr - t * p.group;
         uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((int64_t)(s_join[c0].x + t) * p.n_q_heads + head) * HD);
         auto put = [&](int col, float4 o, float sum) {
-            const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-            dst[col] = sum > 0.0f ? make_uint2(Query<T>::out(o.x * inv, o.y * inv), Query<T>::out(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            dst[col] = sum != 0.0f ? make_uint2(Query<T>::out(o.x * inv, o.y * inv), Query<T>::out(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
         };
         if (!shared) {
 #pragma unroll

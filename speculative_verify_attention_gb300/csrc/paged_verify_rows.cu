@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                 j += seg.t1 - seg.t0;
             }
             if (mine) {
-                inv[row] = l > 0.0f ? 1.0f / l : 0.0f;
+                inv[row] = l != 0.0f ? 1.0f / l : 0.0f;  // (NaN stays one)
                 if (!(seg.begins() && seg.ends()))
                     p.part_ml[(int64_t)(2 * blockIdx.x + (seg.begins() ? 1 : 0)) * p.chunk + row] =
                         make_float2(ref == kNoRef ? -INFINITY : ref, l);

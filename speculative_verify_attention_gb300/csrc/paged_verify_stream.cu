@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_stream_kernel(
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
                             const float sum = __uint_as_float(l[c]);
-                            inv[c] = sum > 0.0f ? 1.0f / sum : 0.0f;
+                            inv[c] = sum != 0.0f ? 1.0f / sum : 0.0f;  // (NaN stays one)
                             if (!whole && tid == c0 + c && tid < seg.n)
                                 p.part_ml[(int64_t)slot * p.chunk + tid] = make_float2(ref[tid] == kNoRef ? -INFINITY : ref[tid], sum);
                         }

@@ -98,3 +98,19 @@ def test_shares_of_single_tiles(lib):
             _widened(b)
             b.check(b.call(), expected)
     _clean()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("hq,hd,rows,row,head", [(4, 128, 2, 1, 2), (6, 256, 1, 0, 3), (6, 256, 4, 2, 1), (6, 256, 9, 8, 0), (6, 256, 32, 30, 5),
+                                                 (6, 256, 32, 3, 4)])
+@pytest.mark.parametrize("n", [40, 3000])
+def test_a_query_that_is_not_a_number_stays_one_and_alone(lib, wide, hq, hd, rows, row, head, n):
+    b = Batch(hd + rows, hq, 1, hd, 16, [n + rows, 300 + rows], [rows, rows], torch.float16, tree=True)
+    if wide:
+        _widened(b)
+    expected = {k: v for k, v in b.expect(rows={0, row, rows}).items() if k != (row, head)}
+    b.q[row, head, 5] = float("nan")
+    out = b.call()
+    assert torch.isnan(out[row, head]).all()
+    b.check(torch.nan_to_num(out, nan=77.0), expected)
+    _clean()
