@@ -72,6 +72,8 @@ __global__ void __launch_bounds__(kAdjThreads, VEC && sizeof(T) == 4 ? 6 : 8) lo
     __shared__ int s_token[kMaxWindowRows];
     const int tid = threadIdx.x, b = blockIdx.y;
     const int v0 = blockIdx.x * kAdjChunk;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // what depends on the request alone, asked for together
     const int first = __ldg(p.row_starts + b), last = __ldg(p.row_starts + b + 1);
     const bool on = p.penalties != nullptr;
@@ -234,11 +236,8 @@ int launch_adjust(const AdjustParams& p, bool vec, cudaStream_t s) {
     // about kAdjRows rows a block, by the mean of the requests' rows
     const int shares = (p.n_rows + p.n_seqs * kAdjRows - 1) / (p.n_seqs * kAdjRows);
     const dim3 grid((unsigned)((p.vocab + kAdjChunk - 1) / kAdjChunk), (unsigned)p.n_seqs, (unsigned)(shares < 65535 ? shares : 65535));
-    if (vec)
-        logits_adjust_kernel<T, true><<<grid, kAdjThreads, 0, s>>>(p);
-    else
-        logits_adjust_kernel<T, false><<<grid, kAdjThreads, 0, s>>>(p);
-    return launch_status();
+    if (vec) return launch_dependent(logits_adjust_kernel<T, true>, grid, kAdjThreads, 0, s, p);
+    return launch_dependent(logits_adjust_kernel<T, false>, grid, kAdjThreads, 0, s, p);
 }
 
 // ---------------------------------------------------------------- counts
@@ -262,6 +261,8 @@ __device__ __forceinline__ int list_state(const CountParams& p, int list) {
 
 // Rows are cleared 16 bytes a thread; a row need not start or end on 16 bytes.
 __global__ void __launch_bounds__(kCountThreads) counts_clear_kernel(const CountParams p) {
+    // the adds read the lists as soon as this kernel runs: not before what came before it is done
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int st = list_state(p, blockIdx.y);
     if (st < 0) return;
@@ -354,8 +355,7 @@ extern "C" int token_counts(const int32_t* tokens, const int32_t* token_starts, 
     cudaStream_t s = (cudaStream_t)stream;
     if (clear) {
         const int gx = (vocab / 4 + 4 * kCountThreads - 1) / (4 * kCountThreads) + 1;
-        counts_clear_kernel<<<dim3((unsigned)(gx < 128 ? gx : 128), (unsigned)n_lists), kCountThreads, 0, s>>>(p);
-        const int rc = launch_status();
+        const int rc = launch_dependent(counts_clear_kernel, dim3((unsigned)(gx < 128 ? gx : 128), (unsigned)n_lists), kCountThreads, 0, s, p);
         if (rc != KVQ8_OK) return rc;
     }
     if (n_tokens == 0) return KVQ8_OK;

@@ -101,10 +101,10 @@ struct Eight<float> {
 // A programmatic dependent launch: the kernel's set-up overlaps the end of the kernel before, and it waits for that
 // one's writes itself (griddepcontrol.wait).
 template <typename Kernel, typename... Args>
-inline int launch_dependent(Kernel* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, Args... args) {
+inline int launch_dependent(Kernel* kernel, dim3 grid, dim3 block, int smem, cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -39,6 +39,8 @@ template <typename T>
 __global__ void __launch_bounds__(kPagedThreads) paged_append_kernel(const __grid_constant__ PagedIO p) {
     constexpr int TOK = kAppendTok<T>;
     const int z = blockIdx.z;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const T* x = static_cast<const T*>(p.x[z]);
     const int g_head = p.head_dim / 8;
     const int j = blockIdx.y * blockDim.x + threadIdx.x;
@@ -113,6 +115,8 @@ __device__ __forceinline__ void store_values(__half* dst, uint2 c, uint16_t scal
 template <typename T>
 __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const __grid_constant__ PagedIO p) {
     const int z = blockIdx.z;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     T* y = static_cast<T*>(p.y[z]);
     const int g_head = p.head_dim / 8;
     const int j = blockIdx.y * blockDim.x + threadIdx.x;
@@ -158,8 +162,7 @@ int launch_paged(Kernel* kernel, const PagedIO& p, int cols, int tok, cudaStream
     const int64_t per = (int64_t)block.y * tok;
     const int64_t gx = (p.n_tok + per - 1) / per;
     const dim3 grid((unsigned)gx, (unsigned)((cols + block.x - 1) / block.x), 2u);
-    kernel<<<grid, block, 0, stream>>>(p);
-    return launch_status();
+    return launch_dependent(kernel, grid, block, 0, stream, p);
 }
 
 PagedIO paged_io(const kvq8_paged_cache* kv, const int64_t* slots, int n_tok) {
