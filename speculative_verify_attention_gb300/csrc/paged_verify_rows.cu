@@ -42,16 +42,13 @@ struct RL {
     // tables: 1 / sum and the factor of the last raise (by tile parity) per row, output rows of two segments, largest query per warp
     static constexpr int kTabInv = 0, kTabAlpha = 4 * NMAX, kTabRow = 12 * NMAX, kTabMisc = 20 * NMAX, kTabScan = kTabMisc + 48,
                          kTabTmem = kTabScan + 64 + (kVerifyThreads / 32 + 1) / 2 * 16, kTabBar = kTabTmem + 16;
-    static constexpr int kMaxSlots = 8, kTabBytes = kTabBar + (2 * kMaxSlots + 11) * 8;
-    static constexpr int kFit = (227 * 1024 - kSmRing - kTabBytes) / kSlot;
-    // K and V have rings of their own, of two tiles, V's of one where there is no room: K^ of tile j + 1 is wanted while the
-    // softmax of tile j runs, V^ of tile j only after it.
-    static constexpr int RK = 2 * H, RV = kFit >= 4 * H ? 2 * H : H, R = RK + RV;
-    static_assert(kFit >= 3 * H && R <= kMaxSlots, "a tile of V^ and two of K^ at least");
-    static constexpr int kSmTab = kSmRing + R * kSlot, kSmBytes = kSmTab + kTabBytes;
-    // Two tiles of scores in tensor memory: one of each group, or two of the one, which then has two of weights too.
-    // barriers: ring slot full / free; a tile of scores ready / read; weights ready; product done; queries ready
-    static constexpr int kFull = 0, kFree = R, kS = 2 * R, kSFree = kS + 2, kP = kSFree + 2, kO = kP + 2, kQ = kO + 2, kRaise = kQ + 1, kR = kQ + 2;
+    static constexpr int kTabBytes = kTabBar + 20 * 8;
+    // K^ has a ring of two tiles, V^ of kBuf: K^ of tile j + 1 is wanted while the softmax of tile j runs, V^ of tile j only after
+    // it.  In tensor memory two tiles of scores: one of each group, or two of the one, which then has two of weights and of V^ too.
+    static constexpr int kTile = H * kSlot, kSmV = kSmRing + 2 * kTile, kSmTab = kSmV + kBuf * kTile, kSmBytes = kSmTab + kTabBytes;
+    // barriers: K^ ready / used; V^ ready; a tile of scores ready / read; weights ready; product done (so weights and V^ used);
+    // queries ready
+    static constexpr int kK = 0, kKFree = 2, kV = 4, kS = 6, kSFree = 8, kP = 10, kO = 12, kQ = 14, kRaise = 15, kR = 16;
     static constexpr uint32_t kTmO = 0, kTmS = kMt * NMAX;
     static_assert(kGroups * kBuf == 2 && kTmS + 128 <= kTmemCols, "tensor memory");
     static_assert(kSmBytes <= 227 * 1024 && kSmP % 1024 == 0 && kSmRing % 1024 == 0, "swizzled tiles are 1024-byte aligned");
@@ -81,7 +78,7 @@ __device__ __forceinline__ bool group_any(int g, bool v) {
 template <typename T, int HD, int NMAX>
 __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(const __grid_constant__ PagedVerifyParams p) {
     using L = RL<HD, NMAX>;
-    constexpr int H = L::H, R = L::R, kGroups = L::kGroups;
+    constexpr int H = L::H, kGroups = L::kGroups;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* tab = smem + L::kSmTab;
@@ -94,12 +91,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
 
     if (tid == 0) {
 #pragma unroll 1
-        for (int s = 0; s < R; ++s) {
-            tc::mbar_init(B(L::kFull + s), 4);
-            tc::mbar_init(B(L::kFree + s), 1);
-        }
-#pragma unroll 1
         for (int g = 0; g < 2; ++g) {
+            tc::mbar_init(B(L::kK + g), 4);
+            tc::mbar_init(B(L::kKFree + g), 1);
+            tc::mbar_init(B(L::kV + g), 4);
             tc::mbar_init(B(L::kS + g), 1);
             tc::mbar_init(B(L::kSFree + g), kGroups > 1 && g ? 2 : 4);
             tc::mbar_init(B(L::kP + g), kGroups > 1 ? 6 : 4);
@@ -155,7 +150,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
         const uint64_t qd = tc::smem_desc_sw128(sbase + L::kSmQ, 16, 1024);
         const uint64_t pd = tc::smem_desc_sw128(sbase + L::kSmP, 16, 1024);
         const uint64_t kd0 = tc::smem_desc_sw128(sbase + L::kSmRing, 16, 1024);
-        const uint64_t vd0 = tc::smem_desc_sw128(sbase + L::kSmRing + L::RK * L::kSlot, L::kVKeys * 128, 1024);
+        const uint64_t vd0 = tc::smem_desc_sw128(sbase + L::kSmV, L::kVKeys * 128, 1024);
         const uint32_t idesc_s = tc::idesc_f16_f32_ab(128, BN, false, false);
         int raises = 0;
         // S of a group and tile j, whose parity is ODD
@@ -163,29 +158,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
             constexpr int ODD = decltype(odd)::value;
             const int b = kGroups > 1 ? g : ODD;  // the group's tile of scores
             if (j >= L::kBuf) wait(L::kSFree + b, j / L::kBuf - 1);
-            if (g == 0 || both) {
+            if (g == 0) wait(L::kK + ODD, j >> 1);
+            tc::fence_after_sync();
+            if (one) {
+                if (g == 0 || both) {
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    constexpr int kFirst = ODD * H;
-                    if (g == 0) wait(L::kFull + kFirst + h, j >> 1);
-                    tc::fence_after_sync();
-                    if (one) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tc::mma_ss(tmem + L::kTmS + b * 64, qd + (uint64_t)(((h * 2 + (k >> 2)) * NMAX * 128 + g * 64 * 128 + (k & 3) * 32) >> 4),
-                                       kd0 + (uint64_t)(((kFirst + h) * L::kSlot + (k >> 2) * 64 * 128 + (k & 3) * 32) >> 4), idesc_s,
-                                       h > 0 || k > 0 ? 1u : 0u);
-                        if (g == 1 || !both) tc::mma_commit(B(L::kFree + kFirst + h));
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < 8 * H; ++k)
+                        tc::mma_ss(tmem + L::kTmS + b * 64, qd + (uint64_t)(((k >> 2) * NMAX * 128 + g * 64 * 128 + (k & 3) * 32) >> 4),
+                                   kd0 + (uint64_t)((ODD * L::kTile + (k >> 2) * 64 * 128 + (k & 3) * 32) >> 4), idesc_s, k > 0 ? 1u : 0u);
                 }
+                tc::mma_commit(B(L::kS + b));
+                if (g == kGroups - 1) tc::mma_commit(B(L::kKFree + ODD));
             }
-            if (one) tc::mma_commit(B(L::kS + b));
             __syncwarp();
         };
         // O^T (+)= V^T P^T of tile j
         auto product = [&](auto odd, int j, uint32_t idesc, int n16, uint32_t more) {
-            constexpr int ODD = decltype(odd)::value, kBufP = L::kBuf > 1 ? ODD : 0, kFirst = L::RV > H ? ODD * H : 0;
+            constexpr int ODD = decltype(odd)::value, kBufP = L::kBuf > 1 ? ODD : 0;
             wait(L::kP + kBufP, pp(j));
             if (kGroups > 1 && more && raised_b[ODD]) {  // its rows' columns in the lanes of the warps that it lacks
                 wait(L::kO + pb(j - 1), pp(j - 1));
@@ -195,22 +184,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                 tc::fence_before_sync();
                 __syncwarp();
             }
+            wait(L::kV + kBufP, pp(j));
+            tc::fence_after_sync();
+            if (one) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                wait(L::kFull + L::RK + kFirst + h, L::RV > H ? j >> 1 : j);
-                tc::fence_after_sync();
-                if (one) {
+                for (int h = 0; h < H; ++h)
 #pragma unroll
                     for (int m = 0; m < L::kMt; ++m)
 #pragma unroll
                         for (int k = 0; k < L::kVKeys / 16; ++k)
-                            tc::mma_ss(tmem + L::kTmO + m * NMAX, vd0 + (uint64_t)(((kFirst + h) * L::kSlot + m * 2 * L::kVKeys * 128 + k * 2048) >> 4),
+                            tc::mma_ss(tmem + L::kTmO + m * NMAX, vd0 + (uint64_t)((kBufP * L::kTile + h * L::kSlot + m * 2 * L::kVKeys * 128 + k * 2048) >> 4),
                                        pd + (uint64_t)((kBufP * NMAX * 128 + h * L::kVKeys * 2 + k * 32) >> 4), idesc, h > 0 || k > 0 ? 1u : more);
-                    tc::mma_commit(B(L::kFree + L::RK + kFirst + h));
-                    if (h == H - 1) tc::mma_commit(B(L::kO + kBufP));
-                }
-                __syncwarp();
+                tc::mma_commit(B(L::kO + kBufP));
             }
+            __syncwarp();
         };
         constexpr std::integral_constant<int, 0> even{};
         constexpr std::integral_constant<int, 1> odd{};
@@ -499,9 +486,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
         // half s of a tile is its keys 32 s .. (V at head_dim 256), or its dims 128 s ..; block i of the thread in it the other
         // way round: its keys are 32 x + 8 w + nn, its blocks 4 y + jj
         const bool by_keys = is_v && H == 2;
-        const int first = is_v ? L::RK : 0, ring = is_v ? L::RV : L::RK;
         const uint32_t next = by_keys ? 8192 : 4096;  // from block 0 to block 1
-        const uint32_t dst = sbase + L::kSmRing + first * L::kSlot + (jj >> 1) * (by_keys ? 4096 : 8192) + (8 * w + nn) * 128 + (((4 * (jj & 1)) ^ nn) << 4);
+        const uint32_t dst = sbase + (is_v ? L::kSmV : L::kSmRing) + (jj >> 1) * (by_keys ? 4096 : 8192) + (8 * w + nn) * 128 + (((4 * (jj & 1)) ^ nn) << 4);
         uint32_t codes[H][2][8], scale[H][2];
         uint32_t row[2];
         bool there[2] = {false, false};
@@ -559,19 +545,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
         for (int i = 0; i < 2 * H; ++i)
 #pragma unroll
             for (int x = 0; x < 8; ++x) codes[i >> 1][i & 1][x] = 0u;
-        int slot = 0, turn = 0;
         ahead();
         if (have) {
 #pragma unroll
             for (int s = 0; s < H; ++s) load(s);
         }
 #pragma unroll 1
-        while (have) {
+        for (int j = 0; have; ++j) {
             ahead();
+            // the place's last use: of K^ by the scores of tile j - 2, of V^ by the product of tile j - kBuf
+            const int place = is_v ? pb(j) : j & 1, free = is_v ? L::kO + place : L::kKFree + place, last = (is_v ? pp(j) : j >> 1) - 1;
+            const bool is_free = last < 0 || tc::mbar_try_wait(B(free), (uint32_t)last & 1u);
+            const uint32_t to = dst + place * L::kTile;
 #pragma unroll
             for (int s = 0; s < H; ++s) {
-                // the slot's state is asked for before the conversion and looked at after it
-                const bool is_free = turn == 0 || tc::mbar_try_wait(B(L::kFree + first + slot), (turn - 1) & 1);
                 uint32_t v[2][16];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -581,17 +568,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) paged_verify_rows_kernel(co
                     values16(make_uint4(c[4], c[5], c[6], c[7]), d, v[i] + 8);
                 }
                 if (have) load(s);
-                if (!is_free) wait(L::kFree + first + slot, turn - 1);
+                if (s == 0 && !is_free) wait(free, last);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        sts128((dst + slot * L::kSlot + i * next) ^ (c << 4), make_uint4(v[i][4 * c], v[i][4 * c + 1], v[i][4 * c + 2], v[i][4 * c + 3]));
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(B(L::kFull + first + slot));
-                if (++slot == ring) slot = 0, ++turn;
+                        sts128((to + s * L::kSlot + i * next) ^ (c << 4), make_uint4(v[i][4 * c], v[i][4 * c + 1], v[i][4 * c + 2], v[i][4 * c + 3]));
             }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(B((is_v ? L::kV : L::kK) + place));
         }
         if (!wait.ok) atomicOr(p.error, 1u);
     }
