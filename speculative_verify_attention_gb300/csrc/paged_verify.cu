@@ -479,10 +479,10 @@ struct VerifyPlan {
 // With more key tiles (of 64) than this an SM, by the tables' capacity, windows of up to 64 rows go to the streaming kernel: it
 // has a deep ring of fetches but takes longer to start, and its time grows with the rows.  Measured with 24 query and 4 KV
 // heads of 256 dims, streaming and by rows, us:
-//   24 rows: one request of 2048 tokens (1 tile an SM) 25 and 16, 8 of 2048 (7) 39 and 27, 8 of 20676 (68) 74 and 88,
-//            16 of 20676 (136) 106 and 145
-//   48 rows: 30 and 17, 48 and 28, 87 and 89, 125 and 149;  60 rows: 35 and 17, 47 and 29, 92 and 91, 133 and 150
-inline int stream_tiles(int rows) { return rows <= 32 ? 32 : 64; }
+//   24 rows: one request of 2048 tokens (1 tile an SM) 25 and 16, 8 of 2048 (7) 40 and 27, 8 of 20676 (68) 74 and 83,
+//            16 of 20676 (136) 106 and 136
+//   48 rows: 30 and 17, 48 and 28, 88 and 85, 125 and 139;  60 rows: 35 and 17, 47 and 28, 92 and 85, 133 and 140
+inline int stream_tiles(int rows) { return rows <= 32 ? 40 : 80; }
 
 // The lengths are on the device, so all of this is by the longest window and the capacity.
 VerifyPlan verify_plan(int sms, int group, int hd, int max_rows) {

@@ -12,15 +12,15 @@
 //         group and tile; the group then rescales its columns of O^T.
 //   4     issues all products; 5: sleeps, and rescales the second group's columns in its lanes when that raises (4 too)
 //   8-15  convert K (8-11) and V: a 32-value block at a time, loaded into registers a tile ahead and asked into L2 a tile
-//         earlier, times its scale and rounded once to fp16, into a ring of 16 KB half tiles (128-byte swizzle)
-// Measured: 16 requests of 20676 tokens (24 / 4 heads of 256 dims, 32-row trees, 144 rows a KV head on average) 204 us, of
-// which 45 us do not depend on the length; without loads 198, without conversion as well 190, with an eighth of the scores'
-// products 180, of O^T's 194, without any of these and the exponentials 138: what is left is the hand-offs from one role to the
-// next, which one tile of scores a group puts in a row.
+//         earlier, times its scale and rounded once to fp16, into rings of tiles (128-byte swizzle)
+// Measured: 16 requests of 20676 tokens (24 / 4 heads of 256 dims, 32-row trees, 144 rows a KV head on average) 195 us, of
+// which 45 us do not depend on the length; without loads 188, without conversion as well 181, with a quarter of O^T's products
+// 185, without the exponentials 191, without any of these 133: what is left is the hand-offs from one role to the next, which
+// one tile of scores a group puts in a row.  24 rows 136 us.
 // Steps: one ring for K and V, and scores in tensor memory until the weights are made 254 us; rings of their own 236; the issuing
-// warp's descriptors as constants instead of worked out from the tile's number 204.  Slower: issuing from a single
-// thread's loop 260 (its operands are no longer uniform), from two warps 257, whatever is ready first 277, O^T before the
-// scores 265; two tiles of weights and a shorter ring 381; loads two tiles ahead 233.
+// warp's descriptors as constants instead of worked out from the tile's number 204; a barrier a tile instead of one for each
+// half 195.  Slower: issuing from a single thread's loop 260 (its operands are no longer uniform), from two warps 257, whatever
+// is ready first 277, O^T before the scores 265; two tiles of weights and a shorter ring 381; loads two tiles ahead 233.
 #include "paged_verify.cuh"
 
 namespace kvq8 {
@@ -31,8 +31,8 @@ constexpr int kMmaWarp = 4, kHelpWarp = 5, kConvWarp0 = 8;
 constexpr int kAhead = 1;                   // tiles between the one being loaded and the one asked into L2
 constexpr int kVerifyThreads = 512;
 constexpr int kSoftThreads = 192;           // warps 0-3, 6 and 7
-// Shapes: NMAX rows of a CTA, 64 or 192, in groups of 128 and 64 (the softmax warps of the lanes); H halves of a tile in
-// the ring, of K^ by dims (64 keys x 128) and of V^ by keys (256 dims x 32; at head_dim 128 all 64), 16 KB each.
+// Shapes: NMAX rows of a CTA, 64 or 192, in groups of 128 and 64 (the softmax warps of the lanes); H halves of a tile, of K^
+// by dims (64 keys x 128) and of V^ by keys (256 dims x 32; at head_dim 128 all 64), 16 KB each.
 template <int HD, int NMAX>
 struct RL {
     static constexpr int H = HD / 128, kMt = HD / 128, kGroups = NMAX > 128 ? 2 : 1, kBuf = NMAX > 128 ? 1 : 2;
