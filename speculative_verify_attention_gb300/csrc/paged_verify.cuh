@@ -98,27 +98,34 @@ struct Walk {
                 if (++b >= p.n_seqs) return false;
                 q = request_of<KEYS>(p, b);
             }
-            s.b = b;
-            s.kvh = kvh;
-            // the team's equal parts of the rows, so that no CTA pays for a tile of a few rows
+            // the team's equal parts of the rows, so that no CTA pays for a tile of a few rows; a window of few rows may leave
+            // the last CTAs of the team none
             const int rows = q.rows * p.group;
-            s.r0 = 0;
-            s.n = rows;
+            int r0 = 0, n = rows;
             if (p.team > 1) {
                 const int per = (rows + p.team - 1) / p.team;
-                s.r0 = (int)(blockIdx.x % p.team) * per;
-                s.n = min(per, rows - s.r0);
+                r0 = (int)(blockIdx.x % p.team) * per;
+                n = min(per, rows - r0);
             }
-            s.t0 = t;
-            s.t1 = (int)min((long long)q.tiles, t + left);
-            s.q = q;
-            left -= s.t1 - s.t0;
-            t = s.t1;
+            const int t0 = t, kv_head = kvh;
+            t = (int)min((long long)q.tiles, t0 + left);
+            const int t1 = t;
+            left -= t1 - t0;
             if (t == q.tiles) {
                 t = 0;
                 ++kvh;
             }
-            if (s.n > 0) return true;  // fewer rows than CTAs in the team: some have none
+            // the caller's segment changes only where it gets a new one: after the last, it is still the last
+            if (n > 0) {
+                s.b = b;
+                s.kvh = kv_head;
+                s.r0 = r0;
+                s.n = n;
+                s.t0 = t0;
+                s.t1 = t1;
+                s.q = q;
+                return true;
+            }
         }
         return false;
     }
@@ -223,7 +230,8 @@ __device__ __forceinline__ Walk<KEYS> walk_from(const PagedVerifyParams& p, cons
     return w;
 }
 
-// What one thread leaves for the joining kernel: the item that this CTA begins and does not end, under its number.
+// What one thread leaves for the joining kernel: the item that this CTA begins and does not end, under its number.  It can only
+// be the last one that it has rows of; where the share ends on an item without, the one before ended in the share.
 template <int KEYS>
 __device__ __forceinline__ void leave_join(const PagedVerifyParams& p, const Place& place) {
     int4 join = make_int4(0, 0, 0, -1);
