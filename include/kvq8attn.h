@@ -517,8 +517,8 @@ size_t attn_verify_paged_q8_workspace_bytes(int n_q_heads, int n_kv_heads, int h
  * K, V and p enter the tensor cores in fp16 (code * scale rounded once), bf16 q as fp16 times a power
  * of two (one for the rows that a thread block holds); scores, softmax statistics and sums are fp32.
  * Values of the cache must stay inside the fp16 range; rows of one window whose bf16 queries are more
- * than 2^25 apart in size lose the small ones.  A query that is not a number gives a row of NaN and
- * changes no other.  The same call gives the same bits.
+ * than 2^25 apart in size lose the small ones.  A query that is not a number gives a row of NaN; one that
+ * is not finite changes no other row.  The same call gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, n_q_heads / n_kv_heads > 64, max_rows > 64,
  * n_seqs > 4096, n_rows > 2^24, a cache of too many rows), WORKSPACE, MISALIGNED (16 bytes; the code planes 32: a block is one load; int32 arrays 4, window_mask 8).  Two launches.
  */

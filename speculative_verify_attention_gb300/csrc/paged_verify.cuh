@@ -278,10 +278,14 @@ struct Query<__half> {
 template <>
 struct Query<__nv_bfloat16> {
     static constexpr bool kLifted = true;
-    // the largest magnitude's bits (NaN and infinity above all)
+    // The bits of the largest finite magnitude.  NaN and infinity have no part in it: they stay what they are under any
+    // power of two, and one of them must not decide how the other rows are scaled.
     static __device__ __forceinline__ uint32_t top(uint4 v) {
         uint32_t t = 0;
-        for (uint32_t w : {v.x, v.y, v.z, v.w}) t = max(t, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+        for (uint32_t w : {v.x, v.y, v.z, v.w}) {
+            const uint32_t a = w & 0x7fffu, b = (w >> 16) & 0x7fffu;
+            t = max(t, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+        }
         return t;
     }
     static __device__ __forceinline__ uint32_t pair(uint32_t w, float lifted) {
@@ -294,11 +298,10 @@ struct Query<__nv_bfloat16> {
     static __device__ __forceinline__ uint16_t one(float a) { return __bfloat16_as_ushort(__float2bfloat16_rn(a)); }
 };
 
-// The power of two that brings a bf16 magnitude (its bits) into [2^14, 2^15); 1 for zeros, subnormals and what is
-// not finite.
+// The power of two that brings a finite bf16 magnitude (its bits) into [2^14, 2^15); 1 for zeros and subnormals.
 __device__ __forceinline__ float lift_of(uint32_t top) {
     const int e = (int)(top >> 7);
-    if (e == 0 || e == 255) return 1.0f;
+    if (e == 0) return 1.0f;
     return __uint_as_float((uint32_t)min(127 + 127 + 14 - e, 254) << 23);
 }
 
