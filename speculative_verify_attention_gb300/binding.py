@@ -700,9 +700,14 @@ def _launch_on(device: int, stream) -> int:
 
 
 def _scratch(nbytes: int, device, stream):
-    """A workspace from the allocator for one call: taken on the stream that uses it."""
-    if stream is None or not hasattr(stream, "cuda_stream"):
+    """Memory for one call, taken on the stream that the call runs on, a raw handle's too: the allocator gives it out
+    again in that stream's order, while the current stream may be far ahead."""
+    if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        # 1 is another name of the default stream, 0
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
