@@ -181,6 +181,23 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory that a call takes for itself or returns, taken on the stream that the call runs on, a raw handle's too: the
+    allocator gives it out again in that stream's order, while the current stream may be far ahead or behind."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        handle = int(stream)
+        # 1 is another name of the default stream, 0
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    return _empty(nbytes, torch.uint8, device, stream)
+
+
 def _ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(0 if t is None else t.data_ptr())
 
@@ -263,11 +280,11 @@ def attn_verify_k8v4(q: torch.Tensor, cache: KVCacheK8V4, kv_len: int, q_pos0: i
     _need(q, "q", torch.float32)
     n_rows, n_q_heads, head_dim = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_verify_q8_workspace_bytes(n_rows, n_q_heads, head_dim, kv_len, cache.n_kv_heads, n_split)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_verify_k8v4(_ptr(q), n_rows, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                          int(q_pos0), float(softmax_scale), _ptr(out), _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), int(n_split), _stream(stream))
@@ -282,11 +299,11 @@ def attn_prompt_k8v4(q: torch.Tensor, cache: KVCacheK8V4, kv_len: int, q_pos0: i
     _need(q, "q", torch.float16)
     n_q, n_q_heads, head_dim = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _empty(q.shape, torch.float32, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_prompt_q8_workspace_bytes(n_q, n_q_heads, head_dim, kv_len, q_pos0, cache.n_kv_heads)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_prompt_k8v4(_ptr(q), n_q, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                          int(q_pos0), float(softmax_scale), _ptr(out), _ptr(workspace),
                                          workspace.numel() * workspace.element_size(), _stream(stream))
@@ -334,11 +351,11 @@ def attn_verify_f16(q: torch.Tensor, cache: KVCacheF16, kv_len: int, q_pos0: int
     _need(q, "q", torch.float32)
     n_rows, n_q_heads, head_dim = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_verify_f16_workspace_bytes(n_rows, n_q_heads, head_dim, kv_len, cache.n_kv_heads, n_split)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_verify_f16(_ptr(q), n_rows, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                         int(q_pos0), float(softmax_scale), _ptr(out), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(), int(n_split), _stream(stream))
@@ -353,11 +370,11 @@ def attn_prompt_f16(q: torch.Tensor, cache: KVCacheF16, kv_len: int, q_pos0: int
     _need(q, "q", torch.float16)
     n_q, n_q_heads, head_dim = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _empty(q.shape, torch.float32, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_prompt_f16_workspace_bytes(n_q, n_q_heads, head_dim, kv_len, q_pos0, cache.n_kv_heads)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_prompt_f16(_ptr(q), n_q, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                         int(q_pos0), float(softmax_scale), _ptr(out), _ptr(workspace),
                                         workspace.numel() * workspace.element_size(), _stream(stream))
@@ -401,11 +418,11 @@ def attn_verify_q8(q: torch.Tensor, cache: KVCacheQ8, kv_len: int, q_pos0: int, 
     _need(q, "q", torch.float32)
     n_rows, n_q_heads, head_dim = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_verify_q8_workspace_bytes(n_rows, n_q_heads, head_dim, kv_len, cache.n_kv_heads, n_split)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_verify_q8(_ptr(q), n_rows, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                        int(q_pos0), float(softmax_scale), _ptr(out), _ptr(workspace),
                                        workspace.numel() * workspace.element_size(), int(n_split), _stream(stream))
@@ -425,11 +442,11 @@ def attn_verify_tree_q8(q: torch.Tensor, cache: KVCacheQ8, kv_len: int, q_pos0: 
     if window_mask.shape != (n_rows,):
         raise ValueError(f"window_mask must hold one word per row ({n_rows})")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_verify_q8_workspace_bytes(n_rows, n_q_heads, head_dim, kv_len, cache.n_kv_heads, n_split)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_verify_tree_q8(_ptr(q), n_rows, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                             int(q_pos0), _ptr(window_mask), float(softmax_scale), _ptr(out),
                                             _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -457,9 +474,9 @@ def attn_verify_q8_partials(q: torch.Tensor, cache: KVCacheQ8, kv_len: int, q_po
         raise KVQ8Error("attn_verify_q8_partials_count", KVQ8_ERR_INVALID_ARG)
     rows = n_rows * n_q_heads
     if part_o is None:
-        part_o = torch.empty((n, rows, head_dim), dtype=torch.float32, device=q.device)
+        part_o = _empty((n, rows, head_dim), torch.float32, q.device, stream)
     if part_ml is None:
-        part_ml = torch.empty((n, rows, 2), dtype=torch.float32, device=q.device)
+        part_ml = _empty((n, rows, 2), torch.float32, q.device, stream)
     _need(part_o, "part_o", torch.float32)
     _need(part_ml, "part_ml", torch.float32)
     if part_o.shape != (n, rows, head_dim) or part_ml.shape != (n, rows, 2):
@@ -490,12 +507,12 @@ def attn_verify_append_q8(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Ten
     if k_new.shape != v_new.shape or k_new.shape != (n_rows, cache.n_kv_heads, cache.head_dim):
         raise ValueError(f"k_new and v_new must both be [{n_rows}][{cache.n_kv_heads}][{cache.head_dim}]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_verify_append_q8_workspace_bytes(n_rows, n_q_heads, head_dim, q_pos0, cache.n_kv_heads,
                                                        n_split)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_verify_append_q8(_ptr(q), _ptr(k_new), _ptr(v_new), n_rows, n_q_heads,
                                               ctypes.byref(cache.struct()), int(q_pos0), float(softmax_scale),
                                               _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -572,15 +589,15 @@ def argmax_rows_top_prob(logits: torch.Tensor, workspace: torch.Tensor | None = 
         raise ValueError("logits must be [T][V]")
     n_rows, vocab = logits.shape
     if argmax is None:
-        argmax = torch.empty(n_rows, dtype=torch.int32, device=logits.device)
+        argmax = _empty(n_rows, torch.int32, logits.device, stream)
     if top_prob is None:
-        top_prob = torch.empty(n_rows, dtype=torch.float32, device=logits.device)
+        top_prob = _empty(n_rows, torch.float32, logits.device, stream)
     _need(argmax, "argmax", torch.int32)
     _need(top_prob, "top_prob", torch.float32)
     lib = load_library()
     if workspace is None:
-        workspace = torch.empty(max(int(lib.argmax_rows_top_prob_workspace_bytes(n_rows, vocab)), 16),
-                                dtype=torch.uint8, device=logits.device)
+        workspace = _scratch(max(int(lib.argmax_rows_top_prob_workspace_bytes(n_rows, vocab)), 16), logits.device,
+                             stream)
     st = lib.argmax_rows_top_prob(_ptr(logits), n_rows, vocab, _ptr(argmax), _ptr(top_prob), _ptr(workspace),
                                   workspace.numel() * workspace.element_size(), _stream(stream))
     _check("argmax_rows_top_prob", st)
@@ -592,7 +609,7 @@ def kvq8_selftest_convert(kind: int, words: torch.Tensor, stream=None) -> torch.
     device; returns the fp16 pairs as int32 words (2 per input word for kinds 0 and 1, 4 for 2 and 3)."""
     _need(words, "words", torch.int32)
     n = words.numel()
-    out = torch.empty(n * (2 if kind in (0, 1) else 4), dtype=torch.int32, device=words.device)
+    out = _empty(n * (2 if kind in (0, 1) else 4), torch.int32, words.device, stream)
     st = load_library().kvq8_selftest_convert(int(kind), _ptr(words), _ptr(out), n, _stream(stream))
     _check("kvq8_selftest_convert", st)
     return out
@@ -612,7 +629,7 @@ def attn_combine(part_o: torch.Tensor, part_ml: torch.Tensor, out: torch.Tensor 
     _need(part_ml, "part_ml", torch.float32)
     n_split, rows, head_dim = part_o.shape
     if out is None:
-        out = torch.empty((rows, head_dim), dtype=torch.float32, device=part_o.device)
+        out = _empty((rows, head_dim), torch.float32, part_o.device, stream)
     _need(out, "out", torch.float32)
     st = load_library().attn_combine(_ptr(part_o), _ptr(part_ml), n_split, rows, head_dim, _ptr(out),
                                      _stream(stream))
@@ -637,11 +654,11 @@ def attn_prompt_q8(q: torch.Tensor, cache: KVCacheQ8, kv_len: int, q_pos0: int, 
     _need(q, "q", torch.float16)
     n_q, n_q_heads, head_dim = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _empty(q.shape, torch.float32, q.device, stream)
     _need(out, "out", torch.float32)
     if workspace is None:
         nbytes = attn_prompt_q8_workspace_bytes(n_q, n_q_heads, head_dim, kv_len, q_pos0, cache.n_kv_heads)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(nbytes, 16), q.device, stream)
     st = load_library().attn_prompt_q8(_ptr(q), n_q, n_q_heads, ctypes.byref(cache.struct()), int(kv_len),
                                        int(q_pos0), float(softmax_scale), _ptr(out), _ptr(workspace),
                                        workspace.numel() * workspace.element_size(), _stream(stream))
@@ -659,7 +676,7 @@ def attn_verify_q8_noalloc(q: torch.Tensor, cache: KVCacheQ8, kv_len: int, q_pos
     _need(q, "q", torch.float32)
     n_rows, n_q_heads, _ = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", torch.float32)
     st = load_library().attn_verify_q8_noalloc(_ptr(q), n_rows, n_q_heads, ctypes.byref(cache.struct()),
                                                int(kv_len), int(q_pos0), float(softmax_scale), _ptr(out),
@@ -697,19 +714,6 @@ def _launch_on(device: int, stream) -> int:
     if hasattr(stream, "device") and stream.device.index != device:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{device}")
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _scratch(nbytes: int, device, stream):
-    """Memory for one call, taken on the stream that the call runs on, a raw handle's too: the allocator gives it out
-    again in that stream's order, while the current stream may be far ahead."""
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        handle = int(stream)
-        # 1 is another name of the default stream, 0
-        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 class KVPagedCacheQ8:
@@ -826,8 +830,7 @@ def attn_verify_paged_q8(q: torch.Tensor, cache: KVPagedCacheQ8, page_table: tor
         raise ValueError("q: the heads of a row must be contiguous")
     n, mp = page_table.shape
     if out is None:
-        out = torch.empty((n_rows, hq, hd), dtype=q.dtype, device=q.device) if stream is None else \
-            _scratch(n_rows * hq * hd * 2, q.device, stream).view(q.dtype).view(n_rows, hq, hd)
+        out = _empty((n_rows, hq, hd), q.dtype, q.device, stream)
     lib = (_lib or load_library())
     if workspace is None:
         workspace = _scratch(max(lib.attn_verify_paged_q8_workspace_bytes(hq, cache.n_kv_heads, hd, int(max_rows)), 16), q.device,
@@ -860,8 +863,7 @@ def logits_adjust(logits: torch.Tensor, row_starts: torch.Tensor, penalties: tor
     rows, vocab = logits.shape
     n = row_starts.shape[0] - 1
     if out is None:
-        out = torch.empty((rows, vocab), dtype=f32, device=logits.device) if stream is None else \
-            _scratch(rows * vocab * 4, logits.device, stream).view(f32).view(rows, vocab)
+        out = _empty((rows, vocab), f32, logits.device, stream)
     if out.dtype is not f32 or out.shape != logits.shape or out.get_device() != dev or (out.stride(1) != 1 and vocab > 1):
         raise ValueError(f"out must be float32 [{rows}][{vocab}] with contiguous rows on {logits.device}")
     n_states = 0 if counts is None else counts.shape[0]
