@@ -42,6 +42,7 @@ inline int check_paged(const kvq8_paged_cache* kv) {
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// 32 bytes that nothing writes while the kernel runs.
 __device__ __forceinline__ void load32(uint32_t (&w)[8], const void* at) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
@@ -85,9 +86,12 @@ struct Eight<float> {
         const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
+    // (not by the read-only path, which load32 takes: the kernel may write its output to the same place)
     __device__ __forceinline__ void load_whole(const float* p) {
         uint32_t w[8];
-        load32(w, p);
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
     }
