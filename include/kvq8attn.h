@@ -532,7 +532,7 @@ int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows,
  * logits_adjust -- penalties for repeated tokens, biases and grammar masks on a window's logits.
  *   logits  : [n_rows][vocab] of `dtype`, logits_stride elements between rows
  *   out     : fp32 [n_rows][vocab], out_stride elements between rows; may be `logits` itself (fp32,
- *             equal strides)
+ *             equal strides); rows of it that share bytes with rows of `logits` in any other way are refused
  *   penalties : fp32 [n_seqs][3] repetition, frequency, presence, or null (none; then counts and
  *             window_tokens must be null)
  *   counts  : uint32 [n_states][vocab] as token_counts keeps them, or null; state_of: int32 [n_seqs],
@@ -552,7 +552,7 @@ int attn_verify_paged_q8(const void* q, int dtype, int64_t q_stride, int n_rows,
  *   x += bias - (frequency * c + (c > 0 ? presence : 0));  not allowed: x = -inf (whatever x was).
  * Tokens outside [0, vocab) are ignored.  Rows of no request, and of a request with more than 64 rows
  * where window_tokens is given, are left as they were.
- * Errors: INVALID_ARG, UNSUPPORTED (n_seqs > 4096, vocab > 2^30, n_rows > 262140), MISALIGNED (element
+ * Errors: INVALID_ARG (an overlap as well), UNSUPPORTED (n_seqs > 4096, vocab > 2^30, n_rows > 262140), MISALIGNED (element
  * size; window_mask 8).  One launch.
  */
 int logits_adjust(const void* logits, int dtype, int64_t logits_stride, int n_rows, int vocab,

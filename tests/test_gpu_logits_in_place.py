@@ -48,3 +48,16 @@ def test_calls_in_place_in_a_graph(lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [4096, 4099])
+def test_rows_between_the_inputs_rows(lib, vocab, dtype):
+    """Output rows in the gaps of the input's are no overlap."""
+    c = _case(42, [3, 12, 6], vocab, dtype, tree=True)
+    rows, want = len(c["logits"]), _call(c)
+    wide = torch.zeros((rows, 2 * vocab), device="cuda")
+    x = wide[:, vocab:].view(dtype)[:, :vocab] if dtype != torch.float32 else wide[:, vocab:]
+    x.copy_(c["logits"].cuda())
+    _call(c, logits=x, out=wide[:, :vocab].fill_(55.0))
+    assert torch.equal(wide[:, :vocab], want) and torch.equal(x, c["logits"].cuda())
