@@ -486,11 +486,11 @@ int kvq8_paged_append(const void* k, const void* v, int dtype, int n_tok, int64_
 /*
  * kvq8_paged_read -- the values code * scale of n_tok slots, rounded once to `dtype`, one launch.
  *   k, v : [token][head][head_dim] of `dtype`; k_strides / v_strides (host, 2 entries): elements
- *          between tokens and between heads, each >= head_dim and a multiple of 16 bytes.  Strides
- *          {head_dim, capacity * head_dim} write the planes of a kvf16_cache, over which
- *          attn_prompt_f16 then runs: a prompt chunk behind a paged context.
+ *          between tokens and between heads, each >= head_dim and a multiple of 16 bytes; no two
+ *          rows of a plane may overlap.  Strides {head_dim, capacity * head_dim} write the planes of a
+ *          kvf16_cache, over which attn_prompt_f16 then runs: a prompt chunk behind a paged context.
  *   slots : int64 [n_tok], device, repeats allowed; a slot outside the cache gives zeros.
- * Errors: as for kvq8_paged_append.
+ * Errors: as for kvq8_paged_append; INVALID_ARG for overlapping rows.
  */
 int kvq8_paged_read(const kvq8_paged_cache* kv, const int64_t* slots, int n_tok, int dtype, void* k, void* v,
                     const int64_t* k_strides, const int64_t* v_strides, kvq8_stream_t stream);

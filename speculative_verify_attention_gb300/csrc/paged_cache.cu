@@ -145,6 +145,17 @@ __global__ void __launch_bounds__(kPagedThreads) paged_read_kernel(const __grid_
     }
 }
 
+// Whether two of the rows of `len` values at t * tok + h * head (t < n_tok, h < heads) share a value.  Both steps are at least
+// len, so rows of one head or one token do not; those h heads apart do where some number of tokens back brings them together.
+bool rows_overlap(int64_t tok, int n_tok, int64_t head, int heads, int len) {
+    for (int h = 1; h < heads; ++h) {
+        const int64_t ahead = h * head, back = ahead / tok < n_tok - 1 ? ahead / tok : n_tok - 1;
+        const int64_t next = back + 1 < n_tok - 1 ? back + 1 : n_tok - 1;
+        if (ahead - back * tok < len || (next > back && next * tok - ahead < len)) return true;
+    }
+    return false;
+}
+
 // Groups of a row that a block covers and its token rows, whole warps in all: a row's groups are a multiple of 16 (half
 // a warp), so an odd multiple takes an even count of rows, or is rounded up where one row fills the block.
 dim3 paged_block(int cols) {
@@ -228,6 +239,8 @@ extern "C" int kvq8_paged_read(const kvq8_paged_cache* kv, const int64_t* slots,
         if ((st[0] * esz) % 16 || (st[1] * esz) % 16) return KVQ8_ERR_MISALIGNED;
     }
     if (!aligned16(k) || !aligned16(v) || !aligned_to(slots, 8)) return KVQ8_ERR_MISALIGNED;
+    for (int z = 0; z < 2; ++z)
+        if (rows_overlap(p.tok_stride[z], n_tok, p.head_stride[z], kv->n_kv_heads, kv->head_dim)) return KVQ8_ERR_INVALID_ARG;
     const int cols = kv->n_kv_heads * (kv->head_dim / 8);
     cudaStream_t s = (cudaStream_t)stream;
     if (dtype == KVQ8_F32) return launch_paged(paged_read_kernel<float>, p, cols, kReadTok, s);
