@@ -734,16 +734,25 @@ class KVPagedCacheQ8:
         return c
 
     def _set(self, k_codes, k_scales, v_codes, v_scales):
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
         shape = tuple(k_codes.shape)
-        self.device, self._index = k_codes.device, k_codes.get_device()
+        n_pages, n_kv_heads, page_size, head_dim = shape
+        index = k_codes.get_device()
         for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-            _addr(t, name, torch.int8, shape, self._index)
+            _addr(t, name, torch.int8, shape, index)
         for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _addr(t, name, torch.float16, shape[:3] + (self.head_dim // 32,), self._index)
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+            _addr(t, name, torch.float16, shape[:3] + (head_dim // 32,), index)
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
+        self.device, self._index = k_codes.device, index
+        self._planes = {"k_codes": k_codes, "k_scales": k_scales, "v_codes": v_codes, "v_scales": v_scales}
         self._struct = kvq8_paged_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
-                                        self.n_kv_heads, self.head_dim, self.page_size, self.n_pages)
+                                        n_kv_heads, head_dim, page_size, n_pages)
+
+    def _plane(name: str):
+        # the C struct is kept, so a plane that is replaced has to reach it; one of another shape, type or device raises
+        return property(lambda self: self._planes[name], lambda self, t: self._set(**{**self._planes, name: t}))
+
+    k_codes, k_scales, v_codes, v_scales = _plane("k_codes"), _plane("k_scales"), _plane("v_codes"), _plane("v_scales")
+    del _plane
 
     def struct(self) -> kvq8_paged_cache:
         return self._struct
