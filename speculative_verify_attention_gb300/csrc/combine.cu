@@ -214,7 +214,7 @@ int launch_combine(const float* part_o, const float* part_ml, int n_split, int r
         e = cudaLaunchKernelEx(&cfg, combine_kernel, reinterpret_cast<const float4*>(part_o),
                                reinterpret_cast<const float2*>(part_ml), n_split, rows, hd4, out);
     }
-    return e == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
+    return launched(e);
 }
 
 }  // namespace kvq8

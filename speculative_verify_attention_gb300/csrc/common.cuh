@@ -45,6 +45,14 @@ inline int launch_status() {
     return e == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
 }
 
+// The status of a launch or copy that returned e.  An error stays the thread's last one until it is read, and the next call's
+// launch_status() would take it for its own.
+inline int launched(cudaError_t e) {
+    if (e == cudaSuccess) return KVQ8_OK;
+    cudaGetLastError();
+    return KVQ8_ERR_CUDA;
+}
+
 // Two int8 codes -> two fp16 values, exactly.  The input word x holds the codes already
 // offset by +128 (sign bit flipped), so each is an unsigned byte u in [1, 255].  Placing u
 // in the low mantissa byte of the fp16 pattern 0x64uu gives 1024 + u exactly; subtracting

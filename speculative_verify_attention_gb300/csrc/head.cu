@@ -223,7 +223,6 @@ extern "C" int argmax_rows_top_prob(const float* logits, int n_rows, int vocab, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, head_merge_kernel, static_cast<const HeadAcc*>(part), B, vocab,
-                                             argmax, top_prob);
-    return e == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, head_merge_kernel, static_cast<const HeadAcc*>(part), B, vocab, argmax,
+                                       top_prob));
 }

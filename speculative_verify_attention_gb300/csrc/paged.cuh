@@ -116,7 +116,7 @@ inline int launch_dependent(Kernel* kernel, dim3 grid, dim3 block, int smem, cud
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 }  // namespace kvq8

@@ -217,5 +217,5 @@ extern "C" int kvq8_paged_tables(const int32_t* lens, const int32_t* n_new, cons
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_tables_kernel, p) == cudaSuccess ? KVQ8_OK : KVQ8_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, paged_tables_kernel, p));
 }

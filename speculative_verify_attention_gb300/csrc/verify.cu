@@ -998,7 +998,7 @@ extern "C" int attn_verify_append_q8_host(const float* h_in, int n_rows, int n_q
         host_copy_kernel<<<(n16 + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer), kCopyThreads, 0, s>>>(
             static_cast<const uint4*>(m_in), reinterpret_cast<uint4*>(base), n16);
         if (kvq8::launch_status() != KVQ8_OK) return KVQ8_ERR_CUDA;
-    } else if (cudaMemcpyAsync(base, h_in, h.in_bytes, cudaMemcpyHostToDevice, s) != cudaSuccess) {
+    } else if (kvq8::launched(cudaMemcpyAsync(base, h_in, h.in_bytes, cudaMemcpyHostToDevice, s)) != KVQ8_OK) {
         return KVQ8_ERR_CUDA;
     }
     const bool direct_out = m_out && kvq8::aligned16(m_out);
@@ -1007,8 +1007,7 @@ extern "C" int attn_verify_append_q8_host(const float* h_in, int n_rows, int n_q
                                      v_new);
     if (rc != KVQ8_OK || direct_out) return rc;
     const size_t out_bytes = (size_t)n_rows * n_q_heads * kv->head_dim * sizeof(float);
-    return cudaMemcpyAsync(h_out, out, out_bytes, cudaMemcpyDeviceToHost, s) == cudaSuccess ? KVQ8_OK
-                                                                                              : KVQ8_ERR_CUDA;
+    return kvq8::launched(cudaMemcpyAsync(h_out, out, out_bytes, cudaMemcpyDeviceToHost, s));
 }
 
 extern "C" int attn_verify_tree_q8(const float* q, int n_rows, int n_q_heads, const kvq8_cache* kv, int kv_len,

@@ -855,8 +855,7 @@ int launch_tc(const VerifyTcParams& vp, dim3 grid, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, verify_tc_kernel<HD, RP, APPEND, TREE, V4>, vp) == cudaSuccess ? KVQ8_OK
-                                                                                                 : KVQ8_ERR_CUDA;
+    return launched(cudaLaunchKernelEx(&cfg, verify_tc_kernel<HD, RP, APPEND, TREE, V4>, vp));
 }
 
 template <int HD, bool APPEND, bool TREE, bool V4 = false>
