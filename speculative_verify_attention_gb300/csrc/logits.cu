@@ -45,14 +45,20 @@ struct AdjustParams {
 __device__ __forceinline__ float repeated(float x, float b, float r) {
     const float q0 = x * r;
     const float q = fmaf(fmaxf(fmaf(-q0, b, x), -FLT_MAX), r, q0);
-    return x > 0.0f ? q : x * b;
+    return x > 0.0f ? q : __fmul_rn(x, b);
+}
+
+// (The functions that round here and below keep products and sums apart, which the compiler could join in one place and not in
+// another: then the rows of a request would differ by their route.)
+__device__ __forceinline__ float penalty_of(int c, float frequency, float presence) {
+    return c > 0 ? __fadd_rn(__fmul_rn(frequency, (float)c), presence) : 0.0f;
 }
 
 // The rare value: one that the row's window tokens raise the count of, or any where b or r is not a normal number.
 __device__ __noinline__ float bend(float x, uint32_t word, int extra, float b, float frequency, float presence, float bias) {
     const int c = (int)(word & ~kInPrompt) + extra;
-    if (c > 0 || word) x = x > 0.0f ? x / b : x * b;
-    return x + (bias - (c > 0 ? frequency * (float)c + presence : 0.0f));
+    if (c > 0 || word) x = x > 0.0f ? __fdiv_rn(x, b) : __fmul_rn(x, b);
+    return __fadd_rn(x, __fsub_rn(bias, penalty_of(c, frequency, presence)));
 }
 
 // Block (chunk of the vocabulary, request, share of its rows): a thread owns the same eight values of every row, so the
@@ -178,7 +184,7 @@ __global__ void __launch_bounds__(kAdjThreads, VEC && sizeof(T) == 4 ? 6 : 8) lo
 #pragma unroll
     for (int i = 0; i < kAdjPer; ++i) {
         const int c = (int)(word[i] & ~kInPrompt);
-        shift[i] = bias[i] - (c > 0 ? frequency * (float)c + presence : 0.0f);
+        shift[i] = __fsub_rn(bias[i], penalty_of(c, frequency, presence));
         if (word[i]) seen |= 1u << i;
         touched |= word[i] || bias[i] != 0.0f;
     }
@@ -210,7 +216,7 @@ __global__ void __launch_bounds__(kAdjThreads, VEC && sizeof(T) == 4 ? 6 : 8) lo
 #pragma unroll
                 for (int i = 0; i < kAdjPer; ++i) {
                     if (seen >> i & 1) y[i] = repeated(y[i], repetition, inverse);
-                    y[i] += shift[i];
+                    y[i] = __fadd_rn(y[i], shift[i]);
                 }
             }
 #pragma unroll
