@@ -455,7 +455,8 @@ int attn_verify_q8_noalloc(const float* q, int n_rows, int n_q_heads, const kvq8
  *                 order; -1 in the rows behind the last
  *   status      : int32 [1]: 0; 1 = too few free pages; 2 = malformed (a length below 0, n_new > lens,
  *                 lens > max_pages * page_size, held outside [0, max_pages], more than n_rows new
- *                 tokens, a ring_state outside its range, or more pages held and free than n_pages)
+ *                 tokens, a ring_state outside its range, or more pages free and given back than
+ *                 n_pages; pages that stay held are not counted)
  * Pages are taken from the ring's head and given back behind its tail in order of request, then of
  * position; a page given back in a call is not taken in the same call.  All or nothing: with a
  * nonzero status held_out and ring_out repeat the inputs, page_table and free_ring are unchanged,

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) paged_tables_kernel(const TablesPara
     }
     const long long rows = before[0], takes = before[1], gives = before[2];
     bad |= rows > p.n_rows;
-    bad |= (long long)count + gives > p.n_pages;  // more pages held and free than there are
+    bad |= (long long)count + gives > p.n_pages;  // the ring has no room for the pages given back
     const bool malformed = __syncthreads_or(bad);
     const int status = malformed ? 2 : takes > count ? 1 : 0;
 
