@@ -517,7 +517,10 @@ size_t attn_verify_paged_q8_workspace_bytes(int n_q_heads, int n_kv_heads, int h
  * codes, but their scales must be finite where they stand before lens.
  * K, V and p enter the tensor cores in fp16 (code * scale rounded once), bf16 q as fp16 times a power
  * of two (one for the rows that a thread block holds); scores, softmax statistics and sums are fp32.
- * Values of the cache must stay inside the fp16 range; rows of one window whose bf16 queries are more
+ * That is 4e-4 of an fp16 output (2-norm, half of it the output's own rounding) and nothing beside the
+ * rounding of a bf16 one; attn_verify_tree_q8 over a contiguous cache is nearer (1.6e-5).  Values of the
+ * cache must stay inside the fp16 range, and scores scale * q . k below 2^24 in size: references are fp32,
+ * and a row far above that may come out as NaN.  Rows of one window whose bf16 queries are more
  * than 2^25 apart in size lose the small ones.  A query that is not a number gives a row of NaN; one that
  * is not finite changes no other row.  The same call gives the same bits.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, n_q_heads / n_kv_heads > 64, max_rows > 64,

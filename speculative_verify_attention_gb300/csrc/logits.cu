@@ -66,7 +66,7 @@ __device__ __noinline__ float bend(float x, uint32_t word, int extra, float b, f
 // tokens are among them (`mine`, one bit a token).  Then the rows stream past, kAdjDepth rows' logits in flight.  No
 // thread reads what another writes, so the output may be the input.
 // Bound by issue: about 180 instructions for a warp's 256 values where every warp has a seen one.  12 requests of 16 to
-// 32 rows over 248320 bf16 logits (451 MB) 98 us, 4.6 TB/s; the same with a division called per seen value 182 us, with
+// 32 rows over 248320 bf16 logits (451 MB) 97 us, 4.7 TB/s; the same with a division called per seen value 182 us, with
 // four rows in flight and 6 blocks of an SM (80 registers) 108 us, with 32 rows a block (fewer prologues, a longer tail)
 // 121 us, with 8 rows 100 us.  Rows of an odd length go by single values: 106299 of them 74 us, and 100 us with 4 blocks of
 // an SM instead of 8.

@@ -4,7 +4,12 @@
 // key ctx + j where bit j of its mask is set (chains: j <= t):
 //   o = sum_n p_n v_n / sum_n p_n,  p_n = exp(scale * q . k_n),  k and v = code * scale of their block.
 // Scores, references, sums and O are fp32; keys, values and weights enter the products as fp16 (code * scale and the weight
-// each rounded once), bf16 queries as fp16 after an exact scaling by a power of two.
+// each rounded once), bf16 queries as fp16 after a scaling by a power of two (exact but for elements 2^25 below the largest
+// that is scaled with them).  Each of the three roundings is off by about 2e-4 of its value, as is that of an fp16 output: 4.1e-4
+// to 4.3e-4 in all, and 1.7e-3 with bf16 outputs, which is those outputs' own rounding.  The calls over one contiguous cache keep
+// pairs of fp16 for K, V and the weights, and fp32 outputs (1.6e-5).  Pairs here would mean every product twice and, in the tile
+// kernels, K^ and V^ twice in tensor and shared memory, which are full; the outputs are 16 bits wide.
+// A row's sum is of its weights as rounded, so that equal values come out as they are.
 //
 // Three kernels, by the T x group rows of the longest window and KV head:
 //   up to 8 (16 at head_dim 128): here, a warp scans for itself on mma.sync;
@@ -36,7 +41,8 @@ template <int HD, int NT>
 struct FL {
     // Warps of a CTA and CTAs of an SM.  At head_dim 128 two CTAs of 6 warps have 168 registers a thread; at 256 that
     // spills, and one CTA of 8 warps has 255.  Measured both ways: 64 requests of 8192 tokens at head_dim 128 151 us
-    // against 171 us, 20 requests of 16000 tokens at head_dim 256 42 us against 33 us.
+    // against 171 us, 20 requests of 16000 tokens at head_dim 256 42 us against 33 us.  (9 to 16 rows at head_dim 128, NT = 2,
+    // spill 52 bytes with bf16 queries and 100 with fp16; all other shapes spill nothing.)
     static constexpr int kWarps = HD == 256 ? 8 : 6, kCtas = HD == 256 ? 1 : 2;
     static constexpr int N = 8 * NT, H = HD / 128;           // rows; 128-dim halves
     static constexpr int kSmO = 0, kSmMl = kWarps * N * HD * 4, kSmBytes = kSmMl + kWarps * N * 8;
@@ -346,8 +352,8 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // The rows of every item that was cut, one after another: o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c over its
 // parts, slot 1 of the CTA that began it and slot 0 of the same place in the later teams.  A row is a warp's, or where there
 // are no more rows than blocks a block's, whose warps share its parts (a long context of few rows has a part per CTA).
-// 16 trees, 9200 rows of two or three parts: the whole call 280 us with a block a row throughout, 254 us so; one chain of 24
-// rows 17.4 and 16.1 us.
+// The whole call with a block a row throughout, with a warp a row throughout, and so: 16 trees, 9200 rows of two or three
+// parts, 215, 193 and 194 us; one chain of 24 rows over 2048 tokens 15.5, 22.3 and 15.1 us, over 20676 28.2, 35.7 and 27.6 us.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedVerifyParams p, int n_ctas) {
     constexpr int V = HD / 128;  // float4 columns of a lane
@@ -477,11 +483,17 @@ struct VerifyPlan {
 };
 
 // With more key tiles (of 64) than this an SM, by the tables' capacity, windows of up to 64 rows go to the streaming kernel: it
-// has a deep ring of fetches but takes longer to start, and its time grows with the rows.  Measured with 24 query and 4 KV
-// heads of 256 dims, streaming and by rows, us:
-//   24 rows: one request of 2048 tokens (1 tile an SM) 25 and 16, 8 of 2048 (7) 40 and 27, 8 of 20676 (68) 74 and 83,
-//            16 of 20676 (136) 106 and 136
-//   48 rows: 30 and 17, 48 and 28, 88 and 85, 125 and 139;  60 rows: 35 and 17, 47 and 28, 92 and 85, 133 and 140
+// has a deep ring of fetches but takes longer to start, and its time grows with the rows.  Requests far shorter than their
+// table's width so get the streaming kernel where the other would be faster: the lengths are on the device, and the choice of a
+// captured call stays.  Measured, streaming and by rows, us (tiles an SM by capacity):
+//   4 KV heads of 256 dims, 6 query heads each: 1 request of 2048 tokens (1), 8 of 2048 (7), 4 of 20676 (34), 8 of 20676 (68), 16 of 20676 (135)
+//     24 rows   24 and 15   37 and 27   53 and 52   72 and 83   104 and 136
+//     48 rows   29 and 16   46 and 28   68 and 57   86 and 85   124 and 138
+//     60 rows   34 and 17   45 and 28   68 and 59   90 and 86   132 and 139
+//   8 KV heads of 128 dims, 4 query heads each: 1 of 2048 (2), 8 of 8192 (53), 4 of 20676 (68), 8 of 20676 (135), 16 of 20676 (270)
+//     24 rows   24 and 18   53 and 53   60 and 63    87 and 108   142 and 196
+//     48 rows   29 and 19   63 and 55   70 and 66   101 and 111   176 and 201
+//     60 rows   34 and 20   72 and 57   78 and 67   115 and 112   200 and 203
 inline int stream_tiles(int rows) { return rows <= 32 ? 40 : 80; }
 
 // The lengths are on the device, so all of this is by the longest window and the capacity.

@@ -13,7 +13,7 @@
 //   4     issues all products; 5: sleeps, and rescales the second group's columns in its lanes when that raises (4 too)
 //   8-15  convert K (8-11) and V: a 32-value block at a time, loaded into registers a tile ahead and asked into L2 a tile
 //         earlier, times its scale and rounded once to fp16, into rings of tiles (128-byte swizzle)
-// Measured: 16 requests of 20676 tokens (24 / 4 heads of 256 dims, 32-row trees, 144 rows a KV head on average) 195 us, of
+// Measured: 16 requests of 20676 tokens (24 / 4 heads of 256 dims, 32-row trees, 144 rows a KV head on average) 194 us, of
 // which 45 us do not depend on the length; without loads 188, without conversion as well 181, with a quarter of O^T's products
 // 185, without the exponentials 191, without any of these 133: what is left is the hand-offs from one role to the next, which
 // one tile of scores a group puts in a row.  24 rows 136 us.

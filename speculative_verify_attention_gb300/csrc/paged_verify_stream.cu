@@ -24,7 +24,7 @@
 //         by its issue: 60-100 ns a copy.)
 // Keys on page ids outside the pool are not fetched.  Those and the rows behind len in a page enter V^ as zeros, and
 // their scores are masked whatever they are.
-// Measured (24 / 4 heads of 256 dims): 8 requests of 32768 tokens, 30 rows 95 us, 3.9 TB/s; every 28672 tokens more cost
+// Measured (24 / 4 heads of 256 dims): 8 requests of 32768 tokens, 30 rows 91 us, 4.1 TB/s; every 28672 tokens more cost
 // 53 us, which is the memory's rate, and 36 us do not depend on the length.
 #include "paged_verify.cuh"
 

@@ -1,5 +1,5 @@
 // tc.cuh -- thin inline-PTX wrappers for sm_100-family tensor memory, tcgen05 MMA,
-// mbarriers and bulk async copies, as used by the prompt kernel.
+// mbarriers and bulk async copies, as used by the prompt kernel and the verify kernels.
 #pragma once
 
 #include <stdint.h>
