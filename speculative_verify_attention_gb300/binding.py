@@ -186,8 +186,8 @@ def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     allocator gives it out again in that stream's order, while the current stream may be far ahead or behind."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        handle = int(stream)
+    if not isinstance(stream, torch.cuda.Stream):  # a handle, or another library's object with one
+        handle = int(getattr(stream, "cuda_stream", stream))
         # 1 is another name of the default stream, 0
         stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
     with torch.cuda.stream(stream):

@@ -34,9 +34,19 @@ def _calls():
             "argmax": lambda s: kv.argmax_rows_top_prob(logits, stream=s)[1]}
 
 
-@pytest.mark.parametrize("raw", [False, True])
+class _Other:
+    """A stream of another library: an object with a handle."""
+
+    def __init__(self, stream):
+        self.cuda_stream = stream.cuda_stream
+
+
+FORMS = {"stream": lambda s: s, "handle": lambda s: s.cuda_stream, "other": _Other}
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("name", ["q8", "tree", "k8v4", "f16", "append", "prompt", "prompt k8v4", "prompt f16", "argmax"])
-def test_memory_is_not_given_out_to_the_current_stream(lib, name, raw, monkeypatch):
+def test_memory_is_not_given_out_to_the_current_stream(lib, name, form, monkeypatch):
     from speculative_verify_attention_gb300 import binding
     call, side = _calls()[name], torch.cuda.Stream()
     want = call(None)
@@ -45,7 +55,7 @@ def test_memory_is_not_given_out_to_the_current_stream(lib, name, raw, monkeypat
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
         torch.cuda._sleep(CYCLES)
-    out = call(side.cuda_stream if raw else side)
+    out = call(FORMS[form](side))
     at, size = {t.data_ptr() for t in taken} | {out.data_ptr()}, taken[0].numel()
     taken.clear()  # the call has returned and holds nothing
     assert torch.empty(size, dtype=torch.uint8, device="cuda").data_ptr() not in at
