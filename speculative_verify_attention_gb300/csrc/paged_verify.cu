@@ -8,7 +8,7 @@
 // that is scaled with them).  Each of the three roundings is off by about 2e-4 of its value, as is that of an fp16 output: 4.1e-4
 // to 4.3e-4 in all, and 1.7e-3 with bf16 outputs, which is those outputs' own rounding.  The calls over one contiguous cache keep
 // pairs of fp16 for K, V and the weights, and fp32 outputs (1.6e-5).  Pairs here would mean every product twice and, in the tile
-// kernels, K^ and V^ twice in tensor and shared memory, which are full; the outputs are 16 bits wide.
+// kernels, V^ twice in shared memory, which has no room for it at head_dim 256; the outputs are 16 bits wide.
 // A row's sum is of its weights as rounded, so that equal values come out as they are.
 //
 // Three kernels, by the T x group rows of the longest window and KV head:
