@@ -583,6 +583,145 @@ int token_counts(const int32_t* tokens, const int32_t* token_starts, int n_lists
                  int vocab, kvq8_stream_t stream);
 
 /*
+ * ---- Beams, trees and rotary positions ---------------------------------------------------------
+ * What stands around the calls above in a step that rotates its keys, searches with beams or verifies trees:
+ *   kvq8_paged_append_rope (in place of kvq8_paged_append, and of the rotation before it); behind the logits beam_select, then
+ *   token_counts_fork and kvq8_paged_fork let the beams' counts and pages follow, and kvq8_paged_copy copies, in every layer's
+ *   cache, the pages that could not be shared; kvq8_paged_compact moves the accepted path of a tree together.
+ * A sequence is what has a row of a page table: a request, or one of its beams.  Like the calls above these neither
+ * synchronise nor read a length on the host, and can be captured into graphs.
+ */
+
+/* Bytes of workspace beam_select needs (0: unsupported sizes). */
+size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs, int n_out);
+
+/*
+ * beam_select -- the n_out best continuations of every request, over all of its beams and the vocabulary.
+ *   logits  : [n_rows][vocab] of `dtype`, logits_stride elements between rows: a row a beam; request b has the rows
+ *             row_starts[b] .. row_starts[b + 1] - 1 (int32 [n_seqs + 1], ascending), 64 at most
+ *   scores  : fp32 [n_rows] or null (zeros): the beams' totals so far
+ *   weights : fp32 [n_rows] or null (ones): positive factors by which totals are compared, 1 / length^a for instance
+ *   ended   : int32 [n_rows] or null: a row with ended[r] >= 0 has come to its end; its logits are not read, and its only
+ *             continuation is itself, with the token ended[r] and the total scores[r]
+ *   n_out   : 1 .. 64
+ *   parents, tokens, totals : int32, int32, fp32 [n_seqs][n_out], best first: row, token and total of each; where a request has
+ *             fewer, -1, -1 and -inf
+ *   workspace : beam_select_workspace_bytes(...) bytes, 16-byte aligned; calls that may overlap need one each
+ * total = scores[r] + (x - log sum exp x) over the row's logits x, the sum to about 1e-8 of itself, the rest in 64 bits; continuations
+ * are ordered by weight * total in 64 bits, equal ones of different rows by row, those of a row by logit, then by token (-0 equals 0).
+ * A logit of -inf is no continuation.  A row with a NaN or +inf among its logits, a score that is not finite or a weight that is
+ * not positive and finite has none.  Requests without rows, with more than 64 or outside [0, n_rows) get -1; rows of no request are
+ * not read for any.  The same call gives the same bits.
+ * Errors: INVALID_ARG, UNSUPPORTED (n_rows > 65535, vocab > 2^30, n_seqs > 4096, n_out > 64), WORKSPACE, MISALIGNED (element size;
+ * workspace 16).  Two launches.
+ */
+int beam_select(const void* logits, int dtype, int64_t logits_stride, int n_rows, int vocab, const int32_t* row_starts,
+                int n_seqs, const float* scores, const float* weights, const int32_t* ended, int n_out, int32_t* parents,
+                int32_t* tokens, float* totals, void* workspace, size_t workspace_bytes, kvq8_stream_t stream);
+
+/* Bytes of workspace token_counts_fork needs (0: unsupported sizes). */
+size_t token_counts_fork_workspace_bytes(int n_children);
+
+/*
+ * token_counts_fork -- the counts rows of n_children sequences that go on from n_seqs ones.
+ *   parents  : int32 [n_children]: the sequence that child i goes on from; < 0: there is no child i
+ *   state_of : int32 [n_seqs] or null (row q): the counts row of each sequence; outside [0, n_states): none, and its children
+ *              have none
+ *   state_of_out : int32 [n_children]: the children's rows (-1: none); may be state_of
+ *   status   : int32 [1]: 0; 1 = too few rows; 2 = malformed (a parent >= n_seqs, or two sequences of one row that both have
+ *              children)
+ * The first child of a sequence, the one of the lowest number, keeps its row; the others get copies of it, in the order of their
+ * numbers in the lowest rows that no first child keeps.  So every row of `counts` belongs to one of the call's sequences or to
+ * nobody.  With a nonzero status no row changes and every state_of_out is -1.  (token_counts then adds the children's tokens.)
+ * Errors: INVALID_ARG (state_of_out over parents or part of state_of as well), UNSUPPORTED (n_children or n_seqs > 4096, n_states > 65536,
+ * vocab > 2^30), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  Two launches.
+ */
+int token_counts_fork(const int32_t* parents, int n_children, const int32_t* state_of, int n_seqs, uint32_t* counts,
+                      int n_states, int vocab, int32_t* state_of_out, int32_t* status, void* workspace,
+                      size_t workspace_bytes, kvq8_stream_t stream);
+
+/* Bytes of workspace kvq8_paged_fork needs (0: unsupported sizes). */
+size_t kvq8_paged_fork_workspace_bytes(int n_seqs, int n_children, int n_pages);
+
+/*
+ * kvq8_paged_fork -- the pages of n_children sequences that go on from n_seqs ones: forks, reorders, cuts short and ends.
+ *   parents  : int32 [n_children]: the sequence that child i goes on from; < 0: there is no child i.  A sequence without
+ *              children ends.
+ *   lens, held : int32 [n_seqs]: the tokens of each sequence that its children take over, and the pages it holds
+ *   page_table : int32 [n_seqs][max_pages]; shares: int32 [n_pages], how many sequences hold a page beyond the first (0 where
+ *              one holds it, and where nobody does); free_ring, ring_state as in kvq8_paged_tables
+ *   page_table_out : int32 [n_children][max_pages]: entries before held_out are filled, others left alone
+ *   lens_out, held_out : int32 [n_children], ceil(lens_out / page_size) pages; 0 where there is no child
+ *   shares_out, ring_out : after the call; may be shares and ring_state themselves
+ *   copy_src, copy_dst, copy_rows : int32 [n_children], for kvq8_paged_copy: pages to copy from and to and how many of their
+ *              rows; -1, -1, 0 where a child copies nothing
+ *   status   : int32 [1]: 0; 1 = too few free pages; 2 = malformed (a parent >= n_seqs, held outside [0, max_pages], a parent's lens
+ *              outside [0, held * page_size], a ring_state outside its range)
+ * Children share their parent's full pages.  A last page that is not full goes to the first child (of the lowest number) if no other
+ * sequence holds it; every other child takes a free page, in the order of their numbers from the ring's head, and a place in the
+ * copy list.  Pages that nobody holds any more go back behind the ring's tail, ascending; one given back in a call is not taken in it,
+ * so the copies may be made until the next call of kvq8_paged_tables or kvq8_paged_fork.
+ * With a nonzero status nothing changes: held_out and lens_out are 0, the copy list is empty, ring_out and shares_out repeat their inputs.
+ * Page ids outside [0, n_pages) are passed on and not counted.  A shares or a ring that does not agree with the tables is not
+ * noticed; the results then are no better, but nothing outside the arrays is touched.
+ * kvq8_paged_tables takes pages for growing sequences as before (a fresh page's share is 0, and a sequence grows only in pages of its
+ * own).  It gives pages back whoever shares them: sequences with shared pages are cut short and ended by this call.
+ * Errors: INVALID_ARG (outputs over the sequences' inputs as well), UNSUPPORTED (n_seqs or n_children > 4096, page_size, n_pages > 2^30, max_pages
+ * > 2^24), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  Two launches.
+ */
+int kvq8_paged_fork(const int32_t* parents, int n_children, const int32_t* lens, const int32_t* held, int n_seqs,
+                    int page_size, const int32_t* page_table, int max_pages, const int32_t* shares, int32_t* free_ring,
+                    int n_pages, const int32_t* ring_state, int32_t* page_table_out, int32_t* lens_out, int32_t* held_out,
+                    int32_t* shares_out, int32_t* ring_out, int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows,
+                    int32_t* status, void* workspace, size_t workspace_bytes, kvq8_stream_t stream);
+
+/*
+ * kvq8_paged_copy -- the first rows[i] rows (null: all) of every head of page src_pages[i] to page dst_pages[i], K and V, codes
+ * and scales, for i < n; one launch.  int32 [n], device.  An entry with a page outside [0, n_pages), or the same page twice, does
+ * nothing.  No page may be written by one entry and read or written by another.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED (the cache as for kvq8_paged_append; lists 4 bytes).
+ */
+int kvq8_paged_copy(const kvq8_paged_cache* kv, const int32_t* src_pages, const int32_t* dst_pages, const int32_t* rows,
+                    int n, kvq8_stream_t stream);
+
+/*
+ * kvq8_paged_compact -- keep some rows of every request's window and move them together, in their order, to its first places:
+ * the accepted path of a tree, whose tokens a step appended behind the context.  One launch.
+ *   page_table, lens, row_starts as in attn_verify_paged_q8: request b's window of T <= 64 rows are its last T tokens
+ *   kept     : uint64 [n_seqs], bit j = place j of the window is kept (bits from T on are ignored; a row's window_mask word is
+ *              its path)
+ *   lens_out : int32 [n_seqs] or null, not lens: lens - T + rows kept
+ * Places behind the kept ones hold what they held or a moved row's old copy.  Rows from or to a page outside [0, n_pages) do not move.
+ * A malformed request (T outside [0, 64], T > lens, lens > max_pages * page_size) is left as it is.  The pages of a window belong
+ * to one request.
+ * Errors: INVALID_ARG, UNSUPPORTED (n_seqs > 4096, the cache), MISALIGNED (4 bytes; kept 8).
+ */
+int kvq8_paged_compact(const kvq8_paged_cache* kv, const int32_t* page_table, int max_pages, const int32_t* lens,
+                       const int32_t* row_starts, int n_seqs, const uint64_t* kept, int32_t* lens_out, kvq8_stream_t stream);
+
+/*
+ * kvq8_paged_append_rope -- kvq8_paged_append of keys that are rotated on the way, and the queries rotated with them, one launch.
+ *   q, k, v  : [n_tok][n_q_heads or n_kv_heads][head_dim] of `dtype`, strides as for kvq8_paged_append (elements between tokens, a
+ *              multiple of 16 bytes)
+ *   positions : int32 [n_axes][n_tok], n_axes 1 .. 4 (time, height and width of an image's patches, for instance)
+ *   turns    : uint64 [rot_dim / 2]: pair i's frequency, in 2^-64 turns a position: frequency / (2 pi) * 2^64 modulo 2^64
+ *   axis_of  : int32 [rot_dim / 2] or null (axis 0): the axis whose position turns pair i; outside [0, n_axes) it does not turn
+ *   rot_dim  : the first rot_dim dims of a head are rotated, a multiple of 64; the others pass as they are
+ *   pairs    : 0: pair i is dims i and i + rot_dim / 2; else 2 i and 2 i + 1.  (a, b) becomes (a cos - b sin, b cos + a sin)
+ *   slots    : int64 [n_tok] as for kvq8_paged_append; a token whose slot lies outside the cache is left alone, its row of q_out too
+ *   q_out    : as q, out_stride elements between tokens; may be q itself (equal strides).  Rows of it that share bytes with rows of
+ *              q in any other way, or of k or v, are refused
+ * Angles are exact modulo a turn to 2^-32 of it at any position (an int32), their sines and cosines fp32 (3e-7), products and sums fp32; q_out
+ * is rounded once, and the rotated keys are quantised from fp32, as kvq8_append would, without a rounding in between.
+ * Errors: INVALID_ARG, UNSUPPORTED (the cache, rot_dim, n_axes > 4, n_q_heads > 65536), MISALIGNED (16 bytes; slots and turns 8,
+ * positions and axis_of 4).
+ */
+int kvq8_paged_append_rope(const void* q, const void* k, const void* v, int dtype, int n_tok, int n_q_heads,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* positions, int n_axes,
+                           const uint64_t* turns, const int32_t* axis_of, int rot_dim, int pairs, const kvq8_paged_cache* kv,
+                           const int64_t* slots, void* q_out, int64_t out_stride, kvq8_stream_t stream);
+
+/*
  * kvq8_selftest_convert -- a self-test hook: runs the code -> fp16 conversions that the verify
  * and prompt kernels use, unchanged, on caller data, so that a test can check them exhaustively.
  *   kind 0: in[i] = 4 int8 codes; out[2i], out[2i+1] = fp16 pairs of codes (0, 1) and (2, 3)

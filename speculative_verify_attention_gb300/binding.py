@@ -35,7 +35,10 @@ EXPORTED = ("kvq8_quantize", "kvq8_append", "attn_verify_q8_workspace_bytes", "a
             "attn_prompt_q8_workspace_bytes", "attn_prompt_q8", "attn_verify_q8_noalloc", "kvq8_device_error", "kvq8_status_str",
             "argmax_rows_top_prob_workspace_bytes", "argmax_rows_top_prob", "kvq8_selftest_convert",
             "kvq8_selftest_wait_timeout", "kvq8_paged_tables", "kvq8_paged_append", "kvq8_paged_read",
-            "attn_verify_paged_q8_workspace_bytes", "attn_verify_paged_q8", "logits_adjust", "token_counts")
+            "attn_verify_paged_q8_workspace_bytes", "attn_verify_paged_q8", "logits_adjust", "token_counts",
+            "beam_select_workspace_bytes", "beam_select", "token_counts_fork_workspace_bytes", "token_counts_fork",
+            "kvq8_paged_fork_workspace_bytes", "kvq8_paged_fork", "kvq8_paged_copy", "kvq8_paged_compact",
+            "kvq8_paged_append_rope")
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024
 
 
@@ -157,6 +160,24 @@ def load_library():
         lib.logits_adjust.restype = i32
         lib.token_counts.argtypes = [vp, vp, i32, i32, vp, vp, i32, vp, i32, i32, vp]
         lib.token_counts.restype = i32
+        lib.beam_select_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.beam_select_workspace_bytes.restype = sz
+        lib.beam_select.argtypes = [vp, i32, i64, i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]
+        lib.beam_select.restype = i32
+        lib.token_counts_fork_workspace_bytes.argtypes = [i32]
+        lib.token_counts_fork_workspace_bytes.restype = sz
+        lib.token_counts_fork.argtypes = [vp, i32, vp, i32, vp, i32, i32, vp, vp, vp, sz, vp]
+        lib.token_counts_fork.restype = i32
+        lib.kvq8_paged_fork_workspace_bytes.argtypes = [i32, i32, i32]
+        lib.kvq8_paged_fork_workspace_bytes.restype = sz
+        lib.kvq8_paged_fork.argtypes = [vp, i32, vp, vp, i32, i32, vp, i32, vp, vp, i32, vp] + [vp] * 10 + [sz, vp]
+        lib.kvq8_paged_fork.restype = i32
+        lib.kvq8_paged_copy.argtypes = [cpg, vp, vp, vp, i32, vp]
+        lib.kvq8_paged_copy.restype = i32
+        lib.kvq8_paged_compact.argtypes = [cpg, vp, i32, vp, vp, i32, vp, vp, vp]
+        lib.kvq8_paged_compact.restype = i32
+        lib.kvq8_paged_append_rope.argtypes = [vp, vp, vp, i32, i32, i32, i64, i64, i64, vp, i32, vp, vp, i32, i32, cpg, vp, vp, i64, vp]
+        lib.kvq8_paged_append_rope.restype = i32
         lib.kvq8_device_error.argtypes = [i32]
         lib.kvq8_device_error.restype = i32
         lib.kvq8_status_str.argtypes = [i32]
@@ -910,3 +931,177 @@ def token_counts(tokens: torch.Tensor, token_starts: torch.Tensor, counts: torch
         _addr(counts, "counts", i32, tuple(counts.shape), dev), counts.shape[0], counts.shape[1], _launch_on(dev, stream))
     _check("token_counts", st)
     return counts
+
+
+# ---------------------------------------------------------------- beams, trees and rotary positions
+
+def _space(workspace, nbytes: int, device: torch.device, index: int, stream) -> torch.Tensor:
+    if workspace is None:
+        return _scratch(max(nbytes, 16), device, stream)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def beam_select_workspace_bytes(n_rows: int, vocab: int, n_seqs: int, n_out: int) -> int:
+    return int((_lib or load_library()).beam_select_workspace_bytes(n_rows, vocab, n_seqs, n_out))
+
+
+def beam_select(logits: torch.Tensor, row_starts: torch.Tensor, n_out: int, scores: torch.Tensor | None = None,
+                weights: torch.Tensor | None = None, ended: torch.Tensor | None = None, parents: torch.Tensor | None = None,
+                tokens: torch.Tensor | None = None, totals: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                stream=None):
+    """The n_out best continuations of every request over its beams, rows of logits [n_rows][V] (fp32, fp16 or bf16; rows may be
+    strided) between row_starts int32 [n + 1], and the vocabulary: by weights (fp32 [n_rows]) times scores (fp32 [n_rows]) + log
+    softmax; rows with ended int32 [n_rows] >= 0 go on as they are.  Returns (parents int32, tokens int32, totals fp32), [n][n_out]
+    each, best first; -1, -1, -inf where a request has fewer."""
+    dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
+    if logits.dim() != 2 or logits.dtype not in _DTYPE or logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("logits must be [n_rows][V] of float32, float16 or bfloat16 with contiguous rows")
+    rows, vocab = logits.shape
+    n, n_out = row_starts.shape[0] - 1, int(n_out)
+    lib = _lib or load_library()
+    raw, shape = _launch_on(dev, stream), (n, n_out)
+    parents = _empty(shape, i32, logits.device, stream) if parents is None else parents
+    tokens = _empty(shape, i32, logits.device, stream) if tokens is None else tokens
+    totals = _empty(shape, f32, logits.device, stream) if totals is None else totals
+    workspace = _space(workspace, lib.beam_select_workspace_bytes(rows, vocab, n, n_out), logits.device, dev, stream)
+    st = lib.beam_select(
+        logits.data_ptr(), _DTYPE[logits.dtype], logits.stride(0) if rows > 1 else vocab, rows, vocab,
+        _addr(row_starts, "row_starts", i32, (n + 1,), dev), n, _maybe(scores, "scores", f32, (rows,), dev),
+        _maybe(weights, "weights", f32, (rows,), dev), _maybe(ended, "ended", i32, (rows,), dev), n_out,
+        _addr(parents, "parents", i32, shape, dev), _addr(tokens, "tokens", i32, shape, dev), _addr(totals, "totals", f32, shape, dev),
+        workspace.data_ptr(), workspace.nbytes, raw)
+    _check("beam_select", st)
+    return parents, tokens, totals
+
+
+def token_counts_fork_workspace_bytes(n_children: int) -> int:
+    return int((_lib or load_library()).token_counts_fork_workspace_bytes(n_children))
+
+
+def token_counts_fork(parents: torch.Tensor, state_of: torch.Tensor | None, counts: torch.Tensor, state_of_out: torch.Tensor,
+                      status: torch.Tensor, n_seqs: int | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Counts rows (counts int32 [n_states][V], updated) for the sequences that go on from others: int32 parents [m] (< 0: none) and
+    state_of [n] (None: sequence q has row q, of n_seqs); outputs state_of_out int32 [m], which may be state_of, and status int32 [1]."""
+    dev, i32 = counts.get_device(), torch.int32
+    if counts.dim() != 2 or parents.dim() != 1:
+        raise ValueError("counts must be [n_states][V] and parents [n_children]")
+    m = parents.shape[0]
+    n = state_of.shape[0] if state_of is not None else counts.shape[0] if n_seqs is None else int(n_seqs)
+    lib = _lib or load_library()
+    raw = _launch_on(dev, stream)
+    workspace = _space(workspace, lib.token_counts_fork_workspace_bytes(m), counts.device, dev, stream)
+    st = lib.token_counts_fork(
+        _addr(parents, "parents", i32, (m,), dev), m, _maybe(state_of, "state_of", i32, (n,), dev), n,
+        _addr(counts, "counts", i32, tuple(counts.shape), dev), counts.shape[0], counts.shape[1],
+        _addr(state_of_out, "state_of_out", i32, (m,), dev), _addr(status, "status", i32, (1,), dev), workspace.data_ptr(),
+        workspace.nbytes, raw)
+    _check("token_counts_fork", st)
+
+
+def kvq8_paged_fork_workspace_bytes(n_seqs: int, n_children: int, n_pages: int) -> int:
+    return int((_lib or load_library()).kvq8_paged_fork_workspace_bytes(n_seqs, n_children, n_pages))
+
+
+def kvq8_paged_fork(parents: torch.Tensor, lens: torch.Tensor, held: torch.Tensor, page_size: int, page_table: torch.Tensor,
+                    shares: torch.Tensor, free_ring: torch.Tensor, ring_state: torch.Tensor, page_table_out: torch.Tensor,
+                    lens_out: torch.Tensor, held_out: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
+                    copy_rows: torch.Tensor, status: torch.Tensor, shares_out: torch.Tensor | None = None,
+                    ring_out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Pages for the m sequences that go on from n others: int32 parents [m] (< 0: none), lens and held [n], page_table [n][max_pages],
+    shares [n_pages] (holders beyond the first), free_ring [n_pages] (updated), ring_state [2]; outputs page_table_out
+    [m][max_pages], lens_out, held_out, the copy list copy_src, copy_dst, copy_rows [m] for kvq8_paged_copy, and status [1].  shares and
+    ring_state are updated in place unless shares_out / ring_out are given."""
+    dev, i32 = page_table.get_device(), torch.int32
+    if page_table.dim() != 2 or free_ring.dim() != 1 or parents.dim() != 1:
+        raise ValueError("page_table must be [n][max_pages], free_ring [n_pages] and parents [n_children]")
+    m, (n, mp), n_pages = parents.shape[0], page_table.shape, free_ring.shape[0]
+    lib = _lib or load_library()
+    raw = _launch_on(dev, stream)
+    workspace = _space(workspace, lib.kvq8_paged_fork_workspace_bytes(n, m, n_pages), page_table.device, dev, stream)
+    st = lib.kvq8_paged_fork(
+        _addr(parents, "parents", i32, (m,), dev), m, _addr(lens, "lens", i32, (n,), dev), _addr(held, "held", i32, (n,), dev), n,
+        int(page_size), _addr(page_table, "page_table", i32, (n, mp), dev), mp, _addr(shares, "shares", i32, (n_pages,), dev),
+        _addr(free_ring, "free_ring", i32, (n_pages,), dev), n_pages, _addr(ring_state, "ring_state", i32, (2,), dev),
+        _addr(page_table_out, "page_table_out", i32, (m, mp), dev), _addr(lens_out, "lens_out", i32, (m,), dev),
+        _addr(held_out, "held_out", i32, (m,), dev), _addr(shares if shares_out is None else shares_out, "shares_out", i32, (n_pages,), dev),
+        _addr(ring_state if ring_out is None else ring_out, "ring_out", i32, (2,), dev), _addr(copy_src, "copy_src", i32, (m,), dev),
+        _addr(copy_dst, "copy_dst", i32, (m,), dev), _addr(copy_rows, "copy_rows", i32, (m,), dev), _addr(status, "status", i32, (1,), dev),
+        workspace.data_ptr(), workspace.nbytes, raw)
+    _check("kvq8_paged_fork", st)
+
+
+def kvq8_paged_copy(cache: KVPagedCacheQ8, src_pages: torch.Tensor, dst_pages: torch.Tensor, rows: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Copy the first rows (int32 [n]; None: all) of pages src_pages to pages dst_pages (int32 [n]; -1: nothing), K and V."""
+    n, dev = src_pages.shape[0], cache._index
+    st = (_lib or load_library()).kvq8_paged_copy(
+        cache._struct, _addr(src_pages, "src_pages", torch.int32, (n,), dev), _addr(dst_pages, "dst_pages", torch.int32, (n,), dev),
+        _maybe(rows, "rows", torch.int32, (n,), dev), n, _launch_on(dev, stream))
+    _check("kvq8_paged_copy", st)
+
+
+def kvq8_paged_compact(cache: KVPagedCacheQ8, page_table: torch.Tensor, lens: torch.Tensor, row_starts: torch.Tensor,
+                       kept: torch.Tensor, lens_out: torch.Tensor | None = None, stream=None) -> None:
+    """Move the kept rows of every request's window (kept int64 [n], bit j = place j) together to its first places; page_table int32
+    [n][max_pages], lens int32 [n], row_starts int32 [n + 1].  lens_out int32 [n]: the lengths afterwards."""
+    dev, i32 = cache._index, torch.int32
+    n, mp = page_table.shape
+    st = (_lib or load_library()).kvq8_paged_compact(
+        cache._struct, _addr(page_table, "page_table", i32, (n, mp), dev), mp, _addr(lens, "lens", i32, (n,), dev),
+        _addr(row_starts, "row_starts", i32, (n + 1,), dev), n, _addr(kept, "kept", torch.int64, (n,), dev),
+        _maybe(lens_out, "lens_out", i32, (n,), dev), _launch_on(dev, stream))
+    _check("kvq8_paged_compact", st)
+
+
+# 1 / (2 pi) * 2^256, rounded down: a frequency is at most a few radians a position, so 256 bits leave none of 2^-64 turns out.
+_TURN = 18428883373056725475459024596439793651824491331936921676307065986443608256856
+
+
+def rope_turns(frequencies: torch.Tensor) -> torch.Tensor:
+    """The table `turns` of kvq8_paged_append_rope (int64, the bits of uint64) of frequencies [rot_dim / 2] in radians a position:
+    each to the nearest 2^-64 of a turn.  Made once, on the host, and put where the frequencies are."""
+    turns = []
+    for f in frequencies.double().cpu().tolist():
+        if f != f or f in (float("inf"), float("-inf")):
+            raise ValueError("frequencies must be finite")
+        num, den = f.as_integer_ratio()
+        bits = ((2 * num * _TURN // (den << 192)) + 1) // 2 % (1 << 64)
+        turns.append(bits - (1 << 64) if bits >> 63 else bits)
+    return torch.tensor(turns, dtype=torch.int64).to(frequencies.device)
+
+
+def kvq8_paged_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: KVPagedCacheQ8, slots: torch.Tensor,
+                           positions: torch.Tensor, turns: torch.Tensor, axis_of: torch.Tensor | None = None, pairs: bool = False,
+                           q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotate q [n_tok][Hq][hd] and k [n_tok][Hkv][hd] by positions int32 [n_tok] or [n_axes][n_tok] and quantise the keys and v into
+    the cache at int64 slots [n_tok] (fp32, fp16 or bf16; tokens may be strided).  turns: rope_turns of the frequencies, [rot_dim / 2];
+    axis_of int32 [rot_dim / 2]: the axis of each pair; pairs: dims 2i and 2i + 1 turn together, else i and i + rot_dim / 2.  Returns
+    q_out (q_out=q works in place); tokens whose slot is outside the cache are left alone."""
+    dev, i32 = cache._index, torch.int32
+    if q.dim() != 3 or q.dtype not in _DTYPE or q.get_device() != dev or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be float32, float16 or bfloat16 [n_tok][n_q_heads][{cache.head_dim}] on {cache.device}")
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or k.shape != v.shape or k.shape[0] != q.shape[0]:
+        raise ValueError("q, k and v must have one type and one number of tokens")
+    n, hq, hd = q.shape
+    ks, vs = _token_stride(k, "k", cache), _token_stride(v, "v", cache)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if turns.dim() != 1:
+        raise ValueError("turns must be [rot_dim / 2]")
+    half = turns.shape[0]
+    raw = _launch_on(dev, stream)
+    if q_out is None:
+        q_out = _empty((n, hq, hd), q.dtype, q.device, stream)
+    strides = []
+    for t, name in ((q, "q"), (q_out, "q_out")):
+        if t.shape != q.shape or t.dtype is not q.dtype or t.get_device() != dev or t.stride(2) != 1 or (t.stride(1) != hd and hq > 1):
+            raise ValueError(f"{name} must be {q.dtype} {tuple(q.shape)} on {cache.device}, the heads of a token contiguous")
+        strides.append(t.stride(0) if n > 1 else hq * hd)
+    st = (_lib or load_library()).kvq8_paged_append_rope(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[q.dtype], n, hq, strides[0], ks, vs,
+        _addr(positions, "positions", i32, (n,) if positions.dim() == 1 else (axes, n), dev), axes,
+        _addr(turns, "turns", torch.int64, (half,), dev), _maybe(axis_of, "axis_of", i32, (half,), dev), 2 * half, 1 if pairs else 0,
+        cache._struct, _addr(slots, "slots", torch.int64, (n,), dev), q_out.data_ptr(), strides[1], raw)
+    _check("kvq8_paged_append_rope", st)
+    return q_out

@@ -1,0 +1,458 @@
+// beam_fork.cu -- what a sequence holds follows the beams that were chosen: its row of token counts (token_counts_fork) and
+// its pages (kvq8_paged_fork).
+//
+// parents[i] is the sequence that child i goes on from (< 0: there is no child i).  A sequence's first child, the one of the
+// lowest number, takes over what cannot be shared; the others get copies.  Both calls plan in one block (counts of children,
+// first children by an atomic minimum, exclusive sums over the children: results do not depend on the order of execution) and
+// then spread the work.
+#include "paged.cuh"
+
+namespace kvq8 {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxStates = 65536;
+
+// Exclusive sum of one value a thread, and the total.
+__device__ __forceinline__ int block_sums(int v, int* s_warp, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        int w = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += up;
+        }
+        s_warp[lane] = w;
+    }
+    __syncthreads();
+    total = s_warp[31];
+    return inc - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// s_first[q]: q's first child (n_children where it has none), s_kids[q]: how many.  True if a parent is out of range.
+__device__ __forceinline__ bool families(const int32_t* parents, int n_children, int n_seqs, int* s_first, int* s_kids) {
+    for (int q = threadIdx.x; q < n_seqs; q += kPlanThreads) s_first[q] = n_children, s_kids[q] = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int i = threadIdx.x; i < n_children; i += kPlanThreads) {
+        const int q = parents[i];
+        if (q >= n_seqs) bad = true;
+        if (q < 0 || q >= n_seqs) continue;
+        atomicMin(s_first + q, i);
+        atomicAdd(s_kids + q, 1);
+    }
+    return __syncthreads_or(bad);
+}
+
+// ---------------------------------------------------------------- counts
+
+struct CountsFork {
+    const int32_t* parents;
+    const int32_t* state_of;
+    int32_t* state_of_out;
+    uint32_t* counts;
+    int32_t* status;
+    int2* copies;   // workspace [n_children]: rows from and to, -1 where the child copies nothing
+    int n_children, n_seqs, n_states, vocab;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) counts_fork_plan_kernel(const __grid_constant__ CountsFork p) {
+    extern __shared__ int sm[];
+    int* s_first = sm;
+    int* s_kids = s_first + p.n_seqs;
+    int* s_state = s_kids + p.n_seqs;                                    // the sequences' rows: state_of_out may be state_of
+    const int n_words = (p.n_states + 31) / 32;
+    uint32_t* s_kept = reinterpret_cast<uint32_t*>(s_state + p.n_seqs);  // [n_words] rows that a first child keeps
+    int* s_free = reinterpret_cast<int*>(s_kept + n_words);              // [n_words] unkept rows before the word
+    __shared__ int s_warp[32];
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int w = tid; w < n_words; w += kPlanThreads) s_kept[w] = 0u;
+    bool bad = families(p.parents, p.n_children, p.n_seqs, s_first, s_kids);
+    for (int q = tid; q < p.n_seqs; q += kPlanThreads) {
+        int st = p.state_of ? p.state_of[q] : q;
+        if (st < 0 || st >= p.n_states) st = -1;
+        s_state[q] = st;
+        // two sequences that are both gone on from cannot have the same row
+        if (st >= 0 && s_kids[q]) bad |= (atomicOr(s_kept + (st >> 5), 1u << (st & 31)) >> (st & 31)) & 1u;
+    }
+    bad = __syncthreads_or(bad);
+    int free_rows = 0;
+    for (int w0 = 0; w0 < n_words; w0 += kPlanThreads) {
+        const int w = w0 + tid;
+        const int rows = w < n_words ? min(32, p.n_states - 32 * w) : 0;
+        const int here = rows > 0 ? rows - __popc(s_kept[w]) : 0;
+        int total;
+        const int before = block_sums(here, s_warp, total);
+        if (w < n_words) s_free[w] = free_rows + before;
+        free_rows += total;
+    }
+    __syncthreads();
+    int copies = 0;
+    for (int i0 = 0; i0 < p.n_children; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int from = -1, state = -1;
+        bool copy = false;
+        if (i < p.n_children) {
+            const int q = p.parents[i];
+            if (q >= 0 && q < p.n_seqs) {
+                state = from = s_state[q];
+                copy = from >= 0 && s_first[q] != i;
+            }
+        }
+        int total;
+        const int k = copies + block_sums(copy, s_warp, total);
+        copies += total;
+        if (copy) {
+            state = -1;
+            if (k < free_rows) {  // the k-th row that nobody keeps
+                int lo = 0, hi = n_words;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_free[mid] <= k)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                state = 32 * lo + (int)__fns(~s_kept[lo], 0, k - s_free[lo] + 1);
+            }
+        }
+        if (i < p.n_children) {
+            p.copies[i] = copy ? make_int2(from, state) : make_int2(-1, -1);
+            p.state_of_out[i] = state;
+        }
+    }
+    const int status = bad ? 2 : copies > free_rows ? 1 : 0;
+    if (status) {  // nothing moves
+        __syncthreads();
+        for (int i = tid; i < p.n_children; i += kPlanThreads) {
+            p.copies[i] = make_int2(-1, -1);
+            p.state_of_out[i] = -1;
+        }
+    }
+    if (tid == 0) p.status[0] = status;
+}
+
+constexpr int kRowThreads = 256;
+constexpr int kRowPer = 4;  // accesses of a thread in flight
+
+// Block (chunk of a row, child).  A row that is copied from is kept by its first child, and one copied to is kept by nobody, so
+// no block reads what another writes.
+template <typename V>
+__global__ void __launch_bounds__(kRowThreads) counts_copy_kernel(const __grid_constant__ CountsFork p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int2 c = p.copies[blockIdx.y];
+    if (c.x < 0) return;
+    const int n = p.vocab / (int)(sizeof(V) / 4);
+    const V* src = reinterpret_cast<const V*>(p.counts + (int64_t)c.x * p.vocab);
+    V* dst = reinterpret_cast<V*>(p.counts + (int64_t)c.y * p.vocab);
+    const int i0 = blockIdx.x * kRowThreads * kRowPer + threadIdx.x;
+    V v[kRowPer];
+#pragma unroll
+    for (int k = 0; k < kRowPer; ++k)
+        if (i0 + k * kRowThreads < n) v[k] = src[i0 + k * kRowThreads];
+#pragma unroll
+    for (int k = 0; k < kRowPer; ++k)
+        if (i0 + k * kRowThreads < n) dst[i0 + k * kRowThreads] = v[k];
+}
+
+// ---------------------------------------------------------------- pages
+
+struct PagedFork {
+    const int32_t* parents;
+    const int32_t* lens;
+    const int32_t* held;
+    const int32_t* table;
+    const int32_t* shares;
+    const int32_t* ring_state;
+    int32_t* ring;
+    int32_t* table_out;
+    int32_t* lens_out;
+    int32_t* held_out;
+    int32_t* shares_out;
+    int32_t* ring_out;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* copy_rows;
+    int32_t* status;
+    // workspace
+    int32_t* take;      // [n_children] the fresh page of a child, -1: none
+    int32_t* holders;   // [n_seqs] children, and bit 30: the first one goes on in the last page
+    uint32_t* freed;    // [ceil(n_pages / 32)] pages that nobody holds any more
+    uint32_t* done;     // blocks of the second kernel that are done
+    int n_children, n_seqs, max_pages, n_pages, page_shift;
+};
+
+constexpr int32_t kGoesOn = 1 << 30;
+constexpr int kCopyPer = 4096;  // pages of the pool that a block of the first kernel clears or copies
+
+// Block 0 plans; the others copy the shares, if they are not updated in place, and clear the marks.
+__global__ void __launch_bounds__(kPlanThreads) paged_fork_plan_kernel(const __grid_constant__ PagedFork p) {
+    extern __shared__ int sm[];
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x > 0) {
+        const int step = kPlanThreads * ((int)gridDim.x - 1), id = ((int)blockIdx.x - 1) * kPlanThreads + tid;
+        if (p.shares != p.shares_out)
+            for (int i = id; i < p.n_pages; i += step) p.shares_out[i] = p.shares[i];
+        for (int i = id; i < (p.n_pages + 31) / 32; i += step) p.freed[i] = 0u;
+        return;
+    }
+    int* s_first = sm;
+    int* s_kids = s_first + p.n_seqs;
+    __shared__ int s_warp[32];
+    const int page = 1 << p.page_shift;
+    const int head = p.ring_state[0], count = p.ring_state[1];
+    bool bad = families(p.parents, p.n_children, p.n_seqs, s_first, s_kids);
+    bad |= head < 0 || head >= p.n_pages || count < 0 || count > p.n_pages;
+    for (int q = tid; q < p.n_seqs; q += kPlanThreads) {
+        const int held = p.held[q], len = p.lens[q], kids = s_kids[q];
+        bool wrong = held < 0 || held > p.max_pages;
+        int32_t holds = kids;
+        if (kids && !wrong) {
+            wrong = len < 0 || len > ((int64_t)held << p.page_shift);
+            if (!wrong && (len & (page - 1))) {
+                // a last page that is not full goes to the first child, if no other sequence holds it
+                const int tail = p.table[(int64_t)q * p.max_pages + (len >> p.page_shift)];
+                if (tail < 0 || tail >= p.n_pages || p.shares[tail] == 0) holds |= kGoesOn;
+            }
+        }
+        bad |= wrong;
+        s_kids[q] = holds;
+        p.holders[q] = holds;
+    }
+    bad = __syncthreads_or(bad);
+    int takes = 0;
+    for (int i0 = 0; i0 < p.n_children; i0 += kPlanThreads) {
+        const int i = i0 + tid, q = i < p.n_children ? p.parents[i] : -1;
+        const bool live = !bad && q >= 0;
+        int len = 0;
+        bool take = false;
+        if (live) {
+            len = p.lens[q];
+            take = (len & (page - 1)) && !(s_first[q] == i && (s_kids[q] & kGoesOn));
+        }
+        int total;
+        const int k = takes + block_sums(take, s_warp, total);
+        takes += total;
+        if (i < p.n_children) {
+            int at = head, fresh = -1, src = -1;
+            if (take && k < count) {
+                at = head + k >= p.n_pages ? head + k - p.n_pages : head + k;
+                fresh = p.ring[at];
+                src = p.table[(int64_t)q * p.max_pages + (len >> p.page_shift)];
+            }
+            p.take[i] = fresh;
+            p.copy_src[i] = src;
+            p.copy_dst[i] = fresh;
+            p.copy_rows[i] = take ? len & (page - 1) : 0;
+            p.lens_out[i] = len;
+            p.held_out[i] = (len + page - 1) >> p.page_shift;
+        }
+    }
+    const int status = bad ? 2 : takes > count ? 1 : 0;
+    if (status) {
+        __syncthreads();
+        for (int i = tid; i < p.n_children; i += kPlanThreads) {
+            p.copy_src[i] = p.copy_dst[i] = -1;
+            p.copy_rows[i] = p.lens_out[i] = p.held_out[i] = 0;
+        }
+    }
+    if (tid == 0) {
+        p.status[0] = status;
+        p.done[0] = 0u;
+        p.done[1] = (uint32_t)takes;
+    }
+}
+
+constexpr int kForkThreads = 256;
+constexpr int kForkPer = 4;  // entries of a table row that a thread takes
+
+// Block (part of a table row, child or sequence): a child's row from its parent's, and what a sequence's pages gain or lose:
+// each is held by its children from now on, not by itself.  shares counts holders beyond the first, so the last one to let a page
+// go takes it below zero; the last block to finish gives those back to the ring, in order of their number.
+__global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const __grid_constant__ PagedFork p) {
+    __shared__ int s_warp[32];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, page = 1 << p.page_shift;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int k0 = blockIdx.x * kForkThreads * kForkPer + tid;
+    const bool moved = p.status[0] == 0;
+    if (moved && (int)blockIdx.y < p.n_children) {
+        const int i = blockIdx.y, q = p.parents[i], need = p.held_out[i];
+        if (need > 0) {
+            const int fresh = p.take[i], tail = fresh >= 0 ? need - 1 : -1;
+            const int32_t* from = p.table + (int64_t)q * p.max_pages;
+            int32_t* to = p.table_out + (int64_t)i * p.max_pages;
+#pragma unroll
+            for (int u = 0; u < kForkPer; ++u) {
+                const int k = k0 + u * kForkThreads;
+                if (k < need) to[k] = k == tail ? fresh : from[k];
+            }
+        }
+    } else if (moved) {
+        const int q = (int)blockIdx.y - p.n_children;
+        const int held = p.held[q], holders = p.holders[q], kids = holders & (kGoesOn - 1);
+        const int full = kids ? p.lens[q] >> p.page_shift : 0;
+        const bool part = kids && (p.lens[q] & (page - 1));
+        const int32_t* from = p.table + (int64_t)q * p.max_pages;
+#pragma unroll
+        for (int u = 0; u < kForkPer; ++u) {
+            const int k = k0 + u * kForkThreads;
+            if (k >= held) continue;
+            const int change = (k < full ? kids : k == full && part && (holders & kGoesOn) ? 1 : 0) - 1;
+            if (change == 0) continue;
+            const int id = from[k];
+            if (id < 0 || id >= p.n_pages) continue;
+            if (atomicAdd(p.shares_out + id, change) + change < 0) atomicOr(p.freed + (id >> 5), 1u << (id & 31));
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    const int head = p.ring_state[0], count = p.ring_state[1], takes = moved ? (int)__ldcg(p.done + 1) : 0;
+    int given = 0;
+    if (moved) {
+        const int n_words = (p.n_pages + 31) / 32;
+        int tail = head + count;
+        if (tail >= p.n_pages) tail -= p.n_pages;
+        for (int w0 = 0; w0 < n_words; w0 += kForkThreads) {
+            const int w = w0 + tid;
+            uint32_t bits = w < n_words ? __ldcg(p.freed + w) : 0u;
+            int total;
+            int k = given + block_sums(__popc(bits), s_warp, total);
+            given += total;
+            for (; bits; bits &= bits - 1, ++k) {
+                const int id = 32 * w + __ffs((int)bits) - 1;
+                p.shares_out[id] = 0;
+                if (k < p.n_pages - count) p.ring[tail + k >= p.n_pages ? tail + k - p.n_pages : tail + k] = id;
+            }
+        }
+    }
+    __syncthreads();  // every thread has read the state
+    if (tid == 0) {
+        const int h = head + takes;
+        p.ring_out[0] = moved && h >= p.n_pages ? h - p.n_pages : moved ? h : head;
+        p.ring_out[1] = moved ? count - takes + min(given, p.n_pages - count) : count;
+    }
+}
+
+size_t fork_carve(PagedFork& p, unsigned char* base) {
+    size_t at = 0;
+    auto take = [&](auto*& ptr, size_t n) {
+        ptr = reinterpret_cast<std::remove_reference_t<decltype(ptr)>>(base + at);
+        at += (n * sizeof(*ptr) + 15) / 16 * 16;
+    };
+    take(p.take, (size_t)p.n_children);
+    take(p.holders, (size_t)p.n_seqs);
+    take(p.freed, ((size_t)p.n_pages + 31) / 32);
+    take(p.done, 2);
+    return at;
+}
+
+}  // namespace
+}  // namespace kvq8
+
+extern "C" size_t token_counts_fork_workspace_bytes(int n_children) {
+    return n_children < 1 || n_children > kvq8::kMaxSeqs ? 0 : ((size_t)n_children * sizeof(int2) + 15) / 16 * 16;
+}
+
+extern "C" int token_counts_fork(const int32_t* parents, int n_children, const int32_t* state_of, int n_seqs, uint32_t* counts,
+                                 int n_states, int vocab, int32_t* state_of_out, int32_t* status, void* workspace,
+                                 size_t workspace_bytes, kvq8_stream_t stream) {
+    using namespace kvq8;
+    if (n_children < 1 || n_seqs < 1 || n_states < 1 || vocab < 1) return KVQ8_ERR_INVALID_ARG;
+    if (!parents || !counts || !state_of_out || !status) return KVQ8_ERR_INVALID_ARG;
+    // state_of_out may be state_of itself
+    const size_t kids = (size_t)n_children * 4, old = (size_t)n_seqs * 4;
+    if (ranges_meet(parents, kids, state_of_out, kids) || (state_of != state_of_out && ranges_meet(state_of, old, state_of_out, kids)))
+        return KVQ8_ERR_INVALID_ARG;
+    if (n_children > kMaxSeqs || n_seqs > kMaxSeqs || n_states > kMaxStates || vocab > (1 << 30)) return KVQ8_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < token_counts_fork_workspace_bytes(n_children)) return KVQ8_ERR_WORKSPACE;
+    for (const void* q : {(const void*)parents, (const void*)state_of, (const void*)counts, (const void*)state_of_out, (const void*)status})
+        if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
+    if (!aligned16(workspace)) return KVQ8_ERR_MISALIGNED;
+    const CountsFork p = {parents, state_of, state_of_out, counts, status, static_cast<int2*>(workspace), n_children, n_seqs, n_states, vocab};
+    const int smem = (3 * n_seqs + 2 * ((n_states + 31) / 32)) * 4;
+    static SmemOptIn opt;
+    int rc = opt.ensure(counts_fork_plan_kernel, (3 * kMaxSeqs + 2 * kMaxStates / 32) * 4);
+    if (rc != KVQ8_OK) return rc;
+    cudaStream_t s = (cudaStream_t)stream;
+    rc = launch_dependent(counts_fork_plan_kernel, 1, kPlanThreads, smem, s, p);
+    if (rc != KVQ8_OK) return rc;
+    const bool vec = vocab % 4 == 0 && aligned16(counts);
+    const int per = kRowThreads * kRowPer * (vec ? 4 : 1);
+    const dim3 grid((unsigned)((vocab + per - 1) / per), (unsigned)n_children);
+    if (vec) return launch_dependent(counts_copy_kernel<uint4>, grid, kRowThreads, 0, s, p);
+    return launch_dependent(counts_copy_kernel<uint32_t>, grid, kRowThreads, 0, s, p);
+}
+
+extern "C" size_t kvq8_paged_fork_workspace_bytes(int n_seqs, int n_children, int n_pages) {
+    using namespace kvq8;
+    if (n_seqs < 1 || n_children < 1 || n_pages < 1 || n_seqs > kMaxSeqs || n_children > kMaxSeqs || n_pages > (1 << 30)) return 0;
+    PagedFork p = {};
+    p.n_seqs = n_seqs, p.n_children = n_children, p.n_pages = n_pages;
+    return fork_carve(p, nullptr);
+}
+
+extern "C" int kvq8_paged_fork(const int32_t* parents, int n_children, const int32_t* lens, const int32_t* held, int n_seqs,
+                               int page_size, const int32_t* page_table, int max_pages, const int32_t* shares,
+                               int32_t* free_ring, int n_pages, const int32_t* ring_state, int32_t* page_table_out,
+                               int32_t* lens_out, int32_t* held_out, int32_t* shares_out, int32_t* ring_out,
+                               int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows, int32_t* status, void* workspace,
+                               size_t workspace_bytes, kvq8_stream_t stream) {
+    using namespace kvq8;
+    if (n_children < 1 || n_seqs < 1 || max_pages < 1 || n_pages < 1) return KVQ8_ERR_INVALID_ARG;
+    const void* in[] = {parents, lens, held, page_table, shares, ring_state};
+    const void* out[] = {free_ring, page_table_out, lens_out, held_out, shares_out, ring_out, copy_src, copy_dst, copy_rows, status};
+    for (const void* q : in)
+        if (!q) return KVQ8_ERR_INVALID_ARG;
+    for (const void* q : out)
+        if (!q) return KVQ8_ERR_INVALID_ARG;
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) || n_seqs > kMaxSeqs || n_children > kMaxSeqs ||
+        n_pages > (1 << 30) || max_pages > (1 << 24))
+        return KVQ8_ERR_UNSUPPORTED;
+    for (const void* q : in)
+        if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
+    for (const void* q : out)
+        if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
+    // the sequences' state is read while the children's is written
+    const size_t old = (size_t)n_seqs * 4, kids = (size_t)n_children * 4;
+    if (ranges_meet(page_table, old * max_pages, page_table_out, kids * max_pages)) return KVQ8_ERR_INVALID_ARG;
+    for (const void* o : {(const void*)lens_out, (const void*)held_out, (const void*)copy_src, (const void*)copy_dst, (const void*)copy_rows})
+        if (ranges_meet(lens, old, o, kids) || ranges_meet(held, old, o, kids) || ranges_meet(parents, kids, o, kids))
+            return KVQ8_ERR_INVALID_ARG;
+    if ((shares != shares_out && ranges_meet(shares, (size_t)n_pages * 4, shares_out, (size_t)n_pages * 4)) ||
+        (ring_state != ring_out && ranges_meet(ring_state, 8, ring_out, 8)))
+        return KVQ8_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kvq8_paged_fork_workspace_bytes(n_seqs, n_children, n_pages)) return KVQ8_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KVQ8_ERR_MISALIGNED;
+    PagedFork p = {parents, lens, held, page_table, shares, ring_state, free_ring, page_table_out, lens_out, held_out, shares_out,
+                   ring_out, copy_src, copy_dst, copy_rows, status, nullptr, nullptr, nullptr, nullptr, n_children, n_seqs,
+                   max_pages, n_pages, log2_of(page_size)};
+    fork_carve(p, static_cast<unsigned char*>(workspace));
+    const int clear = (n_pages + kCopyPer - 1) / kCopyPer;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int rc = launch_dependent(paged_fork_plan_kernel, (unsigned)(1 + (clear < 75 ? clear : 75)), kPlanThreads, 2 * n_seqs * 4, s, p);
+    if (rc != KVQ8_OK) return rc;
+    const int per = kForkThreads * kForkPer;
+    const dim3 grid((unsigned)((max_pages + per - 1) / per), (unsigned)(n_children + n_seqs));
+    return launch_dependent(paged_fork_kernel, grid, kForkThreads, 0, s, p);
+}

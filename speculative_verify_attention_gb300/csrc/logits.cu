@@ -246,23 +246,6 @@ int launch_adjust(const AdjustParams& p, bool vec, cudaStream_t s) {
     return launch_dependent(logits_adjust_kernel<T, false>, grid, kAdjThreads, 0, s, p);
 }
 
-// Whether any of n rows of a_len bytes, a_step apart, shares a byte with any of n rows of b_len bytes, b_step apart (a step is
-// no less than its length).  Rows that lie between the other's are no overlap.
-bool rows_meet(uintptr_t a, int64_t a_len, int64_t a_step, uintptr_t b, int64_t b_len, int64_t b_step, int n) {
-    const uintptr_t a_end = a + (uintptr_t)((n - 1) * a_step + a_len), b_end = b + (uintptr_t)((n - 1) * b_step + b_len);
-    if (a_end <= b || b_end <= a) return false;
-    for (int i = 0, j = 0; i < n && j < n;) {
-        const uintptr_t at_a = a + (uintptr_t)(i * a_step), at_b = b + (uintptr_t)(j * b_step);
-        if (at_a + (uintptr_t)a_len <= at_b)
-            ++i;
-        else if (at_b + (uintptr_t)b_len <= at_a)
-            ++j;
-        else
-            return true;
-    }
-    return false;
-}
-
 // ---------------------------------------------------------------- counts
 
 constexpr int kCountThreads = 256;

@@ -42,6 +42,36 @@ inline int check_paged(const kvq8_paged_cache* kv) {
 
 inline bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether two arrays of a_len and b_len bytes share one.
+inline bool ranges_meet(const void* a, size_t a_len, const void* b, size_t b_len) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + b_len && y < x + a_len;
+}
+
+// Whether any of n rows of a_len bytes, a_step apart, shares a byte with any of n rows of b_len bytes, b_step apart (a step is
+// no less than its length).  Rows that lie between the other's are no overlap.
+inline bool rows_meet(uintptr_t a, int64_t a_len, int64_t a_step, uintptr_t b, int64_t b_len, int64_t b_step, int n) {
+    const uintptr_t a_end = a + (uintptr_t)((n - 1) * a_step + a_len), b_end = b + (uintptr_t)((n - 1) * b_step + b_len);
+    if (a_end <= b || b_end <= a) return false;
+    if (a_step == b_step) {  // rows of one grid: those whose numbers differ by d, for the two d that bring them nearest
+        const int64_t ahead = (int64_t)(a - b);
+        const int64_t d0 = ahead / a_step - (ahead % a_step < 0);
+        for (int64_t d = d0; d <= d0 + 1; ++d)
+            if (d < n && -d < n && ahead - d * a_step > -a_len && ahead - d * a_step < b_len) return true;
+        return false;
+    }
+    for (int i = 0, j = 0; i < n && j < n;) {
+        const uintptr_t at_a = a + (uintptr_t)(i * a_step), at_b = b + (uintptr_t)(j * b_step);
+        if (at_a + (uintptr_t)a_len <= at_b)
+            ++i;
+        else if (at_b + (uintptr_t)b_len <= at_a)
+            ++j;
+        else
+            return true;
+    }
+    return false;
+}
+
 // 32 bytes that nothing writes while the kernel runs.
 __device__ __forceinline__ void load32(uint32_t (&w)[8], const void* at) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
