@@ -18,10 +18,16 @@ namespace {
 
 constexpr int kScanThreads = 256;
 constexpr int kGroup = 256;        // values of a group: eight a lane
-constexpr int kWarpGroups = 4;     // groups that a warp holds at once
-constexpr int kPickThreads = 256;
+// Groups that a warp holds at once: 128 bytes of fp32, as many values twice of the others.
+template <typename T>
+constexpr int kWarpGroups = sizeof(T) == 4 ? 4 : 8;
+constexpr int kPadGroups = 8;      // a row's groups are counted in these
+constexpr int kSearchThreads = 256;
+constexpr int kPickThreads = kSearchThreads + 32;
 constexpr int kMaxOut = 64;
-constexpr int kListCap = 1024;     // candidates that the second kernel keeps
+constexpr int kKeep = 4;           // groups of a row that a searching thread keeps
+constexpr int kGroupCap = 256;     // groups, and values, that the second kernel keeps of a row
+constexpr int kListCap = 512;
 
 // The sum of exp over a warp's values, whose maximum is m: s * 2^e, or s * exp(m) where |m| >= kLarge (e would not be near
 // m log2 e there).  s is NaN if a value is NaN or +infinite.
@@ -45,7 +51,7 @@ struct SelectParams {
     // workspace
     int32_t* group_max;     // [n_rows][n_groups], ordered as whole numbers
     Part* parts;            // [n_rows][n_parts]
-    double* list_order;     // [n_rows][n_out] weight * total, descending
+    int64_t* list_order;    // [n_rows][n_out] weight * total, descending, ordered as whole numbers
     float* list_total;
     int32_t* list_token;
     int32_t* list_count;    // [n_rows]
@@ -60,6 +66,13 @@ __device__ __forceinline__ int32_t ordered(float x) {
     return b ^ ((b >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float from_ordered(int32_t o) { return __int_as_float(o ^ ((o >> 31) & 0x7fffffff)); }
+__device__ __forceinline__ int64_t ordered(double x) {
+    const int64_t b = __double_as_longlong(x + 0.0);
+    return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 // Unique and ascending in quality: larger values first, of equal ones the lower place.
 __device__ __forceinline__ uint64_t key_of(int32_t ord, uint32_t place) {
     return (uint64_t)((uint32_t)ord ^ 0x80000000u) << 32 | (0xffffffffu - place);
@@ -114,12 +127,13 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     }
     if (part >= p.n_parts || (p.ended && __ldg(p.ended + row) >= 0)) return;
     const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-    Eight<T> raw[kWarpGroups];
+    constexpr int G = kWarpGroups<T>;
+    Eight<T> raw[G];
 #pragma unroll
-    for (int u = 0; u < kWarpGroups; ++u) load_eight<T, VEC>(raw[u], x, (part * kWarpGroups + u) * kGroup + lane * 8, p.vocab);
-    int32_t top[kWarpGroups];
+    for (int u = 0; u < G; ++u) load_eight<T, VEC>(raw[u], x, (part * G + u) * kGroup + lane * 8, p.vocab);
+    int32_t top[G], most = ordered(-INFINITY);
 #pragma unroll
-    for (int u = 0; u < kWarpGroups; ++u) {
+    for (int u = 0; u < G; ++u) {
         float v[8];
         raw[u].floats(v);
         float m = fmaxf(v[0], v[1]);
@@ -127,14 +141,15 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         for (int i = 2; i < 8; ++i) m = fmaxf(m, v[i]);
         if (!(m > -INFINITY)) m = -INFINITY;
         top[u] = __reduce_max_sync(0xffffffffu, ordered(m));
+        most = max(most, top[u]);
     }
-    const float m = from_ordered(max(max(top[0], top[1]), max(top[2], top[3])));
+    const float m = from_ordered(most);
     // 2^(x log2 e - e) with e a rounded multiple near the maximum: one rounding a value, and parts join by powers of two
     const float e = rintf(m * kLog2e);
     const bool plain = fabsf(m) < kLarge, any = fabsf(m) < INFINITY;
     float s = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kWarpGroups; ++u) {
+    for (int u = 0; u < G; ++u) {
         float v[8];
         raw[u].floats(v);
         if (plain) {
@@ -149,194 +164,208 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) {
         p.parts[(int64_t)row * p.n_parts + part] = Part{m, e, s};
-        reinterpret_cast<int4*>(p.group_max)[((int64_t)row * p.n_groups >> 2) + part] = make_int4(top[0], top[1], top[2], top[3]);
+        int4* to = reinterpret_cast<int4*>(p.group_max + (int64_t)row * p.n_groups + part * G);
+#pragma unroll
+        for (int u = 0; u < G; u += 4) to[u / 4] = make_int4(top[u], top[u + 1], top[u + 2], top[u + 3]);
     }
 }
 
-// A list of at most kListCap keys in shared memory, cut back to its best n_out where it fills up.
-struct List {
-    uint64_t key[kListCap];
-    uint64_t best[kMaxOut];
-    uint64_t above;     // keys below this are none of the best
-    int n;
+// The threads that search (the others of the block sum).
+__device__ __forceinline__ void search_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+struct Search {
+    uint64_t key[kListCap];      // candidates, as key_of
+    uint64_t best[kMaxOut];      // the row's best, in order
+    uint32_t group[kGroupCap];
+    int32_t top[kSearchThreads];
+    uint64_t above;              // keys below this are none of the best (slow path)
+    int32_t bound;               // values below this are none of the best
+    int n_groups, n;
 };
 
-// The list's n_out best, in order.  All threads; the keys are different.
-__device__ __forceinline__ void prune(List& l, int n_out) {
-    __syncthreads();
-    const int n = l.n;
-    for (int i = threadIdx.x; i < n; i += kPickThreads) {
-        const uint64_t mine = l.key[i];
+// The best n_out of the n keys, in order.  All searching threads; the keys are different.
+__device__ __forceinline__ void rank_keys(Search& s, int n, int n_out) {
+    for (int i = threadIdx.x; i < n; i += kSearchThreads) {
+        const uint64_t mine = s.key[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += l.key[j] > mine;
-        if (rank < n_out) l.best[rank] = mine;
+        for (int j = 0; j < n; ++j) rank += s.key[j] > mine;
+        if (rank < n_out) s.best[rank] = mine;
     }
-    __syncthreads();
-    const int m = min(n, n_out);
-    if ((int)threadIdx.x < m) l.key[threadIdx.x] = l.best[threadIdx.x];
-    if (threadIdx.x == 0) {
-        l.n = m;
-        if (m == n_out) l.above = max(l.above, l.best[n_out - 1]);
-    }
-    __syncthreads();
+    search_sync();
 }
 
-// Every thread's keys that are not below the list's bound join the list.  All threads.
-template <int N>
-__device__ __forceinline__ void push(List& l, const uint64_t (&k)[N], int n_out) {
-    const uint64_t above = l.above;
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine += k[i] >= above && k[i];
-    const int have = l.n, all = __syncthreads_or(mine) ? mine : -1;
-    if (all < 0) return;
-    // where all fit, each thread takes its places at once
-    __shared__ int s_want;
-    if (threadIdx.x == 0) s_want = 0;
-    __syncthreads();
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, incl, o);
-        if ((int)(threadIdx.x & 31) >= o) incl += up;
-    }
-    int base = 0;
-    if ((threadIdx.x & 31) == 31) base = atomicAdd(&s_want, incl);
-    base = __shfl_sync(0xffffffffu, base, 31);
-    __syncthreads();
-    const int want = s_want;
-    if (have + want <= kListCap) {
-        int at = have + base + incl - mine;
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (k[i] >= above && k[i]) l.key[at++] = k[i];
-        if (threadIdx.x == 0) l.n = have + want;
-        __syncthreads();
-        return;
-    }
-    // many equal values: one key a thread at a time, and the bound rises with each cut
-#pragma unroll 1
-    for (int i = 0; i < N; ++i) {
-        if (l.n + kPickThreads > kListCap) prune(l, n_out);
-        uint64_t key = 0;
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (u == i) key = k[u];
-        __syncthreads();
-        if (key && key >= l.above) l.key[atomicAdd(&l.n, 1)] = key;
-        __syncthreads();
-    }
-}
-
+// Where more groups or values reach the bound than the lists hold (many equal values): the row's groups, and then the best ones'
+// values, a key a thread at a time; a full list is cut back to its best n_out, below which nothing is taken any more.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_constant__ SelectParams p) {
-    extern __shared__ __align__(16) unsigned char s_join[];  // the join: 64 rows' orders
-    __shared__ List l;
-    __shared__ uint64_t s_top[kPickThreads];
-    __shared__ unsigned long long s_sum;
-    __shared__ int32_t s_m;
+__device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const T* x, const int32_t* gm) {
+    const int tid = threadIdx.x, n_out = p.n_out;
+    auto cut = [&] {
+        const int n = s.n;
+        rank_keys(s, n, n_out);
+        const int m = min(n, n_out);
+        if (tid < m) s.key[tid] = s.best[tid];
+        if (tid == 0) {
+            s.n = m;
+            if (m == n_out) s.above = s.best[n_out - 1];
+        }
+        search_sync();
+    };
+    auto add = [&](uint64_t k) {
+        if (s.n + kSearchThreads > kListCap) cut();
+        if (k > s.above) s.key[atomicAdd(&s.n, 1)] = k;
+        search_sync();
+    };
+    search_sync();
+    if (tid == 0) s.n = 0, s.above = 0;
+    search_sync();
+#pragma unroll 1
+    for (int g0 = 0; g0 < p.n_groups; g0 += kSearchThreads) add(g0 + tid < p.n_groups ? key_of(gm[g0 + tid], (uint32_t)(g0 + tid)) : 0);
+    cut();
+    const int groups = s.n;
+    if (tid < groups) s.group[tid] = key_place(s.key[tid]);
+    search_sync();
+    if (tid == 0) s.n = 0, s.above = 0;
+    search_sync();
+#pragma unroll 1
+    for (int g = 0; g < groups; ++g) {
+        const int at = (int)s.group[g] * kGroup + tid;
+        const float v = at < p.vocab ? to_float(x[at]) : -INFINITY;
+        add(v > -INFINITY ? key_of(ordered(v), (uint32_t)at) : 0);
+    }
+    cut();
+    return s.n;
+}
+
+// Block: one row.  Its first eight warps look for the row's best values, the ninth sums its exponentials.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid_constant__ SelectParams p) {
+    extern __shared__ __align__(16) unsigned char s_join[];  // the join: the rows' orders
+    __shared__ Search s;
     __shared__ double s_norm;
-    __shared__ int s_bad, s_last;
+    __shared__ int s_last, s_found, s_count[kMaxWindowRows];
     const int tid = threadIdx.x, row = blockIdx.x, n_out = p.n_out;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = p.seq_of[row];
-    int first, rows;
-    if (b < 0 || b >= p.n_seqs || !rows_of(p, b, first, rows) || row < first || row >= first + rows) return;
+    const int32_t* gm = p.group_max + (int64_t)row * p.n_groups;
+    const int b = __ldg(p.seq_of + row);
     const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
     const int ended = p.ended ? __ldg(p.ended + row) : -1;
-    const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY;
-    const int64_t out0 = (int64_t)row * n_out;
-    int count = 0;
-    if (ended >= 0) {
-        count = usable ? 1 : 0;
-        if (tid == 0 && usable) {
-            p.list_order[out0] = (double)score * (double)weight;
-            p.list_total[out0] = score;
-            p.list_token[out0] = ended;
+    int32_t k[kKeep];
+    const int32_t lowest = ordered(-INFINITY);
+    if (tid < kSearchThreads) {
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) {
+            const int g = u * kSearchThreads + tid;
+            k[u] = g < p.n_groups && ended < 0 ? __ldg(gm + g) : lowest;
         }
-    } else if (usable) {
-        // the sum of exponentials: parts scaled by powers of two to the largest one's, added as whole numbers of 2^-32, so
-        // that their order does not matter
-        if (tid == 0) s_sum = 0, s_m = ordered(-INFINITY), s_bad = 0, l.n = 0, l.above = 1;
-        __syncthreads();
+    }
+    if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
+    int first, rows;
+    if (b < 0 || b >= p.n_seqs || !rows_of(p, b, first, rows) || row < first || row >= first + rows) return;
+    const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY, live = usable && ended < 0;
+    if (live && tid < kSearchThreads) {
+        // a bound: the n_out-th best of the threads' best groups
+        int32_t m = k[0];
+#pragma unroll
+        for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
+        for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, __ldg(gm + g));
+        s.top[tid] = m;
+        search_sync();
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < kSearchThreads / 4; ++j) {
+            const int4 o = reinterpret_cast<const int4*>(s.top)[j];
+            rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+        }
+        if (rank < n_out) atomicMin(&s.bound, m);
+        search_sync();
+        // the groups that reach it, and their values that do; -inf is none
+        const int32_t bound = max(s.bound, lowest + 1);
+        auto group = [&](int32_t key, int g) {
+            if (key < bound) return;
+            const int at = atomicAdd(&s.n_groups, 1);
+            if (at < kGroupCap) s.group[at] = (uint32_t)g;
+        };
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) group(k[u], u * kSearchThreads + tid);
+        for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(__ldg(gm + g), g);
+        search_sync();
+        const int groups = s.n_groups;
+        const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+        int found = groups <= kGroupCap ? 0 : kListCap + 1;
+        if (!found) {
+#pragma unroll 2
+            for (int i = tid >> 5; i < groups; i += kSearchThreads / 32) {
+                const int at = (int)s.group[i] * kGroup + (tid & 31) * 8;
+                Eight<T> raw;
+                load_eight<T, VEC>(raw, x, at, p.vocab);
+                float v[8];
+                raw.floats(v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int32_t o = ordered(v[e]);
+                    if (o < bound || v[e] != v[e]) continue;
+                    const int to = atomicAdd(&s.n, 1);
+                    if (to < kListCap) s.key[to] = key_of(o, (uint32_t)(at + e));
+                }
+            }
+            search_sync();
+            found = s.n;
+        }
+        if (found <= kListCap)
+            rank_keys(s, found, n_out);
+        else
+            found = pick_slowly<T, VEC>(s, p, x, gm);
+        if (tid == 0) s_found = min(found, n_out);
+    } else if (live) {
+        // parts scaled by powers of two to the largest one's, added as whole numbers of 2^-32, so that their order does not matter
+        const int lane = tid & 31;
         const Part* parts = p.parts + (int64_t)row * p.n_parts;
-        int32_t m = ordered(-INFINITY);
+        int32_t m = lowest;
         bool bad = false;
-        for (int i = tid; i < p.n_parts; i += kPickThreads) {
-            m = max(m, ordered(parts[i].m));
-            bad |= parts[i].s != parts[i].s;
+        for (int i = lane; i < p.n_parts; i += 32) {
+            const Part q = parts[i];
+            m = max(m, ordered(q.m));
+            bad |= q.s != q.s;
         }
-        m = __reduce_max_sync(0xffffffffu, m);
-        if ((tid & 31) == 0) atomicMax(&s_m, m);
-        if (bad) s_bad = 1;
-        __syncthreads();
-        const float top = from_ordered(s_m);
+        const float top = from_ordered(__reduce_max_sync(0xffffffffu, m));
+        bad = __any_sync(0xffffffffu, bad);
         const float e = rintf(top * kLog2e);
         const bool plain = fabsf(top) < kLarge;
         unsigned long long sum = 0;
-        for (int i = tid; i < p.n_parts; i += kPickThreads) {
+        for (int i = lane; i < p.n_parts; i += 32) {
             const Part q = parts[i];
-            float s = 0.0f;
+            float v = 0.0f;
             if (plain && fabsf(q.m) < kLarge)
-                s = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
+                v = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
             else if (q.m > -INFINITY)
-                s = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
-            sum += __float2ull_rn(s * 0x1p32f);
+                v = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
+            sum += __float2ull_rn(v * 0x1p32f);
         }
-        if (sum) atomicAdd(&s_sum, sum);
-        // the row's best groups: first a bound from the threads' best ones, then those above it
-        uint64_t mine = 0;
-        const int32_t* gm = p.group_max + (int64_t)row * p.n_groups;
-        for (int g = tid; g < p.n_groups; g += kPickThreads) {
-            const uint64_t k = key_of(gm[g], (uint32_t)g);
-            mine = k > mine ? k : mine;
-        }
-        s_top[tid] = mine;
-        __syncthreads();
-        if (tid == 0) s_norm = plain ? ((double)e + log2((double)s_sum * 0x1p-32)) / (double)kLog2e : (double)top + log((double)s_sum * 0x1p-32);
-        {
-            int rank = 0;
-            for (int j = 0; j < kPickThreads; ++j) rank += s_top[j] > mine;
-            if (rank == n_out - 1 && mine) l.above = mine;  // threads without a group have the key 0
-        }
-        __syncthreads();
-        for (int g0 = 0; g0 < p.n_groups; g0 += kPickThreads) {
-            uint64_t k[1] = {g0 + tid < p.n_groups ? key_of(gm[g0 + tid], (uint32_t)(g0 + tid)) : 0};
-            push(l, k, n_out);
-        }
-        prune(l, n_out);
-        const int groups = l.n;
-        __shared__ uint32_t s_group[kMaxOut];
-        if (tid < groups) s_group[tid] = key_place(l.key[tid]);
-        // a value below the last of n_out groups' maxima is none of the best, nor is -inf
-        const uint64_t low = groups == n_out ? (l.key[groups - 1] >> 32) << 32 : 0;
-        const uint64_t nothing = (key_of(ordered(-INFINITY), 0) >> 32 << 32) + (1ull << 32);
-        __syncthreads();
-        if (tid == 0) l.n = 0, l.above = low > nothing ? low : nothing;
-        __syncthreads();
-        const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-        for (int g0 = 0; g0 < groups; g0 += kPickThreads / 32) {
-            uint64_t k[8];
-            const int g = g0 + (tid >> 5);
-            const int at = g < groups ? (int)s_group[g] * kGroup + (tid & 31) * 8 : p.vocab;
-            Eight<T> raw;
-            load_eight<T, VEC>(raw, x, at, p.vocab);
-            float v[8];
-            raw.floats(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) k[i] = at + i < p.vocab && v[i] > -INFINITY ? key_of(ordered(v[i]), (uint32_t)(at + i)) : 0;
-            push(l, k, n_out);
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) {
+            const double total = (double)sum * 0x1p-32;
+            const double norm = plain ? ((double)e + log2(total)) * (1.0 / (double)kLog2e) : (double)top + log(total);
+            s_norm = bad ? (double)INFINITY : norm;
         }
-        prune(l, n_out);
-        const double norm = s_norm;
-        count = s_bad || !(fabs(norm) < (double)INFINITY) ? 0 : l.n;
+    }
+    __syncthreads();
+    const int64_t out0 = (int64_t)row * n_out;
+    int count = usable ? 1 : 0;
+    double total = (double)score;
+    int32_t token = ended;
+    if (live) {
+        count = fabs(s_norm) < (double)INFINITY ? s_found : 0;
         if (tid < count) {
-            const double total = (double)score + ((double)key_value(l.key[tid]) - norm);
-            p.list_order[out0 + tid] = total * (double)weight;
-            p.list_total[out0 + tid] = (float)total;
-            p.list_token[out0 + tid] = (int32_t)key_place(l.key[tid]);
+            total += (double)key_value(s.best[tid]) - s_norm;
+            token = (int32_t)key_place(s.best[tid]);
         }
+    }
+    if (tid < count) {
+        p.list_order[out0 + tid] = ordered(total * (double)weight);
+        p.list_total[out0 + tid] = (float)total;
+        p.list_token[out0 + tid] = token;
     }
     // the last row of a request to be done joins its rows' lists
     if (tid == 0) p.list_count[row] = count;
@@ -346,24 +375,21 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    double* order = reinterpret_cast<double*>(s_join);
-    __shared__ int s_count[kMaxWindowRows];
+    int64_t* order = reinterpret_cast<int64_t*>(s_join);
     if (tid < rows) s_count[tid] = __ldcg(p.list_count + first + tid);
+    for (int i = tid; i < rows * n_out; i += kPickThreads) order[i] = __ldcg(p.list_order + (int64_t)first * n_out + i);
     __syncthreads();
     int n_all = 0;
     for (int r = 0; r < rows; ++r) n_all += s_count[r];
-    for (int i = tid; i < rows * n_out; i += kPickThreads)
-        if (i % n_out < s_count[i / n_out]) order[i] = __ldcg(p.list_order + (int64_t)first * n_out + i);
-    __syncthreads();
     const int64_t to = (int64_t)b * n_out;
     for (int i = tid; i < rows * n_out; i += kPickThreads) {
         const int r = i / n_out, j = i - r * n_out;
         if (j >= s_count[r]) continue;
-        const double mine = order[i];
+        const int64_t mine = order[i];
         int rank = j;
         for (int q = 0; q < rows && rank < n_out; ++q) {
             if (q == r) continue;
-            const double* o = order + q * n_out;
+            const int64_t* o = order + q * n_out;
             int lo = 0, hi = s_count[q];  // how many of row q come before: more, or as much and of a lower row
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
@@ -386,7 +412,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const __grid_co
     }
 }
 
-int groups_of(int vocab) { return (vocab + kGroup * kWarpGroups - 1) / (kGroup * kWarpGroups) * kWarpGroups; }
+int groups_of(int vocab) { return (vocab + kGroup * kPadGroups - 1) / (kGroup * kPadGroups) * kPadGroups; }
 
 // The workspace's arrays, in order of their alignment; the size where base is null.
 size_t carve(SelectParams& p, unsigned char* base) {
@@ -417,7 +443,7 @@ int launch_select(const SelectParams& p, cudaStream_t s) {
     const dim3 grid((unsigned)((p.n_parts + warps - 1) / warps), (unsigned)p.n_rows);
     const int rc = launch_dependent(beam_scan_kernel<T, VEC>, grid, kScanThreads, 0, s, p);
     if (rc != KVQ8_OK) return rc;
-    return launch_dependent(beam_pick_kernel<T, VEC>, (unsigned)p.n_rows, kPickThreads, kMaxWindowRows * p.n_out * (int)sizeof(double), s, p);
+    return launch_dependent(beam_pick_kernel<T, VEC>, (unsigned)p.n_rows, kPickThreads, kMaxWindowRows * p.n_out * (int)sizeof(int64_t), s, p);
 }
 
 }  // namespace
@@ -429,7 +455,7 @@ extern "C" size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs,
     SelectParams p = {};
     p.n_rows = n_rows, p.vocab = vocab, p.n_seqs = n_seqs, p.n_out = n_out;
     p.n_groups = groups_of(vocab);
-    p.n_parts = p.n_groups / kWarpGroups;
+    p.n_parts = p.n_groups / kWarpGroups<float>;  // fp32 has the most
     return carve(p, nullptr);
 }
 
@@ -454,7 +480,7 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t logits_stride,
     p.ended = ended, p.parents = parents, p.tokens = tokens, p.totals = totals;
     p.n_rows = n_rows, p.vocab = vocab, p.n_seqs = n_seqs, p.n_out = n_out;
     p.n_groups = groups_of(vocab);
-    p.n_parts = p.n_groups / kWarpGroups;
+    p.n_parts = p.n_groups / (dtype == KVQ8_F32 ? kWarpGroups<float> : kWarpGroups<__half>);
     carve(p, static_cast<unsigned char*>(workspace));
     // eight values a load where every row starts on their size and holds whole groups of eight
     const bool vec = vocab % 8 == 0 && logits_stride % 8 == 0 && aligned_to(logits, 8 * esz);
