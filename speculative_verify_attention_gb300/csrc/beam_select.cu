@@ -6,10 +6,10 @@
 // One pass over the logits.  A warp holds four groups of 256 consecutive values in registers and leaves behind each group's
 // maximum and one partial sum of exponentials: 1/100 of what it read.  Ordered by (maximum descending, place ascending), the
 // n_out best groups hold the row's n_out best values: a value outside them has n_out values before it, one in each.  So the
-// second kernel, a block per row, picks those groups, reads them again, picks the values, and the last block of a request to
-// finish joins its rows' lists.
+// second kernel, a block per row, picks those groups, reads them again and picks the values; a request's blocks form a cluster,
+// whose first block joins their lists.
 // Bound: the logits' bytes in the first kernel; latency in the second.
-#include <float.h>
+#include <cooperative_groups.h>
 
 #include "paged.cuh"
 
@@ -18,10 +18,8 @@ namespace {
 
 constexpr int kScanThreads = 256;
 constexpr int kGroup = 256;        // values of a group: eight a lane
-// Groups that a warp holds at once: 128 bytes of fp32, as many values twice of the others.
-template <typename T>
-constexpr int kWarpGroups = sizeof(T) == 4 ? 4 : 8;
-constexpr int kPadGroups = 8;      // a row's groups are counted in these
+constexpr int kWarpGroups = 4;     // groups that a warp holds at once
+constexpr int kManyParts = 152 * 40;  // parts that the GPU's warps hold at once
 constexpr int kSearchThreads = 256;
 constexpr int kPickThreads = kSearchThreads + 32;
 constexpr int kMaxOut = 64;
@@ -51,13 +49,7 @@ struct SelectParams {
     // workspace
     int32_t* group_max;     // [n_rows][n_groups], ordered as whole numbers
     Part* parts;            // [n_rows][n_parts]
-    int64_t* list_order;    // [n_rows][n_out] weight * total, descending, ordered as whole numbers
-    float* list_total;
-    int32_t* list_token;
-    int32_t* list_count;    // [n_rows]
-    int32_t* seq_of;        // [n_rows]
-    uint32_t* done;         // [n_seqs] rows finished
-    int n_rows, vocab, n_seqs, n_out, n_groups, n_parts;
+    int n_rows, vocab, n_seqs, n_out, n_groups, n_parts, turns;
 };
 
 // fp32 as whole numbers of the same order (-0 as 0).
@@ -88,6 +80,13 @@ __device__ __forceinline__ bool rows_of(const SelectParams& p, int b, int& first
     return first >= 0 && first < last && last <= p.n_rows && rows <= kMaxWindowRows;
 }
 
+__device__ __forceinline__ void fill_lowest(Eight<float>& x) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.v[i] = -INFINITY;
+}
+__device__ __forceinline__ void fill_lowest(Eight<__half>& x) { x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0xfc00fc00u; }
+__device__ __forceinline__ void fill_lowest(Eight<__nv_bfloat16>& x) { x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0xff80ff80u; }
+
 // Eight values of a group, -inf behind the row's end.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_eight(Eight<T>& x, const T* row, int at, int vocab) {
@@ -95,8 +94,7 @@ __device__ __forceinline__ void load_eight(Eight<T>& x, const T* row, int at, in
         if (at < vocab) {
             x.load_whole(row + at);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x.put(i, T(-INFINITY));
+            fill_lowest(x);
         }
     } else {
 #pragma unroll
@@ -104,69 +102,80 @@ __device__ __forceinline__ void load_eight(Eight<T>& x, const T* row, int at, in
     }
 }
 
+// Every other value's larger neighbour, the larger of both at last; NaN loses.
+__device__ __forceinline__ float largest(const Eight<float>& x) {
+    float m = fmaxf(x.v[0], x.v[1]);
+#pragma unroll
+    for (int i = 2; i < 8; ++i) m = fmaxf(m, x.v[i]);
+    return m;
+}
+__device__ __forceinline__ float largest(const Eight<__half>& x) {
+    const __half2 m = __hmax2(__hmax2(u32_as_h2(x.w[0]), u32_as_h2(x.w[1])), __hmax2(u32_as_h2(x.w[2]), u32_as_h2(x.w[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float largest(const Eight<__nv_bfloat16>& x) {
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(x.w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+// A warp takes p.turns parts of a row, the loads of the next one on their way while it works on one.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ SelectParams p) {
+    constexpr int G = kWarpGroups;
     const int lane = threadIdx.x & 31, row = blockIdx.y;
-    const int part = blockIdx.x * (kScanThreads / 32) + (threadIdx.x >> 5);
+    int part = blockIdx.x * p.turns * (kScanThreads / 32) + (threadIdx.x >> 5);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0 && row == 0) {  // the request of every row; what the second kernel counts; requests without rows
-        for (int b = threadIdx.x; b < p.n_seqs; b += kScanThreads) {
-            int first, rows;
-            p.done[b] = 0u;
-            if (rows_of(p, b, first, rows)) {
-                for (int r = 0; r < rows; ++r) p.seq_of[first + r] = b;
-            } else {
-                for (int k = 0; k < p.n_out; ++k) {
-                    const int64_t o = (int64_t)b * p.n_out + k;
-                    p.parents[o] = p.tokens[o] = -1;
-                    p.totals[o] = -INFINITY;
-                }
+    if (p.ended && __ldg(p.ended + row) >= 0) return;
+    const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride + lane * 8;
+    Eight<T> next[G];
+    auto load = [&](int part) {
+#pragma unroll
+        for (int u = 0; u < G; ++u) load_eight<T, VEC>(next[u], x, (part * G + u) * kGroup, p.vocab - lane * 8);
+    };
+    if (part < p.n_parts) load(part);
+    for (int turn = 0; turn < p.turns && part < p.n_parts; ++turn, part += kScanThreads / 32) {
+        Eight<T> raw[G];
+#pragma unroll
+        for (int u = 0; u < G; ++u) raw[u] = next[u];
+        if (turn + 1 < p.turns && part + kScanThreads / 32 < p.n_parts) load(part + kScanThreads / 32);
+        int32_t top[G], most = ordered(-INFINITY);
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
+            float m = largest(raw[u]);
+            if (!(m > -INFINITY)) m = -INFINITY;
+            top[u] = __reduce_max_sync(0xffffffffu, ordered(m));
+            most = max(most, top[u]);
+        }
+        const float m = from_ordered(most);
+        // 2^(x log2 e - e) with e a whole number near the maximum: one rounding a value, and parts join by powers of two
+        const float e = rintf(m * kLog2e);
+        float s = 0.0f;
+        if (fabsf(m) < kLarge) {
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                float v[8];
+                raw[u].floats(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += ex2_approx(__fmaf_rn(v[i], kLog2e, -e));
+            }
+        } else {
+            const bool any = fabsf(m) < INFINITY;
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                float v[8];
+                raw[u].floats(v);  // of -inf alone nothing; a NaN or +inf makes the sum NaN
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += any ? ex2_approx((v[i] - m) * kLog2e) : v[i] == -INFINITY ? 0.0f : NAN;
             }
         }
-    }
-    if (part >= p.n_parts || (p.ended && __ldg(p.ended + row) >= 0)) return;
-    const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-    constexpr int G = kWarpGroups<T>;
-    Eight<T> raw[G];
 #pragma unroll
-    for (int u = 0; u < G; ++u) load_eight<T, VEC>(raw[u], x, (part * G + u) * kGroup + lane * 8, p.vocab);
-    int32_t top[G], most = ordered(-INFINITY);
-#pragma unroll
-    for (int u = 0; u < G; ++u) {
-        float v[8];
-        raw[u].floats(v);
-        float m = fmaxf(v[0], v[1]);
-#pragma unroll
-        for (int i = 2; i < 8; ++i) m = fmaxf(m, v[i]);
-        if (!(m > -INFINITY)) m = -INFINITY;
-        top[u] = __reduce_max_sync(0xffffffffu, ordered(m));
-        most = max(most, top[u]);
-    }
-    const float m = from_ordered(most);
-    // 2^(x log2 e - e) with e a rounded multiple near the maximum: one rounding a value, and parts join by powers of two
-    const float e = rintf(m * kLog2e);
-    const bool plain = fabsf(m) < kLarge, any = fabsf(m) < INFINITY;
-    float s = 0.0f;
-#pragma unroll
-    for (int u = 0; u < G; ++u) {
-        float v[8];
-        raw[u].floats(v);
-        if (plain) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s += ex2_approx(__fmaf_rn(v[i], kLog2e, -e));
-        } else {  // of -inf alone nothing; a NaN or +inf makes the sum NaN
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s += any ? ex2_approx((v[i] - m) * kLog2e) : v[i] == -INFINITY ? 0.0f : NAN;
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            p.parts[(int64_t)row * p.n_parts + part] = Part{m, e, s};
+            *reinterpret_cast<int4*>(p.group_max + (int64_t)row * p.n_groups + part * G) = make_int4(top[0], top[1], top[2], top[3]);
         }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-        p.parts[(int64_t)row * p.n_parts + part] = Part{m, e, s};
-        int4* to = reinterpret_cast<int4*>(p.group_max + (int64_t)row * p.n_groups + part * G);
-#pragma unroll
-        for (int u = 0; u < G; u += 4) to[u / 4] = make_int4(top[u], top[u + 1], top[u + 2], top[u + 3]);
     }
 }
 
@@ -211,7 +220,9 @@ __device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const 
         search_sync();
     };
     auto add = [&](uint64_t k) {
-        if (s.n + kSearchThreads > kListCap) cut();
+        const bool full = s.n + kSearchThreads > kListCap;
+        search_sync();  // every thread has seen the same count before the first one adds to it
+        if (full) cut();
         if (k > s.above) s.key[atomicAdd(&s.n, 1)] = k;
         search_sync();
     };
@@ -236,183 +247,212 @@ __device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const 
     return s.n;
 }
 
-// Block: one row.  Its first eight warps look for the row's best values, the ninth sums its exponentials.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid_constant__ SelectParams p) {
-    extern __shared__ __align__(16) unsigned char s_join[];  // the join: the rows' orders
-    __shared__ Search s;
-    __shared__ double s_norm;
-    __shared__ int s_last, s_found, s_count[kMaxWindowRows];
-    const int tid = threadIdx.x, row = blockIdx.x, n_out = p.n_out;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int32_t* gm = p.group_max + (int64_t)row * p.n_groups;
-    const int b = __ldg(p.seq_of + row);
-    const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
-    const int ended = p.ended ? __ldg(p.ended + row) : -1;
-    int32_t k[kKeep];
-    const int32_t lowest = ordered(-INFINITY);
-    if (tid < kSearchThreads) {
-#pragma unroll
-        for (int u = 0; u < kKeep; ++u) {
-            const int g = u * kSearchThreads + tid;
-            k[u] = g < p.n_groups && ended < 0 ? __ldg(gm + g) : lowest;
-        }
-    }
-    if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
-    int first, rows;
-    if (b < 0 || b >= p.n_seqs || !rows_of(p, b, first, rows) || row < first || row >= first + rows) return;
-    const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY, live = usable && ended < 0;
-    if (live && tid < kSearchThreads) {
-        // a bound: the n_out-th best of the threads' best groups
-        int32_t m = k[0];
-#pragma unroll
-        for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
-        for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, __ldg(gm + g));
-        s.top[tid] = m;
-        search_sync();
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < kSearchThreads / 4; ++j) {
-            const int4 o = reinterpret_cast<const int4*>(s.top)[j];
-            rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
-        }
-        if (rank < n_out) atomicMin(&s.bound, m);
-        search_sync();
-        // the groups that reach it, and their values that do; -inf is none
-        const int32_t bound = max(s.bound, lowest + 1);
-        auto group = [&](int32_t key, int g) {
-            if (key < bound) return;
-            const int at = atomicAdd(&s.n_groups, 1);
-            if (at < kGroupCap) s.group[at] = (uint32_t)g;
-        };
-#pragma unroll
-        for (int u = 0; u < kKeep; ++u) group(k[u], u * kSearchThreads + tid);
-        for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(__ldg(gm + g), g);
-        search_sync();
-        const int groups = s.n_groups;
-        const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-        int found = groups <= kGroupCap ? 0 : kListCap + 1;
-        if (!found) {
-#pragma unroll 2
-            for (int i = tid >> 5; i < groups; i += kSearchThreads / 32) {
-                const int at = (int)s.group[i] * kGroup + (tid & 31) * 8;
-                Eight<T> raw;
-                load_eight<T, VEC>(raw, x, at, p.vocab);
-                float v[8];
-                raw.floats(v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int32_t o = ordered(v[e]);
-                    if (o < bound || v[e] != v[e]) continue;
-                    const int to = atomicAdd(&s.n, 1);
-                    if (to < kListCap) s.key[to] = key_of(o, (uint32_t)(at + e));
-                }
-            }
-            search_sync();
-            found = s.n;
-        }
-        if (found <= kListCap)
-            rank_keys(s, found, n_out);
-        else
-            found = pick_slowly<T, VEC>(s, p, x, gm);
-        if (tid == 0) s_found = min(found, n_out);
-    } else if (live) {
-        // parts scaled by powers of two to the largest one's, added as whole numbers of 2^-32, so that their order does not matter
-        const int lane = tid & 31;
-        const Part* parts = p.parts + (int64_t)row * p.n_parts;
-        int32_t m = lowest;
-        bool bad = false;
-        for (int i = lane; i < p.n_parts; i += 32) {
-            const Part q = parts[i];
-            m = max(m, ordered(q.m));
-            bad |= q.s != q.s;
-        }
-        const float top = from_ordered(__reduce_max_sync(0xffffffffu, m));
-        bad = __any_sync(0xffffffffu, bad);
-        const float e = rintf(top * kLog2e);
-        const bool plain = fabsf(top) < kLarge;
-        unsigned long long sum = 0;
-        for (int i = lane; i < p.n_parts; i += 32) {
-            const Part q = parts[i];
-            float v = 0.0f;
-            if (plain && fabsf(q.m) < kLarge)
-                v = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
-            else if (q.m > -INFINITY)
-                v = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
-            sum += __float2ull_rn(v * 0x1p32f);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) {
-            const double total = (double)sum * 0x1p-32;
-            const double norm = plain ? ((double)e + log2(total)) * (1.0 / (double)kLog2e) : (double)top + log(total);
-            s_norm = bad ? (double)INFINITY : norm;
-        }
-    }
-    __syncthreads();
-    const int64_t out0 = (int64_t)row * n_out;
-    int count = usable ? 1 : 0;
-    double total = (double)score;
-    int32_t token = ended;
-    if (live) {
-        count = fabs(s_norm) < (double)INFINITY ? s_found : 0;
-        if (tid < count) {
-            total += (double)key_value(s.best[tid]) - s_norm;
-            token = (int32_t)key_place(s.best[tid]);
-        }
-    }
-    if (tid < count) {
-        p.list_order[out0 + tid] = ordered(total * (double)weight);
-        p.list_total[out0 + tid] = (float)total;
-        p.list_token[out0 + tid] = token;
-    }
-    // the last row of a request to be done joins its rows' lists
-    if (tid == 0) p.list_count[row] = count;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(p.done + b, 1u) == (uint32_t)(rows - 1);
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    int64_t* order = reinterpret_cast<int64_t*>(s_join);
-    if (tid < rows) s_count[tid] = __ldcg(p.list_count + first + tid);
-    for (int i = tid; i < rows * n_out; i += kPickThreads) order[i] = __ldcg(p.list_order + (int64_t)first * n_out + i);
-    __syncthreads();
-    int n_all = 0;
-    for (int r = 0; r < rows; ++r) n_all += s_count[r];
-    const int64_t to = (int64_t)b * n_out;
-    for (int i = tid; i < rows * n_out; i += kPickThreads) {
-        const int r = i / n_out, j = i - r * n_out;
-        if (j >= s_count[r]) continue;
-        const int64_t mine = order[i];
-        int rank = j;
-        for (int q = 0; q < rows && rank < n_out; ++q) {
-            if (q == r) continue;
-            const int64_t* o = order + q * n_out;
-            int lo = 0, hi = s_count[q];  // how many of row q come before: more, or as much and of a lower row
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (o[mid] > mine || (o[mid] == mine && q < r))
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            rank += lo;
-        }
-        if (rank < n_out) {
-            p.parents[to + rank] = first + r;
-            p.tokens[to + rank] = __ldcg(p.list_token + (int64_t)first * n_out + i);
-            p.totals[to + rank] = __ldcg(p.list_total + (int64_t)first * n_out + i);
-        }
-    }
-    for (int k = n_all + tid; k < n_out; k += kPickThreads) {
-        p.parents[to + k] = p.tokens[to + k] = -1;
-        p.totals[to + k] = -INFINITY;
-    }
+// What the blocks of a request's cluster have found: block c has the rows c, c + cluster, ...; n_out places each.
+struct Lists {
+    int64_t* order;     // weight * total, descending, ordered as whole numbers
+    float* total;
+    int32_t* token;
+    int64_t* joined;    // the join: all rows' orders, in the first block
+    __device__ Lists(unsigned char* at, int rows, int n_out)
+        : order(reinterpret_cast<int64_t*>(at)), total(reinterpret_cast<float*>(order + rows * n_out)),
+          token(reinterpret_cast<int32_t*>(total + rows * n_out)), joined(reinterpret_cast<int64_t*>(token + rows * n_out)) {}
+};
+int lists_bytes(int cluster, int n_out) {
+    const int rows = (kMaxWindowRows + cluster - 1) / cluster;
+    return rows * n_out * 16 + kMaxWindowRows * n_out * 8;
 }
 
-int groups_of(int vocab) { return (vocab + kGroup * kPadGroups - 1) / (kGroup * kPadGroups) * kPadGroups; }
+// A cluster of blocks: one request.  A block's first eight warps look for a row's best values, the ninth sums its exponentials.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid_constant__ SelectParams p) {
+    extern __shared__ __align__(16) unsigned char s_lists[];
+    __shared__ Search s;
+    __shared__ double s_norm;
+    __shared__ int s_found, s_count[kMaxWindowRows], s_counts[kMaxWindowRows];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int size = (int)cluster.num_blocks(), me = (int)cluster.block_rank(), b = (int)blockIdx.x / size;
+    const int tid = threadIdx.x, n_out = p.n_out;
+    const Lists lists(s_lists, (kMaxWindowRows + size - 1) / size, n_out);
+    const int64_t to = (int64_t)b * n_out;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int first, rows;
+    if (!rows_of(p, b, first, rows)) {
+        for (int k = tid; k < n_out && me == 0; k += kPickThreads) {
+            p.parents[to + k] = p.tokens[to + k] = -1;
+            p.totals[to + k] = -INFINITY;
+        }
+        return;
+    }
+    const int32_t lowest = ordered(-INFINITY);
+    for (int mine = me; mine < rows; mine += size) {
+        const int row = first + mine;
+        const int32_t* gm = p.group_max + (int64_t)row * p.n_groups;
+        const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
+        const int ended = p.ended ? __ldg(p.ended + row) : -1;
+        int32_t k[kKeep];
+        if (tid < kSearchThreads) {
+#pragma unroll
+            for (int u = 0; u < kKeep; ++u) {
+                const int g = u * kSearchThreads + tid;
+                k[u] = g < p.n_groups ? __ldg(gm + g) : lowest;
+            }
+        }
+        if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
+        const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY, live = usable && ended < 0;
+        if (live && tid < kSearchThreads) {
+            // a bound: the n_out-th best of the threads' best groups
+            int32_t m = k[0];
+#pragma unroll
+            for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
+            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, __ldg(gm + g));
+            s.top[tid] = m;
+            search_sync();
+            int rank = 0;
+#pragma unroll 8
+            for (int j = 0; j < kSearchThreads / 4; ++j) {
+                const int4 o = reinterpret_cast<const int4*>(s.top)[j];
+                rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+            }
+            if (rank < n_out) atomicMin(&s.bound, m);
+            search_sync();
+            // the groups that reach it, and their values that do; -inf is none
+            const int32_t bound = max(s.bound, lowest + 1);
+            auto group = [&](int32_t key, int g) {
+                if (key < bound) return;
+                const int at = atomicAdd(&s.n_groups, 1);
+                if (at < kGroupCap) s.group[at] = (uint32_t)g;
+            };
+#pragma unroll
+            for (int u = 0; u < kKeep; ++u) group(k[u], u * kSearchThreads + tid);
+            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(__ldg(gm + g), g);
+            search_sync();
+            const int groups = s.n_groups;
+            const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+            int found = groups <= kGroupCap ? 0 : kListCap + 1;
+            if (!found) {
+#pragma unroll 2
+                for (int i = tid >> 5; i < groups; i += kSearchThreads / 32) {
+                    const int at = (int)s.group[i] * kGroup + (tid & 31) * 8;
+                    Eight<T> raw;
+                    load_eight<T, VEC>(raw, x, at, p.vocab);
+                    float v[8];
+                    raw.floats(v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int32_t o = ordered(v[e]);
+                        if (o < bound || v[e] != v[e]) continue;
+                        const int place = atomicAdd(&s.n, 1);
+                        if (place < kListCap) s.key[place] = key_of(o, (uint32_t)(at + e));
+                    }
+                }
+                search_sync();
+                found = s.n;
+            }
+            if (found <= kListCap)
+                rank_keys(s, found, n_out);
+            else
+                found = pick_slowly<T, VEC>(s, p, x, gm);
+            if (tid == 0) s_found = min(found, n_out);
+        } else if (live) {
+            // parts scaled by powers of two to the largest one's, added as whole numbers of 2^-32, so that their order does not
+            // matter
+            const int lane = tid & 31;
+            const Part* parts = p.parts + (int64_t)row * p.n_parts;
+            int32_t m = lowest;
+            bool bad = false;
+            for (int i = lane; i < p.n_parts; i += 32) {
+                const Part q = parts[i];
+                m = max(m, ordered(q.m));
+                bad |= q.s != q.s;
+            }
+            const float top = from_ordered(__reduce_max_sync(0xffffffffu, m));
+            bad = __any_sync(0xffffffffu, bad);
+            const float e = rintf(top * kLog2e);
+            const bool plain = fabsf(top) < kLarge;
+            unsigned long long sum = 0;
+            for (int i = lane; i < p.n_parts; i += 32) {
+                const Part q = parts[i];
+                float v = 0.0f;
+                if (plain && fabsf(q.m) < kLarge)
+                    v = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
+                else if (q.m > -INFINITY)
+                    v = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
+                sum += __float2ull_rn(v * 0x1p32f);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) {
+                const double total = (double)sum * 0x1p-32;
+                const double norm = plain ? ((double)e + log2(total)) * (1.0 / (double)kLog2e) : (double)top + log(total);
+                s_norm = bad ? (double)INFINITY : norm;
+            }
+        }
+        __syncthreads();
+        int count = usable ? 1 : 0;
+        double total = (double)score;
+        int32_t token = ended;
+        if (live) {
+            count = fabs(s_norm) < (double)INFINITY ? s_found : 0;
+            if (tid < count) {
+                total += (double)key_value(s.best[tid]) - s_norm;
+                token = (int32_t)key_place(s.best[tid]);
+            }
+        }
+        const int at = mine / size * n_out + tid;
+        if (tid < count) {
+            lists.order[at] = ordered(total * (double)weight);
+            lists.total[at] = (float)total;
+            lists.token[at] = token;
+        }
+        if (tid == 0) s_count[mine / size] = count;
+        __syncthreads();
+    }
+    cluster.sync();
+    if (me == 0) {
+        if (tid < rows) s_counts[tid] = cluster.map_shared_rank(s_count, tid % size)[tid / size];
+        for (int i = tid; i < rows * n_out; i += kPickThreads) {
+            const int r = i / n_out, j = i - r * n_out;
+            lists.joined[i] = cluster.map_shared_rank(lists.order, r % size)[r / size * n_out + j];
+        }
+        __syncthreads();
+        int n_all = 0;
+        for (int r = 0; r < rows; ++r) n_all += s_counts[r];
+        for (int i = tid; i < rows * n_out; i += kPickThreads) {
+            const int r = i / n_out, j = i - r * n_out;
+            if (j >= s_counts[r]) continue;
+            const int64_t mine = lists.joined[i];
+            int rank = j;
+            for (int q = 0; q < rows && rank < n_out; ++q) {
+                if (q == r) continue;
+                const int64_t* o = lists.joined + q * n_out;
+                int lo = 0, hi = s_counts[q];  // how many of row q come before: more, or as much and of a lower row
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (o[mid] > mine || (o[mid] == mine && q < r))
+                        lo = mid + 1;
+                    else
+                        hi = mid;
+                }
+                rank += lo;
+            }
+            if (rank < n_out) {
+                const int from = r / size * n_out + j;
+                p.parents[to + rank] = first + r;
+                p.tokens[to + rank] = cluster.map_shared_rank(lists.token, r % size)[from];
+                p.totals[to + rank] = cluster.map_shared_rank(lists.total, r % size)[from];
+            }
+        }
+        for (int k = n_all + tid; k < n_out; k += kPickThreads) {
+            p.parents[to + k] = p.tokens[to + k] = -1;
+            p.totals[to + k] = -INFINITY;
+        }
+    }
+    cluster.sync();  // the others' lists are read
+}
+
+int groups_of(int vocab) { return (vocab + kGroup * kWarpGroups - 1) / (kGroup * kWarpGroups) * kWarpGroups; }
 
 // The workspace's arrays, in order of their alignment; the size where base is null.
 size_t carve(SelectParams& p, unsigned char* base) {
@@ -423,13 +463,7 @@ size_t carve(SelectParams& p, unsigned char* base) {
     };
     const size_t rows = (size_t)p.n_rows;
     take(p.group_max, rows * p.n_groups);
-    take(p.list_order, rows * p.n_out);
     take(p.parts, rows * p.n_parts);
-    take(p.list_total, rows * p.n_out);
-    take(p.list_token, rows * p.n_out);
-    take(p.list_count, rows);
-    take(p.seq_of, rows);
-    take(p.done, (size_t)p.n_seqs);
     return at;
 }
 
@@ -438,12 +472,34 @@ bool select_shape(int n_rows, int vocab, int n_seqs, int n_out) {
 }
 
 template <typename T, bool VEC>
-int launch_select(const SelectParams& p, cudaStream_t s) {
+int launch_select(SelectParams p, cudaStream_t s) {
     const int warps = kScanThreads / 32;
-    const dim3 grid((unsigned)((p.n_parts + warps - 1) / warps), (unsigned)p.n_rows);
+    // one part a warp where that leaves warps idle, up to four where there are many
+    const int64_t all = (int64_t)p.n_parts * p.n_rows;
+    p.turns = all < 2 * kManyParts ? 1 : all < 4 * kManyParts ? 2 : 4;
+    const dim3 grid((unsigned)((p.n_parts + warps * p.turns - 1) / (warps * p.turns)), (unsigned)p.n_rows);
     const int rc = launch_dependent(beam_scan_kernel<T, VEC>, grid, kScanThreads, 0, s, p);
     if (rc != KVQ8_OK) return rc;
-    return launch_dependent(beam_pick_kernel<T, VEC>, (unsigned)p.n_rows, kPickThreads, kMaxWindowRows * p.n_out * (int)sizeof(int64_t), s, p);
+    // a block a row, by the mean of the requests' rows
+    int cluster = 1;
+    while (cluster < 8 && (int64_t)cluster * p.n_seqs < p.n_rows) cluster *= 2;
+    static SmemOptIn opt;
+    const int opted = opt.ensure(beam_pick_kernel<T, VEC>, lists_bytes(1, kMaxOut));
+    if (opted != KVQ8_OK) return opted;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.n_seqs * cluster));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = (size_t)lists_bytes(cluster, p.n_out);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return launched(cudaLaunchKernelEx(&cfg, beam_pick_kernel<T, VEC>, p));
 }
 
 }  // namespace
@@ -455,7 +511,7 @@ extern "C" size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs,
     SelectParams p = {};
     p.n_rows = n_rows, p.vocab = vocab, p.n_seqs = n_seqs, p.n_out = n_out;
     p.n_groups = groups_of(vocab);
-    p.n_parts = p.n_groups / kWarpGroups<float>;  // fp32 has the most
+    p.n_parts = p.n_groups / kWarpGroups;
     return carve(p, nullptr);
 }
 
@@ -480,7 +536,7 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t logits_stride,
     p.ended = ended, p.parents = parents, p.tokens = tokens, p.totals = totals;
     p.n_rows = n_rows, p.vocab = vocab, p.n_seqs = n_seqs, p.n_out = n_out;
     p.n_groups = groups_of(vocab);
-    p.n_parts = p.n_groups / (dtype == KVQ8_F32 ? kWarpGroups<float> : kWarpGroups<__half>);
+    p.n_parts = p.n_groups / kWarpGroups;
     carve(p, static_cast<unsigned char*>(workspace));
     // eight values a load where every row starts on their size and holds whole groups of eight
     const bool vec = vocab % 8 == 0 && logits_stride % 8 == 0 && aligned_to(logits, 8 * esz);
