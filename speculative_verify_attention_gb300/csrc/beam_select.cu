@@ -7,7 +7,7 @@
 // maximum and one partial sum of exponentials: 1/100 of what it read.  Ordered by (maximum descending, place ascending), the
 // n_out best groups hold the row's n_out best values: a value outside them has n_out values before it, one in each.  So the
 // second kernel, a block per row, picks those groups, reads them again and picks the values; a request's blocks form a cluster,
-// whose first block joins their lists.
+// which joins their lists through shared memory.
 // Bound: the logits' bytes in the first kernel; latency in the second.
 #include <cooperative_groups.h>
 
@@ -24,6 +24,8 @@ constexpr int kSearchThreads = 256;
 constexpr int kPickThreads = kSearchThreads + 32;
 constexpr int kMaxOut = 64;
 constexpr int kKeep = 4;           // groups of a row that a searching thread keeps
+constexpr int kPartKeep = 8;       // parts of a row that a lane of the summing warp keeps
+constexpr int kFetch = 3;          // groups that a warp fetches at once
 constexpr int kGroupCap = 256;     // groups, and values, that the second kernel keeps of a row
 constexpr int kListCap = 512;
 
@@ -186,7 +188,7 @@ struct Search {
     uint64_t key[kListCap];      // candidates, as key_of
     uint64_t best[kMaxOut];      // the row's best, in order
     uint32_t group[kGroupCap];
-    int32_t top[kSearchThreads];
+    int32_t top[kSearchThreads / 2];
     uint64_t above;              // keys below this are none of the best (slow path)
     int32_t bound;               // values below this are none of the best
     int n_groups, n;
@@ -252,7 +254,7 @@ struct Lists {
     int64_t* order;     // weight * total, descending, ordered as whole numbers
     float* total;
     int32_t* token;
-    int64_t* joined;    // the join: all rows' orders, in the first block
+    int64_t* joined;    // the join: all rows' orders
     __device__ Lists(unsigned char* at, int rows, int n_out)
         : order(reinterpret_cast<int64_t*>(at)), total(reinterpret_cast<float*>(order + rows * n_out)),
           token(reinterpret_cast<int32_t*>(total + rows * n_out)), joined(reinterpret_cast<int64_t*>(token + rows * n_out)) {}
@@ -302,20 +304,26 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
         if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
         const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY, live = usable && ended < 0;
         if (live && tid < kSearchThreads) {
-            // a bound: the n_out-th best of the threads' best groups
+            // a bound: the n_out-th best of 64 or 128 shares of the groups; about 1.1 n_out groups reach it
+            const int lanes = n_out <= 16 ? 4 : 2;
             int32_t m = k[0];
 #pragma unroll
             for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
             for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, __ldg(gm + g));
-            s.top[tid] = m;
+            for (int o = 1; o < lanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (tid % lanes == 0) s.top[tid / lanes] = m;
             search_sync();
-            int rank = 0;
-#pragma unroll 8
-            for (int j = 0; j < kSearchThreads / 4; ++j) {
-                const int4 o = reinterpret_cast<const int4*>(s.top)[j];
-                rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+            const int tops = kSearchThreads / lanes;
+            if (tid < tops) {
+                m = s.top[tid];
+                int rank = 0;
+#pragma unroll 4
+                for (int j = 0; j < tops / 4; ++j) {
+                    const int4 o = reinterpret_cast<const int4*>(s.top)[j];
+                    rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+                }
+                if (rank < n_out) atomicMin(&s.bound, m);
             }
-            if (rank < n_out) atomicMin(&s.bound, m);
             search_sync();
             // the groups that reach it, and their values that do; -inf is none
             const int32_t bound = max(s.bound, lowest + 1);
@@ -332,19 +340,30 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
             const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
             int found = groups <= kGroupCap ? 0 : kListCap + 1;
             if (!found) {
-#pragma unroll 2
-                for (int i = tid >> 5; i < groups; i += kSearchThreads / 32) {
-                    const int at = (int)s.group[i] * kGroup + (tid & 31) * 8;
-                    Eight<T> raw;
-                    load_eight<T, VEC>(raw, x, at, p.vocab);
-                    float v[8];
-                    raw.floats(v);
+                const float least = from_ordered(bound);
+                for (int i0 = tid >> 5; i0 < groups; i0 += kFetch * (kSearchThreads / 32)) {
+                    Eight<T> raw[kFetch];
+                    int at[kFetch];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int32_t o = ordered(v[e]);
-                        if (o < bound || v[e] != v[e]) continue;
-                        const int place = atomicAdd(&s.n, 1);
-                        if (place < kListCap) s.key[place] = key_of(o, (uint32_t)(at + e));
+                    for (int u = 0; u < kFetch; ++u) {
+                        const int i = i0 + u * (kSearchThreads / 32);
+                        at[u] = i < groups ? (int)s.group[i] * kGroup + (tid & 31) * 8 : p.vocab;
+                        load_eight<T, VEC>(raw[u], x, at[u], p.vocab);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kFetch; ++u) {
+                        if (!(largest(raw[u]) >= least)) continue;  // few lanes have one
+                        float v[8];
+                        raw[u].floats(v);
+#pragma unroll 1
+                        for (int e = 0; e < 8; ++e) {
+                            if (v[0] >= least) {
+                                const int place = atomicAdd(&s.n, 1);
+                                if (place < kListCap) s.key[place] = key_of(ordered(v[0]), (uint32_t)(at[u] + e));
+                            }
+#pragma unroll
+                            for (int w = 0; w < 7; ++w) v[w] = v[w + 1];
+                        }
                     }
                 }
                 search_sync();
@@ -362,25 +381,32 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
             const Part* parts = p.parts + (int64_t)row * p.n_parts;
             int32_t m = lowest;
             bool bad = false;
-            for (int i = lane; i < p.n_parts; i += 32) {
-                const Part q = parts[i];
+            Part kept[kPartKeep];
+#pragma unroll
+            for (int u = 0; u < kPartKeep; ++u) kept[u] = u * 32 + lane < p.n_parts ? parts[u * 32 + lane] : Part{-INFINITY, -INFINITY, 0.0f};
+            auto look = [&](const Part& q) {
                 m = max(m, ordered(q.m));
                 bad |= q.s != q.s;
-            }
+            };
+#pragma unroll
+            for (int u = 0; u < kPartKeep; ++u) look(kept[u]);
+            for (int i = kPartKeep * 32 + lane; i < p.n_parts; i += 32) look(parts[i]);
             const float top = from_ordered(__reduce_max_sync(0xffffffffu, m));
             bad = __any_sync(0xffffffffu, bad);
             const float e = rintf(top * kLog2e);
             const bool plain = fabsf(top) < kLarge;
             unsigned long long sum = 0;
-            for (int i = lane; i < p.n_parts; i += 32) {
-                const Part q = parts[i];
+            auto add = [&](const Part& q) {
                 float v = 0.0f;
                 if (plain && fabsf(q.m) < kLarge)
                     v = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
                 else if (q.m > -INFINITY)
                     v = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
                 sum += __float2ull_rn(v * 0x1p32f);
-            }
+            };
+#pragma unroll
+            for (int u = 0; u < kPartKeep; ++u) add(kept[u]);
+            for (int i = kPartKeep * 32 + lane; i < p.n_parts; i += 32) add(parts[i]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0) {
@@ -410,43 +436,49 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
         __syncthreads();
     }
     cluster.sync();
-    if (me == 0) {
+    if (me < rows) {  // each block places its own rows' continuations among all
         if (tid < rows) s_counts[tid] = cluster.map_shared_rank(s_count, tid % size)[tid / size];
-        for (int i = tid; i < rows * n_out; i += kPickThreads) {
-            const int r = i / n_out, j = i - r * n_out;
-            lists.joined[i] = cluster.map_shared_rank(lists.order, r % size)[r / size * n_out + j];
+        for (int r = tid / 32; r < rows; r += kPickThreads / 32) {
+            const int64_t* from = cluster.map_shared_rank(lists.order, r % size) + r / size * n_out;
+            for (int j = tid % 32; j < n_out; j += 32) lists.joined[r * n_out + j] = from[j];
         }
         __syncthreads();
-        int n_all = 0;
-        for (int r = 0; r < rows; ++r) n_all += s_counts[r];
-        for (int i = tid; i < rows * n_out; i += kPickThreads) {
-            const int r = i / n_out, j = i - r * n_out;
-            if (j >= s_counts[r]) continue;
-            const int64_t mine = lists.joined[i];
-            int rank = j;
-            for (int q = 0; q < rows && rank < n_out; ++q) {
-                if (q == r) continue;
-                const int64_t* o = lists.joined + q * n_out;
-                int lo = 0, hi = s_counts[q];  // how many of row q come before: more, or as much and of a lower row
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (o[mid] > mine || (o[mid] == mine && q < r))
-                        lo = mid + 1;
-                    else
-                        hi = mid;
+        // eight lanes a continuation, each with an eighth of the other rows
+        const int lane = tid % 8;
+        for (int r = me; r < rows; r += size) {
+            const int count = s_counts[r];
+            for (int j0 = 0; j0 < count; j0 += kPickThreads / 8) {
+                const int j = min(j0 + tid / 8, count - 1);
+                const int64_t mine = lists.joined[r * n_out + j];
+                int rank = lane == 0 ? j : 0;
+                for (int q = lane; q < rows; q += 8) {
+                    const int64_t* o = lists.joined + q * n_out;
+                    int lo = 0, hi = q == r ? 0 : s_counts[q];  // how many of row q come before: more, or as much and of a lower row
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (o[mid] > mine || (o[mid] == mine && q < r))
+                            lo = mid + 1;
+                        else
+                            hi = mid;
+                    }
+                    rank += lo;
                 }
-                rank += lo;
-            }
-            if (rank < n_out) {
-                const int from = r / size * n_out + j;
-                p.parents[to + rank] = first + r;
-                p.tokens[to + rank] = cluster.map_shared_rank(lists.token, r % size)[from];
-                p.totals[to + rank] = cluster.map_shared_rank(lists.total, r % size)[from];
+#pragma unroll
+                for (int o = 1; o < 8; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+                if (lane == 0 && j0 + tid / 8 < count && rank < n_out) {
+                    p.parents[to + rank] = first + r;
+                    p.tokens[to + rank] = lists.token[r / size * n_out + j];
+                    p.totals[to + rank] = lists.total[r / size * n_out + j];
+                }
             }
         }
-        for (int k = n_all + tid; k < n_out; k += kPickThreads) {
-            p.parents[to + k] = p.tokens[to + k] = -1;
-            p.totals[to + k] = -INFINITY;
+        if (me == 0) {
+            int n_all = 0;
+            for (int r = 0; r < rows; ++r) n_all += s_counts[r];
+            for (int k = n_all + tid; k < n_out; k += kPickThreads) {
+                p.parents[to + k] = p.tokens[to + k] = -1;
+                p.totals[to + k] = -INFINITY;
+            }
         }
     }
     cluster.sync();  // the others' lists are read
