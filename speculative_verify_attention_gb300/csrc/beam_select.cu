@@ -82,27 +82,88 @@ __device__ __forceinline__ bool rows_of(const SelectParams& p, int b, int& first
     return first >= 0 && first < last && last <= p.n_rows && rows <= kMaxWindowRows;
 }
 
-__device__ __forceinline__ void fill_lowest(Eight<float>& x) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x.v[i] = -INFINITY;
-}
-__device__ __forceinline__ void fill_lowest(Eight<__half>& x) { x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0xfc00fc00u; }
-__device__ __forceinline__ void fill_lowest(Eight<__nv_bfloat16>& x) { x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0xff80ff80u; }
+template <typename T>
+constexpr uint32_t kLowestWord = 0xff800000u;  // -inf, or two of them
+template <>
+constexpr uint32_t kLowestWord<__half> = 0xfc00fc00u;
+template <>
+constexpr uint32_t kLowestWord<__nv_bfloat16> = 0xff80ff80u;
 
-// Eight values of a group, -inf behind the row's end.
+// Eight consecutive values of a row as they are fetched, -inf outside the row.  VEC: the row starts on eight values' size and holds
+// whole groups of them.  Else the 16-byte pieces around them, and `shift` (of the row alone, as places are multiples of eight)
+// says where among those they start: a row of odd length costs a few selections instead of single loads.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_eight(Eight<T>& x, const T* row, int at, int vocab) {
-    if (VEC) {
-        if (at < vocab) {
-            x.load_whole(row + at);
-        } else {
-            fill_lowest(x);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x.put(i, at + i < vocab ? row[at + i] : T(-INFINITY));
+struct Fetch {
+    static constexpr int kPiece = 16 / (int)sizeof(T), kPieces = VEC ? 8 / kPiece : 8 / kPiece + 1;
+    uint32_t w[4 * kPieces];
+
+    static __device__ __forceinline__ int shift_of(const T* row) {
+        return VEC ? 0 : (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
     }
-}
+    __device__ __forceinline__ void load(const T* row, int at, int vocab, int shift) {
+        if constexpr (VEC) {
+            if (at < vocab) {
+                Eight<T> x;
+                x.load_whole(row + at);
+#pragma unroll
+                for (int i = 0; i < 4 * kPieces; ++i) w[i] = reinterpret_cast<const uint32_t*>(&x)[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4 * kPieces; ++i) w[i] = kLowestWord<T>;
+            }
+        } else {
+            load_pieces(row, at, vocab, shift);
+        }
+    }
+    __device__ __forceinline__ void load_pieces(const T* row, int at, int vocab, int shift) {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const int from = at - shift + k * kPiece;
+            if (from >= 0 && from + kPiece <= vocab) {
+                const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + from));
+                w[4 * k] = r.x, w[4 * k + 1] = r.y, w[4 * k + 2] = r.z, w[4 * k + 3] = r.w;
+            } else {  // the row's first and last piece
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[4 * k + i] = kLowestWord<T>;
+                if (from > -kPiece && from < vocab) {
+#pragma unroll
+                    for (int i = 0; i < kPiece; ++i)
+                        if (from + i >= 0 && from + i < vocab) put(k * kPiece + i, row[from + i]);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void put(int i, float v) { w[i] = __float_as_uint(v); }
+    template <typename H>
+    __device__ __forceinline__ void put(int i, H v) {
+        const uint32_t bits = *reinterpret_cast<const uint16_t*>(&v);
+        w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | bits << 16 : (w[i >> 1] & 0xffff0000u) | bits;
+    }
+    __device__ __forceinline__ Eight<T> eight(int shift) const {
+        Eight<T> x;
+        uint32_t v[4 * kPieces];
+#pragma unroll
+        for (int i = 0; i < 4 * kPieces; ++i) v[i] = w[i];
+        if constexpr (!VEC) {
+            const int words = sizeof(T) == 4 ? shift : shift >> 1;
+            if (words & 2) {
+#pragma unroll
+                for (int i = 0; i + 2 < 4 * kPieces; ++i) v[i] = v[i + 2];
+            }
+            if (words & 1) {
+#pragma unroll
+                for (int i = 0; i + 1 < 4 * kPieces; ++i) v[i] = v[i + 1];
+            }
+            if (sizeof(T) == 2 && (shift & 1)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < (int)(8 * sizeof(T) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = v[i];
+        return x;
+    }
+};
 
 // Every other value's larger neighbour, the larger of both at last; NaN loses.
 __device__ __forceinline__ float largest(const Eight<float>& x) {
@@ -130,17 +191,18 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.ended && __ldg(p.ended + row) >= 0) return;
-    const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride + lane * 8;
-    Eight<T> next[G];
+    const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+    const int shift = Fetch<T, VEC>::shift_of(x);
+    Fetch<T, VEC> next[G];
     auto load = [&](int part) {
 #pragma unroll
-        for (int u = 0; u < G; ++u) load_eight<T, VEC>(next[u], x, (part * G + u) * kGroup, p.vocab - lane * 8);
+        for (int u = 0; u < G; ++u) next[u].load(x, (part * G + u) * kGroup + lane * 8, p.vocab, shift);
     };
     if (part < p.n_parts) load(part);
     for (int turn = 0; turn < p.turns && part < p.n_parts; ++turn, part += kScanThreads / 32) {
         Eight<T> raw[G];
 #pragma unroll
-        for (int u = 0; u < G; ++u) raw[u] = next[u];
+        for (int u = 0; u < G; ++u) raw[u] = next[u].eight(shift);
         if (turn + 1 < p.turns && part + kScanThreads / 32 < p.n_parts) load(part + kScanThreads / 32);
         int32_t top[G], most = ordered(-INFINITY);
 #pragma unroll
@@ -180,6 +242,9 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         }
     }
 }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The threads that search (the others of the block sum).
 __device__ __forceinline__ void search_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -249,32 +314,41 @@ __device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const 
     return s.n;
 }
 
-// What the blocks of a request's cluster have found: block c has the rows c, c + cluster, ...; n_out places each.
+// What the blocks of a request's cluster have found: each has its rows' totals and tokens, n_out places a row (block c has the
+// rows c, c + cluster, ...), and all rows' orders.
 struct Lists {
     int64_t* order;     // weight * total, descending, ordered as whole numbers
     float* total;
     int32_t* token;
-    int64_t* joined;    // the join: all rows' orders
     __device__ Lists(unsigned char* at, int rows, int n_out)
-        : order(reinterpret_cast<int64_t*>(at)), total(reinterpret_cast<float*>(order + rows * n_out)),
-          token(reinterpret_cast<int32_t*>(total + rows * n_out)), joined(reinterpret_cast<int64_t*>(token + rows * n_out)) {}
+        : order(reinterpret_cast<int64_t*>(at)), total(reinterpret_cast<float*>(order + kMaxWindowRows * n_out)),
+          token(reinterpret_cast<int32_t*>(total + rows * n_out)) {}
 };
 int lists_bytes(int cluster, int n_out) {
     const int rows = (kMaxWindowRows + cluster - 1) / cluster;
-    return rows * n_out * 16 + kMaxWindowRows * n_out * 8;
+    return rows * n_out * 8 + kMaxWindowRows * n_out * 8;
 }
 
 // A cluster of blocks: one request.  A block's first eight warps look for a row's best values, the ninth sums its exponentials.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid_constant__ SelectParams p) {
     extern __shared__ __align__(16) unsigned char s_lists[];
     __shared__ Search s;
-    __shared__ double s_norm;
-    __shared__ int s_found, s_count[kMaxWindowRows], s_counts[kMaxWindowRows];
+    __shared__ double s_base;  // the row's score less its log sum exp
+    __shared__ int s_found, s_counts[kMaxWindowRows];
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = (int)cluster.num_blocks(), me = (int)cluster.block_rank(), b = (int)blockIdx.x / size;
     const int tid = threadIdx.x, n_out = p.n_out;
+    const int lane = tid & 31;
+    const bool sums = tid >= kSearchThreads;
+    // log2 near 1 + (lane + 1/2) / 32, by the summing warp's lanes, while the kernel before ends
+    double inverse = 0.0, log_of = 0.0;
+    if (sums) {
+        inverse = (double)__frcp_rn(1.0f + ((float)lane + 0.5f) * 0x1p-5f);
+        log_of = -log2(inverse);
+    }
+    cluster_arrive();  // (a block's shared memory is written by others once it has started)
     const Lists lists(s_lists, (kMaxWindowRows + size - 1) / size, n_out);
     const int64_t to = (int64_t)b * n_out;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -285,6 +359,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
             p.parents[to + k] = p.tokens[to + k] = -1;
             p.totals[to + k] = -INFINITY;
         }
+        cluster_wait();
         return;
     }
     const int32_t lowest = ordered(-INFINITY);
@@ -294,7 +369,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
         const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
         const int ended = p.ended ? __ldg(p.ended + row) : -1;
         int32_t k[kKeep];
-        if (tid < kSearchThreads) {
+        if (!sums) {
 #pragma unroll
             for (int u = 0; u < kKeep; ++u) {
                 const int g = u * kSearchThreads + tid;
@@ -303,7 +378,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
         }
         if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
         const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY, live = usable && ended < 0;
-        if (live && tid < kSearchThreads) {
+        if (live && !sums) {
             // a bound: the n_out-th best of 64 or 128 shares of the groups; about 1.1 n_out groups reach it
             const int lanes = n_out <= 16 ? 4 : 2;
             int32_t m = k[0];
@@ -341,28 +416,25 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
             int found = groups <= kGroupCap ? 0 : kListCap + 1;
             if (!found) {
                 const float least = from_ordered(bound);
+                const int shift = Fetch<T, VEC>::shift_of(x);
                 for (int i0 = tid >> 5; i0 < groups; i0 += kFetch * (kSearchThreads / 32)) {
-                    Eight<T> raw[kFetch];
+                    Fetch<T, VEC> raw[kFetch];
                     int at[kFetch];
 #pragma unroll
                     for (int u = 0; u < kFetch; ++u) {
                         const int i = i0 + u * (kSearchThreads / 32);
                         at[u] = i < groups ? (int)s.group[i] * kGroup + (tid & 31) * 8 : p.vocab;
-                        load_eight<T, VEC>(raw[u], x, at[u], p.vocab);
+                        raw[u].load(x, at[u], p.vocab, shift);
                     }
 #pragma unroll
                     for (int u = 0; u < kFetch; ++u) {
-                        if (!(largest(raw[u]) >= least)) continue;  // few lanes have one
                         float v[8];
-                        raw[u].floats(v);
-#pragma unroll 1
-                        for (int e = 0; e < 8; ++e) {
-                            if (v[0] >= least) {
-                                const int place = atomicAdd(&s.n, 1);
-                                if (place < kListCap) s.key[place] = key_of(ordered(v[0]), (uint32_t)(at[u] + e));
-                            }
+                        raw[u].eight(shift).floats(v);
 #pragma unroll
-                            for (int w = 0; w < 7; ++w) v[w] = v[w + 1];
+                        for (int e = 0; e < 8; ++e) {
+                            if (!(v[e] >= least)) continue;
+                            const int place = atomicAdd(&s.n, 1);
+                            if (place < kListCap) s.key[place] = key_of(ordered(v[e]), (uint32_t)(at[u] + e));
                         }
                     }
                 }
@@ -377,7 +449,6 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
         } else if (live) {
             // parts scaled by powers of two to the largest one's, added as whole numbers of 2^-32, so that their order does not
             // matter
-            const int lane = tid & 31;
             const Part* parts = p.parts + (int64_t)row * p.n_parts;
             int32_t m = lowest;
             bool bad = false;
@@ -409,10 +480,19 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
             for (int i = kPartKeep * 32 + lane; i < p.n_parts; i += 32) add(parts[i]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            // log2 of the sum = 2^k (1 + m): by the lane nearest to 1 + m, and the series of log2(1 + f), |f| <= 1/64 (its terms
+            // from f^2 on in fp32: 2^-13 of 2^-24)
+            const int k = 63 - __clzll((long long)(sum | 1));
+            const uint64_t mantissa = sum << 1 << (63 - k);
+            const int near = (int)(mantissa >> 59);
+            const double m1 = __longlong_as_double((long long)(0x3ff0000000000000ull | mantissa >> 12));
+            const double f = fma(m1, __shfl_sync(0xffffffffu, inverse, near), -1.0);
+            const float g = (float)f;
+            const float tail = g * g * (-0.5f + g * (1.0f / 3.0f + g * (-0.25f + g * (0.2f + g * (-1.0f / 6.0f)))));
+            const double log2_sum = (double)(k - 32) + (__shfl_sync(0xffffffffu, log_of, near) + (f + (double)tail) * 1.4426950408889634074);
             if (lane == 0) {
-                const double total = (double)sum * 0x1p-32;
-                const double norm = plain ? ((double)e + log2(total)) * (1.0 / (double)kLog2e) : (double)top + log(total);
-                s_norm = bad ? (double)INFINITY : norm;
+                const double norm = plain ? ((double)e + log2_sum) * (1.0 / (double)kLog2e) : (double)top + log2_sum * 0.69314718055994530942;
+                s_base = bad || sum == 0 ? (double)INFINITY : (double)score - norm;
             }
         }
         __syncthreads();
@@ -420,39 +500,36 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
         double total = (double)score;
         int32_t token = ended;
         if (live) {
-            count = fabs(s_norm) < (double)INFINITY ? s_found : 0;
+            count = fabs(s_base) < (double)INFINITY ? s_found : 0;
             if (tid < count) {
-                total += (double)key_value(s.best[tid]) - s_norm;
+                total = (double)key_value(s.best[tid]) + s_base;
                 token = (int32_t)key_place(s.best[tid]);
             }
         }
-        const int at = mine / size * n_out + tid;
+        if (mine == me) cluster_wait();
         if (tid < count) {
-            lists.order[at] = ordered(total * (double)weight);
+            const int at = mine / size * n_out + tid;
             lists.total[at] = (float)total;
             lists.token[at] = token;
+            const int64_t order = ordered(p.weights ? total * (double)weight : total);
+            for (int c = 0; c < size; ++c) cluster.map_shared_rank(lists.order, c)[mine * n_out + tid] = order;
         }
-        if (tid == 0) s_count[mine / size] = count;
+        if (tid < size) cluster.map_shared_rank(s_counts, tid)[mine] = count;
         __syncthreads();
     }
+    if (me >= rows) cluster_wait();
     cluster.sync();
     if (me < rows) {  // each block places its own rows' continuations among all
-        if (tid < rows) s_counts[tid] = cluster.map_shared_rank(s_count, tid % size)[tid / size];
-        for (int r = tid / 32; r < rows; r += kPickThreads / 32) {
-            const int64_t* from = cluster.map_shared_rank(lists.order, r % size) + r / size * n_out;
-            for (int j = tid % 32; j < n_out; j += 32) lists.joined[r * n_out + j] = from[j];
-        }
-        __syncthreads();
         // eight lanes a continuation, each with an eighth of the other rows
-        const int lane = tid % 8;
+        const int share = tid % 8;
         for (int r = me; r < rows; r += size) {
             const int count = s_counts[r];
             for (int j0 = 0; j0 < count; j0 += kPickThreads / 8) {
                 const int j = min(j0 + tid / 8, count - 1);
-                const int64_t mine = lists.joined[r * n_out + j];
-                int rank = lane == 0 ? j : 0;
-                for (int q = lane; q < rows; q += 8) {
-                    const int64_t* o = lists.joined + q * n_out;
+                const int64_t mine = lists.order[r * n_out + j];
+                int rank = share == 0 ? j : 0;
+                for (int q = share; q < rows; q += 8) {
+                    const int64_t* o = lists.order + q * n_out;
                     int lo = 0, hi = q == r ? 0 : s_counts[q];  // how many of row q come before: more, or as much and of a lower row
                     while (lo < hi) {
                         const int mid = (lo + hi) >> 1;
@@ -465,7 +542,7 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
                 }
 #pragma unroll
                 for (int o = 1; o < 8; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-                if (lane == 0 && j0 + tid / 8 < count && rank < n_out) {
+                if (share == 0 && j0 + tid / 8 < count && rank < n_out) {
                     p.parents[to + rank] = first + r;
                     p.tokens[to + rank] = lists.token[r / size * n_out + j];
                     p.totals[to + rank] = lists.total[r / size * n_out + j];
@@ -481,7 +558,6 @@ __global__ void __launch_bounds__(kPickThreads, 4) beam_pick_kernel(const __grid
             }
         }
     }
-    cluster.sync();  // the others' lists are read
 }
 
 int groups_of(int vocab) { return (vocab + kGroup * kWarpGroups - 1) / (kGroup * kWarpGroups) * kWarpGroups; }
