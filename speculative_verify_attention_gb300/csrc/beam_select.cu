@@ -3,8 +3,8 @@
 // Row r (a beam) with score c continues with value v at  total = c + x[v] - log sum_v exp x[v],  ordered by weight * total.
 // The n_out best of a request lie among the n_out best of each of its rows, which are the n_out best logits x.
 //
-// One pass over the logits.  A warp holds four groups of 256 consecutive values in registers and leaves behind each group's
-// maximum and one partial sum of exponentials: 1/100 of what it read.  Ordered by (maximum descending, place ascending), the
+// One pass over the logits.  A warp holds a kilobyte's groups of consecutive values in registers and leaves behind each group's
+// maximum, and one partial sum of exponentials of all that it has held: 1/200 of what it read.  Ordered by (maximum descending, place ascending), the
 // n_out best groups hold the row's n_out best values: a value outside them has n_out values before it, one in each.  So the
 // second kernel, a block per row, picks those groups, reads them again and picks the values; a request's blocks form a cluster,
 // which joins their lists through shared memory.
@@ -17,9 +17,12 @@ namespace kvq8 {
 namespace {
 
 constexpr int kScanThreads = 256;
-constexpr int kGroup = 256;        // values of a group: eight a lane
-constexpr int kWarpGroups = 4;     // groups that a warp holds at once
-constexpr int kManyParts = 152 * 40;  // parts that the GPU's warps hold at once
+// Values of a group: a kilobyte.  A warp holds 1024 values at once, kLoads times eight a lane.
+template <typename T>
+constexpr int kGroup = 1024 / (int)sizeof(T);
+constexpr int kChunk = 1024, kLoads = kChunk / 256;
+constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kManyChunks = 152 * 40;  // chunks that the GPU's warps hold at once
 constexpr int kSearchThreads = 256;
 constexpr int kPickThreads = kSearchThreads + 32;
 constexpr int kMaxOut = 64;
@@ -49,9 +52,9 @@ struct SelectParams {
     int32_t* tokens;
     float* totals;
     // workspace
-    int32_t* group_max;     // [n_rows][n_groups], ordered as whole numbers
+    float* group_max;       // [n_rows][n_groups]
     Part* parts;            // [n_rows][n_parts]
-    int n_rows, vocab, n_seqs, n_out, n_groups, n_parts, turns;
+    int n_rows, vocab, n_seqs, n_out, n_groups, n_parts, n_chunks, turns;
 };
 
 // fp32 as whole numbers of the same order (-0 as 0).
@@ -182,65 +185,77 @@ __device__ __forceinline__ float largest(const Eight<__nv_bfloat16>& x) {
     return fmaxf(__low2float(m), __high2float(m));
 }
 
-// A warp takes p.turns parts of a row, the loads of the next one on their way while it works on one.
+__device__ __forceinline__ float warp_max(float x) {  // NaN loses here too
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+
+// A warp takes p.turns chunks of a row, and is one of its n_parts.  The sum so far is of 2^(x log2 e - e), e a whole number near the
+// largest value so far (one rounding a value); a larger one scales it by a power of two.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int G = kWarpGroups;
-    const int lane = threadIdx.x & 31, row = blockIdx.y;
-    int part = blockIdx.x * p.turns * (kScanThreads / 32) + (threadIdx.x >> 5);
+    constexpr int kPerGroup = kGroup<T> / 256;  // loads of a group
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.ended && __ldg(p.ended + row) >= 0) return;
     const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
     const int shift = Fetch<T, VEC>::shift_of(x);
-    Fetch<T, VEC> next[G];
-    auto load = [&](int part) {
+    Part sum = {-INFINITY, -INFINITY, 0.0f};
+    int chunk = (int)blockIdx.x * p.turns * kScanWarps + warp;
+    for (int turn = 0; turn < p.turns && chunk < p.n_chunks; ++turn, chunk += kScanWarps) {
+        Fetch<T, VEC> raw[kLoads];
 #pragma unroll
-        for (int u = 0; u < G; ++u) next[u].load(x, (part * G + u) * kGroup + lane * 8, p.vocab, shift);
-    };
-    if (part < p.n_parts) load(part);
-    for (int turn = 0; turn < p.turns && part < p.n_parts; ++turn, part += kScanThreads / 32) {
-        Eight<T> raw[G];
+        for (int u = 0; u < kLoads; ++u) raw[u].load(x, chunk * kChunk + u * 256 + lane * 8, p.vocab, shift);
+        Eight<T> v8[kLoads];
 #pragma unroll
-        for (int u = 0; u < G; ++u) raw[u] = next[u].eight(shift);
-        if (turn + 1 < p.turns && part + kScanThreads / 32 < p.n_parts) load(part + kScanThreads / 32);
-        int32_t top[G], most = ordered(-INFINITY);
+        for (int u = 0; u < kLoads; ++u) v8[u] = raw[u].eight(shift);
+        float top[kLoads / kPerGroup], m = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < G; ++u) {
-            float m = largest(raw[u]);
-            if (!(m > -INFINITY)) m = -INFINITY;
-            top[u] = __reduce_max_sync(0xffffffffu, ordered(m));
-            most = max(most, top[u]);
+        for (int g = 0; g < kLoads / kPerGroup; ++g) {
+            top[g] = warp_max(kPerGroup == 1 ? largest(v8[g]) : fmaxf(largest(v8[g * kPerGroup]), largest(v8[g * kPerGroup + kPerGroup - 1])));
+            m = fmaxf(m, top[g]);
         }
-        const float m = from_ordered(most);
-        // 2^(x log2 e - e) with e a whole number near the maximum: one rounding a value, and parts join by powers of two
-        const float e = rintf(m * kLog2e);
-        float s = 0.0f;
+        if (lane == 0) {
+            float* to = p.group_max + (int64_t)row * p.n_groups + chunk * (kLoads / kPerGroup);
+            if (kPerGroup == 1)
+                *reinterpret_cast<float4*>(to) = make_float4(top[0], top[1], top[kLoads / kPerGroup - 2], top[kLoads / kPerGroup - 1]);
+            else
+                *reinterpret_cast<float2*>(to) = make_float2(top[0], top[1]);
+        }
+        m = fmaxf(m, sum.m);
         if (fabsf(m) < kLarge) {
+            const float e = rintf(m * kLog2e);
+            float s = fabsf(sum.m) < kLarge ? sum.s * ex2_approx(sum.e - e) : sum.m > -INFINITY ? sum.s * exp2f((float)(scale_of_part(sum.m, sum.e) - (double)e)) : sum.s;
 #pragma unroll
-            for (int u = 0; u < G; ++u) {
+            for (int u = 0; u < kLoads; ++u) {
                 float v[8];
-                raw[u].floats(v);
+                v8[u].floats(v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s += ex2_approx(__fmaf_rn(v[i], kLog2e, -e));
             }
+            sum = {m, e, s};
         } else {
             const bool any = fabsf(m) < INFINITY;
+            float s = sum.m > -INFINITY ? sum.s * exp2f((float)(scale_of_part(sum.m, sum.e) - scale_of_part(m, 0.0f))) : sum.s;
 #pragma unroll
-            for (int u = 0; u < G; ++u) {
+            for (int u = 0; u < kLoads; ++u) {
                 float v[8];
-                raw[u].floats(v);  // of -inf alone nothing; a NaN or +inf makes the sum NaN
+                v8[u].floats(v);  // of -inf alone nothing; a NaN or +inf makes the sum NaN
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    s += any ? ex2_approx((v[0] - m) * kLog2e) : v[0] == -INFINITY ? 0.0f : NAN;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s += any ? ex2_approx((v[i] - m) * kLog2e) : v[i] == -INFINITY ? 0.0f : NAN;
+                    for (int w = 0; w < 7; ++w) v[w] = v[w + 1];
+                }
             }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) {
-            p.parts[(int64_t)row * p.n_parts + part] = Part{m, e, s};
-            *reinterpret_cast<int4*>(p.group_max + (int64_t)row * p.n_groups + part * G) = make_int4(top[0], top[1], top[2], top[3]);
+            sum = {m, 0.0f, s};
         }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
+    if (lane == 0) p.parts[(int64_t)row * p.n_parts + (int)blockIdx.x * kScanWarps + warp] = sum;
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -273,7 +288,7 @@ __device__ __forceinline__ void rank_keys(Search& s, int n, int n_out) {
 // Where more groups or values reach the bound than the lists hold (many equal values): the row's groups, and then the best ones'
 // values, a key a thread at a time; a full list is cut back to its best n_out, below which nothing is taken any more.
 template <typename T, bool VEC>
-__device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const T* x, const int32_t* gm) {
+__device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const T* x, const float* gm) {
     const int tid = threadIdx.x, n_out = p.n_out;
     auto cut = [&] {
         const int n = s.n;
@@ -297,7 +312,7 @@ __device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const 
     if (tid == 0) s.n = 0, s.above = 0;
     search_sync();
 #pragma unroll 1
-    for (int g0 = 0; g0 < p.n_groups; g0 += kSearchThreads) add(g0 + tid < p.n_groups ? key_of(gm[g0 + tid], (uint32_t)(g0 + tid)) : 0);
+    for (int g0 = 0; g0 < p.n_groups; g0 += kSearchThreads) add(g0 + tid < p.n_groups ? key_of(ordered(gm[g0 + tid]), (uint32_t)(g0 + tid)) : 0);
     cut();
     const int groups = s.n;
     if (tid < groups) s.group[tid] = key_place(s.key[tid]);
@@ -305,8 +320,8 @@ __device__ __noinline__ int pick_slowly(Search& s, const SelectParams& p, const 
     if (tid == 0) s.n = 0, s.above = 0;
     search_sync();
 #pragma unroll 1
-    for (int g = 0; g < groups; ++g) {
-        const int at = (int)s.group[g] * kGroup + tid;
+    for (int i = 0; i < groups * (kGroup<T> / kSearchThreads); ++i) {
+        const int at = (int)s.group[i / (kGroup<T> / kSearchThreads)] * kGroup<T> + i % (kGroup<T> / kSearchThreads) * kSearchThreads + tid;
         const float v = at < p.vocab ? to_float(x[at]) : -INFINITY;
         add(v > -INFINITY ? key_of(ordered(v), (uint32_t)at) : 0);
     }
@@ -365,7 +380,7 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     const int32_t lowest = ordered(-INFINITY);
     for (int mine = me; mine < rows; mine += size) {
         const int row = first + mine;
-        const int32_t* gm = p.group_max + (int64_t)row * p.n_groups;
+        const float* gm = p.group_max + (int64_t)row * p.n_groups;
         const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
         const int ended = p.ended ? __ldg(p.ended + row) : -1;
         int32_t k[kKeep];
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
 #pragma unroll
             for (int u = 0; u < kKeep; ++u) {
                 const int g = u * kSearchThreads + tid;
-                k[u] = g < p.n_groups ? __ldg(gm + g) : lowest;
+                k[u] = g < p.n_groups ? ordered(__ldg(gm + g)) : lowest;
             }
         }
         if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
@@ -384,7 +399,7 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
             int32_t m = k[0];
 #pragma unroll
             for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
-            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, __ldg(gm + g));
+            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, ordered(__ldg(gm + g)));
             for (int o = 1; o < lanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             if (tid % lanes == 0) s.top[tid / lanes] = m;
             search_sync();
@@ -409,7 +424,7 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
             };
 #pragma unroll
             for (int u = 0; u < kKeep; ++u) group(k[u], u * kSearchThreads + tid);
-            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(__ldg(gm + g), g);
+            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(ordered(__ldg(gm + g)), g);
             search_sync();
             const int groups = s.n_groups;
             const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
@@ -417,13 +432,14 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
             if (!found) {
                 const float least = from_ordered(bound);
                 const int shift = Fetch<T, VEC>::shift_of(x);
-                for (int i0 = tid >> 5; i0 < groups; i0 += kFetch * (kSearchThreads / 32)) {
+                constexpr int kPerGroup = kGroup<T> / 256;
+                for (int i0 = tid >> 5; i0 < groups * kPerGroup; i0 += kFetch * (kSearchThreads / 32)) {
                     Fetch<T, VEC> raw[kFetch];
                     int at[kFetch];
 #pragma unroll
                     for (int u = 0; u < kFetch; ++u) {
                         const int i = i0 + u * (kSearchThreads / 32);
-                        at[u] = i < groups ? (int)s.group[i] * kGroup + (tid & 31) * 8 : p.vocab;
+                        at[u] = i < groups * kPerGroup ? (int)s.group[i / kPerGroup] * kGroup<T> + i % kPerGroup * 256 + lane * 8 : p.vocab;
                         raw[u].load(x, at[u], p.vocab, shift);
                     }
 #pragma unroll
@@ -560,7 +576,15 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     }
 }
 
-int groups_of(int vocab) { return (vocab + kGroup * kWarpGroups - 1) / (kGroup * kWarpGroups) * kWarpGroups; }
+// What the sizes give: chunks, groups and parts of a row.  A warp takes two chunks of 16-bit values where there are many (320 rows of
+// 248320: the call 34.1 us, 35.5 with one, 34.1 with four; 96 rows 17.2 and 17.3), else one (160 rows of fp32: 30.9 us, 31.2 with two).
+void plan(SelectParams& p, size_t value_bytes) {
+    p.n_chunks = (p.vocab + kChunk - 1) / kChunk;
+    p.n_groups = p.n_chunks * (int)value_bytes;
+    const int64_t all = (int64_t)p.n_chunks * p.n_rows;
+    p.turns = value_bytes == 2 && all >= 3 * kManyChunks ? 2 : 1;
+    p.n_parts = (p.n_chunks + kScanWarps * p.turns - 1) / (kScanWarps * p.turns) * kScanWarps;
+}
 
 // The workspace's arrays, in order of their alignment; the size where base is null.
 size_t carve(SelectParams& p, unsigned char* base) {
@@ -580,12 +604,8 @@ bool select_shape(int n_rows, int vocab, int n_seqs, int n_out) {
 }
 
 template <typename T, bool VEC>
-int launch_select(SelectParams p, cudaStream_t s) {
-    const int warps = kScanThreads / 32;
-    // one part a warp where that leaves warps idle, up to four where there are many
-    const int64_t all = (int64_t)p.n_parts * p.n_rows;
-    p.turns = all < 2 * kManyParts ? 1 : all < 4 * kManyParts ? 2 : 4;
-    const dim3 grid((unsigned)((p.n_parts + warps * p.turns - 1) / (warps * p.turns)), (unsigned)p.n_rows);
+int launch_select(const SelectParams& p, cudaStream_t s) {
+    const dim3 grid((unsigned)(p.n_parts / kScanWarps), (unsigned)p.n_rows);
     const int rc = launch_dependent(beam_scan_kernel<T, VEC>, grid, kScanThreads, 0, s, p);
     if (rc != KVQ8_OK) return rc;
     // a block a row, by the mean of the requests' rows
@@ -618,8 +638,7 @@ extern "C" size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs,
     if (n_rows < 1 || vocab < 1 || n_seqs < 1 || n_out < 1 || !select_shape(n_rows, vocab, n_seqs, n_out)) return 0;
     SelectParams p = {};
     p.n_rows = n_rows, p.vocab = vocab, p.n_seqs = n_seqs, p.n_out = n_out;
-    p.n_groups = groups_of(vocab);
-    p.n_parts = p.n_groups / kWarpGroups;
+    plan(p, 4);  // the groups of fp32 are the most
     return carve(p, nullptr);
 }
 
@@ -643,8 +662,7 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t logits_stride,
     p.logits = logits, p.stride = logits_stride, p.row_starts = row_starts, p.scores = scores, p.weights = weights;
     p.ended = ended, p.parents = parents, p.tokens = tokens, p.totals = totals;
     p.n_rows = n_rows, p.vocab = vocab, p.n_seqs = n_seqs, p.n_out = n_out;
-    p.n_groups = groups_of(vocab);
-    p.n_parts = p.n_groups / kWarpGroups;
+    plan(p, esz);
     carve(p, static_cast<unsigned char*>(workspace));
     // eight values a load where every row starts on their size and holds whole groups of eight
     const bool vec = vocab % 8 == 0 && logits_stride % 8 == 0 && aligned_to(logits, 8 * esz);
