@@ -6,8 +6,8 @@
 // the position: no rounding but the frequency's own, 2^-64 of a turn a position.  Its two upper bits are the quarter, and what is
 // left, within an eighth of a turn of zero, goes through sincospif.
 //
-// A block works out the sines and cosines of its tokens once for all of their heads; then a thread has sixteen values of a row,
-// eight and their partners eight.  Keys are quantised as they come out of the rotation in fp32 (the block quantiser of
+// A block works out the sines and cosines of its tokens, two or four, once for all of its heads.  A thread has sixteen values of a
+// row, eight and their partners eight, the same ones of several heads: its eight sines and cosines stay in its registers.  Keys are quantised as they come out of the rotation in fp32 (the block quantiser of
 // kvq8_paged_append), without a rounding in between.
 #include "paged.cuh"
 #include "q8_0.cuh"
@@ -15,8 +15,9 @@
 namespace kvq8 {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
 constexpr int kMaxAxes = 4;
+constexpr unsigned kFullBlocks = 152 * 4;
 
 struct RopeParams {
     const void* q;
@@ -78,97 +79,127 @@ __device__ __forceinline__ void load_now(Eight<float>& x, const float* from) {
     asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.v[4]), "=f"(x.v[5]), "=f"(x.v[6]), "=f"(x.v[7]) : "l"(from + 4));
 }
 
-// (a, b)[i] turned by t[i].
-__device__ __forceinline__ void turn(float& a, float& b, float2 t) {
-    const float x = a, y = b;
-    a = __fmaf_rn(x, t.x, -__fmul_rn(y, t.y));
-    b = __fmaf_rn(y, t.x, __fmul_rn(x, t.y));
-}
-
-// Eight values at group g of a row, and eight at its partner group h = g + half the groups of their part of the row: the
-// rotated part, whose halves turn together (PAIRS: neighbours do, in both groups), or the part behind it.
+// The cosines and sines of a thread's eight pairs.  Halves turn two pairs an instruction: (c, c'), (s, s') and (-s, -s').
 template <bool PAIRS>
-__device__ __forceinline__ void rotate16(float (&a)[8], float (&b)[8], int g, int h, int rot, const float2* t) {
-    if (g * 8 >= rot) return;
-    if (PAIRS) {
+struct Turns {
+    F2 c[4], s[4], minus[4];
+    __device__ __forceinline__ void load(const float2* t, int g, int) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            turn(a[2 * i], a[2 * i + 1], t[g * 4 + i]);
-            turn(b[2 * i], b[2 * i + 1], t[h * 4 + i]);
+            const float4 x = *reinterpret_cast<const float4*>(t + g * 8 + 2 * i);
+            c[i] = F2::of(x.x, x.z);
+            s[i] = F2::of(x.y, x.w);
+            minus[i] = F2::of(-x.y, -x.w);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn(a[i], b[i], t[g * 8 + i]);
     }
-}
+    // a cos - b sin, b cos + a sin: a product rounded once, and the sum once
+    __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 x = F2::of(a[2 * i], a[2 * i + 1]), y = F2::of(b[2 * i], b[2 * i + 1]);
+            fma2(x, c[i], mul2(y, minus[i])).get(a[2 * i], a[2 * i + 1]);
+            fma2(y, c[i], mul2(x, s[i])).get(b[2 * i], b[2 * i + 1]);
+        }
+    }
+};
+template <>
+struct Turns<true> {
+    float2 t[8];
+    __device__ __forceinline__ void load(const float2* from, int g, int h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(from + (i < 2 ? g * 4 + 2 * i : h * 4 + 2 * i - 4));
+            t[2 * i] = make_float2(x.x, x.y), t[2 * i + 1] = make_float2(x.z, x.w);
+        }
+    }
+    __device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float& u = i < 4 ? a[2 * (i & 3)] : b[2 * (i & 3)];
+            float& v = i < 4 ? a[2 * (i & 3) + 1] : b[2 * (i & 3) + 1];
+            const float x = u, y = v;
+            u = __fmaf_rn(x, t[i].x, -__fmul_rn(y, t[i].y));
+            v = __fmaf_rn(y, t[i].x, __fmul_rn(x, t[i].y));
+        }
+    }
+};
 
-// Block: `tok` tokens.  The groups g and h of item j of a row: in the rotated part its first and second half, then the same of
-// the part behind it; both parts are multiples of 64, so four neighbouring lanes have a 32-value block in each.
+// Block (two or four tokens, a share of the heads): the lanes of a warp are the items of its tokens' rows, its heads every eighth of the
+// block's, queries, then keys, then values.  The groups g and h of item j: in the rotated part of a row its first and second half,
+// then the same of the part behind it; both parts are multiples of 64, so four neighbouring lanes have a 32-value block in each.
 template <typename T, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads) paged_rope_kernel(const __grid_constant__ RopeParams p, int tok) {
-    extern __shared__ __align__(16) float2 s_turn[];  // [tok][rot / 2]
-    const int tid = threadIdx.x, tok0 = blockIdx.x * tok, half = p.rot / 2;
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 3 : 4) paged_rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float2 s_turns[4 * 128];  // [tokens][rot / 2]
+    const int lane = threadIdx.x & 31, item_shift = p.head_shift - 4, j = lane & ((1 << item_shift) - 1);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int toks = min(tok, p.n_tok - tok0);
-    for (int i = tid; i < toks * half; i += kRopeThreads) {
-        const int t = i / half, j = i - t * half;
-        const int axis = p.axis_of ? __ldg(p.axis_of + j) : 0;
-        const int64_t pos = axis >= 0 && axis < p.n_axes ? __ldg(p.positions + (int64_t)axis * p.n_tok + tok0 + t) : 0;
-        s_turn[i] = cos_sin((uint64_t)pos * __ldg(p.turns + j));
+    const int tokens = 32 >> item_shift, tok0 = (int)blockIdx.x * tokens, mine = lane >> item_shift, tok = tok0 + mine;
+    const int64_t slot = tok < p.n_tok ? __ldg(p.slots + tok) : -1;
+    const bool there = slot >= 0 && slot < p.n_slots;
+    const int rot_items = p.rot / 16, rest = ((1 << p.head_shift) - p.rot) / 16;
+    const int g = j < rot_items ? j : rot_items + j, h = g + (j < rot_items ? rot_items : rest);
+    const int warp = (int)blockIdx.y * kRopeWarps + (int)(threadIdx.x >> 5), step = kRopeWarps * (int)gridDim.y;
+    const T* q = static_cast<const T*>(p.q) + (int64_t)tok * p.q_stride + g * 8;
+    const int far = (h - g) * 8;
+    Eight<T> ra, rb;
+    auto load = [&](const T* x, bool on) {
+        ra.clear();
+        rb.clear();
+        if (!on) return;
+        load_now(ra, x);
+        load_now(rb, x + far);
+    };
+    int head = warp;
+    load(q + ((int64_t)head << p.head_shift), there && head < p.n_q_heads);
+    const int half = p.rot / 2;
+    {  // as many threads a token as a row has pairs at most
+        const int t = (int)threadIdx.x >> (p.head_shift - 1), pair = (int)threadIdx.x & ((1 << (p.head_shift - 1)) - 1);
+        if (pair < half && tok0 + t < p.n_tok) {
+            const int axis = p.axis_of ? __ldg(p.axis_of + pair) : 0;
+            const int64_t pos = axis >= 0 && axis < p.n_axes ? __ldg(p.positions + (int64_t)axis * p.n_tok + tok0 + t) : 0;
+            s_turns[t * half + pair] = cos_sin((uint64_t)pos * __ldg(p.turns + pair));
+        }
     }
     __syncthreads();
-    const int items = 1 << (p.head_shift - 4), hd = 1 << p.head_shift;  // items of a row
-    const int rot_items = p.rot / 16, rest = (hd - p.rot) / 16;
-    for (int t = 0; t < toks; ++t) {
-        const int64_t slot = __ldg(p.slots + tok0 + t);
-        if (slot < 0 || slot >= p.n_slots) continue;
-        const float2* turns = s_turn + t * half;
-        const T* q = static_cast<const T*>(p.q) + (int64_t)(tok0 + t) * p.q_stride;
-        T* o = static_cast<T*>(p.q_out) + (int64_t)(tok0 + t) * p.out_stride;
-        for (int i = tid; i < p.n_q_heads * items; i += kRopeThreads) {
-            const int j = i & (items - 1), row = (i >> (p.head_shift - 4)) << p.head_shift;
-            const int g = j < rot_items ? j : rot_items + j, h = g + (j < rot_items ? rot_items : rest);
-            Eight<T> ra, rb;
-            load_now(ra, q + row + g * 8);
-            load_now(rb, q + row + h * 8);
-            float a[8], b[8];
-            ra.floats(a);
-            rb.floats(b);
-            rotate16<PAIRS>(a, b, g, h, p.rot, turns);
-            store8(o + row + g * 8, a);
-            store8(o + row + h * 8, b);
+    const bool turned = j < rot_items;
+    Turns<PAIRS> turns;
+    if (turned) turns.load(s_turns + mine * half, g, h);
+    float a[8], b[8];
+    T* o = static_cast<T*>(p.q_out) + (int64_t)tok * p.out_stride + g * 8;
+    for (; head < p.n_q_heads; head += step) {
+        ra.floats(a);
+        rb.floats(b);
+        load(q + ((int64_t)(head + step) << p.head_shift), there && head + step < p.n_q_heads);
+        if (turned) turns.rotate(a, b);
+        if (there) {
+            T* to = o + ((int64_t)head << p.head_shift);
+            store8(to, a);
+            store8(to + far, b);
         }
-        const int n = 2 * p.n_kv_heads * items;  // keys, then values; every lane of a warp takes part in the shuffles
-        for (int i0 = 0; i0 < n; i0 += kRopeThreads) {
-            const int i = i0 + tid, j = i & (items - 1), row = i >> (p.head_shift - 4);
-            const int z = row >= p.n_kv_heads, head = row - z * p.n_kv_heads;
-            const int g = j < rot_items ? j : rot_items + j, h = g + (j < rot_items ? rot_items : rest);
-            Eight<T> ra, rb;
-            ra.clear();
-            rb.clear();
-            if (i < n) {
-                const T* x = z ? static_cast<const T*>(p.v) + (int64_t)(tok0 + t) * p.v_stride
-                               : static_cast<const T*>(p.k) + (int64_t)(tok0 + t) * p.k_stride;
-                ra.load(x + (head << p.head_shift) + g * 8);
-                rb.load(x + (head << p.head_shift) + h * 8);
-            }
-            float a[8], b[8];
-            ra.floats(a);
-            rb.floats(b);
-            if (i < n && !z) rotate16<PAIRS>(a, b, g, h, p.rot, turns);
-            uint16_t sa, sb;
-            const uint2 ca = q8_0_block8(a, &sa), cb = q8_0_block8(b, &sb);
-            if (i < n) {
-                const uint64_t r = paged_row((uint32_t)slot, head, p.n_kv_heads, p.page_shift);
-                int8_t* codes = p.codes[z] + (r << p.head_shift);
-                *reinterpret_cast<uint2*>(codes + g * 8) = ca;
-                *reinterpret_cast<uint2*>(codes + h * 8) = cb;
-                if ((j & 3) == 0) {
-                    uint16_t* scales = p.scales[z] + (r << (p.head_shift - 5));
-                    scales[g >> 2] = sa;
-                    scales[h >> 2] = sb;
-                }
+    }
+    // keys, then values: the next warps in turn, as the queries' heads may not have come out even
+    int first = warp - p.n_q_heads % step;
+    if (first < 0) first += step;
+    const uint64_t row0 = there ? paged_row((uint32_t)slot, 0, p.n_kv_heads, p.page_shift) : 0;
+    for (int kv = first; kv < 2 * p.n_kv_heads; kv += step) {
+        const int z = kv >= p.n_kv_heads;
+        head = kv - z * p.n_kv_heads;
+        const T* x = z ? static_cast<const T*>(p.v) + (int64_t)tok * p.v_stride : static_cast<const T*>(p.k) + (int64_t)tok * p.k_stride;
+        load(x + ((int64_t)head << p.head_shift) + g * 8, there);
+        ra.floats(a);
+        rb.floats(b);
+        if (turned && !z) turns.rotate(a, b);
+        uint16_t sa, sb;  // every lane takes part in the shuffles
+        const uint2 ca = q8_0_block8(a, &sa), cb = q8_0_block8(b, &sb);
+        if (there) {
+            const uint64_t r = row0 + ((uint32_t)head << p.page_shift);
+            int8_t* codes = p.codes[z] + (r << p.head_shift) + g * 8;
+            *reinterpret_cast<uint2*>(codes) = ca;
+            *reinterpret_cast<uint2*>(codes + far) = cb;
+            if ((j & 3) == 0) {
+                uint16_t* scales = p.scales[z] + (r << (p.head_shift - 5)) + (g >> 2);
+                scales[0] = sa;
+                scales[far >> 5] = sb;
             }
         }
     }
@@ -176,11 +207,15 @@ __global__ void __launch_bounds__(kRopeThreads) paged_rope_kernel(const __grid_c
 
 template <typename T>
 int launch_rope(const RopeParams& p, bool pairs, cudaStream_t s) {
-    const int tok = p.n_tok >= 2048 ? 4 : 1;
-    const unsigned grid = (unsigned)(((int64_t)p.n_tok + tok - 1) / tok);
-    const int smem = tok * p.rot / 2 * (int)sizeof(float2);
-    if (pairs) return launch_dependent(paged_rope_kernel<T, true>, grid, kRopeThreads, smem, s, p, tok);
-    return launch_dependent(paged_rope_kernel<T, false>, grid, kRopeThreads, smem, s, p, tok);
+    const int tokens = 32 >> (p.head_shift - 4);
+    const unsigned gx = (unsigned)(((int64_t)p.n_tok + tokens - 1) / tokens);
+    // few tokens: their heads over more blocks, a head a warp at last
+    unsigned gy = 1;
+    const unsigned most = (unsigned)(p.n_q_heads + 2 * p.n_kv_heads + kRopeWarps - 1) / kRopeWarps;
+    while (gy < most && gx * gy < kFullBlocks) ++gy;
+    const dim3 grid(gx, gy);
+    if (pairs) return launch_dependent(paged_rope_kernel<T, true>, grid, kRopeThreads, 0, s, p);
+    return launch_dependent(paged_rope_kernel<T, false>, grid, kRopeThreads, 0, s, p);
 }
 
 }  // namespace

@@ -82,38 +82,72 @@ __device__ __forceinline__ uint32_t q8_0_block(float4 v, uint16_t* scale_bits) {
     return packed;
 }
 
+// Two fp32 values in a register pair, and operations on both at once, each value rounded as by the single ones.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ static F2 of(float x, float y) {
+        F2 r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+        return r;
+    }
+    __device__ __forceinline__ void get(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // of the sizes; a NaN wins
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return m;
+}
+
 // The same block held by 4 consecutive lanes, 8 values per lane in block order, for kernels that are bound by issue:
-// two shuffles a lane instead of three a half lane, and no conversion instruction a value.  With r as above and M =
-// 1.5 * 2^23, t = fl(x r + M) is M plus the nearest integer n of x r (the spacing of floats at M is 1), so n is the low
-// byte of t's bits, and fl(x r - n) is within 2^-25 of x r - n.  x r differs from fl(x / d) by less than 2^-15, so
-// where |x r - n| <= 1/2 - 2^-12 the code is n, as above; other lanes, and those with a value that is not finite
-// (max.NaN keeps it), take the IEEE division.
+// two shuffles a lane instead of three a half lane, no conversion instruction a value, and two values an instruction.  With r
+// as above and M = 1.5 * 2^23, t = fl(x r + M) is M plus the nearest integer n of x r (the spacing of floats at M is 1), so n is
+// the low byte of t's bits, and fl(x r - n) is within 2^-25 of x r - n.  x r differs from fl(x / d) by less than 2^-15, so
+// where |x r - n| <= 1/2 - 2^-14 the code is n, as above; other lanes (3 % of the warps have one), and those with a value that
+// is not finite (max.NaN keeps it), take the IEEE division.  d == 0 gives codes 0: r = 0 makes them so.
 __device__ __forceinline__ uint2 q8_0_block8(const float (&x)[8], uint16_t* scale_bits) {
-    float amax = 0.0f;
+    float amax = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    for (int e = 2; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const float d = scale_of<127>(amax);
     *scale_bits = __half_as_ushort(__float2half_rn(d));
     constexpr float kMagic = 12582912.0f;
-    float r, far = 0.0f;
+    float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+    if (d == 0.0f) r = 0.0f;
+    const F2 rr = F2::of(r, r), magic = F2::of(kMagic, kMagic), back = F2::of(-kMagic, -kMagic), minus = F2::of(-1.0f, -1.0f);
+    float far[4];
     uint32_t c[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float t = __fmaf_rn(x[e], r, kMagic);
-        const float off = fabsf(__fmaf_rn(x[e], r, -__fsub_rn(t, kMagic)));
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(off));
-        c[e] = __float_as_uint(t);
+    for (int e = 0; e < 4; ++e) {
+        const F2 v = F2::of(x[2 * e], x[2 * e + 1]);
+        const F2 t = fma2(v, rr, magic);
+        // x r - n, through -n = n * -1 (exact)
+        float o0, o1, t0, t1;
+        fma2(v, rr, mul2(add2(t, back), minus)).get(o0, o1);
+        t.get(t0, t1);
+        far[e] = max_nan(o0, o1);
+        c[2 * e] = __float_as_uint(t0), c[2 * e + 1] = __float_as_uint(t1);
     }
-    if (!(far <= 0.5f - 0x1p-12f)) {
+    if (!(max_nan(max_nan(far[0], far[1]), max_nan(far[2], far[3])) <= 0.5f - 0x1p-14f)) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = (uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x[e], d)), -127.0f), 127.0f);
-    }
-    if (d == 0.0f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = 0u;
+        for (int e = 0; e < 8; ++e) c[e] = d == 0.0f ? 0u : (uint32_t)(int)fminf(fmaxf(roundf(__fdiv_rn(x[e], d)), -127.0f), 127.0f);
     }
     uint32_t w[2];
 #pragma unroll
