@@ -720,6 +720,13 @@ def _addr(t, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
                      f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
 
 
+def _addrs(dtype: torch.dtype, shape: tuple, device: int, **tensors) -> list:
+    """The addresses of several such tensors."""
+    at = [t.data_ptr() for t in tensors.values()
+          if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()]
+    return at if len(at) == len(tensors) else [_addr(t, name, dtype, shape, device) for name, t in tensors.items()]
+
+
 def _maybe(t, name: str, dtype: torch.dtype, shape: tuple, device: int):
     return None if t is None else _addr(t, name, dtype, shape, device)
 
@@ -728,7 +735,7 @@ def _launch_on(device: int, stream) -> int:
     """The raw stream to launch on, after checking that the tensors live on the current device."""
     if device < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if torch.cuda.current_device() != device:
+    if torch._C._cuda_getDevice() != device:  # (a CUDA tensor has initialised CUDA)
         raise ValueError(f"the tensors are on cuda:{device}, which is not the current device")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
@@ -804,11 +811,13 @@ def kvq8_paged_tables(lens: torch.Tensor, n_new: torch.Tensor, held: torch.Tenso
 
 
 def _token_stride(t: torch.Tensor, name: str, cache: KVPagedCacheQ8) -> int:
-    if t.dim() != 3 or t.shape[1:] != (cache.n_kv_heads, cache.head_dim) or t.get_device() != cache._index:
-        raise ValueError(f"{name} must be [n_tok][{cache.n_kv_heads}][{cache.head_dim}] on {cache.device}")
-    if t.stride(2) != 1 or (t.stride(1) != cache.head_dim and cache.n_kv_heads > 1):
+    shape, heads, dim = t.shape, cache.n_kv_heads, cache.head_dim
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.get_device() != cache._index:
+        raise ValueError(f"{name} must be [n_tok][{heads}][{dim}] on {cache.device}")
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else cache.n_kv_heads * cache.head_dim
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def kvq8_paged_append(k: torch.Tensor, v: torch.Tensor, cache: KVPagedCacheQ8, slots: torch.Tensor, stream=None) -> None:
@@ -935,9 +944,10 @@ def token_counts(tokens: torch.Tensor, token_starts: torch.Tensor, counts: torch
 
 # ---------------------------------------------------------------- beams, trees and rotary positions
 
-def _space(workspace, nbytes: int, device: torch.device, index: int, stream) -> torch.Tensor:
+def _space(workspace, device: torch.device, index: int, stream, nbytes, *sizes) -> torch.Tensor:
+    """The workspace, or one of nbytes(*sizes) bytes."""
     if workspace is None:
-        return _scratch(max(nbytes, 16), device, stream)
+        return _scratch(max(nbytes(*sizes), 16), device, stream)
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     return workspace
@@ -965,7 +975,7 @@ def beam_select(logits: torch.Tensor, row_starts: torch.Tensor, n_out: int, scor
     parents = _empty(shape, i32, logits.device, stream) if parents is None else parents
     tokens = _empty(shape, i32, logits.device, stream) if tokens is None else tokens
     totals = _empty(shape, f32, logits.device, stream) if totals is None else totals
-    workspace = _space(workspace, lib.beam_select_workspace_bytes(rows, vocab, n, n_out), logits.device, dev, stream)
+    workspace = _space(workspace, logits.device, dev, stream, lib.beam_select_workspace_bytes, rows, vocab, n, n_out)
     st = lib.beam_select(
         logits.data_ptr(), _DTYPE[logits.dtype], logits.stride(0) if rows > 1 else vocab, rows, vocab,
         _addr(row_starts, "row_starts", i32, (n + 1,), dev), n, _maybe(scores, "scores", f32, (rows,), dev),
@@ -991,7 +1001,7 @@ def token_counts_fork(parents: torch.Tensor, state_of: torch.Tensor | None, coun
     n = state_of.shape[0] if state_of is not None else counts.shape[0] if n_seqs is None else int(n_seqs)
     lib = _lib or load_library()
     raw = _launch_on(dev, stream)
-    workspace = _space(workspace, lib.token_counts_fork_workspace_bytes(m), counts.device, dev, stream)
+    workspace = _space(workspace, counts.device, dev, stream, lib.token_counts_fork_workspace_bytes, m)
     st = lib.token_counts_fork(
         _addr(parents, "parents", i32, (m,), dev), m, _maybe(state_of, "state_of", i32, (n,), dev), n,
         _addr(counts, "counts", i32, tuple(counts.shape), dev), counts.shape[0], counts.shape[1],
@@ -1019,16 +1029,17 @@ def kvq8_paged_fork(parents: torch.Tensor, lens: torch.Tensor, held: torch.Tenso
     m, (n, mp), n_pages = parents.shape[0], page_table.shape, free_ring.shape[0]
     lib = _lib or load_library()
     raw = _launch_on(dev, stream)
-    workspace = _space(workspace, lib.kvq8_paged_fork_workspace_bytes(n, m, n_pages), page_table.device, dev, stream)
+    workspace = _space(workspace, page_table.device, dev, stream, lib.kvq8_paged_fork_workspace_bytes, n, m, n_pages)
+    at, lens_at, held_at, src_at, dst_at, rows_at = _addrs(i32, (m,), dev, parents=parents, lens_out=lens_out, held_out=held_out,
+                                                           copy_src=copy_src, copy_dst=copy_dst, copy_rows=copy_rows)
+    old_lens, old_held = _addrs(i32, (n,), dev, lens=lens, held=held)
+    shares_at, ring, shares_to = _addrs(i32, (n_pages,), dev, shares=shares, free_ring=free_ring,
+                                        shares_out=shares if shares_out is None else shares_out)
+    state, state_to = _addrs(i32, (2,), dev, ring_state=ring_state, ring_out=ring_state if ring_out is None else ring_out)
     st = lib.kvq8_paged_fork(
-        _addr(parents, "parents", i32, (m,), dev), m, _addr(lens, "lens", i32, (n,), dev), _addr(held, "held", i32, (n,), dev), n,
-        int(page_size), _addr(page_table, "page_table", i32, (n, mp), dev), mp, _addr(shares, "shares", i32, (n_pages,), dev),
-        _addr(free_ring, "free_ring", i32, (n_pages,), dev), n_pages, _addr(ring_state, "ring_state", i32, (2,), dev),
-        _addr(page_table_out, "page_table_out", i32, (m, mp), dev), _addr(lens_out, "lens_out", i32, (m,), dev),
-        _addr(held_out, "held_out", i32, (m,), dev), _addr(shares if shares_out is None else shares_out, "shares_out", i32, (n_pages,), dev),
-        _addr(ring_state if ring_out is None else ring_out, "ring_out", i32, (2,), dev), _addr(copy_src, "copy_src", i32, (m,), dev),
-        _addr(copy_dst, "copy_dst", i32, (m,), dev), _addr(copy_rows, "copy_rows", i32, (m,), dev), _addr(status, "status", i32, (1,), dev),
-        workspace.data_ptr(), workspace.nbytes, raw)
+        at, m, old_lens, old_held, n, int(page_size), _addr(page_table, "page_table", i32, (n, mp), dev), mp, shares_at, ring, n_pages, state,
+        _addr(page_table_out, "page_table_out", i32, (m, mp), dev), lens_at, held_at, shares_to, state_to, src_at, dst_at, rows_at,
+        _addr(status, "status", i32, (1,), dev), workspace.data_ptr(), workspace.nbytes, raw)
     _check("kvq8_paged_fork", st)
 
 
@@ -1080,13 +1091,15 @@ def kvq8_paged_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ca
     axis_of int32 [rot_dim / 2]: the axis of each pair; pairs: dims 2i and 2i + 1 turn together, else i and i + rot_dim / 2.  Returns
     q_out (q_out=q works in place); tokens whose slot is outside the cache are left alone."""
     dev, i32 = cache._index, torch.int32
-    if q.dim() != 3 or q.dtype not in _DTYPE or q.get_device() != dev or q.shape[2] != cache.head_dim:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype not in _DTYPE or q.get_device() != dev or shape[2] != cache.head_dim:
         raise ValueError(f"q must be float32, float16 or bfloat16 [n_tok][n_q_heads][{cache.head_dim}] on {cache.device}")
-    if k.dtype is not q.dtype or v.dtype is not q.dtype or k.shape != v.shape or k.shape[0] != q.shape[0]:
+    n, hq, hd = shape
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or k.shape != v.shape or k.shape[0] != n:
         raise ValueError("q, k and v must have one type and one number of tokens")
-    n, hq, hd = q.shape
     ks, vs = _token_stride(k, "k", cache), _token_stride(v, "v", cache)
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    one = positions.dim() == 1
+    axes = 1 if one else positions.shape[0]
     if turns.dim() != 1:
         raise ValueError("turns must be [rot_dim / 2]")
     half = turns.shape[0]
@@ -1095,12 +1108,13 @@ def kvq8_paged_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ca
         q_out = _empty((n, hq, hd), q.dtype, q.device, stream)
     strides = []
     for t, name in ((q, "q"), (q_out, "q_out")):
-        if t.shape != q.shape or t.dtype is not q.dtype or t.get_device() != dev or t.stride(2) != 1 or (t.stride(1) != hd and hq > 1):
-            raise ValueError(f"{name} must be {q.dtype} {tuple(q.shape)} on {cache.device}, the heads of a token contiguous")
-        strides.append(t.stride(0) if n > 1 else hq * hd)
+        stride = t.stride()
+        if t.shape != shape or t.dtype is not q.dtype or t.get_device() != dev or stride[2] != 1 or (stride[1] != hd and hq > 1):
+            raise ValueError(f"{name} must be {q.dtype} {tuple(shape)} on {cache.device}, the heads of a token contiguous")
+        strides.append(stride[0] if n > 1 else hq * hd)
     st = (_lib or load_library()).kvq8_paged_append_rope(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[q.dtype], n, hq, strides[0], ks, vs,
-        _addr(positions, "positions", i32, (n,) if positions.dim() == 1 else (axes, n), dev), axes,
+        _addr(positions, "positions", i32, (n,) if one else (axes, n), dev), axes,
         _addr(turns, "turns", torch.int64, (half,), dev), _maybe(axis_of, "axis_of", i32, (half,), dev), 2 * half, 1 if pairs else 0,
         cache._struct, _addr(slots, "slots", torch.int64, (n,), dev), q_out.data_ptr(), strides[1], raw)
     _check("kvq8_paged_append_rope", st)

@@ -198,22 +198,18 @@ struct PagedFork {
 constexpr int32_t kGoesOn = 1 << 30;
 constexpr int kCopyPer = 4096;  // pages of the pool that a block of the first kernel clears or copies
 
-// Block 0 plans; the others copy the shares, if they are not updated in place, and clear the marks.
-__global__ void __launch_bounds__(kPlanThreads) paged_fork_plan_kernel(const __grid_constant__ PagedFork p) {
-    extern __shared__ int sm[];
+// Thread id of n: the shares, if they are not updated in place, and no marks.
+__device__ __forceinline__ void fork_clear(const PagedFork& p, int id, int n) {
+    if (p.shares != p.shares_out)
+        for (int i = id; i < p.n_pages; i += n) p.shares_out[i] = p.shares[i];
+    for (int i = id; i < (p.n_pages + 31) / 32; i += n) p.freed[i] = 0u;
+}
+
+// One block: who goes on from whom, which pages are taken, and the children's lengths and copies.  Returns whether anything moves.
+__device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_warp) {
     const int tid = threadIdx.x;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x > 0) {
-        const int step = kPlanThreads * ((int)gridDim.x - 1), id = ((int)blockIdx.x - 1) * kPlanThreads + tid;
-        if (p.shares != p.shares_out)
-            for (int i = id; i < p.n_pages; i += step) p.shares_out[i] = p.shares[i];
-        for (int i = id; i < (p.n_pages + 31) / 32; i += step) p.freed[i] = 0u;
-        return;
-    }
     int* s_first = sm;
     int* s_kids = s_first + p.n_seqs;
-    __shared__ int s_warp[32];
     const int page = 1 << p.page_shift;
     const int head = p.ring_state[0], count = p.ring_state[1];
     bool bad = families(p.parents, p.n_children, p.n_seqs, s_first, s_kids);
@@ -249,10 +245,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_fork_plan_kernel(const __g
         const int k = takes + block_sums(take, s_warp, total);
         takes += total;
         if (i < p.n_children) {
-            int at = head, fresh = -1, src = -1;
+            int fresh = -1, src = -1;
             if (take && k < count) {
-                at = head + k >= p.n_pages ? head + k - p.n_pages : head + k;
-                fresh = p.ring[at];
+                fresh = p.ring[head + k >= p.n_pages ? head + k - p.n_pages : head + k];
                 src = p.table[(int64_t)q * p.max_pages + (len >> p.page_shift)];
             }
             p.take[i] = fresh;
@@ -276,82 +271,124 @@ __global__ void __launch_bounds__(kPlanThreads) paged_fork_plan_kernel(const __g
         p.done[0] = 0u;
         p.done[1] = (uint32_t)takes;
     }
+    return status == 0;
 }
 
-constexpr int kForkThreads = 256;
-constexpr int kForkPer = 4;  // entries of a table row that a thread takes
-
-// Block (part of a table row, child or sequence): a child's row from its parent's, and what a sequence's pages gain or lose:
-// each is held by its children from now on, not by itself.  shares counts holders beyond the first, so the last one to let a page
-// go takes it below zero; the last block to finish gives those back to the ring, in order of their number.
-__global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const __grid_constant__ PagedFork p) {
-    __shared__ int s_warp[32];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, page = 1 << p.page_shift;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int k0 = blockIdx.x * kForkThreads * kForkPer + tid;
-    const bool moved = p.status[0] == 0;
-    if (moved && (int)blockIdx.y < p.n_children) {
-        const int i = blockIdx.y, q = p.parents[i], need = p.held_out[i];
-        if (need > 0) {
-            const int fresh = p.take[i], tail = fresh >= 0 ? need - 1 : -1;
-            const int32_t* from = p.table + (int64_t)q * p.max_pages;
-            int32_t* to = p.table_out + (int64_t)i * p.max_pages;
-#pragma unroll
-            for (int u = 0; u < kForkPer; ++u) {
-                const int k = k0 + u * kForkThreads;
-                if (k < need) to[k] = k == tail ? fresh : from[k];
-            }
-        }
-    } else if (moved) {
-        const int q = (int)blockIdx.y - p.n_children;
-        const int held = p.held[q], holders = p.holders[q], kids = holders & (kGoesOn - 1);
-        const int full = kids ? p.lens[q] >> p.page_shift : 0;
-        const bool part = kids && (p.lens[q] & (page - 1));
-        const int32_t* from = p.table + (int64_t)q * p.max_pages;
-#pragma unroll
-        for (int u = 0; u < kForkPer; ++u) {
-            const int k = k0 + u * kForkThreads;
-            if (k >= held) continue;
-            const int change = (k < full ? kids : k == full && part && (holders & kGoesOn) ? 1 : 0) - 1;
-            if (change == 0) continue;
-            const int id = from[k];
-            if (id < 0 || id >= p.n_pages) continue;
-            if (atomicAdd(p.shares_out + id, change) + change < 0) atomicOr(p.freed + (id >> 5), 1u << (id & 31));
-        }
+// Entries k0, k0 + step, ... of row y: a child's row of the table from its parent's, or, behind the children, what a sequence's pages
+// gain or lose: each is held by its children from now on, not by itself.  shares counts holders beyond the first, so the last one to
+// let a page go takes it below zero.
+__device__ __forceinline__ void fork_row(const PagedFork& p, int y, int k0, int step) {
+    if (y < p.n_children) {
+        const int need = p.held_out[y];
+        if (need <= 0) return;
+        const int fresh = p.take[y], tail = fresh >= 0 ? need - 1 : -1;
+        const int32_t* from = p.table + (int64_t)p.parents[y] * p.max_pages;
+        int32_t* to = p.table_out + (int64_t)y * p.max_pages;
+#pragma unroll 4
+        for (int k = k0; k < need; k += step) to[k] = k == tail ? fresh : from[k];
+        return;
     }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
+    const int q = y - p.n_children, page = 1 << p.page_shift;
+    const int held = p.held[q], holders = p.holders[q], kids = holders & (kGoesOn - 1);
+    const int full = kids ? p.lens[q] >> p.page_shift : 0;
+    const bool goes_on = kids && (p.lens[q] & (page - 1)) && (holders & kGoesOn);
+    const int32_t* from = p.table + (int64_t)q * p.max_pages;
+#pragma unroll 4
+    for (int k = k0; k < held; k += step) {
+        const int change = (k < full ? kids : k == full && goes_on ? 1 : 0) - 1;
+        if (change == 0) continue;
+        const int id = from[k];
+        if (id < 0 || id >= p.n_pages) continue;
+        if (atomicAdd(p.shares_out + id, change) + change < 0) atomicOr(p.freed + (id >> 5), 1u << (id & 31));
+    }
+}
+
+// One block, after all rows: the pages that nobody holds any more go behind the ring's tail, in order of their number.
+__device__ __forceinline__ void fork_give(const PagedFork& p, bool moved, int* s_warp) {
+    constexpr int kWords = 4;  // words of marks of a thread at a time
+    const int tid = threadIdx.x, threads = (int)blockDim.x;
     const int head = p.ring_state[0], count = p.ring_state[1], takes = moved ? (int)__ldcg(p.done + 1) : 0;
     int given = 0;
     if (moved) {
         const int n_words = (p.n_pages + 31) / 32;
         int tail = head + count;
         if (tail >= p.n_pages) tail -= p.n_pages;
-        for (int w0 = 0; w0 < n_words; w0 += kForkThreads) {
-            const int w = w0 + tid;
-            uint32_t bits = w < n_words ? __ldcg(p.freed + w) : 0u;
-            int total;
-            int k = given + block_sums(__popc(bits), s_warp, total);
-            given += total;
-            for (; bits; bits &= bits - 1, ++k) {
-                const int id = 32 * w + __ffs((int)bits) - 1;
-                p.shares_out[id] = 0;
-                if (k < p.n_pages - count) p.ring[tail + k >= p.n_pages ? tail + k - p.n_pages : tail + k] = id;
+        for (int w0 = 0; w0 < n_words; w0 += threads * kWords) {
+            uint32_t bits[kWords];
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < kWords; ++u) {
+                const int w = w0 + tid * kWords + u;
+                bits[u] = w < n_words ? __ldcg(p.freed + w) : 0u;
+                n += __popc(bits[u]);
             }
+            int total;
+            int k = given + block_sums(n, s_warp, total);
+            given += total;
+#pragma unroll
+            for (int u = 0; u < kWords; ++u)
+                for (; bits[u]; bits[u] &= bits[u] - 1, ++k) {
+                    const int id = 32 * (w0 + tid * kWords + u) + __ffs((int)bits[u]) - 1;
+                    p.shares_out[id] = 0;
+                    if (k < p.n_pages - count) p.ring[tail + k >= p.n_pages ? tail + k - p.n_pages : tail + k] = id;
+                }
         }
     }
     __syncthreads();  // every thread has read the state
     if (tid == 0) {
         const int h = head + takes;
-        p.ring_out[0] = moved && h >= p.n_pages ? h - p.n_pages : moved ? h : head;
+        p.ring_out[0] = moved && h >= p.n_pages ? h - p.n_pages : h;  // (a malformed one is repeated)
         p.ring_out[1] = moved ? count - takes + min(given, p.n_pages - count) : count;
     }
+}
+
+// Few entries: everything in one block.
+__global__ void __launch_bounds__(kPlanThreads) paged_fork_small_kernel(const __grid_constant__ PagedFork p) {
+    extern __shared__ int sm[];
+    __shared__ int s_warp[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    fork_clear(p, threadIdx.x, kPlanThreads);
+    const bool moved = fork_plan(p, sm, s_warp);
+    __syncthreads();
+    if (moved)
+        for (int y = threadIdx.x >> 5; y < p.n_children + p.n_seqs; y += kPlanThreads / 32) fork_row(p, y, threadIdx.x & 31, 32);
+    __syncthreads();
+    fork_give(p, moved, s_warp);
+}
+
+// Block 0 plans, the others clear.
+__global__ void __launch_bounds__(kPlanThreads) paged_fork_plan_kernel(const __grid_constant__ PagedFork p) {
+    extern __shared__ int sm[];
+    __shared__ int s_warp[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0)
+        fork_plan(p, sm, s_warp);
+    else
+        fork_clear(p, ((int)blockIdx.x - 1) * kPlanThreads + threadIdx.x, kPlanThreads * ((int)gridDim.x - 1));
+}
+
+constexpr int kSmallEntries = 16384;  // of the tables, and pages of the pool
+constexpr int kForkThreads = 256;
+constexpr int kForkPer = 4;  // entries of a table row that a thread takes
+
+// Block (part of a table row, child or sequence); the last block to finish gives pages back.
+__global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const __grid_constant__ PagedFork p) {
+    __shared__ int s_warp[32];
+    __shared__ int s_last;
+    const int tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool moved = p.status[0] == 0;
+    if (moved) fork_row(p, blockIdx.y, blockIdx.x * kForkThreads + tid, gridDim.x * kForkThreads);
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    fork_give(p, moved, s_warp);
 }
 
 size_t fork_carve(PagedFork& p, unsigned char* base) {
@@ -448,8 +485,10 @@ extern "C" int kvq8_paged_fork(const int32_t* parents, int n_children, const int
                    ring_out, copy_src, copy_dst, copy_rows, status, nullptr, nullptr, nullptr, nullptr, n_children, n_seqs,
                    max_pages, n_pages, log2_of(page_size)};
     fork_carve(p, static_cast<unsigned char*>(workspace));
-    const int clear = (n_pages + kCopyPer - 1) / kCopyPer;
     cudaStream_t s = (cudaStream_t)stream;
+    if ((int64_t)max_pages * (n_children + n_seqs) <= kSmallEntries && n_pages <= kSmallEntries)
+        return launch_dependent(paged_fork_small_kernel, 1, kPlanThreads, 2 * n_seqs * 4, s, p);
+    const int clear = (n_pages + kCopyPer - 1) / kCopyPer;
     const int rc = launch_dependent(paged_fork_plan_kernel, (unsigned)(1 + (clear < 75 ? clear : 75)), kPlanThreads, 2 * n_seqs * 4, s, p);
     if (rc != KVQ8_OK) return rc;
     const int per = kForkThreads * kForkPer;
