@@ -18,6 +18,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_calls = None  # csrc/calls.cpp: the argument checks of the calls below that stand in steps of a few microseconds
 
 KVQ8_OK = 0
 KVQ8_ERR_INVALID_ARG = 1
@@ -78,7 +79,7 @@ def library_path() -> str:
 
 def load_library():
     """Load the in-tree library (built by ``build.build()``); raises if it is missing."""
-    global _lib
+    global _lib, _calls
     with _lock:
         if _lib is not None:
             return _lib
@@ -182,6 +183,8 @@ def load_library():
         lib.kvq8_device_error.restype = i32
         lib.kvq8_status_str.argtypes = [i32]
         lib.kvq8_status_str.restype = ctypes.c_char_p
+        from . import _calls as calls  # linked to the library
+        _calls = calls
         _lib = lib
         return lib
 
@@ -720,13 +723,6 @@ def _addr(t, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
                      f"(got {t.dtype}, {tuple(t.shape)}, {t.device})")
 
 
-def _addrs(dtype: torch.dtype, shape: tuple, device: int, **tensors) -> list:
-    """The addresses of several such tensors."""
-    at = [t.data_ptr() for t in tensors.values()
-          if t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()]
-    return at if len(at) == len(tensors) else [_addr(t, name, dtype, shape, device) for name, t in tensors.items()]
-
-
 def _maybe(t, name: str, dtype: torch.dtype, shape: tuple, device: int):
     return None if t is None else _addr(t, name, dtype, shape, device)
 
@@ -772,8 +768,9 @@ class KVPagedCacheQ8:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = shape
         self.device, self._index = k_codes.device, index
         self._planes = {"k_codes": k_codes, "k_scales": k_scales, "v_codes": v_codes, "v_scales": v_scales}
-        self._struct = kvq8_paged_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
+        self._struct = struct = kvq8_paged_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                                         n_kv_heads, head_dim, page_size, n_pages)
+        self._at = ctypes.addressof(struct)
 
     def _plane(name: str):
         # the C struct is kept, so a plane that is replaced has to reach it; one of another shape, type or device raises
@@ -835,18 +832,15 @@ def kvq8_paged_append(k: torch.Tensor, v: torch.Tensor, cache: KVPagedCacheQ8, s
 def kvq8_paged_read(cache: KVPagedCacheQ8, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Write the values of int64 slots [n_tok] into k and v [n_tok][n_kv_heads][head_dim] (fp32, fp16 or bf16; tokens
     and heads may be strided, so a KVCacheF16's planes can be given as k.transpose(0, 1)[:n_tok])."""
-    n = slots.shape[0]
-    if k.dtype is not v.dtype or k.dtype not in _DTYPE:
-        raise ValueError("k and v must have one type (float32, float16 or bfloat16)")
-    strides = []
-    for t, name in ((k, "k"), (v, "v")):
-        if t.shape != (n, cache.n_kv_heads, cache.head_dim) or t.stride(2) != 1 or t.get_device() != cache._index:
-            raise ValueError(f"{name} must be [{n}][{cache.n_kv_heads}][{cache.head_dim}] with contiguous dims on {cache.device}")
-        strides.append((ctypes.c_int64 * 2)(t.stride(0) if n > 1 else cache.head_dim,
-                                            t.stride(1) if cache.n_kv_heads > 1 else cache.head_dim))
-    st = (_lib or load_library()).kvq8_paged_read(cache._struct, _addr(slots, "slots", torch.int64, (n,), cache._index), n,
-                                        _DTYPE[k.dtype], k.data_ptr(), v.data_ptr(), strides[0], strides[1],
-                                        _launch_on(cache._index, stream))
+    st = _native().paged_read(cache._at, cache._index, slots, k, v, _launch_on(cache._index, stream))
+    if st is None:
+        n = slots.shape[0]
+        if k.dtype is not v.dtype or k.dtype not in _DTYPE:
+            raise ValueError("k and v must have one type (float32, float16 or bfloat16)")
+        for t, name in ((k, "k"), (v, "v")):
+            if t.shape != (n, cache.n_kv_heads, cache.head_dim) or t.stride(2) != 1 or t.get_device() != cache._index:
+                raise ValueError(f"{name} must be [{n}][{cache.n_kv_heads}][{cache.head_dim}] with contiguous dims on {cache.device}")
+        _refuse(cache._index, (slots, "slots", torch.int64, (n,)))
     _check("kvq8_paged_read", st)
 
 
@@ -943,14 +937,26 @@ def token_counts(tokens: torch.Tensor, token_starts: torch.Tensor, counts: torch
 
 
 # ---------------------------------------------------------------- beams, trees and rotary positions
+# The tensors' types, shapes and devices are checked in csrc/calls.cpp; where one does not fit, _refuse says which.
 
-def _space(workspace, device: torch.device, index: int, stream, nbytes, *sizes) -> torch.Tensor:
+def _native():
+    if _calls is None:
+        load_library()
+    return _calls
+
+
+def _refuse(device: int, *wanted) -> None:
+    """Raise for the first of (tensor, name, type, shape) that is not such a tensor on the device; a shape of None: not looked at."""
+    for t, name, dtype, shape in wanted:
+        if t is None:
+            raise ValueError(f"{name} is wanted")
+        _addr(t, name, dtype or t.dtype, t.shape if shape is None else shape, device)
+    raise ValueError("sizes or tensors that the call does not take")
+
+
+def _space(workspace, device: torch.device, stream, nbytes, *sizes) -> torch.Tensor:
     """The workspace, or one of nbytes(*sizes) bytes."""
-    if workspace is None:
-        return _scratch(max(nbytes(*sizes), 16), device, stream)
-    if workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+    return workspace if workspace is not None else _scratch(max(nbytes(*sizes), 16), device, stream)
 
 
 def beam_select_workspace_bytes(n_rows: int, vocab: int, n_seqs: int, n_out: int) -> int:
@@ -965,23 +971,24 @@ def beam_select(logits: torch.Tensor, row_starts: torch.Tensor, n_out: int, scor
     strided) between row_starts int32 [n + 1], and the vocabulary: by weights (fp32 [n_rows]) times scores (fp32 [n_rows]) + log
     softmax; rows with ended int32 [n_rows] >= 0 go on as they are.  Returns (parents int32, tokens int32, totals fp32), [n][n_out]
     each, best first; -1, -1, -inf where a request has fewer."""
-    dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
-    if logits.dim() != 2 or logits.dtype not in _DTYPE or logits.stride(1) != 1 and logits.shape[1] > 1:
-        raise ValueError("logits must be [n_rows][V] of float32, float16 or bfloat16 with contiguous rows")
-    rows, vocab = logits.shape
-    n, n_out = row_starts.shape[0] - 1, int(n_out)
-    lib = _lib or load_library()
-    raw, shape = _launch_on(dev, stream), (n, n_out)
-    parents = _empty(shape, i32, logits.device, stream) if parents is None else parents
-    tokens = _empty(shape, i32, logits.device, stream) if tokens is None else tokens
-    totals = _empty(shape, f32, logits.device, stream) if totals is None else totals
-    workspace = _space(workspace, logits.device, dev, stream, lib.beam_select_workspace_bytes, rows, vocab, n, n_out)
-    st = lib.beam_select(
-        logits.data_ptr(), _DTYPE[logits.dtype], logits.stride(0) if rows > 1 else vocab, rows, vocab,
-        _addr(row_starts, "row_starts", i32, (n + 1,), dev), n, _maybe(scores, "scores", f32, (rows,), dev),
-        _maybe(weights, "weights", f32, (rows,), dev), _maybe(ended, "ended", i32, (rows,), dev), n_out,
-        _addr(parents, "parents", i32, shape, dev), _addr(tokens, "tokens", i32, shape, dev), _addr(totals, "totals", f32, shape, dev),
-        workspace.data_ptr(), workspace.nbytes, raw)
+    dev, calls = logits.get_device(), _native()
+    raw = _launch_on(dev, stream)
+    if parents is None or tokens is None or totals is None or workspace is None:
+        shape, on = (row_starts.shape[0] - 1, int(n_out)), logits.device
+        parents = _empty(shape, torch.int32, on, stream) if parents is None else parents
+        tokens = _empty(shape, torch.int32, on, stream) if tokens is None else tokens
+        totals = _empty(shape, torch.float32, on, stream) if totals is None else totals
+        workspace = _space(workspace, on, stream, beam_select_workspace_bytes, *logits.shape, *shape)
+    st = calls.select(logits, row_starts, n_out, scores, weights, ended, parents, tokens, totals, workspace, raw)
+    if st is None:
+        if logits.dim() != 2 or logits.dtype not in _DTYPE or logits.stride(1) != 1 and logits.shape[1] > 1:
+            raise ValueError("logits must be [n_rows][V] of float32, float16 or bfloat16 with contiguous rows")
+        rows, n, i32, f32 = logits.shape[0], row_starts.shape[0] - 1, torch.int32, torch.float32
+        _refuse(dev, (row_starts, "row_starts", i32, (n + 1,)),
+                *[(t, name, ty, (rows,)) for t, name, ty in ((scores, "scores", f32), (weights, "weights", f32), (ended, "ended", i32))
+                  if t is not None],
+                *[(t, name, ty, (n, int(n_out))) for t, name, ty in ((parents, "parents", i32), (tokens, "tokens", i32), (totals, "totals", f32))],
+                (workspace, "workspace", None, None))
     _check("beam_select", st)
     return parents, tokens, totals
 
@@ -994,19 +1001,20 @@ def token_counts_fork(parents: torch.Tensor, state_of: torch.Tensor | None, coun
                       status: torch.Tensor, n_seqs: int | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
     """Counts rows (counts int32 [n_states][V], updated) for the sequences that go on from others: int32 parents [m] (< 0: none) and
     state_of [n] (None: sequence q has row q, of n_seqs); outputs state_of_out int32 [m], which may be state_of, and status int32 [1]."""
-    dev, i32 = counts.get_device(), torch.int32
-    if counts.dim() != 2 or parents.dim() != 1:
-        raise ValueError("counts must be [n_states][V] and parents [n_children]")
-    m = parents.shape[0]
-    n = state_of.shape[0] if state_of is not None else counts.shape[0] if n_seqs is None else int(n_seqs)
-    lib = _lib or load_library()
+    dev, calls = counts.get_device(), _native()
     raw = _launch_on(dev, stream)
-    workspace = _space(workspace, counts.device, dev, stream, lib.token_counts_fork_workspace_bytes, m)
-    st = lib.token_counts_fork(
-        _addr(parents, "parents", i32, (m,), dev), m, _maybe(state_of, "state_of", i32, (n,), dev), n,
-        _addr(counts, "counts", i32, tuple(counts.shape), dev), counts.shape[0], counts.shape[1],
-        _addr(state_of_out, "state_of_out", i32, (m,), dev), _addr(status, "status", i32, (1,), dev), workspace.data_ptr(),
-        workspace.nbytes, raw)
+    if n_seqs is None:
+        n_seqs = counts.shape[0]
+    if workspace is None:
+        workspace = _space(None, counts.device, stream, token_counts_fork_workspace_bytes, parents.shape[0])
+    st = calls.counts_fork(parents, state_of, counts, state_of_out, status, n_seqs, workspace, raw)
+    if st is None:
+        if counts.dim() != 2 or parents.dim() != 1:
+            raise ValueError("counts must be [n_states][V] and parents [n_children]")
+        i32, m = torch.int32, parents.shape[0]
+        _refuse(dev, (parents, "parents", i32, None), *([] if state_of is None else [(state_of, "state_of", i32, tuple(state_of.shape[:1]))]),
+                (counts, "counts", i32, None), (state_of_out, "state_of_out", i32, (m,)), (status, "status", i32, (1,)),
+                (workspace, "workspace", None, None))
     _check("token_counts_fork", st)
 
 
@@ -1023,33 +1031,38 @@ def kvq8_paged_fork(parents: torch.Tensor, lens: torch.Tensor, held: torch.Tenso
     shares [n_pages] (holders beyond the first), free_ring [n_pages] (updated), ring_state [2]; outputs page_table_out
     [m][max_pages], lens_out, held_out, the copy list copy_src, copy_dst, copy_rows [m] for kvq8_paged_copy, and status [1].  shares and
     ring_state are updated in place unless shares_out / ring_out are given."""
-    dev, i32 = page_table.get_device(), torch.int32
-    if page_table.dim() != 2 or free_ring.dim() != 1 or parents.dim() != 1:
-        raise ValueError("page_table must be [n][max_pages], free_ring [n_pages] and parents [n_children]")
-    m, (n, mp), n_pages = parents.shape[0], page_table.shape, free_ring.shape[0]
-    lib = _lib or load_library()
+    dev, calls = page_table.get_device(), _native()
     raw = _launch_on(dev, stream)
-    workspace = _space(workspace, page_table.device, dev, stream, lib.kvq8_paged_fork_workspace_bytes, n, m, n_pages)
-    at, lens_at, held_at, src_at, dst_at, rows_at = _addrs(i32, (m,), dev, parents=parents, lens_out=lens_out, held_out=held_out,
-                                                           copy_src=copy_src, copy_dst=copy_dst, copy_rows=copy_rows)
-    old_lens, old_held = _addrs(i32, (n,), dev, lens=lens, held=held)
-    shares_at, ring, shares_to = _addrs(i32, (n_pages,), dev, shares=shares, free_ring=free_ring,
-                                        shares_out=shares if shares_out is None else shares_out)
-    state, state_to = _addrs(i32, (2,), dev, ring_state=ring_state, ring_out=ring_state if ring_out is None else ring_out)
-    st = lib.kvq8_paged_fork(
-        at, m, old_lens, old_held, n, int(page_size), _addr(page_table, "page_table", i32, (n, mp), dev), mp, shares_at, ring, n_pages, state,
-        _addr(page_table_out, "page_table_out", i32, (m, mp), dev), lens_at, held_at, shares_to, state_to, src_at, dst_at, rows_at,
-        _addr(status, "status", i32, (1,), dev), workspace.data_ptr(), workspace.nbytes, raw)
+    if workspace is None:
+        workspace = _space(None, page_table.device, stream, kvq8_paged_fork_workspace_bytes, page_table.shape[0], parents.shape[0],
+                           free_ring.shape[0])
+    if shares_out is None:
+        shares_out = shares
+    if ring_out is None:
+        ring_out = ring_state
+    st = calls.paged_fork(parents, lens, held, page_size, page_table, shares, free_ring, ring_state, page_table_out, lens_out, held_out,
+                          shares_out, ring_out, copy_src, copy_dst, copy_rows, status, workspace, raw)
+    if st is None:
+        if page_table.dim() != 2 or free_ring.dim() != 1 or parents.dim() != 1:
+            raise ValueError("page_table must be [n][max_pages], free_ring [n_pages] and parents [n_children]")
+        i32, m, (n, mp), n_pages = torch.int32, parents.shape[0], page_table.shape, free_ring.shape[0]
+        _refuse(dev, *[(t, name, i32, shape) for shape, named in (
+            ((m,), dict(parents=parents, lens_out=lens_out, held_out=held_out, copy_src=copy_src, copy_dst=copy_dst, copy_rows=copy_rows)),
+            ((n,), dict(lens=lens, held=held)), ((n, mp), dict(page_table=page_table)), ((m, mp), dict(page_table_out=page_table_out)),
+            ((n_pages,), dict(shares=shares, free_ring=free_ring, shares_out=shares_out)), ((2,), dict(ring_state=ring_state, ring_out=ring_out)),
+            ((1,), dict(status=status))) for name, t in named.items()], (workspace, "workspace", None, None))
     _check("kvq8_paged_fork", st)
 
 
 def kvq8_paged_copy(cache: KVPagedCacheQ8, src_pages: torch.Tensor, dst_pages: torch.Tensor, rows: torch.Tensor | None = None,
                     stream=None) -> None:
     """Copy the first rows (int32 [n]; None: all) of pages src_pages to pages dst_pages (int32 [n]; -1: nothing), K and V."""
-    n, dev = src_pages.shape[0], cache._index
-    st = (_lib or load_library()).kvq8_paged_copy(
-        cache._struct, _addr(src_pages, "src_pages", torch.int32, (n,), dev), _addr(dst_pages, "dst_pages", torch.int32, (n,), dev),
-        _maybe(rows, "rows", torch.int32, (n,), dev), n, _launch_on(dev, stream))
+    dev = cache._index
+    st = _native().paged_copy(cache._at, dev, src_pages, dst_pages, rows, _launch_on(dev, stream))
+    if st is None:
+        i32, shape = torch.int32, tuple(src_pages.shape[:1])
+        _refuse(dev, (src_pages, "src_pages", i32, shape), (dst_pages, "dst_pages", i32, shape),
+                *([] if rows is None else [(rows, "rows", i32, shape)]))
     _check("kvq8_paged_copy", st)
 
 
@@ -1057,12 +1070,14 @@ def kvq8_paged_compact(cache: KVPagedCacheQ8, page_table: torch.Tensor, lens: to
                        kept: torch.Tensor, lens_out: torch.Tensor | None = None, stream=None) -> None:
     """Move the kept rows of every request's window (kept int64 [n], bit j = place j) together to its first places; page_table int32
     [n][max_pages], lens int32 [n], row_starts int32 [n + 1].  lens_out int32 [n]: the lengths afterwards."""
-    dev, i32 = cache._index, torch.int32
-    n, mp = page_table.shape
-    st = (_lib or load_library()).kvq8_paged_compact(
-        cache._struct, _addr(page_table, "page_table", i32, (n, mp), dev), mp, _addr(lens, "lens", i32, (n,), dev),
-        _addr(row_starts, "row_starts", i32, (n + 1,), dev), n, _addr(kept, "kept", torch.int64, (n,), dev),
-        _maybe(lens_out, "lens_out", i32, (n,), dev), _launch_on(dev, stream))
+    dev = cache._index
+    st = _native().paged_compact(cache._at, dev, page_table, lens, row_starts, kept, lens_out, _launch_on(dev, stream))
+    if st is None:
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [n][max_pages]")
+        i32, n = torch.int32, page_table.shape[0]
+        _refuse(dev, (page_table, "page_table", i32, None), (lens, "lens", i32, (n,)), (row_starts, "row_starts", i32, (n + 1,)),
+                (kept, "kept", torch.int64, (n,)), *([] if lens_out is None else [(lens_out, "lens_out", i32, (n,))]))
     _check("kvq8_paged_compact", st)
 
 
@@ -1090,32 +1105,26 @@ def kvq8_paged_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ca
     the cache at int64 slots [n_tok] (fp32, fp16 or bf16; tokens may be strided).  turns: rope_turns of the frequencies, [rot_dim / 2];
     axis_of int32 [rot_dim / 2]: the axis of each pair; pairs: dims 2i and 2i + 1 turn together, else i and i + rot_dim / 2.  Returns
     q_out (q_out=q works in place); tokens whose slot is outside the cache are left alone."""
-    dev, i32 = cache._index, torch.int32
-    shape = q.shape
-    if len(shape) != 3 or q.dtype not in _DTYPE or q.get_device() != dev or shape[2] != cache.head_dim:
-        raise ValueError(f"q must be float32, float16 or bfloat16 [n_tok][n_q_heads][{cache.head_dim}] on {cache.device}")
-    n, hq, hd = shape
-    if k.dtype is not q.dtype or v.dtype is not q.dtype or k.shape != v.shape or k.shape[0] != n:
-        raise ValueError("q, k and v must have one type and one number of tokens")
-    ks, vs = _token_stride(k, "k", cache), _token_stride(v, "v", cache)
-    one = positions.dim() == 1
-    axes = 1 if one else positions.shape[0]
-    if turns.dim() != 1:
-        raise ValueError("turns must be [rot_dim / 2]")
-    half = turns.shape[0]
+    dev, calls = cache._index, _native()
     raw = _launch_on(dev, stream)
     if q_out is None:
-        q_out = _empty((n, hq, hd), q.dtype, q.device, stream)
-    strides = []
-    for t, name in ((q, "q"), (q_out, "q_out")):
-        stride = t.stride()
-        if t.shape != shape or t.dtype is not q.dtype or t.get_device() != dev or stride[2] != 1 or (stride[1] != hd and hq > 1):
-            raise ValueError(f"{name} must be {q.dtype} {tuple(shape)} on {cache.device}, the heads of a token contiguous")
-        strides.append(stride[0] if n > 1 else hq * hd)
-    st = (_lib or load_library()).kvq8_paged_append_rope(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _DTYPE[q.dtype], n, hq, strides[0], ks, vs,
-        _addr(positions, "positions", i32, (n,) if one else (axes, n), dev), axes,
-        _addr(turns, "turns", torch.int64, (half,), dev), _maybe(axis_of, "axis_of", i32, (half,), dev), 2 * half, 1 if pairs else 0,
-        cache._struct, _addr(slots, "slots", torch.int64, (n,), dev), q_out.data_ptr(), strides[1], raw)
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    st = calls.paged_append_rope(cache._at, dev, q, k, v, slots, positions, turns, axis_of, bool(pairs), q_out, raw)
+    if st is None:
+        heads, dim = cache.n_kv_heads, cache.head_dim
+        if q.dim() != 3 or q.dtype not in _DTYPE or q.get_device() != dev or q.shape[2] != dim:
+            raise ValueError(f"q must be float32, float16 or bfloat16 [n_tok][n_q_heads][{dim}] on {cache.device}")
+        if k.dtype is not q.dtype or v.dtype is not q.dtype or k.shape != v.shape or k.shape[0] != q.shape[0]:
+            raise ValueError("q, k and v must have one type and one number of tokens")
+        _token_stride(k, "k", cache)
+        _token_stride(v, "v", cache)
+        for t, name in ((q, "q"), (q_out, "q_out")):
+            if t.shape != q.shape or t.dtype is not q.dtype or t.get_device() != dev or t.stride(2) != 1 or (t.stride(1) != dim and q.shape[1] > 1):
+                raise ValueError(f"{name} must be {q.dtype} {tuple(q.shape)} on {cache.device}, the heads of a token contiguous")
+        if turns.dim() != 1 or positions.dim() > 2:
+            raise ValueError("turns must be [rot_dim / 2] and positions [n_tok] or [n_axes][n_tok]")
+        n, half = q.shape[0], turns.shape[0]
+        _refuse(dev, (slots, "slots", torch.int64, (n,)), (positions, "positions", torch.int32, (*positions.shape[:-1], n)),
+                (turns, "turns", torch.int64, (half,)), *([] if axis_of is None else [(axis_of, "axis_of", torch.int32, (half,))]))
     _check("kvq8_paged_append_rope", st)
     return q_out

@@ -2,16 +2,20 @@
 
 Every .cu file under csrc/ is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` and linked into one shared
-library next to this file.  No CMake, no torch extension machinery.
+library next to this file.  csrc/calls.cpp, the binding's argument checks of the calls that stand in steps
+of a few microseconds, is compiled beside them with the host compiler against torch's headers, and linked
+to that library.  No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libkvq8attn.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -37,13 +43,13 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "kvq8attn.h")]
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [CALLS_SOURCE, os.path.join(INCLUDE, "kvq8attn.h")]
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -66,14 +72,34 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    calls_obj = os.path.join(BUILD_DIR, "calls.cpp.o")
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+
+    def compile_calls():
+        include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                   sysconfig.get_paths()["include"], INCLUDE]
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *[f"-I{d}" for d in include], "-c", CALLS_SOURCE, "-o", calls_obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the host compiler failed for {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = LIB_PATH + f".{os.getpid()}.tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = CALLS_PATH + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, calls_obj, f"-L{HERE}", "-lkvq8attn", f"-L{os.path.join(torch_dir, 'lib')}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
     return LIB_PATH
 
 

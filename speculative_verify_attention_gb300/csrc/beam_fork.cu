@@ -189,13 +189,16 @@ struct PagedFork {
     int32_t* status;
     // workspace
     int32_t* take;      // [n_children] the fresh page of a child, -1: none
-    int32_t* holders;   // [n_seqs] children, and bit 30: the first one goes on in the last page
+    int32_t* holders;   // [n_seqs] children, and kGoesOn: the first one goes on in the last page; kStays: nothing moves
     uint32_t* freed;    // [ceil(n_pages / 32)] pages that nobody holds any more
-    uint32_t* done;     // blocks of the second kernel that are done
+    int32_t* head;      // the ring's head and count as they were, pages taken, and whether anything moves
     int n_children, n_seqs, max_pages, n_pages, page_shift;
 };
 
-constexpr int32_t kGoesOn = 1 << 30;
+constexpr int32_t kGoesOn = 1 << 30, kStays = 1 << 29;
+constexpr int kSmallTasks = 128, kSmallPages = 16384;  // what one block does alone
+constexpr int kForkThreads = 256;
+constexpr int kForkBlocks = 152 * 8;
 constexpr int kCopyPer = 4096;  // pages of the pool that a block of the first kernel clears or copies
 
 // Thread id of n: the shares, if they are not updated in place, and no marks.
@@ -210,25 +213,40 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
     const int tid = threadIdx.x;
     int* s_first = sm;
     int* s_kids = s_first + p.n_seqs;
+    int* s_len = s_kids + p.n_seqs;
+    int* s_tail = s_len + p.n_seqs;  // its last page, if that is not full
     const int page = 1 << p.page_shift;
     const int head = p.ring_state[0], count = p.ring_state[1];
+    // what the sequences alone say, asked for before the children are counted
+    constexpr int kPer = kMaxSeqs / kPlanThreads;
+    int holds[kPer];  // 0, or kGoesOn; -1: held is wrong, -2: its children's length is
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int q = tid + u * kPlanThreads;
+        holds[u] = 0;
+        if (q >= p.n_seqs) continue;
+        const int held = p.held[q], len = p.lens[q];
+        s_len[q] = len;
+        if (held < 0 || held > p.max_pages) {
+            holds[u] = -1;
+        } else if (len < 0 || len > ((int64_t)held << p.page_shift)) {
+            holds[u] = -2;
+        } else if (len & (page - 1)) {
+            // a last page that is not full goes to the first child, if no other sequence holds it
+            const int tail = p.table[(int64_t)q * p.max_pages + (len >> p.page_shift)];
+            if (tail < 0 || tail >= p.n_pages || p.shares[tail] == 0) holds[u] = kGoesOn;
+            s_tail[q] = tail;
+        }
+    }
     bool bad = families(p.parents, p.n_children, p.n_seqs, s_first, s_kids);
     bad |= head < 0 || head >= p.n_pages || count < 0 || count > p.n_pages;
-    for (int q = tid; q < p.n_seqs; q += kPlanThreads) {
-        const int held = p.held[q], len = p.lens[q], kids = s_kids[q];
-        bool wrong = held < 0 || held > p.max_pages;
-        int32_t holds = kids;
-        if (kids && !wrong) {
-            wrong = len < 0 || len > ((int64_t)held << p.page_shift);
-            if (!wrong && (len & (page - 1))) {
-                // a last page that is not full goes to the first child, if no other sequence holds it
-                const int tail = p.table[(int64_t)q * p.max_pages + (len >> p.page_shift)];
-                if (tail < 0 || tail >= p.n_pages || p.shares[tail] == 0) holds |= kGoesOn;
-            }
-        }
-        bad |= wrong;
-        s_kids[q] = holds;
-        p.holders[q] = holds;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int q = tid + u * kPlanThreads;
+        if (q >= p.n_seqs) continue;
+        const int kids = s_kids[q];
+        bad |= holds[u] == -1 || (holds[u] == -2 && kids);
+        s_kids[q] = kids | (kids && holds[u] == kGoesOn ? kGoesOn : 0);
     }
     bad = __syncthreads_or(bad);
     int takes = 0;
@@ -238,7 +256,7 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
         int len = 0;
         bool take = false;
         if (live) {
-            len = p.lens[q];
+            len = s_len[q];
             take = (len & (page - 1)) && !(s_first[q] == i && (s_kids[q] & kGoesOn));
         }
         int total;
@@ -248,7 +266,7 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
             int fresh = -1, src = -1;
             if (take && k < count) {
                 fresh = p.ring[head + k >= p.n_pages ? head + k - p.n_pages : head + k];
-                src = p.table[(int64_t)q * p.max_pages + (len >> p.page_shift)];
+                src = s_tail[q];
             }
             p.take[i] = fresh;
             p.copy_src[i] = src;
@@ -259,6 +277,7 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
         }
     }
     const int status = bad ? 2 : takes > count ? 1 : 0;
+    for (int q = tid; q < p.n_seqs; q += kPlanThreads) p.holders[q] = status ? kStays : s_kids[q];
     if (status) {
         __syncthreads();
         for (int i = tid; i < p.n_children; i += kPlanThreads) {
@@ -268,74 +287,116 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
     }
     if (tid == 0) {
         p.status[0] = status;
-        p.done[0] = 0u;
-        p.done[1] = (uint32_t)takes;
+        p.head[0] = head, p.head[1] = count, p.head[2] = status ? 0 : takes, p.head[3] = status == 0;
     }
     return status == 0;
 }
 
-// Entries k0, k0 + step, ... of row y: a child's row of the table from its parent's, or, behind the children, what a sequence's pages
-// gain or lose: each is held by its children from now on, not by itself.  shares counts holders beyond the first, so the last one to
-// let a page go takes it below zero.
-__device__ __forceinline__ void fork_row(const PagedFork& p, int y, int k0, int step) {
-    if (y < p.n_children) {
-        const int need = p.held_out[y];
-        if (need <= 0) return;
-        const int fresh = p.take[y], tail = fresh >= 0 ? need - 1 : -1;
-        const int32_t* from = p.table + (int64_t)p.parents[y] * p.max_pages;
-        int32_t* to = p.table_out + (int64_t)y * p.max_pages;
-#pragma unroll 4
-        for (int k = k0; k < need; k += step) to[k] = k == tail ? fresh : from[k];
-        return;
-    }
-    const int q = y - p.n_children, page = 1 << p.page_shift;
-    const int held = p.held[q], holders = p.holders[q], kids = holders & (kGoesOn - 1);
-    const int full = kids ? p.lens[q] >> p.page_shift : 0;
-    const bool goes_on = kids && (p.lens[q] & (page - 1)) && (holders & kGoesOn);
+constexpr int kPiece = 128;  // entries of a table's row that a warp takes
+
+// A lane's four entries of child i's row of the table, from k0 on, from its parent's.
+__device__ __forceinline__ void fork_child(const PagedFork& p, int i, int k0) {
+    const int need = p.held_out[i], q = p.parents[i], fresh = p.take[i];
+    if (need <= 0) return;
+    const int tail = fresh >= 0 ? need - 1 : -1;
     const int32_t* from = p.table + (int64_t)q * p.max_pages;
-#pragma unroll 4
-    for (int k = k0; k < held; k += step) {
-        const int change = (k < full ? kids : k == full && goes_on ? 1 : 0) - 1;
-        if (change == 0) continue;
-        const int id = from[k];
-        if (id < 0 || id >= p.n_pages) continue;
-        if (atomicAdd(p.shares_out + id, change) + change < 0) atomicOr(p.freed + (id >> 5), 1u << (id & 31));
+    int32_t* to = p.table_out + (int64_t)i * p.max_pages;
+    int v[kPiece / 32];
+#pragma unroll
+    for (int u = 0; u < kPiece / 32; ++u) v[u] = k0 + u * 32 < need ? from[k0 + u * 32] : 0;
+#pragma unroll
+    for (int u = 0; u < kPiece / 32; ++u)
+        if (k0 + u * 32 < need) to[k0 + u * 32] = k0 + u * 32 == tail ? fresh : v[u];
+}
+
+// What the pages at place k of kTogether sequences gain or lose: each is held by their children from now on, not by themselves.  shares
+// counts holders beyond the first, so the last one to let a page go takes it below zero.  A request's beams stand together and share
+// most of their pages, which as many children hold again: the changes of neighbours of one page are added up first, and most come
+// to nothing.  The atomics that are left go out together: one after another they took longer than all the rest.
+constexpr int kTogether = 8;
+__device__ __forceinline__ void fork_pages(const PagedFork& p, int group, int k) {
+    const int q0 = group * kTogether;
+    int page[kTogether], change[kTogether];
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u) {
+        const int q = q0 + u;
+        const bool there = q < p.n_seqs;
+        const int held = there ? p.held[q] : 0, holders = there ? p.holders[q] : kStays, len = there ? p.lens[q] : 0;
+        const int kids = holders & ~(kGoesOn | kStays), full = len >> p.page_shift;  // (without children a length means nothing)
+        const bool on = k < held && !(holders & kStays);
+        page[u] = on ? p.table[(int64_t)q * p.max_pages + k] : -1;
+        change[u] = on ? (kids == 0 ? 0 : k < full ? kids : k == full && (holders & kGoesOn) ? 1 : 0) - 1 : 0;
+    }
+#pragma unroll
+    for (int u = 0; u + 1 < kTogether; ++u)
+        if (page[u] == page[u + 1]) change[u + 1] += change[u], change[u] = 0;
+    int left[kTogether];
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u) {
+        if (page[u] < 0 || page[u] >= p.n_pages) change[u] = 0;
+        left[u] = change[u] ? atomicAdd(p.shares_out + page[u], change[u]) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u)
+        if (change[u] && left[u] + change[u] < 0) atomicOr(p.freed + (page[u] >> 5), 1u << (page[u] & 31));
+}
+
+// Warp `warp` of n: a piece of a child's row of the table at a time, or a place a lane of a group of sequences.
+__host__ __device__ __forceinline__ int64_t fork_tasks(const PagedFork& p, int64_t& children) {
+    children = (int64_t)p.n_children * ((p.max_pages + kPiece - 1) / kPiece);
+    return children + (int64_t)((p.n_seqs + kTogether - 1) / kTogether) * ((p.max_pages + 31) / 32);
+}
+__device__ __forceinline__ void fork_all(const PagedFork& p, int warp, int n) {
+    const int pieces = (p.max_pages + kPiece - 1) / kPiece, parts = (p.max_pages + 31) / 32, lane = threadIdx.x & 31;
+    int64_t children;
+    const int64_t all = fork_tasks(p, children);
+    for (int64_t w = warp; w < all; w += n) {
+        if (w < children) {
+            const int i = (int)(w / pieces);
+            fork_child(p, i, (int)(w - (int64_t)i * pieces) * kPiece + lane);
+        } else {
+            const int group = (int)((w - children) / parts);
+            fork_pages(p, group, (int)(w - children - (int64_t)group * parts) * 32 + lane);
+        }
     }
 }
 
-// One block, after all rows: the pages that nobody holds any more go behind the ring's tail, in order of their number.
-__device__ __forceinline__ void fork_give(const PagedFork& p, bool moved, int* s_warp) {
-    constexpr int kWords = 4;  // words of marks of a thread at a time
-    const int tid = threadIdx.x, threads = (int)blockDim.x;
-    const int head = p.ring_state[0], count = p.ring_state[1], takes = moved ? (int)__ldcg(p.done + 1) : 0;
-    int given = 0;
+// After all tasks: the pages that nobody holds any more go behind the ring's tail, in order of their number.  Block `block` of n
+// has a part of the marks, and counts those before it itself; a warp writes a word's pages at once.
+constexpr int kGiveThreads = 1024;  // or fewer
+constexpr int kGiveWords = 64;      // words of marks that a block of the wide form takes, in up to 64 blocks
+__device__ __forceinline__ void fork_give(const PagedFork& p, int block, int n, int* s_warp) {
+    __shared__ uint32_t s_bits[kGiveThreads];
+    __shared__ int s_at[kGiveThreads];
+    const int tid = threadIdx.x, threads = (int)blockDim.x, lane = tid & 31;
+    const int head = p.head[0], count = p.head[1], takes = p.head[2];
+    const bool moved = p.head[3] != 0;
+    int given = 0, tail = head + count;
     if (moved) {
-        const int n_words = (p.n_pages + 31) / 32;
-        int tail = head + count;
         if (tail >= p.n_pages) tail -= p.n_pages;
-        for (int w0 = 0; w0 < n_words; w0 += threads * kWords) {
-            uint32_t bits[kWords];
-            int n = 0;
-#pragma unroll
-            for (int u = 0; u < kWords; ++u) {
-                const int w = w0 + tid * kWords + u;
-                bits[u] = w < n_words ? __ldcg(p.freed + w) : 0u;
-                n += __popc(bits[u]);
-            }
+        const int n_words = (p.n_pages + 31) / 32, per = (n_words + n - 1) / n, first = min(block * per, n_words), last = min(first + per, n_words);
+        int before = 0;
+#pragma unroll 8
+        for (int w = tid; w < first; w += threads) before += __popc(__ldcg(p.freed + w));
+        block_sums(before, s_warp, given);
+        for (int w0 = first; w0 < last; w0 += threads) {
+            const uint32_t bits = w0 + tid < last ? __ldcg(p.freed + w0 + tid) : 0u;
             int total;
-            int k = given + block_sums(n, s_warp, total);
+            s_at[tid] = given + block_sums(__popc(bits), s_warp, total);
+            s_bits[tid] = bits;
             given += total;
-#pragma unroll
-            for (int u = 0; u < kWords; ++u)
-                for (; bits[u]; bits[u] &= bits[u] - 1, ++k) {
-                    const int id = 32 * (w0 + tid * kWords + u) + __ffs((int)bits[u]) - 1;
-                    p.shares_out[id] = 0;
-                    if (k < p.n_pages - count) p.ring[tail + k >= p.n_pages ? tail + k - p.n_pages : tail + k] = id;
-                }
+            __syncthreads();
+            for (int w = tid >> 5; w < min(threads, last - w0); w += threads / 32) {
+                const uint32_t word = s_bits[w];
+                if (!(word >> lane & 1u)) continue;
+                const int id = 32 * (w0 + w) + lane, k = s_at[w] + __popc(word & ((1u << lane) - 1));
+                p.shares_out[id] = 0;
+                if (k < p.n_pages - count) p.ring[tail + k >= p.n_pages ? tail + k - p.n_pages : tail + k] = id;
+            }
+            __syncthreads();
         }
     }
-    __syncthreads();  // every thread has read the state
-    if (tid == 0) {
+    if (block == n - 1 && tid == 0) {  // its sum is the whole one
         const int h = head + takes;
         p.ring_out[0] = moved && h >= p.n_pages ? h - p.n_pages : h;  // (a malformed one is repeated)
         p.ring_out[1] = moved ? count - takes + min(given, p.n_pages - count) : count;
@@ -351,10 +412,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_fork_small_kernel(const __
     fork_clear(p, threadIdx.x, kPlanThreads);
     const bool moved = fork_plan(p, sm, s_warp);
     __syncthreads();
-    if (moved)
-        for (int y = threadIdx.x >> 5; y < p.n_children + p.n_seqs; y += kPlanThreads / 32) fork_row(p, y, threadIdx.x & 31, 32);
+    if (moved) fork_all(p, threadIdx.x >> 5, kPlanThreads / 32);
     __syncthreads();
-    fork_give(p, moved, s_warp);
+    fork_give(p, 0, 1, s_warp);
 }
 
 // Block 0 plans, the others clear.
@@ -369,26 +429,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_fork_plan_kernel(const __g
         fork_clear(p, ((int)blockIdx.x - 1) * kPlanThreads + threadIdx.x, kPlanThreads * ((int)gridDim.x - 1));
 }
 
-constexpr int kSmallEntries = 16384;  // of the tables, and pages of the pool
-constexpr int kForkThreads = 256;
-constexpr int kForkPer = 4;  // entries of a table row that a thread takes
 
-// Block (part of a table row, child or sequence); the last block to finish gives pages back.
 __global__ void __launch_bounds__(kForkThreads) paged_fork_kernel(const __grid_constant__ PagedFork p) {
-    __shared__ int s_warp[32];
-    __shared__ int s_last;
-    const int tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const bool moved = p.status[0] == 0;
-    if (moved) fork_row(p, blockIdx.y, blockIdx.x * kForkThreads + tid, gridDim.x * kForkThreads);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(p.done, 1u) == gridDim.x * gridDim.y - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    fork_give(p, moved, s_warp);
+    fork_all(p, (int)blockIdx.x * (kForkThreads / 32) + (int)(threadIdx.x >> 5), (int)gridDim.x * (kForkThreads / 32));
+}
+
+__global__ void __launch_bounds__(kForkThreads) paged_fork_give_kernel(const __grid_constant__ PagedFork p) {
+    __shared__ int s_warp[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    fork_give(p, (int)blockIdx.x, (int)gridDim.x, s_warp);
 }
 
 size_t fork_carve(PagedFork& p, unsigned char* base) {
@@ -400,7 +452,7 @@ size_t fork_carve(PagedFork& p, unsigned char* base) {
     take(p.take, (size_t)p.n_children);
     take(p.holders, (size_t)p.n_seqs);
     take(p.freed, ((size_t)p.n_pages + 31) / 32);
-    take(p.done, 2);
+    take(p.head, 4);
     return at;
 }
 
@@ -486,12 +538,22 @@ extern "C" int kvq8_paged_fork(const int32_t* parents, int n_children, const int
                    max_pages, n_pages, log2_of(page_size)};
     fork_carve(p, static_cast<unsigned char*>(workspace));
     cudaStream_t s = (cudaStream_t)stream;
-    if ((int64_t)max_pages * (n_children + n_seqs) <= kSmallEntries && n_pages <= kSmallEntries)
-        return launch_dependent(paged_fork_small_kernel, 1, kPlanThreads, 2 * n_seqs * 4, s, p);
-    const int clear = (n_pages + kCopyPer - 1) / kCopyPer;
-    const int rc = launch_dependent(paged_fork_plan_kernel, (unsigned)(1 + (clear < 75 ? clear : 75)), kPlanThreads, 2 * n_seqs * 4, s, p);
+    int64_t children;
+    const int64_t tasks = fork_tasks(p, children);
+    const int smem = 4 * n_seqs * 4;
+    static SmemOptIn opt_small, opt_plan;
+    if (tasks <= kSmallTasks && n_pages <= kSmallPages) {
+        const int rc = opt_small.ensure(paged_fork_small_kernel, 4 * kMaxSeqs * 4);
+        return rc != KVQ8_OK ? rc : launch_dependent(paged_fork_small_kernel, 1, kPlanThreads, smem, s, p);
+    }
+    int rc = opt_plan.ensure(paged_fork_plan_kernel, 4 * kMaxSeqs * 4);
     if (rc != KVQ8_OK) return rc;
-    const int per = kForkThreads * kForkPer;
-    const dim3 grid((unsigned)((max_pages + per - 1) / per), (unsigned)(n_children + n_seqs));
-    return launch_dependent(paged_fork_kernel, grid, kForkThreads, 0, s, p);
+    const int clear = (n_pages + kCopyPer - 1) / kCopyPer;
+    rc = launch_dependent(paged_fork_plan_kernel, (unsigned)(1 + (clear < 75 ? clear : 75)), kPlanThreads, smem, s, p);
+    if (rc != KVQ8_OK) return rc;
+    const int64_t blocks = (tasks + kForkThreads / 32 - 1) / (kForkThreads / 32);
+    rc = launch_dependent(paged_fork_kernel, (unsigned)(blocks < kForkBlocks ? blocks : kForkBlocks), kForkThreads, 0, s, p);
+    if (rc != KVQ8_OK) return rc;
+    const int words = (n_pages + 31) / 32, give = (words + kGiveWords - 1) / kGiveWords;
+    return launch_dependent(paged_fork_give_kernel, (unsigned)(give < 64 ? give : 64), kForkThreads, 0, s, p);
 }

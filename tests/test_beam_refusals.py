@@ -133,3 +133,44 @@ def test_rope_on_the_rows_of_one_product(out, status):
     supported is refused after that, so nothing is launched.)"""
     rows = dict(q=A, k=A + 1024 * 2, v=A + 1280 * 2, q_stride=2560, k_stride=2560, v_stride=2560, q_out=out, out_stride=2560, n_tok=1000)
     assert _call("kvq8_paged_append_rope", ROPE, {**rows, "n_axes": 5}) == status
+
+
+def test_the_binding_refuses_tensors_it_cannot_pass_on():
+    import torch
+
+    import speculative_verify_attention_gb300 as kv
+    i32 = torch.int32
+    host = kv.KVPagedCacheQ8(2, 128, 16, 3, device="cpu")
+    z = torch.zeros(4, dtype=i32)
+    with pytest.raises(ValueError, match="CUDA device"):
+        kv.beam_select(torch.zeros((4, 10)), torch.zeros(2, dtype=i32), 3)
+    with pytest.raises(ValueError, match="CUDA device"):
+        kv.token_counts_fork(z, z, torch.zeros((4, 10), dtype=i32), z, z[:1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        kv.kvq8_paged_fork(z, z, z, 16, torch.zeros((4, 2), dtype=i32), z, z, z[:2], torch.zeros((4, 2), dtype=i32), z, z, z, z, z, z[:1])
+    with pytest.raises(ValueError, match="CUDA device"):
+        kv.kvq8_paged_copy(host, z, z)
+    with pytest.raises(ValueError, match="CUDA device"):
+        kv.kvq8_paged_compact(host, torch.zeros((4, 2), dtype=i32), z, torch.zeros(5, dtype=i32), torch.zeros(4, dtype=torch.int64))
+    with pytest.raises(ValueError, match="CUDA device"):
+        x = torch.zeros((4, 2, 128))
+        kv.kvq8_paged_append_rope(x, x, x, host, torch.zeros(4, dtype=torch.int64), z, kv.rope_turns(torch.ones(64)))
+
+
+def test_turns_of_frequencies():
+    """To the nearest 2^-64 of a turn, modulo a turn, against whole-number arithmetic from pi's digits."""
+    import math
+    from fractions import Fraction
+
+    import torch
+
+    from speculative_verify_attention_gb300 import rope_turns
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798214808651")
+    f = [1.0, 10000.0 ** -0.5, 1e-12, 0.0, -0.25, math.pi, 2 * math.pi, 100.0, 1e6 + 0.5, -1e-30]
+    for x, got in zip(f, rope_turns(torch.tensor(f, dtype=torch.float64)).tolist()):
+        exact = Fraction(x) / (2 * pi) * 2 ** 64
+        want = math.floor(exact + Fraction(1, 2)) % 2 ** 64
+        assert got % 2 ** 64 == want, x
+    for bad in (float("nan"), float("inf")):
+        with pytest.raises(ValueError):
+            rope_turns(torch.tensor([bad]))
