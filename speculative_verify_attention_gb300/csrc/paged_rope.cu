@@ -32,7 +32,7 @@ struct RopeParams {
     int8_t* codes[2];
     uint16_t* scales[2];
     int64_t n_slots;
-    int n_tok, n_q_heads, n_kv_heads, head_shift, page_shift, rot, n_axes;
+    int n_tok, n_q_heads, n_kv_heads, page_shift, rot, n_axes;
 };
 
 // cos and sin of phase / 2^64 turns.
@@ -127,33 +127,30 @@ struct Turns<true> {
 // Block (two or four tokens, a share of the heads): the lanes of a warp are the items of its tokens' rows, its heads every eighth of the
 // block's, queries, then keys, then values.  The groups g and h of item j: in the rotated part of a row its first and second half,
 // then the same of the part behind it; both parts are multiples of 64, so four neighbouring lanes have a 32-value block in each.
-template <typename T, bool PAIRS>
+template <typename T, int HD, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 3 : 4) paged_rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ __align__(16) float2 s_turns[4 * 128];  // [tokens][rot / 2]
-    const int lane = threadIdx.x & 31, item_shift = p.head_shift - 4, j = lane & ((1 << item_shift) - 1);
+    constexpr int kItems = HD / 16, kTokens = 32 / kItems;
+    __shared__ __align__(16) float2 s_turns[kTokens * HD / 2];  // [tokens][rot / 2]
+    const int tid = threadIdx.x, lane = tid & 31, j = lane % kItems, mine = lane / kItems;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tokens = 32 >> item_shift, tok0 = (int)blockIdx.x * tokens, mine = lane >> item_shift, tok = tok0 + mine;
+    const int tok0 = (int)blockIdx.x * kTokens, tok = tok0 + mine;
     const int64_t slot = tok < p.n_tok ? __ldg(p.slots + tok) : -1;
     const bool there = slot >= 0 && slot < p.n_slots;
-    const int rot_items = p.rot / 16, rest = ((1 << p.head_shift) - p.rot) / 16;
-    const int g = j < rot_items ? j : rot_items + j, h = g + (j < rot_items ? rot_items : rest);
-    const int warp = (int)blockIdx.y * kRopeWarps + (int)(threadIdx.x >> 5), step = kRopeWarps * (int)gridDim.y;
-    const T* q = static_cast<const T*>(p.q) + (int64_t)tok * p.q_stride + g * 8;
-    const int far = (h - g) * 8;
-    Eight<T> ra, rb;
-    auto load = [&](const T* x, bool on) {
-        ra.clear();
-        rb.clear();
-        if (!on) return;
-        load_now(ra, x);
-        load_now(rb, x + far);
-    };
-    int head = warp;
-    load(q + ((int64_t)head << p.head_shift), there && head < p.n_q_heads);
-    const int half = p.rot / 2;
+    const int rot_items = p.rot / 16, half = p.rot / 2;
+    const int g = j < rot_items ? j : rot_items + j, far = j < rot_items ? half : (HD - p.rot) / 2;
+    const bool turned = j < rot_items;
+    const int step = kRopeWarps * (int)gridDim.y, warp = (int)blockIdx.y * kRopeWarps + (tid >> 5);
+    Eight<T> ra, rb;  // lanes without a token compute with zeros, and store nothing
+    ra.clear();
+    rb.clear();
+    const T* q = static_cast<const T*>(p.q) + (int64_t)tok * p.q_stride + (warp * HD + g * 8);
+    if (there && warp < p.n_q_heads) {
+        load_now(ra, q);
+        load_now(rb, q + far);
+    }
     {  // as many threads a token as a row has pairs at most
-        const int t = (int)threadIdx.x >> (p.head_shift - 1), pair = (int)threadIdx.x & ((1 << (p.head_shift - 1)) - 1);
+        const int t = tid / (HD / 2), pair = tid % (HD / 2);
         if (pair < half && tok0 + t < p.n_tok) {
             const int axis = p.axis_of ? __ldg(p.axis_of + pair) : 0;
             const int64_t pos = axis >= 0 && axis < p.n_axes ? __ldg(p.positions + (int64_t)axis * p.n_tok + tok0 + t) : 0;
@@ -161,43 +158,51 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 3 : 4) paged_ro
         }
     }
     __syncthreads();
-    const bool turned = j < rot_items;
     Turns<PAIRS> turns;
-    if (turned) turns.load(s_turns + mine * half, g, h);
+    if (turned) turns.load(s_turns + mine * half, g, g + far / 8);
     float a[8], b[8];
-    T* o = static_cast<T*>(p.q_out) + (int64_t)tok * p.out_stride + g * 8;
+    T* o = static_cast<T*>(p.q_out) + (int64_t)tok * p.out_stride + (warp * HD + g * 8);
+    int head = warp;
     for (; head < p.n_q_heads; head += step) {
         ra.floats(a);
         rb.floats(b);
-        load(q + ((int64_t)(head + step) << p.head_shift), there && head + step < p.n_q_heads);
+        q += step * HD;
+        if (there && head + step < p.n_q_heads) {
+            load_now(ra, q);
+            load_now(rb, q + far);
+        }
         if (turned) turns.rotate(a, b);
         if (there) {
-            T* to = o + ((int64_t)head << p.head_shift);
-            store8(to, a);
-            store8(to + far, b);
+            store8(o, a);
+            store8(o + far, b);
         }
+        o += step * HD;
     }
     // keys, then values: the next warps in turn, as the queries' heads may not have come out even
-    int first = warp - p.n_q_heads % step;
-    if (first < 0) first += step;
-    const uint64_t row0 = there ? paged_row((uint32_t)slot, 0, p.n_kv_heads, p.page_shift) : 0;
-    for (int kv = first; kv < 2 * p.n_kv_heads; kv += step) {
-        const int z = kv >= p.n_kv_heads;
-        head = kv - z * p.n_kv_heads;
-        const T* x = z ? static_cast<const T*>(p.v) + (int64_t)tok * p.v_stride : static_cast<const T*>(p.k) + (int64_t)tok * p.k_stride;
-        load(x + ((int64_t)head << p.head_shift) + g * 8, there);
+    for (head -= p.n_q_heads; head >= step; head -= step) {
+    }
+    const uint32_t row0 = there ? paged_row((uint32_t)slot, 0, p.n_kv_heads, p.page_shift) : 0;
+    const T* k = static_cast<const T*>(p.k) + (int64_t)tok * p.k_stride + g * 8;
+    const T* v = static_cast<const T*>(p.v) + (int64_t)tok * p.v_stride + (g * 8 - p.n_kv_heads * HD);
+    for (; head < 2 * p.n_kv_heads; head += step) {
+        const bool value = head >= p.n_kv_heads;
+        if (there) {
+            const T* x = (value ? v : k) + head * HD;
+            load_now(ra, x);
+            load_now(rb, x + far);
+        }
         ra.floats(a);
         rb.floats(b);
-        if (turned && !z) turns.rotate(a, b);
+        if (turned && !value) turns.rotate(a, b);
         uint16_t sa, sb;  // every lane takes part in the shuffles
         const uint2 ca = q8_0_block8(a, &sa), cb = q8_0_block8(b, &sb);
         if (there) {
-            const uint64_t r = row0 + ((uint32_t)head << p.page_shift);
-            int8_t* codes = p.codes[z] + (r << p.head_shift) + g * 8;
+            const uint64_t row = row0 + ((uint32_t)(head - (value ? p.n_kv_heads : 0)) << p.page_shift);
+            int8_t* codes = p.codes[value] + (row * HD + g * 8);
             *reinterpret_cast<uint2*>(codes) = ca;
             *reinterpret_cast<uint2*>(codes + far) = cb;
             if ((j & 3) == 0) {
-                uint16_t* scales = p.scales[z] + (r << (p.head_shift - 5)) + (g >> 2);
+                uint16_t* scales = p.scales[value] + (row * (HD / kQBlock) + (g >> 2));
                 scales[0] = sa;
                 scales[far >> 5] = sb;
             }
@@ -205,17 +210,21 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 3 : 4) paged_ro
     }
 }
 
-template <typename T>
+template <typename T, int HD>
 int launch_rope(const RopeParams& p, bool pairs, cudaStream_t s) {
-    const int tokens = 32 >> (p.head_shift - 4);
-    const unsigned gx = (unsigned)(((int64_t)p.n_tok + tokens - 1) / tokens);
+    constexpr int kTokens = 32 / (HD / 16);
+    const unsigned gx = (unsigned)(((int64_t)p.n_tok + kTokens - 1) / kTokens);
     // few tokens: their heads over more blocks, a head a warp at last
     unsigned gy = 1;
     const unsigned most = (unsigned)(p.n_q_heads + 2 * p.n_kv_heads + kRopeWarps - 1) / kRopeWarps;
-    while (gy < most && gx * gy < kFullBlocks) ++gy;
+    while (gy < most && gy < 65535u && (uint64_t)gx * gy < kFullBlocks) ++gy;
     const dim3 grid(gx, gy);
-    if (pairs) return launch_dependent(paged_rope_kernel<T, true>, grid, kRopeThreads, 0, s, p);
-    return launch_dependent(paged_rope_kernel<T, false>, grid, kRopeThreads, 0, s, p);
+    if (pairs) return launch_dependent(paged_rope_kernel<T, HD, true>, grid, kRopeThreads, 0, s, p);
+    return launch_dependent(paged_rope_kernel<T, HD, false>, grid, kRopeThreads, 0, s, p);
+}
+template <typename T>
+int launch_rope(const RopeParams& p, int head_dim, bool pairs, cudaStream_t s) {
+    return head_dim == 128 ? launch_rope<T, 128>(p, pairs, s) : launch_rope<T, 256>(p, pairs, s);
 }
 
 }  // namespace
@@ -252,10 +261,9 @@ extern "C" int kvq8_paged_append_rope(const void* q, const void* k, const void* 
     RopeParams p = {q, k, v, q_out, q_stride, k_stride, v_stride, out_stride, positions, turns, axis_of, slots,
                     {const_cast<int8_t*>(kv->k_codes), const_cast<int8_t*>(kv->v_codes)},
                     {const_cast<uint16_t*>(kv->k_scales), const_cast<uint16_t*>(kv->v_scales)},
-                    (int64_t)kv->n_pages * kv->page_size, n_tok, n_q_heads, kv->n_kv_heads, log2_of(kv->head_dim),
-                    log2_of(kv->page_size), rot_dim, n_axes};
+                    (int64_t)kv->n_pages * kv->page_size, n_tok, n_q_heads, kv->n_kv_heads, log2_of(kv->page_size), rot_dim, n_axes};
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == KVQ8_F32) return launch_rope<float>(p, pairs != 0, s);
-    if (dtype == KVQ8_F16) return launch_rope<__half>(p, pairs != 0, s);
-    return launch_rope<__nv_bfloat16>(p, pairs != 0, s);
+    if (dtype == KVQ8_F32) return launch_rope<float>(p, kv->head_dim, pairs != 0, s);
+    if (dtype == KVQ8_F16) return launch_rope<__half>(p, kv->head_dim, pairs != 0, s);
+    return launch_rope<__nv_bfloat16>(p, kv->head_dim, pairs != 0, s);
 }

@@ -92,11 +92,6 @@ struct F2 {
     }
     __device__ __forceinline__ void get(float& x, float& y) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
 };
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     F2 r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
@@ -131,16 +126,16 @@ __device__ __forceinline__ uint2 q8_0_block8(const float (&x)[8], uint16_t* scal
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
     if (d == 0.0f) r = 0.0f;
-    const F2 rr = F2::of(r, r), magic = F2::of(kMagic, kMagic), back = F2::of(-kMagic, -kMagic), minus = F2::of(-1.0f, -1.0f);
+    const F2 rr = F2::of(r, r), magic = F2::of(kMagic, kMagic), minus = F2::of(-1.0f, -1.0f);
     float far[4];
     uint32_t c[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const F2 v = F2::of(x[2 * e], x[2 * e + 1]);
         const F2 t = fma2(v, rr, magic);
-        // x r - n, through -n = n * -1 (exact)
+        // x r - n, through -n = M - t (exact)
         float o0, o1, t0, t1;
-        fma2(v, rr, mul2(add2(t, back), minus)).get(o0, o1);
+        fma2(v, rr, fma2(t, minus, magic)).get(o0, o1);
         t.get(t0, t1);
         far[e] = max_nan(o0, o1);
         c[2 * e] = __float_as_uint(t0), c[2 * e + 1] = __float_as_uint(t1);
