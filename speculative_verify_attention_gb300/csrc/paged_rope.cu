@@ -16,8 +16,11 @@ namespace kvq8 {
 namespace {
 
 constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32;
+template <typename T>
+constexpr int kRopeDepth = sizeof(T) == 4 ? 3 : 4;   // heads of a thread in flight
+template <typename T>
+constexpr int kRopeBlocks = sizeof(T) == 4 ? 2 : 3;  // of an SM
 constexpr int kMaxAxes = 4;
-constexpr unsigned kFullBlocks = 152 * 4;
 
 struct RopeParams {
     const void* q;
@@ -49,17 +52,18 @@ __device__ __forceinline__ float2 cos_sin(uint64_t phase) {
     return make_float2(c, s);
 }
 
-__device__ __forceinline__ void store8(float* dst, const float (&v)[8]) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+// Eight values, four at `dst` and four `apart` behind them.
+__device__ __forceinline__ void store8(float* dst, int apart, const float (&v)[8]) {
+    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(dst + apart) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void store8(__half* dst, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__half* dst, int, const float (&v)[8]) {
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[k] = h2_as_u32(__floats2half2_rn(v[2 * k], v[2 * k + 1]));
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, int, const float (&v)[8]) {
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -69,24 +73,24 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) 
     *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Eight values, not by the read-only path: queries may be rotated in place.
 template <typename T>
-__device__ __forceinline__ void load_now(Eight<T>& x, const T* from) {
-    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]) : "l"(from));
-}
-__device__ __forceinline__ void load_now(Eight<float>& x, const float* from) {
-    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.v[0]), "=f"(x.v[1]), "=f"(x.v[2]), "=f"(x.v[3]) : "l"(from));
-    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.v[4]), "=f"(x.v[5]), "=f"(x.v[6]), "=f"(x.v[7]) : "l"(from + 4));
+__device__ __forceinline__ void from_shared(Eight<T>& x, const uint4* at) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+        const uint4 r = at[i * kRopeThreads];
+        reinterpret_cast<uint32_t*>(&x)[4 * i] = r.x, reinterpret_cast<uint32_t*>(&x)[4 * i + 1] = r.y;
+        reinterpret_cast<uint32_t*>(&x)[4 * i + 2] = r.z, reinterpret_cast<uint32_t*>(&x)[4 * i + 3] = r.w;
+    }
 }
 
 // The cosines and sines of a thread's eight pairs.  Halves turn two pairs an instruction: (c, c'), (s, s') and (-s, -s').
 template <bool PAIRS>
 struct Turns {
     F2 c[4], s[4], minus[4];
-    __device__ __forceinline__ void load(const float2* t, int g, int) {
+    __device__ __forceinline__ void load(const float2* t, int at0, int at1, int) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4*>(t + g * 8 + 2 * i);
+            const float4 x = *reinterpret_cast<const float4*>(t + (i < 2 ? at0 : at1) + 2 * (i & 1));
             c[i] = F2::of(x.x, x.z);
             s[i] = F2::of(x.y, x.w);
             minus[i] = F2::of(-x.y, -x.w);
@@ -105,10 +109,10 @@ struct Turns {
 template <>
 struct Turns<true> {
     float2 t[8];
-    __device__ __forceinline__ void load(const float2* from, int g, int h) {
+    __device__ __forceinline__ void load(const float2* from, int at0, int at1, int far) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 x = *reinterpret_cast<const float4*>(from + (i < 2 ? g * 4 + 2 * i : h * 4 + 2 * i - 4));
+            const float4 x = *reinterpret_cast<const float4*>(from + ((i & 1 ? at1 : at0) + (i < 2 ? 0 : far)) / 2);
             t[2 * i] = make_float2(x.x, x.y), t[2 * i + 1] = make_float2(x.z, x.w);
         }
     }
@@ -124,103 +128,137 @@ struct Turns<true> {
     }
 };
 
-// Block (two or four tokens, a share of the heads): the lanes of a warp are the items of its tokens' rows, its heads every eighth of the
-// block's, queries, then keys, then values.  The groups g and h of item j: in the rotated part of a row its first and second half,
-// then the same of the part behind it; both parts are multiples of 64, so four neighbouring lanes have a 32-value block in each.
+// Block (every gridDim.x-th group of two or four tokens, a share of the heads): the lanes of a warp are the items of its tokens' rows, its
+// heads every eighth of the block's, queries, then keys, then values.  An item is eight values and the eight that lie `far` behind
+// them: in the rotated part of a row the same places of its two halves, then of the two halves of the part behind it; both parts are
+// multiples of 64, so four neighbouring lanes have a 32-value block in each.  A lane's eight of a block are consecutive (16 bytes); of
+// fp32 they are its fourth of the block's first half and of the second, as four lanes' pieces have to fill whole 32-byte sectors.
 template <typename T, int HD, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 4 ? 3 : 4) paged_rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kItems = HD / 16, kTokens = 32 / kItems;
-    __shared__ __align__(16) float2 s_turns[kTokens * HD / 2];  // [tokens][rot / 2]
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) paged_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int kItems = HD / 16, kTokens = 32 / kItems, kPieces = (int)sizeof(T) / 2, kDepth = kRopeDepth<T>;  // 16-byte pieces of eight values
+    extern __shared__ __align__(16) uint4 s_ring[];               // [kDepth][2 kPieces][threads]
+    __shared__ __align__(16) float2 s_turns[2][kTokens * HD / 2];  // [tokens][rot / 2], of this group and the next
     const int tid = threadIdx.x, lane = tid & 31, j = lane % kItems, mine = lane / kItems;
+    const int rot_items = p.rot / 16, half = p.rot / 2, stride = (int)gridDim.x * kTokens;
+    constexpr bool kWide = sizeof(T) == 4;
+    constexpr int kApart = kWide ? 16 : 4;  // between a lane's first four values and its next
+    const int g = j < rot_items ? j : rot_items + j, far = j < rot_items ? half : (HD - p.rot) / 2;
+    const int at = kWide ? (g >> 2) * 32 + (g & 3) * 4 : g * 8;
+    const bool turned = j < rot_items;
+    // this warp's heads: of the queries, then of the keys, then of the values
+    const int step = kRopeWarps * (int)gridDim.y, warp = (int)blockIdx.y * kRopeWarps + (tid >> 5);
+    const int all = p.n_q_heads + 2 * p.n_kv_heads, v_first = p.n_q_heads + p.n_kv_heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tok0 = (int)blockIdx.x * kTokens, tok = tok0 + mine;
-    const int64_t slot = tok < p.n_tok ? __ldg(p.slots + tok) : -1;
-    const bool there = slot >= 0 && slot < p.n_slots;
-    const int rot_items = p.rot / 16, half = p.rot / 2;
-    const int g = j < rot_items ? j : rot_items + j, far = j < rot_items ? half : (HD - p.rot) / 2;
-    const bool turned = j < rot_items;
-    const int step = kRopeWarps * (int)gridDim.y, warp = (int)blockIdx.y * kRopeWarps + (tid >> 5);
-    Eight<T> ra, rb;  // lanes without a token compute with zeros, and store nothing
-    ra.clear();
-    rb.clear();
-    const T* q = static_cast<const T*>(p.q) + (int64_t)tok * p.q_stride + (warp * HD + g * 8);
-    if (there && warp < p.n_q_heads) {
-        load_now(ra, q);
-        load_now(rb, q + far);
-    }
-    {  // as many threads a token as a row has pairs at most
-        const int t = tid / (HD / 2), pair = tid % (HD / 2);
-        if (pair < half && tok0 + t < p.n_tok) {
-            const int axis = p.axis_of ? __ldg(p.axis_of + pair) : 0;
-            const int64_t pos = axis >= 0 && axis < p.n_axes ? __ldg(p.positions + (int64_t)axis * p.n_tok + tok0 + t) : 0;
-            s_turns[t * half + pair] = cos_sin((uint64_t)pos * __ldg(p.turns + pair));
-        }
-    }
-    __syncthreads();
-    Turns<PAIRS> turns;
-    if (turned) turns.load(s_turns + mine * half, g, g + far / 8);
-    float a[8], b[8];
-    T* o = static_cast<T*>(p.q_out) + (int64_t)tok * p.out_stride + (warp * HD + g * 8);
-    int head = warp;
-    for (; head < p.n_q_heads; head += step) {
-        ra.floats(a);
-        rb.floats(b);
-        q += step * HD;
-        if (there && head + step < p.n_q_heads) {
-            load_now(ra, q);
-            load_now(rb, q + far);
-        }
-        if (turned) turns.rotate(a, b);
-        if (there) {
-            store8(o, a);
-            store8(o + far, b);
-        }
-        o += step * HD;
-    }
-    // keys, then values: the next warps in turn, as the queries' heads may not have come out even
-    for (head -= p.n_q_heads; head >= step; head -= step) {
-    }
-    const uint32_t row0 = there ? paged_row((uint32_t)slot, 0, p.n_kv_heads, p.page_shift) : 0;
-    const T* k = static_cast<const T*>(p.k) + (int64_t)tok * p.k_stride + g * 8;
-    const T* v = static_cast<const T*>(p.v) + (int64_t)tok * p.v_stride + (g * 8 - p.n_kv_heads * HD);
-    for (; head < 2 * p.n_kv_heads; head += step) {
-        const bool value = head >= p.n_kv_heads;
-        if (there) {
-            const T* x = (value ? v : k) + head * HD;
-            load_now(ra, x);
-            load_now(rb, x + far);
-        }
-        ra.floats(a);
-        rb.floats(b);
-        if (turned && !value) turns.rotate(a, b);
-        uint16_t sa, sb;  // every lane takes part in the shuffles
-        const uint2 ca = q8_0_block8(a, &sa), cb = q8_0_block8(b, &sb);
-        if (there) {
-            const uint64_t row = row0 + ((uint32_t)(head - (value ? p.n_kv_heads : 0)) << p.page_shift);
-            int8_t* codes = p.codes[value] + (row * HD + g * 8);
-            *reinterpret_cast<uint2*>(codes) = ca;
-            *reinterpret_cast<uint2*>(codes + far) = cb;
-            if ((j & 3) == 0) {
-                uint16_t* scales = p.scales[value] + (row * (HD / kQBlock) + (g >> 2));
-                scales[0] = sa;
-                scales[far >> 5] = sb;
+    const uint32_t ring = smem_u32(s_ring + tid);
+    int ahead_tok = (int)blockIdx.x * kTokens + mine, ahead = warp, ahead_place = 0;
+    auto fetch = [&] {
+        if (ahead_tok < p.n_tok && ahead < all) {
+            const T* x = ahead < p.n_q_heads ? static_cast<const T*>(p.q) + (int64_t)ahead_tok * p.q_stride + ahead * HD
+                         : ahead < v_first   ? static_cast<const T*>(p.k) + (int64_t)ahead_tok * p.k_stride + (ahead - p.n_q_heads) * HD
+                                             : static_cast<const T*>(p.v) + (int64_t)ahead_tok * p.v_stride + (ahead - v_first) * HD;
+            x += at;
+            const uint32_t to = ring + ahead_place * (2 * kPieces * kRopeThreads * 16);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                cp_async_16(to + i * (kRopeThreads * 16), x + i * kApart, 16);
+                cp_async_16(to + (kPieces + i) * (kRopeThreads * 16), x + far + i * kApart, 16);
             }
         }
+        cp_async_commit();
+        ahead += step;
+        if (ahead >= all) ahead = warp, ahead_tok += stride;
+        ahead_place = ahead_place + 1 == kDepth ? 0 : ahead_place + 1;
+    };
+    for (int i = 0; i < kDepth; ++i) fetch();
+    // as many threads a token as a row has pairs at most; what a group needs of indexes is loaded a group ahead
+    const int pair = tid % (HD / 2), pair_tok = tid / (HD / 2);
+    uint64_t frequency = 0;
+    const int32_t* positions = nullptr;
+    if (pair < half) {
+        const int axis = p.axis_of ? __ldg(p.axis_of + pair) : 0;
+        frequency = __ldg(p.turns + pair);
+        if (axis >= 0 && axis < p.n_axes) positions = p.positions + (int64_t)axis * p.n_tok;
     }
+    int32_t next_pos = 0;
+    int64_t next_slot = -1;
+    auto indexes = [&](int tok0) {
+        next_pos = positions && tok0 + pair_tok < p.n_tok ? __ldg(positions + tok0 + pair_tok) : 0;
+        next_slot = tok0 + mine < p.n_tok ? __ldg(p.slots + tok0 + mine) : -1;
+    };
+    indexes((int)blockIdx.x * kTokens);
+    int buffer = 0, place = 0;
+    for (int tok0 = (int)blockIdx.x * kTokens; tok0 < p.n_tok; tok0 += stride, buffer ^= 1) {
+        const int64_t slot = next_slot;
+        const bool there = slot >= 0 && slot < p.n_slots;
+        if (pair < half) s_turns[buffer][pair_tok * half + pair] = cos_sin((uint64_t)(int64_t)next_pos * frequency);
+        if (tok0 + stride < p.n_tok) indexes(tok0 + stride);
+        __syncthreads();  // (the other buffer's readers have passed the barrier before)
+        Turns<PAIRS> turns;
+        if (turned) turns.load(s_turns[buffer] + mine * half, at, at + kApart, far);
+        T* o = static_cast<T*>(p.q_out) + (int64_t)(tok0 + mine) * p.out_stride + (warp * HD + at);
+        const uint32_t row0 = there ? paged_row((uint32_t)slot, 0, p.n_kv_heads, p.page_shift) : 0;
+        for (int head = warp; head < all; head += step) {
+            cp_async_wait<kDepth - 1>();
+            const uint4* from = s_ring + place * (2 * kPieces * kRopeThreads) + tid;
+            place = place + 1 == kDepth ? 0 : place + 1;
+            Eight<T> ra, rb;
+            from_shared(ra, from);
+            from_shared(rb, from + kPieces * kRopeThreads);
+            float a[8], b[8];
+            ra.floats(a);
+            rb.floats(b);
+            if (turned && head < v_first) turns.rotate(a, b);
+            if (head < p.n_q_heads) {
+                if (there) {
+                    store8(o, kApart, a);
+                    store8(o + far, kApart, b);
+                }
+                o += step * HD;
+            } else {
+                uint16_t sa, sb;  // every lane takes part in the shuffles
+                const uint2 ca = q8_0_block8(a, &sa), cb = q8_0_block8(b, &sb);
+                if (there) {
+                    const bool value = head >= v_first;
+                    const uint64_t row = row0 + ((uint32_t)(head - (value ? v_first : p.n_q_heads)) << p.page_shift);
+                    int8_t* codes = p.codes[value] + (row * HD + at);
+                    if (kWide) {
+                        *reinterpret_cast<uint32_t*>(codes) = ca.x;
+                        *reinterpret_cast<uint32_t*>(codes + kApart) = ca.y;
+                        *reinterpret_cast<uint32_t*>(codes + far) = cb.x;
+                        *reinterpret_cast<uint32_t*>(codes + far + kApart) = cb.y;
+                    } else {
+                        *reinterpret_cast<uint2*>(codes) = ca;
+                        *reinterpret_cast<uint2*>(codes + far) = cb;
+                    }
+                    if ((j & 3) == 0) {
+                        uint16_t* scales = p.scales[value] + (row * (HD / kQBlock) + (g >> 2));
+                        scales[0] = sa;
+                        scales[far >> 5] = sb;
+                    }
+                }
+            }
+            fetch();  // into the place just read
+        }
+    }
+    cp_async_wait<0>();
 }
 
 template <typename T, int HD>
 int launch_rope(const RopeParams& p, bool pairs, cudaStream_t s) {
     constexpr int kTokens = 32 / (HD / 16);
-    const unsigned gx = (unsigned)(((int64_t)p.n_tok + kTokens - 1) / kTokens);
-    // few tokens: their heads over more blocks, a head a warp at last
-    unsigned gy = 1;
-    const unsigned most = (unsigned)(p.n_q_heads + 2 * p.n_kv_heads + kRopeWarps - 1) / kRopeWarps;
-    while (gy < most && gy < 65535u && (uint64_t)gx * gy < kFullBlocks) ++gy;
+    const int64_t groups = ((int64_t)p.n_tok + kTokens - 1) / kTokens, full = 152 * kRopeBlocks<T>;
+    // as many blocks as the GPU holds; few tokens: their heads over more blocks, a head a warp at last
+    const int64_t most = (p.n_q_heads + 2 * p.n_kv_heads + kRopeWarps - 1) / kRopeWarps, share = full / groups;
+    const unsigned gy = (unsigned)(share < 1 ? 1 : share < most ? share : most);
+    const unsigned gx = (unsigned)(groups < full ? groups : full);
+    constexpr int smem = kRopeDepth<T> * (int)sizeof(T) * kRopeThreads * 16;
+    static SmemOptIn opt[2];
+    const int rc = pairs ? opt[1].ensure(paged_rope_kernel<T, HD, true>, smem) : opt[0].ensure(paged_rope_kernel<T, HD, false>, smem);
+    if (rc != KVQ8_OK) return rc;
     const dim3 grid(gx, gy);
-    if (pairs) return launch_dependent(paged_rope_kernel<T, HD, true>, grid, kRopeThreads, 0, s, p);
-    return launch_dependent(paged_rope_kernel<T, HD, false>, grid, kRopeThreads, 0, s, p);
+    if (pairs) return launch_dependent(paged_rope_kernel<T, HD, true>, grid, kRopeThreads, smem, s, p);
+    return launch_dependent(paged_rope_kernel<T, HD, false>, grid, kRopeThreads, smem, s, p);
 }
 template <typename T>
 int launch_rope(const RopeParams& p, int head_dim, bool pairs, cudaStream_t s) {
