@@ -39,13 +39,27 @@ __device__ __forceinline__ int block_sums(int v, int* s_warp, int& total) {
     return inc - v + (warp ? s_warp[warp - 1] : 0);
 }
 
+// The parents of a planning thread's children, -1: none.  They are asked for first of all.
+constexpr int kPlanPer = kMaxSeqs / kPlanThreads;
+struct Children {
+    int of[kPlanPer];
+    __device__ __forceinline__ Children(const int32_t* parents, int n_children) {
+#pragma unroll
+        for (int u = 0; u < kPlanPer; ++u) {
+            const int i = threadIdx.x + u * kPlanThreads;
+            of[u] = i < n_children ? parents[i] : -1;
+        }
+    }
+};
+
 // s_first[q]: q's first child (n_children where it has none), s_kids[q]: how many.  True if a parent is out of range.
-__device__ __forceinline__ bool families(const int32_t* parents, int n_children, int n_seqs, int* s_first, int* s_kids) {
+__device__ __forceinline__ bool families(const Children& c, int n_children, int n_seqs, int* s_first, int* s_kids) {
     for (int q = threadIdx.x; q < n_seqs; q += kPlanThreads) s_first[q] = n_children, s_kids[q] = 0;
     __syncthreads();
     bool bad = false;
-    for (int i = threadIdx.x; i < n_children; i += kPlanThreads) {
-        const int q = parents[i];
+#pragma unroll
+    for (int u = 0; u < kPlanPer; ++u) {
+        const int i = threadIdx.x + u * kPlanThreads, q = c.of[u];
         if (q >= n_seqs) bad = true;
         if (q < 0 || q >= n_seqs) continue;
         atomicMin(s_first + q, i);
@@ -78,11 +92,20 @@ __global__ void __launch_bounds__(kPlanThreads) counts_fork_plan_kernel(const __
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Children children(p.parents, p.n_children);
+    int states[kPlanPer];
+#pragma unroll
+    for (int u = 0; u < kPlanPer; ++u) {
+        const int q = tid + u * kPlanThreads;
+        states[u] = q >= p.n_seqs ? -1 : p.state_of ? p.state_of[q] : q;
+    }
     for (int w = tid; w < n_words; w += kPlanThreads) s_kept[w] = 0u;
-    bool bad = families(p.parents, p.n_children, p.n_seqs, s_first, s_kids);
-    for (int q = tid; q < p.n_seqs; q += kPlanThreads) {
-        int st = p.state_of ? p.state_of[q] : q;
-        if (st < 0 || st >= p.n_states) st = -1;
+    bool bad = families(children, p.n_children, p.n_seqs, s_first, s_kids);
+#pragma unroll
+    for (int u = 0; u < kPlanPer; ++u) {
+        const int q = tid + u * kPlanThreads;
+        if (q >= p.n_seqs) continue;
+        const int st = states[u] < 0 || states[u] >= p.n_states ? -1 : states[u];
         s_state[q] = st;
         // two sequences that are both gone on from cannot have the same row
         if (st >= 0 && s_kids[q]) bad |= (atomicOr(s_kept + (st >> 5), 1u << (st & 31)) >> (st & 31)) & 1u;
@@ -100,16 +123,15 @@ __global__ void __launch_bounds__(kPlanThreads) counts_fork_plan_kernel(const __
     }
     __syncthreads();
     int copies = 0;
-    for (int i0 = 0; i0 < p.n_children; i0 += kPlanThreads) {
-        const int i = i0 + tid;
+#pragma unroll
+    for (int u = 0; u < kPlanPer; ++u) {
+        if (u * kPlanThreads >= p.n_children) break;
+        const int i = tid + u * kPlanThreads, q = children.of[u];
         int from = -1, state = -1;
         bool copy = false;
-        if (i < p.n_children) {
-            const int q = p.parents[i];
-            if (q >= 0 && q < p.n_seqs) {
-                state = from = s_state[q];
-                copy = from >= 0 && s_first[q] != i;
-            }
+        if (q >= 0 && q < p.n_seqs) {
+            state = from = s_state[q];
+            copy = from >= 0 && s_first[q] != i;
         }
         int total;
         const int k = copies + block_sums(copy, s_warp, total);
@@ -218,10 +240,10 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
     const int page = 1 << p.page_shift;
     const int head = p.ring_state[0], count = p.ring_state[1];
     // what the sequences alone say, asked for before the children are counted
-    constexpr int kPer = kMaxSeqs / kPlanThreads;
-    int holds[kPer];  // 0, or kGoesOn; -1: held is wrong, -2: its children's length is
+    const Children children(p.parents, p.n_children);
+    int holds[kPlanPer];  // 0, or kGoesOn; -1: held is wrong, -2: its children's length is
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
+    for (int u = 0; u < kPlanPer; ++u) {
         const int q = tid + u * kPlanThreads;
         holds[u] = 0;
         if (q >= p.n_seqs) continue;
@@ -238,10 +260,10 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
             s_tail[q] = tail;
         }
     }
-    bool bad = families(p.parents, p.n_children, p.n_seqs, s_first, s_kids);
+    bool bad = families(children, p.n_children, p.n_seqs, s_first, s_kids);
     bad |= head < 0 || head >= p.n_pages || count < 0 || count > p.n_pages;
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
+    for (int u = 0; u < kPlanPer; ++u) {
         const int q = tid + u * kPlanThreads;
         if (q >= p.n_seqs) continue;
         const int kids = s_kids[q];
@@ -250,8 +272,10 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
     }
     bad = __syncthreads_or(bad);
     int takes = 0;
-    for (int i0 = 0; i0 < p.n_children; i0 += kPlanThreads) {
-        const int i = i0 + tid, q = i < p.n_children ? p.parents[i] : -1;
+#pragma unroll
+    for (int u = 0; u < kPlanPer; ++u) {
+        if (u * kPlanThreads >= p.n_children) break;
+        const int i = tid + u * kPlanThreads, q = children.of[u];
         const bool live = !bad && q >= 0;
         int len = 0;
         bool take = false;

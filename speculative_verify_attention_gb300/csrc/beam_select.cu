@@ -366,10 +366,20 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     cluster_arrive();  // (a block's shared memory is written by others once it has started)
     const Lists lists(s_lists, (kMaxWindowRows + size - 1) / size, n_out);
     const int64_t to = (int64_t)b * n_out;
+    // (the scan lets this kernel start when it has waited for what came before it, so the call's own inputs may be read already)
+    int first, rows;
+    const bool any = rows_of(p, b, first, rows);
+    float score = 0.0f, weight = 1.0f;
+    int ended = -1;
+    auto about = [&](int row) {
+        if (p.scores) score = __ldg(p.scores + row);
+        if (p.weights) weight = __ldg(p.weights + row);
+        if (p.ended) ended = __ldg(p.ended + row);
+    };
+    if (any && me < rows) about(first + me);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int first, rows;
-    if (!rows_of(p, b, first, rows)) {
+    if (!any) {
         for (int k = tid; k < n_out && me == 0; k += kPickThreads) {
             p.parents[to + k] = p.tokens[to + k] = -1;
             p.totals[to + k] = -INFINITY;
@@ -381,8 +391,7 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     for (int mine = me; mine < rows; mine += size) {
         const int row = first + mine;
         const float* gm = p.group_max + (int64_t)row * p.n_groups;
-        const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
-        const int ended = p.ended ? __ldg(p.ended + row) : -1;
+        if (mine != me) about(row);
         int32_t k[kKeep];
         if (!sums) {
 #pragma unroll
