@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kPlanThreads) counts_fork_plan_kernel(const __
 constexpr int kRowThreads = 256;
 constexpr int kRowPer = 4;  // accesses of a thread in flight
 
-// Block (16 KB of a row, child), four 16-byte accesses a thread in flight; siblings read a row from L2.  A row that is copied from is kept by its first child, and one copied to is kept by nobody, so
-// no block reads what another writes.
+// Block (16 KB of a row, child), four 16-byte accesses a thread in flight; siblings read a row from L2.  A row that is copied from is
+// kept by its first child, and one copied to is kept by nobody, so no block reads what another writes.
 template <typename V>
 __global__ void __launch_bounds__(kRowThreads) counts_copy_kernel(const __grid_constant__ CountsFork p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -3,11 +3,11 @@
 // Row r (a beam) with score c continues with value v at  total = c + x[v] - log sum_v exp x[v],  ordered by weight * total.
 // The n_out best of a request lie among the n_out best of each of its rows, which are the n_out best logits x.
 //
-// One pass over the logits.  A warp holds a kilobyte's groups of consecutive values in registers and leaves behind each group's
-// maximum, and one partial sum of exponentials of all that it has held: 1/200 of what it read.  Ordered by (maximum descending, place ascending), the
-// n_out best groups hold the row's n_out best values: a value outside them has n_out values before it, one in each.  So the
-// second kernel, a block per row, picks those groups, reads them again and picks the values; a request's blocks form a cluster,
-// which joins their lists through shared memory.
+// One pass over the logits.  A warp holds groups of a kilobyte of consecutive values in registers and leaves behind each group's
+// maximum, and one partial sum of exponentials of all that it has held: 1/200 of what it read.  Ordered by (maximum descending, place
+// ascending), the n_out best groups hold the row's n_out best values: a value outside them has n_out values before it, one in each.
+// So the second kernel, a block per row, picks those groups, reads them again and picks the values; a request's blocks form a
+// cluster, which joins their lists through shared memory.
 // Bound: the logits' bytes in the first kernel, latency in the second.  48 requests of 8 beams over 248320 bf16 logits (159 MB), 16 of
 // each: 34.5 us, of which the scan 27.5 (5.8 TB/s, 85 % of a copy's rate; issue slots 69 % busy) and the second kernel 7; one request of
 // 4 fp32 beams 6.9 us; 21 of up to 5 over 106299 fp16 logits (21 MB) 11.7 us.  As first built, with groups picked by rounds of five
@@ -31,7 +31,7 @@ constexpr int kPickThreads = kSearchThreads + 32;
 constexpr int kMaxOut = 64;
 constexpr int kKeep = 4;           // groups of a row that a searching thread keeps: all of 262144 fp32 values
 constexpr int kPartKeep = 8;       // parts of a row that a lane of the summing warp keeps
-constexpr int kFetch = 3;          // loads of a lane at once: the groups of 16 continuations in one round
+constexpr int kFetch = 3;          // loads of a lane at once (five spill, and are no faster)
 constexpr int kGroupCap = 256;     // groups, and values, that the second kernel keeps of a row
 constexpr int kListCap = 512;
 
@@ -171,7 +171,7 @@ struct Fetch {
     }
 };
 
-// Every other value's larger neighbour, the larger of both at last; NaN loses.
+// The largest of eight values; NaN loses.
 __device__ __forceinline__ float largest(const Eight<float>& x) {
     float m = fmaxf(x.v[0], x.v[1]);
 #pragma unroll
@@ -230,7 +230,11 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
         m = fmaxf(m, sum.m);
         if (fabsf(m) < kLarge) {
             const float e = rintf(m * kLog2e);
-            float s = fabsf(sum.m) < kLarge ? sum.s * ex2_approx(sum.e - e) : sum.m > -INFINITY ? sum.s * exp2f((float)(scale_of_part(sum.m, sum.e) - (double)e)) : sum.s;
+            float s = sum.s;
+            if (fabsf(sum.m) < kLarge)
+                s *= ex2_approx(sum.e - e);
+            else if (sum.m > -INFINITY)
+                s *= exp2f((float)(scale_of_part(sum.m, sum.e) - (double)e));
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 float v[8];

@@ -7,8 +7,10 @@
 // left, within an eighth of a turn of zero, goes through sincospif.
 //
 // A block works out the sines and cosines of its tokens, two or four, once for all of its heads.  A thread has sixteen values of a
-// row, eight and their partners eight, the same ones of several heads: its eight sines and cosines stay in its registers.  Keys are quantised as they come out of the rotation in fp32 (the block quantiser of
-// kvq8_paged_append), without a rounding in between.
+// row, eight and their partners eight, the same ones of several heads: its eight sines and cosines stay in its registers.  What it
+// will work on next is fetched by asynchronous copies into its own places in shared memory, some heads ahead and on into its next
+// tokens, so that neither the sines nor a barrier holds the loads up.  Keys are quantised as they come out of the rotation in fp32
+// (the block quantiser of kvq8_paged_append), without a rounding in between.
 // Bound: bytes and issue slots together.  16401 tokens of 32q/8kv/hd128 bf16 (372 MB) 65 us, 5.7 TB/s, 84 % of a copy's rate, 63 % of
 // the issue slots; 2051 of 24q/4kv/hd256 fp32 (122 MB) 22 us; 32 tokens 3.6 us.  With the next head alone ahead, in registers, 76 and
 // 26.5 us; with more blocks an SM (and spills) 74; two or six heads ahead instead of four 66.

@@ -124,6 +124,16 @@ def test_pages_follow(lib, n, m, width, in_place):
         assert _pages(parents, s, in_place)[-1] == 0
 
 
+@pytest.mark.parametrize("n,width,spare", [(64, 600, 100), (40, 12, 200000), (9, 5, 20000), (700, 40, 800)])
+def test_long_tables_and_large_pools(lib, n, width, spare):
+    rng = np.random.default_rng(spare)
+    s = _state(spare, n, 16, width, share=0.8, spare=spare)
+    for k in range(2):
+        parents = rng.integers(0, n, n)
+        parents[rng.random(n) < 0.5 * k] = -1
+        assert _pages(parents, s, bool(k))[-1] == 0
+
+
 def test_full_pages_and_lengths_of_nothing(lib):
     s = list(_state(3, 12, 16, 6, spare=30))
     s[0] = s[1] * 16                                        # every last page is full: nothing is copied

@@ -51,6 +51,18 @@ def test_many_rows_of_one_large_vocabulary(lib):
     _run(x.bfloat16(), list(range(0, 41, 8)), 16, scores=-20 - np.random.default_rng(1).random(40))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [300001, 2000008])
+def test_vocabularies_of_more_groups_than_a_block_keeps(lib, dtype, vocab):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(vocab)
+    x = torch.randn((5, vocab), generator=gen, device="cuda").mul_(3.0).to(dtype)
+    x[3] = x[3].round()            # many equal values
+    x[4] = 1.0
+    _run(x, [0, 3, 5], 12, scores=[-1.0, -1.5, -0.5, -2.0, -2.0])
+    _run(x, [0, 5], 64)
+
+
 def test_equal_values_go_to_the_lowest_token_and_row(lib):
     """Rows of a few levels: most values tie.  Equal rows tie as wholes: the lower row first."""
     rng = np.random.default_rng(6)

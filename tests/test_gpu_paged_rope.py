@@ -85,7 +85,8 @@ def _case(seed, n, hq, hkv, hd, dtype, rot, pairs=False, axes=1, far=30000, page
     ok = ~left
     pg, o = slots[ok] // page, slots[ok] % page
     kc, ks = cache.k_codes.cpu().numpy()[pg, :, o], cache.k_scales.float().cpu().numpy()[pg, :, o]
-    _check_k(kc, ks, rotated(xk, ang, pairs)[ok], _bound(xk, pairs, half)[ok])
+    if ok.any():
+        _check_k(kc, ks, rotated(xk, ang, pairs)[ok], _bound(xk, pairs, half)[ok])
     vc, vs = cache.v_codes.cpu().numpy()[pg, :, o], cache.v_scales.cpu().numpy().view(np.uint16)[pg, :, o]
     if ok.any():
         ref = oracle.Cache(hkv, hd, int(ok.sum()))
