@@ -95,79 +95,81 @@ constexpr uint32_t kLowestWord<__half> = 0xfc00fc00u;
 template <>
 constexpr uint32_t kLowestWord<__nv_bfloat16> = 0xff80ff80u;
 
-// Eight consecutive values of a row as they are fetched, -inf outside the row.  VEC: the row starts on eight values' size and holds
-// whole groups of them.  Else the 16-byte pieces around them, and `shift` (of the row alone, as places are multiples of eight)
-// says where among those they start: a row of odd length costs a few selections instead of single loads.
+// How a warp reads 256 consecutive values of a row, eight a lane, -inf outside the row.
+//   VEC: eight consecutive ones a load; the row starts on their size and holds whole groups of them.
+//   Rows of odd length in 16 bits: the two 16-byte pieces around a lane's eight, and where among those they start (`shift`, of the row
+//     alone) comes to a funnel shift a word; 320 rows of 106299 bf16 values 24.9 us (by selections 26; 106304 values 20.7).
+//   Of fp32: a value a load, neighbours to neighbouring lanes (100 rows of 106299: 13.9 us; by three pieces and selections 17.6).
 template <typename T, bool VEC>
-struct Fetch {
-    static constexpr int kPiece = 16 / (int)sizeof(T), kPieces = VEC ? 8 / kPiece : 8 / kPiece + 1;
-    uint32_t w[4 * kPieces];
+struct Tile {
+    static constexpr bool kSpread = sizeof(T) == 4 && !VEC;
+    // the place of value e of a lane, in the 256 from `at` on
+    static __device__ __forceinline__ int place(int at, int lane, int e) { return kSpread ? at + e * 32 + lane : at + lane * 8 + e; }
 
-    static __device__ __forceinline__ int shift_of(const T* row) {
-        return VEC ? 0 : (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
-    }
-    __device__ __forceinline__ void load(const T* row, int at, int vocab, int shift) {
-        if constexpr (VEC) {
-            if (at < vocab) {
-                Eight<T> x;
-                x.load_whole(row + at);
+    // 16 bits, odd: pieces of eight values
+    static __device__ __forceinline__ void pieces(uint32_t (&w)[8], const T* row, int from, int vocab) {
 #pragma unroll
-                for (int i = 0; i < 4 * kPieces; ++i) w[i] = reinterpret_cast<const uint32_t*>(&x)[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4 * kPieces; ++i) w[i] = kLowestWord<T>;
-            }
-        } else {
-            load_pieces(row, at, vocab, shift);
-        }
-    }
-    __device__ __forceinline__ void load_pieces(const T* row, int at, int vocab, int shift) {
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int from = at - shift + k * kPiece;
-            if (from >= 0 && from + kPiece <= vocab) {
+        for (int k = 0; k < 2; ++k, from += 8) {
+            if (from >= 0 && from + 8 <= vocab) {
                 const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + from));
                 w[4 * k] = r.x, w[4 * k + 1] = r.y, w[4 * k + 2] = r.z, w[4 * k + 3] = r.w;
             } else {  // the row's first and last piece
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[4 * k + i] = kLowestWord<T>;
-                if (from > -kPiece && from < vocab) {
+                if (from > -8 && from < vocab) {
 #pragma unroll
-                    for (int i = 0; i < kPiece; ++i)
-                        if (from + i >= 0 && from + i < vocab) put(k * kPiece + i, row[from + i]);
+                    for (int i = 0; i < 8; ++i)
+                        if (from + i >= 0 && from + i < vocab) {
+                            const uint32_t bits = *reinterpret_cast<const uint16_t*>(row + from + i);
+                            uint32_t& to = w[4 * k + i / 2];
+                            to = i & 1 ? (to & 0xffffu) | bits << 16 : (to & 0xffff0000u) | bits;
+                        }
                 }
             }
         }
     }
-    __device__ __forceinline__ void put(int i, float v) { w[i] = __float_as_uint(v); }
-    template <typename H>
-    __device__ __forceinline__ void put(int i, H v) {
-        const uint32_t bits = *reinterpret_cast<const uint16_t*>(&v);
-        w[i >> 1] = i & 1 ? (w[i >> 1] & 0xffffu) | bits << 16 : (w[i >> 1] & 0xffff0000u) | bits;
-    }
-    __device__ __forceinline__ Eight<T> eight(int shift) const {
-        Eight<T> x;
-        uint32_t v[4 * kPieces];
+    // N times 256 values, from at[u] on
+    template <int N>
+    static __device__ __forceinline__ void load(Eight<T> (&x)[N], const T* row, const int (&at)[N], int vocab, int lane) {
+        if constexpr (kSpread) {
 #pragma unroll
-        for (int i = 0; i < 4 * kPieces; ++i) v[i] = w[i];
-        if constexpr (!VEC) {
-            const int words = sizeof(T) == 4 ? shift : shift >> 1;
-            if (words & 2) {
+            for (int u = 0; u < N; ++u)
 #pragma unroll
-                for (int i = 0; i + 2 < 4 * kPieces; ++i) v[i] = v[i + 2];
+                for (int e = 0; e < 8; ++e) {
+                    const int i = place(at[u], lane, e);
+                    x[u].put(e, i < vocab ? __ldg(row + i) : -INFINITY);
+                }
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const int i = at[u] + lane * 8;
+                if (i < vocab) {
+                    x[u].load_whole(row + i);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < (int)sizeof(T) * 2; ++k) reinterpret_cast<uint32_t*>(&x[u])[k] = kLowestWord<T>;
+                }
             }
-            if (words & 1) {
+        } else {
+            const int shift = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T)), bits = (shift & 1) * 16;
+            uint32_t w[N][8];
 #pragma unroll
-                for (int i = 0; i + 1 < 4 * kPieces; ++i) v[i] = v[i + 1];
-            }
-            if (sizeof(T) == 2 && (shift & 1)) {
+            for (int u = 0; u < N; ++u) pieces(w[u], row, at[u] + lane * 8 - shift, vocab);
+            auto take = [&](auto words) {  // one branch for all, as the shift is the warp's
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
-            }
+                for (int u = 0; u < N; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[u].w[i] = __funnelshift_r(w[u][i + words.value], w[u][i + words.value + 1], bits);
+            };
+            if (shift < 2)
+                take(std::integral_constant<int, 0>{});
+            else if (shift < 4)
+                take(std::integral_constant<int, 1>{});
+            else if (shift < 6)
+                take(std::integral_constant<int, 2>{});
+            else
+                take(std::integral_constant<int, 3>{});
         }
-#pragma unroll
-        for (int i = 0; i < (int)(8 * sizeof(T) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = v[i];
-        return x;
     }
 };
 
@@ -204,16 +206,14 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.ended && __ldg(p.ended + row) >= 0) return;
     const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-    const int shift = Fetch<T, VEC>::shift_of(x);
     Part sum = {-INFINITY, -INFINITY, 0.0f};
     int chunk = (int)blockIdx.x * p.turns * kScanWarps + warp;
     for (int turn = 0; turn < p.turns && chunk < p.n_chunks; ++turn, chunk += kScanWarps) {
-        Fetch<T, VEC> raw[kLoads];
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) raw[u].load(x, chunk * kChunk + u * 256 + lane * 8, p.vocab, shift);
         Eight<T> v8[kLoads];
+        int at[kLoads];
 #pragma unroll
-        for (int u = 0; u < kLoads; ++u) v8[u] = raw[u].eight(shift);
+        for (int u = 0; u < kLoads; ++u) at[u] = chunk * kChunk + u * 256;
+        Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
         float top[kLoads / kPerGroup], m = -INFINITY;
 #pragma unroll
         for (int g = 0; g < kLoads / kPerGroup; ++g) {
@@ -447,26 +447,25 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
             int found = groups <= kGroupCap ? 0 : kListCap + 1;
             if (!found) {
                 const float least = from_ordered(bound);
-                const int shift = Fetch<T, VEC>::shift_of(x);
                 constexpr int kPerGroup = kGroup<T> / 256;
                 for (int i0 = tid >> 5; i0 < groups * kPerGroup; i0 += kFetch * (kSearchThreads / 32)) {
-                    Fetch<T, VEC> raw[kFetch];
+                    Eight<T> v8[kFetch];
                     int at[kFetch];
 #pragma unroll
                     for (int u = 0; u < kFetch; ++u) {
                         const int i = i0 + u * (kSearchThreads / 32);
-                        at[u] = i < groups * kPerGroup ? (int)s.group[i / kPerGroup] * kGroup<T> + i % kPerGroup * 256 + lane * 8 : p.vocab;
-                        raw[u].load(x, at[u], p.vocab, shift);
+                        at[u] = i < groups * kPerGroup ? (int)s.group[i / kPerGroup] * kGroup<T> + i % kPerGroup * 256 : p.vocab;
                     }
+                    Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
 #pragma unroll
                     for (int u = 0; u < kFetch; ++u) {
                         float v[8];
-                        raw[u].eight(shift).floats(v);
+                        v8[u].floats(v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             if (!(v[e] >= least)) continue;
                             const int place = atomicAdd(&s.n, 1);
-                            if (place < kListCap) s.key[place] = key_of(ordered(v[e]), (uint32_t)(at[u] + e));
+                            if (place < kListCap) s.key[place] = key_of(ordered(v[e]), (uint32_t)Tile<T, VEC>::place(at[u], lane, e));
                         }
                     }
                 }
