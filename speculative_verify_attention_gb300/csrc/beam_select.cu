@@ -7,10 +7,11 @@
 // maximum, and one partial sum of exponentials of all that it has held: 1/200 of what it read.  Ordered by (maximum descending, place
 // ascending), the n_out best groups hold the row's n_out best values: a value outside them has n_out values before it, one in each.
 // So the second kernel, a block per row, picks those groups, reads them again and picks the values; a request's blocks form a
-// cluster, which joins their lists through shared memory.
-// Bound: the logits' bytes in the first kernel, latency in the second.  48 requests of 8 beams over 248320 bf16 logits (159 MB), 16 of
-// each: 34.5 us, of which the scan 27.5 (5.8 TB/s, 85 % of a copy's rate; issue slots 69 % busy) and the second kernel 7; one request of
-// 4 fp32 beams 6.9 us; 21 of up to 5 over 106299 fp16 logits (21 MB) 11.7 us.  As first built, with groups picked by rounds of five
+// cluster, which joins their lists through shared memory.  Where there are many rows it has a warp per row and a block per request
+// instead, and where the vocabulary is small that kernel does it all.
+// Bound: the logits' bytes in the first kernel, latency in the others.  48 requests of 8 beams over 248320 bf16 logits (159 MB), 16 of
+// each: 34.2 us, of which the scan 27.5 (5.8 TB/s, 85 % of a copy's rate; issue slots 69 % busy) and the second kernel 6.7; one request of
+// 4 fp32 beams 6.7 us; 21 of up to 5 over 106299 fp16 logits (21 MB) 11.7 us.  As first built, with groups picked by rounds of five
 // barriers and the join by the last block to finish: 74, 26 and 31 us.
 #include <cooperative_groups.h>
 
@@ -31,7 +32,9 @@ constexpr int kPickThreads = kSearchThreads + 32;
 constexpr int kMaxOut = 64;
 constexpr int kKeep = 4;           // groups of a row that a searching thread keeps: all of 262144 fp32 values
 constexpr int kPartKeep = 8;       // parts of a row that a lane of the summing warp keeps
-constexpr int kFetch = 3;          // loads of a lane at once (five spill, and are no faster)
+// Tiles of 256 values that a searching lane loads at once: 24 registers.
+template <typename T, bool VEC>
+constexpr int kFetch = sizeof(T) == 2 && VEC ? 6 : 3;
 constexpr int kGroupCap = 256;     // groups, and values, that the second kernel keeps of a row
 constexpr int kListCap = 512;
 
@@ -196,6 +199,119 @@ __device__ __forceinline__ float warp_max(float x) {  // NaN loses here too
     return m;
 }
 
+// The exponentials of a chunk join a lane's sum, m the largest value of both.
+template <typename T>
+__device__ __forceinline__ void add_to(Part& sum, const Eight<T> (&v8)[kLoads], float m) {
+    if (fabsf(m) < kLarge) {
+        const float e = rintf(m * kLog2e);
+        float s = sum.s;
+        if (fabsf(sum.m) < kLarge)
+            s *= ex2_approx(sum.e - e);
+        else if (sum.m > -INFINITY)
+            s *= exp2f((float)(scale_of_part(sum.m, sum.e) - (double)e));
+        float add[kLoads];  // (short chains: a value goes through 10 additions and one for each chunk after its own)
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            float v[8];
+            v8[u].floats(v);
+            add[u] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) add[u] += ex2_approx(__fmaf_rn(v[i], kLog2e, -e));
+        }
+        sum = {m, e, s + ((add[0] + add[1]) + (add[2] + add[3]))};
+    } else {
+        const bool any = fabsf(m) < INFINITY;
+        float s = sum.m > -INFINITY ? sum.s * exp2f((float)(scale_of_part(sum.m, sum.e) - scale_of_part(m, 0.0f))) : sum.s;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            float v[8];
+            v8[u].floats(v);  // of -inf alone nothing; a NaN or +inf makes the sum NaN
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                s += any ? ex2_approx((v[0] - m) * kLog2e) : v[0] == -INFINITY ? 0.0f : NAN;
+#pragma unroll
+                for (int w = 0; w < 7; ++w) v[w] = v[w + 1];
+            }
+        }
+        sum = {m, 0.0f, s};
+    }
+}
+
+// log2 near 1 + (i + 1/2) / 32, i < 32, made when this file is compiled: 64-bit arithmetic is slow here (2 a clock on a multiprocessor).
+struct LogValues {
+    float inverse[32];
+    double log_of[32];
+    constexpr LogValues() : inverse{}, log_of{} {
+        for (int i = 0; i < 32; ++i) {
+            inverse[i] = (float)(64.0 / (64 + 2 * i + 1));
+            const double z = (1.0 - inverse[i]) / (1.0 + inverse[i]);  // -log(inverse) = 2 (z + z^3/3 + z^5/5 + ...), z <= 1/3
+            double s = 0.0;
+            for (int k = 41; k >= 1; k -= 2) s = s * z * z + 1.0 / k;
+            log_of[i] = 2.0 * z * s * 1.4426950408889634074;
+        }
+    }
+};
+__device__ const LogValues kLogs{};
+// One entry a lane, loaded ahead of its use.
+struct LogTable {
+    float inverse;
+    double log_of;
+    __device__ __forceinline__ explicit LogTable(int lane) : inverse(kLogs.inverse[lane]), log_of(kLogs.log_of[lane]) {}
+    // log2 of a sum in units of 2^-32, by the lane nearest to its mantissa m and the series of log2(1 + f), 1 + f = m * inverse,
+    // |f| <= 1/64.  f is exact to half a step of fp32 (2^-31) for m's upper 24 bits, and so is what is added for the others; with the
+    // series' terms the result is off by 2^-28 at most.  All lanes of the warp; a sum of 0 gives no more than some number.
+    __device__ __forceinline__ double log2_of(unsigned long long sum) const {
+        const int top = 63 - __clzll((long long)(sum | 1));
+        const uint64_t mantissa = sum << 1 << (63 - top);  // behind the leading one
+        const int near = (int)(mantissa >> 59);
+        const float i = __shfl_sync(0xffffffffu, inverse, near);
+        const float f = __fmaf_rn(__uint_as_float(0x3f800000u | (uint32_t)(mantissa >> 41)), i, -1.0f) +
+                        (float)((uint32_t)(mantissa >> 17) & 0xffffffu) * 0x1p-47f * i;
+        const float tail = f * f * (-0.5f + f * (1.0f / 3.0f + f * (-0.25f + f * (0.2f + f * (-1.0f / 6.0f)))));
+        return (double)(top - 32) + (__shfl_sync(0xffffffffu, log_of, near) + (double)((f + tail) * 1.44269504f));
+    }
+};
+// log sum exp, of a sum whose log2 is that and whose values' largest is top
+__device__ __forceinline__ double norm_of(float top, float e, double log2_sum) {
+    return fabsf(top) < kLarge ? ((double)e + log2_sum) * (1.0 / (double)kLog2e) : (double)top + log2_sum * 0.69314718055994530942;
+}
+
+// A row's parts, scaled by powers of two to the largest one's and added as whole numbers of 2^-32, so that their order does not matter.
+// True where a value was NaN or +infinite.  All lanes of a warp.
+__device__ __forceinline__ bool add_parts(const Part* parts, int n, int lane, float& top, float& e, unsigned long long& sum) {
+    int32_t m = ordered(-INFINITY);
+    bool bad = false;
+    Part kept[kPartKeep];
+#pragma unroll
+    for (int u = 0; u < kPartKeep; ++u) kept[u] = u * 32 + lane < n ? parts[u * 32 + lane] : Part{-INFINITY, -INFINITY, 0.0f};
+    auto look = [&](const Part& q) {
+        m = max(m, ordered(q.m));
+        bad |= q.s != q.s;
+    };
+#pragma unroll
+    for (int u = 0; u < kPartKeep; ++u) look(kept[u]);
+    for (int i = kPartKeep * 32 + lane; i < n; i += 32) look(parts[i]);
+    top = from_ordered(__reduce_max_sync(0xffffffffu, m));
+    bad = __any_sync(0xffffffffu, bad);
+    e = rintf(top * kLog2e);
+    const bool plain = fabsf(top) < kLarge;
+    sum = 0;
+    auto add = [&](const Part& q) {
+        float v = 0.0f;
+        if (plain && fabsf(q.m) < kLarge)
+            v = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
+        else if (q.m > -INFINITY)
+            v = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
+        sum += __float2ull_rn(v * 0x1p32f);
+    };
+#pragma unroll
+    for (int u = 0; u < kPartKeep; ++u) add(kept[u]);
+    for (int i = kPartKeep * 32 + lane; i < n; i += 32) add(parts[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return bad;
+}
+
 // A warp takes p.turns chunks of a row, and is one of its n_parts.  The sum so far is of 2^(x log2 e - e), e a whole number near the
 // largest value so far (one rounding a value); a larger one scales it by a power of two.
 template <typename T, bool VEC>
@@ -227,38 +343,7 @@ __global__ void __launch_bounds__(kScanThreads) beam_scan_kernel(const __grid_co
             else
                 *reinterpret_cast<float2*>(to) = make_float2(top[0], top[1]);
         }
-        m = fmaxf(m, sum.m);
-        if (fabsf(m) < kLarge) {
-            const float e = rintf(m * kLog2e);
-            float s = sum.s;
-            if (fabsf(sum.m) < kLarge)
-                s *= ex2_approx(sum.e - e);
-            else if (sum.m > -INFINITY)
-                s *= exp2f((float)(scale_of_part(sum.m, sum.e) - (double)e));
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                float v[8];
-                v8[u].floats(v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s += ex2_approx(__fmaf_rn(v[i], kLog2e, -e));
-            }
-            sum = {m, e, s};
-        } else {
-            const bool any = fabsf(m) < INFINITY;
-            float s = sum.m > -INFINITY ? sum.s * exp2f((float)(scale_of_part(sum.m, sum.e) - scale_of_part(m, 0.0f))) : sum.s;
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                float v[8];
-                v8[u].floats(v);  // of -inf alone nothing; a NaN or +inf makes the sum NaN
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i) {
-                    s += any ? ex2_approx((v[0] - m) * kLog2e) : v[0] == -INFINITY ? 0.0f : NAN;
-#pragma unroll
-                    for (int w = 0; w < 7; ++w) v[w] = v[w + 1];
-                }
-            }
-            sum = {m, 0.0f, s};
-        }
+        add_to(sum, v8, fmaxf(m, sum.m));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum.s += __shfl_xor_sync(0xffffffffu, sum.s, o);
@@ -271,11 +356,11 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // The threads that search (the others of the block sum).
 __device__ __forceinline__ void search_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-struct Search {
+struct alignas(16) Search {
     uint64_t key[kListCap];      // candidates, as key_of
     uint64_t best[kMaxOut];      // the row's best, in order
     uint32_t group[kGroupCap];
-    int32_t top[kSearchThreads / 2];
+    int32_t top[kSearchThreads];
     uint64_t above;              // keys below this are none of the best (slow path)
     int32_t bound;               // values below this are none of the best
     int n_groups, n;
@@ -290,6 +375,78 @@ __device__ __forceinline__ void rank_keys(Search& s, int n, int n_out) {
         if (rank < n_out) s.best[rank] = mine;
     }
     search_sync();
+}
+
+// A bound of the row's n_out best, from a share's maximum in every `lanes` threads: the n_out-th best of them.
+__device__ __forceinline__ void find_bound(Search& s, int32_t m, int lanes, int n_out) {
+    const int tid = threadIdx.x, tops = kSearchThreads / lanes;
+    for (int o = 1; o < lanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (tid % lanes == 0) s.top[tid / lanes] = m;
+    search_sync();
+    if (tid < tops) {
+        m = s.top[tid];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < tops / 4; ++j) {
+            const int4 o = reinterpret_cast<const int4*>(s.top)[j];
+            rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
+        }
+        if (rank < n_out) atomicMin(&s.bound, m);
+    }
+    search_sync();
+}
+
+// The values of n tiles that reach least become candidates.
+template <typename T, bool VEC, typename At>
+__device__ __forceinline__ void gather(Search& s, const T* x, float least, int n, int vocab, At at_of) {
+    constexpr int kTiles = kFetch<T, VEC>;
+    const int lane = threadIdx.x & 31;
+    for (int i0 = threadIdx.x >> 5; i0 < n; i0 += kTiles * (kSearchThreads / 32)) {
+        Eight<T> v8[kTiles];
+        {
+            int at[kTiles];
+#pragma unroll
+            for (int u = 0; u < kTiles; ++u) {
+                const int i = i0 + u * (kSearchThreads / 32);
+                at[u] = i < n ? at_of(i) : vocab;
+            }
+            Tile<T, VEC>::load(v8, x, at, vocab, lane);
+        }
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) {
+            if (!(largest(v8[u]) >= least)) continue;
+            const int at = at_of(i0 + u * (kSearchThreads / 32));
+            float v[8];
+            v8[u].floats(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!(v[e] >= least)) continue;
+                const int place = atomicAdd(&s.n, 1);  // (one for all that a lane has is no faster)
+                if (place < kListCap) s.key[place] = key_of(ordered(v[e]), (uint32_t)Tile<T, VEC>::place(at, lane, e));
+            }
+        }
+    }
+    search_sync();
+}
+
+// The candidates of a row of too few groups for a bound: by shares of the row itself, which is read twice.
+template <typename T, bool VEC>
+__device__ __noinline__ void gather_all(Search& s, const SelectParams& p, const T* x) {
+    const int lane = threadIdx.x & 31, tiles = (p.vocab + 255) / 256;
+    const int32_t lowest = ordered(-INFINITY);
+    constexpr int kTiles = kFetch<T, VEC>;
+    int32_t m = lowest;
+    for (int i0 = threadIdx.x >> 5; i0 < tiles; i0 += kTiles * (kSearchThreads / 32)) {
+        Eight<T> v8[kTiles];
+        int at[kTiles];
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) at[u] = min((i0 + u * (kSearchThreads / 32)) * 256, p.vocab);
+        Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
+#pragma unroll
+        for (int u = 0; u < kTiles; ++u) m = max(m, ordered(largest(v8[u])));
+    }
+    find_bound(s, m, p.n_out <= 16 ? 4 : 2, p.n_out);
+    gather<T, VEC>(s, x, from_ordered(max(s.bound, lowest + 1)), tiles, p.vocab, [](int i) { return i * 256; });
 }
 
 // Where more groups or values reach the bound than the lists hold (many equal values): the row's groups, and then the best ones'
@@ -346,9 +503,114 @@ struct Lists {
         : order(reinterpret_cast<int64_t*>(at)), total(reinterpret_cast<float*>(order + kMaxWindowRows * n_out)),
           token(reinterpret_cast<int32_t*>(total + rows * n_out)) {}
 };
-int lists_bytes(int cluster, int n_out) {
+__host__ __device__ __forceinline__ int lists_bytes(int cluster, int n_out) {
     const int rows = (kMaxWindowRows + cluster - 1) / cluster;
     return rows * n_out * 8 + kMaxWindowRows * n_out * 8;
+}
+
+// The places of the continuations of a request's rows me, me + size, ... among all of its rows', each row's in order.
+// Continuations of all rows are ordered by (order descending, row, place in the row).  For 2^l <= n_out the ceil(n_out / 2^l)-th best of
+// the rows' 2^l-th continuations has n_out continuations before it or is the n_out-th.  The best of these bounds leaves at most
+// n_out / 2^l rounded up that have a 2^l-th one, so at most (levels) n_out + 2^levels in all, which are counted off against each other.
+// Where there is little to place, eight lanes a continuation search the other rows for it instead: 48 requests of 8 beams 34.8 us (this
+// way 36.0); searched for always, 125 requests of 32 beams over 1000 values, 64 of each, took 123 us (this way 32).
+struct alignas(16) Placed {
+    int64_t order;
+    int32_t id, pad;  // row * kMaxOut + place
+};
+constexpr int kLevels = 7;  // 2^6 = kMaxOut
+struct PlaceBounds {
+    int64_t order[kLevels];
+    int32_t id[kLevels];
+    int n;
+    __device__ __forceinline__ void clear(int i) {
+        if (i < kLevels) order[i] = INT64_MIN, id[i] = -1;
+        if (i == kLevels) n = 0;
+    }
+};
+__host__ __device__ __forceinline__ int placed_bytes(int n_out) { return (kLevels * n_out + 128) * (int)sizeof(Placed); }
+
+__device__ __forceinline__ bool before(int64_t a, int32_t a_id, int64_t b, int32_t b_id) { return a > b || (a == b && a_id < b_id); }
+
+// The block's threads, all of them; `at` has been cleared and all orders and counts have been written before a barrier.
+__device__ __forceinline__ void place_all(const SelectParams& p, const Lists& lists, const int* counts, PlaceBounds& at, Placed* list, int first,
+                                          int rows, int me, int size, int64_t to) {
+    const int tid = threadIdx.x, lane = tid & 31, n_out = p.n_out, warps = (int)blockDim.x >> 5;
+    auto put = [&](int r, int j, int rank) {
+        const int mine = (r - me) / size * n_out + j;
+        p.parents[to + rank] = first + r;
+        p.tokens[to + rank] = lists.token[mine];
+        p.totals[to + rank] = lists.total[mine];
+    };
+    if (rows == 1) {
+        for (int j = tid; j < counts[0]; j += (int)blockDim.x) put(0, j, j);
+        return;
+    }
+    const int mine_rows = (rows - me + size - 1) / size;
+    if (rows <= 8 && mine_rows * n_out <= (int)blockDim.x / 4) {
+        for (int c0 = 0; c0 < mine_rows * n_out; c0 += (int)blockDim.x / 8) {
+            const int c = c0 + tid / 8, at = c / n_out, j = c - at * n_out, r = me + at * size, q = tid % 8;
+            const bool there = c < mine_rows * n_out && j < counts[r];
+            const int64_t mine = there ? lists.order[r * n_out + j] : 0;
+            int lo = 0, hi = there && q < rows && q != r ? counts[q] : 0;  // how many of row q come before
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (before(lists.order[q * n_out + mid], q, mine, r))
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) lo += __shfl_xor_sync(0xffffffffu, lo, o);
+            if (q == 0 && there && j + lo < n_out) put(r, j, j + lo);
+        }
+        return;
+    }
+    for (int l = tid >> 5; l < kLevels && n_out >> l; l += warps) {
+        const int j = (1 << l) - 1, place = (n_out + j) >> l;
+        for (int r = lane; r < rows; r += 32) {
+            if (j >= counts[r]) continue;
+            const int64_t mine = lists.order[r * n_out + j];
+            int rank = 0;
+            for (int q = 0; q < rows; ++q) rank += j < counts[q] && before(lists.order[q * n_out + j], q, mine, r);
+            if (rank == place - 1) at.order[l] = mine, at.id[l] = r * kMaxOut + j;
+        }
+    }
+    __syncthreads();
+    int64_t bound = INT64_MIN;
+    int32_t bound_id = INT32_MAX;
+#pragma unroll
+    for (int l = 0; l < kLevels; ++l)
+        if (at.id[l] >= 0 && before(at.order[l], at.id[l], bound, bound_id)) bound = at.order[l], bound_id = at.id[l];
+    for (int r = tid >> 5; r < rows; r += warps)
+        for (int j = lane; j < counts[r]; j += 32) {
+            const int64_t o = lists.order[r * n_out + j];
+            if (!before(bound, bound_id, o, r * kMaxOut + j)) list[atomicAdd(&at.n, 1)] = {o, r * kMaxOut + j, 0};
+        }
+    __syncthreads();
+    const int n = at.n;
+    for (int i = tid; i < n; i += (int)blockDim.x) {
+        const Placed mine = list[i];
+        const int r = mine.id / kMaxOut;
+        if (r % size != me) continue;
+        int rank = 0;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const Placed o = list[k];
+            rank += before(o.order, o.id, mine.order, mine.id);
+        }
+        if (rank < n_out) put(r, mine.id % kMaxOut, rank);
+    }
+}
+// The places that no continuation has.
+__device__ __forceinline__ void fill_rest(const SelectParams& p, const int* counts, int rows, int64_t to) {
+    const int tid = threadIdx.x, n_out = p.n_out;
+    int n_all = 0;
+    for (int r = 0; r < rows; ++r) n_all += counts[r];
+    for (int k = n_all + tid; k < n_out; k += (int)blockDim.x) {
+        p.parents[to + k] = p.tokens[to + k] = -1;
+        p.totals[to + k] = -INFINITY;
+    }
 }
 
 // A cluster of blocks: one request.  A block's first eight warps look for a row's best values, the ninth sums its exponentials.
@@ -356,6 +618,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid_constant__ SelectParams p) {
     extern __shared__ __align__(16) unsigned char s_lists[];
     __shared__ Search s;
+    __shared__ PlaceBounds s_places;
     __shared__ double s_base;  // the row's score less its log sum exp
     __shared__ int s_found, s_counts[kMaxWindowRows];
     namespace cg = cooperative_groups;
@@ -364,12 +627,8 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     const int tid = threadIdx.x, n_out = p.n_out;
     const int lane = tid & 31;
     const bool sums = tid >= kSearchThreads;
-    // log2 near 1 + (lane + 1/2) / 32, by the summing warp's lanes, while the kernel before ends
-    double inverse = 0.0, log_of = 0.0;
-    if (sums) {
-        inverse = (double)__frcp_rn(1.0f + ((float)lane + 0.5f) * 0x1p-5f);
-        log_of = -log2(inverse);
-    }
+    const LogTable logs(lane);  // for the summing warp
+    s_places.clear(tid);
     cluster_arrive();  // (a block's shared memory is written by others once it has started)
     const Lists lists(s_lists, (kMaxWindowRows + size - 1) / size, n_out);
     const int64_t to = (int64_t)b * n_out;
@@ -410,67 +669,37 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
         if (tid == 0) s.n_groups = s.n = 0, s.bound = 0x7fffffff;
         const bool usable = fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY, live = usable && ended < 0;
         if (live && !sums) {
-            // a bound: the n_out-th best of 64 or 128 shares of the groups; about 1.1 n_out groups reach it
-            const int lanes = n_out <= 16 ? 4 : 2;
-            int32_t m = k[0];
-#pragma unroll
-            for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
-            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, ordered(__ldg(gm + g)));
-            for (int o = 1; o < lanes; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (tid % lanes == 0) s.top[tid / lanes] = m;
-            search_sync();
-            const int tops = kSearchThreads / lanes;
-            if (tid < tops) {
-                m = s.top[tid];
-                int rank = 0;
-#pragma unroll 4
-                for (int j = 0; j < tops / 4; ++j) {
-                    const int4 o = reinterpret_cast<const int4*>(s.top)[j];
-                    rank += (o.x > m) + (o.y > m) + (o.z > m) + (o.w > m);
-                }
-                if (rank < n_out) atomicMin(&s.bound, m);
-            }
-            search_sync();
-            // the groups that reach it, and their values that do; -inf is none
-            const int32_t bound = max(s.bound, lowest + 1);
-            auto group = [&](int32_t key, int g) {
-                if (key < bound) return;
-                const int at = atomicAdd(&s.n_groups, 1);
-                if (at < kGroupCap) s.group[at] = (uint32_t)g;
-            };
-#pragma unroll
-            for (int u = 0; u < kKeep; ++u) group(k[u], u * kSearchThreads + tid);
-            for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(ordered(__ldg(gm + g)), g);
-            search_sync();
-            const int groups = s.n_groups;
             const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
-            int found = groups <= kGroupCap ? 0 : kListCap + 1;
-            if (!found) {
-                const float least = from_ordered(bound);
-                constexpr int kPerGroup = kGroup<T> / 256;
-                for (int i0 = tid >> 5; i0 < groups * kPerGroup; i0 += kFetch * (kSearchThreads / 32)) {
-                    Eight<T> v8[kFetch];
-                    int at[kFetch];
-#pragma unroll
-                    for (int u = 0; u < kFetch; ++u) {
-                        const int i = i0 + u * (kSearchThreads / 32);
-                        at[u] = i < groups * kPerGroup ? (int)s.group[i / kPerGroup] * kGroup<T> + i % kPerGroup * 256 : p.vocab;
-                    }
-                    Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
-#pragma unroll
-                    for (int u = 0; u < kFetch; ++u) {
-                        float v[8];
-                        v8[u].floats(v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (!(v[e] >= least)) continue;
-                            const int place = atomicAdd(&s.n, 1);
-                            if (place < kListCap) s.key[place] = key_of(ordered(v[e]), (uint32_t)Tile<T, VEC>::place(at[u], lane, e));
-                        }
-                    }
-                }
-                search_sync();
+            int found = kListCap + 1;
+            if (4 * p.n_groups < 5 * n_out) {
+                gather_all<T, VEC>(s, p, x);
                 found = s.n;
+            } else {
+                // a bound: the n_out-th best of 64, 128 or 256 shares of the groups, 5/4 n_out at least; about 1.1 n_out groups reach it
+                const int lanes = n_out <= 16 && p.n_groups >= 5 * n_out ? 4 : 2 * p.n_groups >= 5 * n_out ? 2 : 1;
+                int32_t m = k[0];
+#pragma unroll
+                for (int u = 1; u < kKeep; ++u) m = max(m, k[u]);
+                for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) m = max(m, ordered(__ldg(gm + g)));
+                find_bound(s, m, lanes, n_out);
+                // the groups that reach it, and their values that do; -inf is none
+                const int32_t bound = max(s.bound, lowest + 1);
+                auto group = [&](int32_t key, int g) {
+                    if (key < bound) return;
+                    const int at = atomicAdd(&s.n_groups, 1);
+                    if (at < kGroupCap) s.group[at] = (uint32_t)g;
+                };
+#pragma unroll
+                for (int u = 0; u < kKeep; ++u) group(k[u], u * kSearchThreads + tid);
+                for (int g = kKeep * kSearchThreads + tid; g < p.n_groups; g += kSearchThreads) group(ordered(__ldg(gm + g)), g);
+                search_sync();
+                const int groups = s.n_groups;
+                if (groups <= kGroupCap) {
+                    constexpr int kPerGroup = kGroup<T> / 256;
+                    gather<T, VEC>(s, x, from_ordered(bound), groups * kPerGroup, p.vocab,
+                                   [&](int i) { return (int)s.group[i / kPerGroup] * kGroup<T> + i % kPerGroup * 256; });
+                    found = s.n;
+                }
             }
             if (found <= kListCap)
                 rank_keys(s, found, n_out);
@@ -478,51 +707,12 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
                 found = pick_slowly<T, VEC>(s, p, x, gm);
             if (tid == 0) s_found = min(found, n_out);
         } else if (live) {
-            // parts scaled by powers of two to the largest one's, added as whole numbers of 2^-32, so that their order does not
-            // matter
-            const Part* parts = p.parts + (int64_t)row * p.n_parts;
-            int32_t m = lowest;
-            bool bad = false;
-            Part kept[kPartKeep];
-#pragma unroll
-            for (int u = 0; u < kPartKeep; ++u) kept[u] = u * 32 + lane < p.n_parts ? parts[u * 32 + lane] : Part{-INFINITY, -INFINITY, 0.0f};
-            auto look = [&](const Part& q) {
-                m = max(m, ordered(q.m));
-                bad |= q.s != q.s;
-            };
-#pragma unroll
-            for (int u = 0; u < kPartKeep; ++u) look(kept[u]);
-            for (int i = kPartKeep * 32 + lane; i < p.n_parts; i += 32) look(parts[i]);
-            const float top = from_ordered(__reduce_max_sync(0xffffffffu, m));
-            bad = __any_sync(0xffffffffu, bad);
-            const float e = rintf(top * kLog2e);
-            const bool plain = fabsf(top) < kLarge;
-            unsigned long long sum = 0;
-            auto add = [&](const Part& q) {
-                float v = 0.0f;
-                if (plain && fabsf(q.m) < kLarge)
-                    v = q.e - e > -126.0f ? q.s * __int_as_float((127 + (int)(q.e - e)) << 23) : 0.0f;
-                else if (q.m > -INFINITY)
-                    v = q.s * exp2f((float)(scale_of_part(q.m, q.e) - scale_of_part(top, e)));
-                sum += __float2ull_rn(v * 0x1p32f);
-            };
-#pragma unroll
-            for (int u = 0; u < kPartKeep; ++u) add(kept[u]);
-            for (int i = kPartKeep * 32 + lane; i < p.n_parts; i += 32) add(parts[i]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            // log2 of the sum = 2^k (1 + m): by the lane nearest to 1 + m, and the series of log2(1 + f), |f| <= 1/64 (its terms
-            // from f^2 on in fp32: 2^-13 of 2^-24)
-            const int k = 63 - __clzll((long long)(sum | 1));
-            const uint64_t mantissa = sum << 1 << (63 - k);
-            const int near = (int)(mantissa >> 59);
-            const double m1 = __longlong_as_double((long long)(0x3ff0000000000000ull | mantissa >> 12));
-            const double f = fma(m1, __shfl_sync(0xffffffffu, inverse, near), -1.0);
-            const float g = (float)f;
-            const float tail = g * g * (-0.5f + g * (1.0f / 3.0f + g * (-0.25f + g * (0.2f + g * (-1.0f / 6.0f)))));
-            const double log2_sum = (double)(k - 32) + (__shfl_sync(0xffffffffu, log_of, near) + (f + (double)tail) * 1.4426950408889634074);
+            float top, e;
+            unsigned long long sum;
+            const bool bad = add_parts(p.parts + (int64_t)row * p.n_parts, p.n_parts, lane, top, e, sum);
+            const double log2_sum = logs.log2_of(sum);
             if (lane == 0) {
-                const double norm = plain ? ((double)e + log2_sum) * (1.0 / (double)kLog2e) : (double)top + log2_sum * 0.69314718055994530942;
+                const double norm = norm_of(top, e, log2_sum);
                 s_base = bad || sum == 0 ? (double)INFINITY : (double)score - norm;
             }
         }
@@ -551,44 +741,280 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     if (me >= rows) cluster_wait();
     cluster.sync();
     if (me < rows) {  // each block places its own rows' continuations among all
-        // eight lanes a continuation, each with an eighth of the other rows
-        const int share = tid % 8;
-        for (int r = me; r < rows; r += size) {
-            const int count = s_counts[r];
-            for (int j0 = 0; j0 < count; j0 += kPickThreads / 8) {
-                const int j = min(j0 + tid / 8, count - 1);
-                const int64_t mine = lists.order[r * n_out + j];
-                int rank = share == 0 ? j : 0;
-                for (int q = share; q < rows; q += 8) {
-                    const int64_t* o = lists.order + q * n_out;
-                    int lo = 0, hi = q == r ? 0 : s_counts[q];  // how many of row q come before: more, or as much and of a lower row
-                    while (lo < hi) {
-                        const int mid = (lo + hi) >> 1;
-                        if (o[mid] > mine || (o[mid] == mine && q < r))
-                            lo = mid + 1;
-                        else
-                            hi = mid;
-                    }
-                    rank += lo;
-                }
+        Placed* list = reinterpret_cast<Placed*>(s_lists + lists_bytes(size, n_out));
+        place_all(p, lists, s_counts, s_places, list, first, rows, me, size, to);
+        if (me == 0) fill_rest(p, s_counts, rows, to);
+    }
+}
+
+// A block per request and a warp per row; what needs 64-bit arithmetic is done for all rows together, a thread each.
+//   SCANNED: after beam_scan_kernel, where there are so many rows that blocks for each would queue.
+//   Else in one launch, for small vocabularies: the row is read (and a second time from L1, if it is more than the lanes hold at once).
+// The bound is the n_out-th best of 32, 64 or 128 shares, which the lanes have of the groups or of the row.
+// 4000 rows of 1000 bf16 values, 16 of each 250 requests: 10.5 us in one launch (304 by beam_pick_kernel); one row 4.0 (25.7).  2048 rows
+// of 32000, 8 of each 256: 36.6 (60.1).
+constexpr int kRowWarps = 16;
+constexpr int kRowList = 384;   // candidates of a row
+struct alignas(16) RowSearch {  // (read 16 bytes at a time)
+    uint64_t key[kRowList];
+    uint64_t best[kMaxOut];
+    int32_t share[128];
+    uint32_t place[kRowList];
+};
+static_assert(sizeof(RowSearch) % 16 == 0 && offsetof(RowSearch, share) % 16 == 0 && offsetof(Search, top) % 16 == 0);
+static_assert(kRowList >= kMaxOut + 256);
+struct RowBlock {
+    unsigned long long sum[kMaxWindowRows];  // of exponentials, in units of 2^-32
+    double base[kMaxWindowRows];
+    float top[kMaxWindowRows], e[kMaxWindowRows], score[kMaxWindowRows], weight[kMaxWindowRows];
+    int32_t ended[kMaxWindowRows];  // -2: the row is not usable
+    int counts[kMaxWindowRows];
+};
+
+// The best n_out of a warp's n keys, in order.
+__device__ __forceinline__ void rank_row(RowSearch& s, int n, int n_out, int lane) {
+    for (int i = lane; i < n; i += 32) {
+        const uint64_t key = s.key[i];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += s.key[j] > key;
+        if (rank < n_out) s.best[rank] = key;
+    }
+    __syncwarp();
+}
+
+// A row of which more values reach `least` than the list holds (many equal ones): those above the list's worst, a full list cut back to
+// its best n_out.
+template <typename T>
+__device__ __noinline__ int search_slowly(RowSearch& s, const T* x, int vocab, float least, int n_out, int lane) {
+    int n = 0;
+    uint64_t above = 0;
+    auto cut = [&] {
+        __syncwarp();
+        rank_row(s, n, n_out, lane);
+        n = min(n, n_out);
+        for (int i = lane; i < n; i += 32) s.key[i] = s.best[i];
+        __syncwarp();
+        if (n == n_out) above = s.key[n - 1];
+    };
+    for (int at = 0; at < vocab; at += 256) {
+        uint64_t key[8];
+        int hits = 0;
 #pragma unroll
-                for (int o = 1; o < 8; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-                if (share == 0 && j0 + tid / 8 < count && rank < n_out) {
-                    p.parents[to + rank] = first + r;
-                    p.tokens[to + rank] = lists.token[r / size * n_out + j];
-                    p.totals[to + rank] = lists.total[r / size * n_out + j];
-                }
-            }
+        for (int e = 0; e < 8; ++e) {
+            const int i = at + e * 32 + lane;
+            const float v = i < vocab ? to_float(x[i]) : -INFINITY;
+            key[e] = i < vocab && v >= least ? key_of(ordered(v), (uint32_t)i) : 0;
+            hits += __popc(__ballot_sync(0xffffffffu, key[e] > above));
         }
-        if (me == 0) {
-            int n_all = 0;
-            for (int r = 0; r < rows; ++r) n_all += s_counts[r];
-            for (int k = n_all + tid; k < n_out; k += kPickThreads) {
-                p.parents[to + k] = p.tokens[to + k] = -1;
-                p.totals[to + k] = -INFINITY;
-            }
+        if (!hits) continue;
+        if (n + hits > kRowList) cut();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t who = __ballot_sync(0xffffffffu, key[e] > above);
+            if (key[e] > above) s.key[n + __popc(who & ((1u << lane) - 1))] = key[e];
+            n += __popc(who);
         }
     }
+    cut();
+    return n;
+}
+
+template <typename T, bool VEC, bool SCANNED>
+__global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_constant__ SelectParams p) {
+    constexpr int kPerGroup = kGroup<T> / 256;
+    extern __shared__ __align__(16) unsigned char s_lists[];
+    __shared__ RowBlock s_all;
+    __shared__ PlaceBounds s_places;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5, b = blockIdx.x, n_out = p.n_out;
+    const LogTable logs(lane);
+    for (int i = tid; i <= kLevels; i += (int)blockDim.x) s_places.clear(i);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Lists lists(s_lists, kMaxWindowRows, n_out);
+    unsigned char* behind = s_lists + lists_bytes(1, n_out);
+    RowSearch& s = reinterpret_cast<RowSearch*>(behind + placed_bytes(n_out))[warp];
+    int first, rows;
+    if (!rows_of(p, b, first, rows)) rows = 0;
+    const int32_t lowest = ordered(-INFINITY);
+    for (int mine = warp; mine < rows; mine += warps) {
+        const int row = first + mine;
+        const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
+        Eight<T> v8[kLoads];
+        auto load = [&](int chunk) {
+            int at[kLoads];
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) at[u] = chunk * kChunk + u * 256;
+            Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
+        };
+        const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
+        int ended = p.ended ? __ldg(p.ended + row) : -1;
+        if (!SCANNED) load(0);
+        if (!(fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY)) ended = -2;
+        float top = 0.0f, e = 0.0f;
+        unsigned long long sum = 0;
+        int count = ended >= 0;
+        if (ended == -1) {
+            const float* gm = p.group_max + (int64_t)row * p.n_groups;
+            int32_t most[4] = {lowest, lowest, lowest, lowest};
+            bool bad;
+            if (SCANNED) {
+                for (int g0 = lane; g0 < p.n_groups; g0 += 128)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) most[u] = max(most[u], g0 + u * 32 < p.n_groups ? ordered(__ldg(gm + g0 + u * 32)) : lowest);
+                bad = add_parts(p.parts + (int64_t)row * p.n_parts, p.n_parts, lane, top, e, sum);
+            } else {
+                Part part = {-INFINITY, -INFINITY, 0.0f};
+                for (int chunk = 0;;) {
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u) {
+                        const float l = largest(v8[u]);
+                        most[u] = max(most[u], ordered(l));
+                        m = fmaxf(m, l);
+                    }
+                    add_to(part, v8, fmaxf(warp_max(m), part.m));
+                    if (++chunk == p.n_chunks) break;
+                    load(chunk);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) part.s += __shfl_xor_sync(0xffffffffu, part.s, o);
+                top = part.m, e = part.e;
+                bad = !(part.s < INFINITY);
+                sum = bad ? 0 : __float2ull_rn(part.s * 0x1p32f);  // exact: part.s is 0, or about 0.7 at least
+            }
+            int32_t reach = 0x7fffffff;
+            auto rank = [&](auto n) {  // n shares a lane
+                __syncwarp();
+#pragma unroll
+                for (int u = 0; u < n.value; ++u) s.share[u * 32 + lane] = most[u];
+                __syncwarp();
+                int better[n.value] = {};
+#pragma unroll
+                for (int j = 0; j < 8 * n.value; ++j) {
+                    const int4 o = reinterpret_cast<const int4*>(s.share)[j];
+#pragma unroll
+                    for (int u = 0; u < n.value; ++u) better[u] += (o.x > most[u]) + (o.y > most[u]) + (o.z > most[u]) + (o.w > most[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < n.value; ++u)
+                    if (better[u] < n_out) reach = min(reach, most[u]);
+            };
+            if (n_out > 32) {
+                rank(std::integral_constant<int, 4>{});
+            } else {
+                most[0] = max(most[0], most[2]), most[1] = max(most[1], most[3]);
+                if (n_out > 16) {
+                    rank(std::integral_constant<int, 2>{});
+                } else {
+                    most[0] = max(most[0], most[1]);
+                    rank(std::integral_constant<int, 1>{});
+                }
+            }
+            const int32_t bound = max(__reduce_min_sync(0xffffffffu, reach), lowest + 1);
+            const float least = from_ordered(bound);
+            int n = 0;
+            // lanes with `here` more entries each: where a lane's begin
+            auto begin = [&](int here) {
+                int upto = here;
+#pragma unroll
+                for (int o = 1; o < 32; o *= 2) {
+                    const int below = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += below;
+                }
+                const int at = n + upto - here;
+                n += __shfl_sync(0xffffffffu, upto, 31);
+                return at;
+            };
+            uint32_t* groups = reinterpret_cast<uint32_t*>(s.key);
+            int tiles = p.n_chunks * kLoads;
+            if (SCANNED) {
+                for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
+                    const bool hit = g0 + lane < p.n_groups && ordered(__ldg(gm + g0 + lane)) >= bound;
+                    const uint32_t who = __ballot_sync(0xffffffffu, hit);
+                    const int at = n + __popc(who & ((1u << lane) - 1));
+                    if (hit && at < kRowList) groups[at] = (uint32_t)(g0 + lane);
+                    n += __popc(who);
+                }
+                __syncwarp();
+                tiles = n <= kRowList ? n * kPerGroup : 0;
+                n = n <= kRowList ? 0 : kRowList + 1;
+            }
+            for (int t = 0; t < tiles; t += kLoads) {
+                int at[kLoads];
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int i = t + u;
+                    if (SCANNED)
+                        at[u] = i < tiles ? (int)groups[i / kPerGroup] * kGroup<T> + i % kPerGroup * 256 : p.vocab;
+                    else
+                        at[u] = i * 256;
+                }
+                if (SCANNED || p.n_chunks > 1) Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
+                uint32_t hit = 0;
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    float v[8];
+                    v8[u].floats(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) hit |= (v[i] >= least ? 1u : 0u) << (u * 8 + i);
+                }
+                if (!__any_sync(0xffffffffu, hit)) continue;
+                for (int place = begin(__popc(hit)); hit; hit &= hit - 1, ++place) {
+                    const int i = __ffs(hit) - 1;
+                    int from = at[0];
+#pragma unroll
+                    for (int u = 1; u < kLoads; ++u) from = i >= u * 8 ? at[u] : from;
+                    if (place < kRowList) s.place[place] = (uint32_t)Tile<T, VEC>::place(from, lane, i & 7);
+                }
+            }
+            __syncwarp();
+            if (n <= kRowList) {
+                for (int i = lane; i < n; i += 32) {
+                    const uint32_t place = s.place[i];
+                    s.key[i] = key_of(ordered(to_float(x[place])), place);
+                }
+                __syncwarp();
+                rank_row(s, n, n_out, lane);
+                count = min(n, n_out);
+            } else {
+                count = search_slowly(s, x, p.vocab, least, n_out, lane);
+            }
+            if (bad || sum == 0) count = 0;
+            for (int k = lane; k < count; k += 32) lists.order[mine * n_out + k] = (int64_t)s.best[k];
+            __syncwarp();
+        }
+        if (lane == 0) {
+            s_all.sum[mine] = sum;
+            s_all.top[mine] = top;
+            s_all.e[mine] = e;
+            s_all.score[mine] = score;
+            s_all.weight[mine] = weight;
+            s_all.ended[mine] = ended;
+            s_all.counts[mine] = count;
+        }
+    }
+    __syncthreads();
+    for (int r0 = warp * 32; r0 < rows; r0 += warps * 32) {
+        const int r = min(r0 + lane, rows - 1);
+        const double log2_sum = logs.log2_of(s_all.sum[r]);
+        const double base = (double)s_all.score[r] - (s_all.ended[r] == -1 ? norm_of(s_all.top[r], s_all.e[r], log2_sum) : 0.0);
+        if (r0 + lane < rows) s_all.base[r] = base;
+    }
+    __syncthreads();
+    for (int c = tid; c < rows * n_out; c += (int)blockDim.x) {
+        const int r = c / n_out;
+        if (c - r * n_out >= s_all.counts[r]) continue;
+        const int ended = s_all.ended[r];
+        const uint64_t key = (uint64_t)lists.order[c];
+        const double total = ended >= 0 ? s_all.base[r] : (double)key_value(key) + s_all.base[r];
+        lists.order[c] = ordered(p.weights ? total * (double)s_all.weight[r] : total);
+        lists.total[c] = (float)total;
+        lists.token[c] = ended >= 0 ? ended : (int32_t)key_place(key);
+    }
+    __syncthreads();
+    const int64_t to = (int64_t)b * n_out;
+    if (rows) place_all(p, lists, s_all.counts, s_places, reinterpret_cast<Placed*>(behind), first, rows, 0, 1, to);
+    fill_rest(p, s_all.counts, rows, to);
 }
 
 // What the sizes give: chunks, groups and parts of a row.  A warp takes two chunks of 16-bit values where there are many (320 rows of
@@ -618,21 +1044,53 @@ bool select_shape(int n_rows, int vocab, int n_seqs, int n_out) {
     return n_rows <= 65535 && vocab <= (1 << 30) && n_seqs <= kMaxSeqs && n_out <= kMaxOut;
 }
 
+// A warp per row (beam_rows_kernel) or a block per row (beam_pick_kernel)?  bf16, beams of 8 (of 4 where there is one request), n_out 8
+// (4), us; a row read as a whole / a warp per row after the scan / a block per row after it:
+//   rows    vocab 1000       vocab 4096       vocab 8000           vocab 32000          vocab 106304
+//   4       4.5 /  - / 6.9   7.3 /  - / 8.0   10.5 / 8.0 / 7.2     27.4 / 8.4 / 7.1
+//   304     5.5 /  - / 8.0   9.1 /  - / 8.6   13.3 / 14.9 / 12.7   34.4 / 17.8 / 10.9     - / 27.4 / 19.0
+//   608     5.7 /  - / 14.1  9.2 /  - / 14.7  13.4 / 15.7 / 20.4   43.6 / 22.2 / 21.4     - / 37.3 / 34.6
+//   2048    7.2 /  - / 39.0  13.4 / - / 39.9  21.1 / 20.6 / 52.1   71.3 / 36.6 / 60.1     - / 81.6 / 102.6
+// Of 32 continuations 1024 rows, 16 of each request, 15 / - / 33 at 4096, 59 / 39 / 57 at 32000; of 64 (32 rows of each) a block is faster
+// from 2048 values on: 36 us for 41 at 4096, 103 for 152 at 106304.
+constexpr int kSmallVocab = 2048;    // rows of no more are read as a whole,
+constexpr int kMediumVocab = 10240;  // and of no more where there are more than kSomeRows of them
+constexpr int kSomeRows = 152 * 2, kManyRows = 152 * 5;
+constexpr int kFewOut = 32;
 template <typename T, bool VEC>
 int launch_select(const SelectParams& p, cudaStream_t s) {
+    auto rows_kernel = [&](auto kernel, SmemOptIn& opt) {
+        int warps = 1;  // a row each, by the mean of the requests' rows
+        while (warps < kRowWarps && (int64_t)warps * p.n_seqs < p.n_rows) warps *= 2;
+        const int opted = opt.ensure(kernel, lists_bytes(1, kMaxOut) + placed_bytes(kMaxOut) + kRowWarps * (int)sizeof(RowSearch));
+        if (opted != KVQ8_OK) return opted;
+        return launch_dependent(kernel, (unsigned)p.n_seqs, 32u * (unsigned)warps,
+                                lists_bytes(1, p.n_out) + placed_bytes(p.n_out) + warps * (int)sizeof(RowSearch), s, p);
+    };
+    const bool few_out = p.n_out <= kFewOut, few_groups = 4 * p.n_groups < 5 * p.n_out;
+    if (p.vocab <= kSmallVocab || (few_out && (p.vocab <= kMediumVocab ? p.n_rows > kSomeRows : p.n_rows > kManyRows && few_groups))) {
+        static SmemOptIn opt;
+        return rows_kernel(beam_rows_kernel<T, VEC, false>, opt);
+    }
     const dim3 grid((unsigned)(p.n_parts / kScanWarps), (unsigned)p.n_rows);
     const int rc = launch_dependent(beam_scan_kernel<T, VEC>, grid, kScanThreads, 0, s, p);
     if (rc != KVQ8_OK) return rc;
-    // a block a row, by the mean of the requests' rows
+    if (p.n_rows > kManyRows && few_out) {
+        static SmemOptIn opt;
+        return rows_kernel(beam_rows_kernel<T, VEC, true>, opt);
+    }
+    // A block a row, by the mean of the requests' rows.  Clusters of 16 where the GPU holds all of them at once: 12 requests of 32 beams, 64
+    // of each, over 106304 bf16 logits 48.2 us (of 8: 72.8); 24 of 16 beams 39.3 us (of 8: 35.1).
     int cluster = 1;
     while (cluster < 8 && (int64_t)cluster * p.n_seqs < p.n_rows) cluster *= 2;
+    if ((int64_t)p.n_seqs * 8 < p.n_rows && p.n_seqs * 16 <= kSomeRows) cluster = 16;
     static SmemOptIn opt;
-    const int opted = opt.ensure(beam_pick_kernel<T, VEC>, lists_bytes(1, kMaxOut));
+    const int opted = opt.ensure(beam_pick_kernel<T, VEC>, lists_bytes(1, kMaxOut) + placed_bytes(kMaxOut), true);
     if (opted != KVQ8_OK) return opted;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.n_seqs * cluster));
     cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = (size_t)lists_bytes(cluster, p.n_out);
+    cfg.dynamicSmemBytes = (size_t)(lists_bytes(cluster, p.n_out) + placed_bytes(p.n_out));
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -27,12 +27,14 @@ struct SmemOptIn {
     std::mutex mu;
     bool done[kMaxDev] = {};
     template <typename Kernel>
-    int ensure(Kernel* kernel, int bytes) {
+    int ensure(Kernel* kernel, int bytes, bool clusters_of_16 = false) {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return KVQ8_ERR_CUDA;
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev]) {
             if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+                return KVQ8_ERR_CUDA;
+            if (clusters_of_16 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
                 return KVQ8_ERR_CUDA;
             done[dev] = true;
         }

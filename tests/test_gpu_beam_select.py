@@ -206,3 +206,58 @@ def test_calls_that_overlap_on_two_streams(lib):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, one))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("vocab,n_out", [(1001, 16), (2500, 16), (9000, 12), (10240, 16), (10250, 16), (15000, 32), (25001, 32), (32501, 1), (32504, 9)])
+def test_many_rows(lib, dtype, vocab, n_out):
+    """Rows of every kind by the hundreds: normal, of few levels, of one, masked by -inf and by the type's lowest value, NaN, +inf, -inf
+    alone, at their end; requests of no rows and of 65."""
+    from speculative_verify_attention_gb300 import beam_select as lib_select
+    rng = np.random.default_rng(vocab + n_out)
+    beams = [8] * 60 + [0, 65, 1, 33] + list(rng.integers(0, 12, 60))
+    starts = starts_of(beams)
+    n = int(starts[-1])
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(vocab)
+    x = torch.randn((n, vocab), generator=gen, device="cuda").mul_(3.0)
+    low = torch.finfo(dtype).min
+    x[1::9] = x[1::9].round()
+    x[2::27] = 1.0
+    x[3::27, 40:] = low
+    x[4::27, :vocab - 5] = -float("inf")
+    x[5::27, vocab // 2] = float("nan")
+    x[6::27, vocab - 1] = float("inf")
+    x[7::27] = -float("inf")
+    x[8::27] = x[9::27][:len(x[8::27])].round().clamp_(min=0) if len(x[9::27]) == len(x[8::27]) else 0.0
+    x = x.to(dtype)
+    scores, weights = (-20 - 3 * rng.random(n)).astype(np.float32), (0.5 + rng.random(n)).astype(np.float32)
+    ended = np.where(rng.random(n) < 0.1, 2, -1)
+    host = x.float().cpu().numpy()
+    for more in ((scores, weights, ended), (None, None, None)):
+        got = lib_select(x, i32(starts), n_out, scores=_f32(more[0]), weights=_f32(more[1]), ended=None if more[2] is None else i32(ended))
+        assert torch.all(got[0][61] == -1) and torch.all(got[1][61] == -1) and torch.all(got[2][61] == -float("inf"))    # of 65 rows
+        check_selection(host, starts[:62], n_out, [t[:61] for t in got], *more)
+        check_selection(host, starts[62:], n_out, [t[62:] for t in got], *more)
+
+
+def test_many_rows_of_requests_of_one(lib):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(4)
+    for vocab in (3, 1000, 4096, 12345):
+        x = torch.randn((1000, vocab), generator=gen, device="cuda").bfloat16()
+        _run(x, list(range(1001)), 16)
+
+
+@pytest.mark.parametrize("vocab,n_out", [(2049, 64), (20003, 64), (41000, 33), (98000, 64), (700, 64)])
+def test_requests_of_many_beams(lib, vocab, n_out):
+    """Vocabularies of fewer groups than continuations, and of a few more; equal totals across rows."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(vocab)
+    beams = [64, 32, 17, 1, 40]
+    x = torch.randn((sum(beams), vocab), generator=gen, device="cuda").mul_(3.0)
+    x[70:80] = x[70]
+    scores = -torch.rand(sum(beams), generator=gen, device="cuda").cpu().numpy()
+    scores[70:80] = scores[70]
+    for dtype in (F32, BF16):
+        _run(x.to(dtype), starts_of(beams), n_out, scores=scores)
