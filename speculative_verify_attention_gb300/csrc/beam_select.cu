@@ -1131,6 +1131,13 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t logits_stride,
     for (const void* q : {(const void*)row_starts, (const void*)scores, (const void*)weights, (const void*)ended,
                           (const void*)parents, (const void*)tokens, (const void*)totals})
         if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
+    // (a request's outputs are written while others' inputs are still read)
+    for (const void* out : {(const void*)parents, (const void*)tokens, (const void*)totals}) {
+        const size_t bytes = (size_t)n_seqs * n_out * 4;
+        if (ranges_meet(out, bytes, row_starts, ((size_t)n_seqs + 1) * 4)) return KVQ8_ERR_INVALID_ARG;
+        for (const void* in : {(const void*)scores, (const void*)weights, (const void*)ended})
+            if (in && ranges_meet(out, bytes, in, (size_t)n_rows * 4)) return KVQ8_ERR_INVALID_ARG;
+    }
     SelectParams p = {};
     p.logits = logits, p.stride = logits_stride, p.row_starts = row_starts, p.scores = scores, p.weights = weights;
     p.ended = ended, p.parents = parents, p.tokens = tokens, p.totals = totals;

@@ -36,6 +36,13 @@ def test_select(but, status):
     assert _call("beam_select", SELECT, but) == status
 
 
+@pytest.mark.parametrize("name", ["parents", "tokens", "totals"])
+@pytest.mark.parametrize("over,at", [("row_starts", 8), ("scores", 0), ("scores", -36), ("scores", 12), ("weights", 12), ("ended", -36)])
+def test_select_writes_over_nothing_that_it_reads(name, over, at):
+    apart = dict(SELECT, row_starts=2 * A, scores=3 * A, weights=4 * A, ended=5 * A, parents=6 * A, tokens=7 * A, totals=8 * A)
+    assert _call("beam_select", apart, {name: apart[over] + at}) == INVALID
+
+
 def test_workspaces_are_asked_for_as_the_calls_want_them():
     lib = load_library()
     need = lib.beam_select_workspace_bytes(4, 1000, 2, 5)
