@@ -246,3 +246,23 @@ def test_a_captured_fork_replays_on_new_parents(lib):
         want = fork_pages(p.tolist(), lens, held, page, table, shares, ring, state, old)
         for a, w in zip((new, rest[0], rest[1], so, t[4], ro, rest[2], rest[3], rest[4], status), want):
             assert np.array_equal(a.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1))
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 5, 1000, 1001, 1002, 1003, 20001])
+@pytest.mark.parametrize("first", [1, 2, 3])
+def test_counts_that_start_anywhere(lib, vocab, first):
+    """Rows at every distance from 16 bytes to rows at every other; values beside the counts stay."""
+    from speculative_verify_attention_gb300 import token_counts_fork
+    rng = np.random.default_rng(vocab + first)
+    states = 19
+    whole = rng.integers(-2 ** 31, 2 ** 31, states * vocab + 8).astype(np.int32)
+    on = torch.from_numpy(whole).cuda()
+    counts = on[first:first + states * vocab].view(states, vocab)
+    assert counts.data_ptr() % 16 == 4 * first
+    parents, state_of = rng.integers(0, 9, 17), rng.permutation(states)[:9]
+    out, status = i32(np.full(17, -7)), i32([-1])
+    token_counts_fork(i32(parents), i32(state_of), counts, out, status, n_seqs=9)
+    want = fork_counts(list(parents), list(state_of), whole[first:first + states * vocab].reshape(states, vocab))
+    assert int(status) == want[2] == 0 and np.array_equal(out.cpu().numpy(), want[0])
+    whole[first:first + states * vocab] = want[1].reshape(-1)
+    assert np.array_equal(on.cpu().numpy(), whole)
