@@ -13,7 +13,9 @@
 // (the block quantiser of kvq8_paged_append), without a rounding in between.
 // Bound: bytes and issue slots together.  16401 tokens of 32q/8kv/hd128 bf16 (372 MB) 65 us, 5.7 TB/s, 84 % of a copy's rate, 63 % of
 // the issue slots; 2051 of 24q/4kv/hd256 fp32 (122 MB) 22 us; 32 tokens 3.6 us.  With the next head alone ahead, in registers, 76 and
-// 26.5 us; with more blocks an SM (and spills) 74; two or six heads ahead instead of four 66.
+// 26.5 us; with more blocks an SM (and spills) 74; two or six heads ahead instead of four 66.  Few heads leave some of eight warps idle
+// between two barriers, so a block may take two groups of tokens, four warps each: 18788 tokens of 8q/2kv/hd128 bf16 25 us (33 with one),
+// 8000 of 12q/1kv/hd256 24.5 (27.6); 16401 of 32q/8kv 72 with two, 67 with one.
 #include "paged.cuh"
 #include "q8_0.cuh"
 
@@ -133,30 +135,30 @@ struct Turns<true> {
     }
 };
 
-// Block (every gridDim.x-th group of two or four tokens, a share of the heads): the lanes of a warp are the items of its tokens' rows, its
-// heads every eighth of the block's, queries, then keys, then values.  An item is eight values and the eight that lie `far` behind
+// Block (every gridDim.x-th group of two or four tokens, or of twice as many, half of the warps each; a share of the heads): the lanes of a warp are the items of its tokens' rows, its
+// heads every eighth (or fourth) of the block's, queries, then keys, then values.  An item is eight values and the eight that lie `far` behind
 // them: in the rotated part of a row the same places of its two halves, then of the two halves of the part behind it; both parts are
 // multiples of 64, so four neighbouring lanes have a 32-value block in each.  A lane's eight of a block are consecutive (16 bytes); of
 // fp32 they are its fourth of the block's first half and of the second, as four lanes' pieces have to fill whole 32-byte sectors.
-template <typename T, int HD, bool PAIRS>
+template <typename T, int HD, bool PAIRS, int SUBS>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) paged_rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int kItems = HD / 16, kTokens = 32 / kItems, kPieces = (int)sizeof(T) / 2, kDepth = kRopeDepth<T>;  // 16-byte pieces of eight values
+    constexpr int kItems = HD / 16, kTokens = 32 / kItems, kAll = kTokens * SUBS, kWarps = kRopeWarps / SUBS, kPieces = (int)sizeof(T) / 2, kDepth = kRopeDepth<T>;  // 16-byte pieces of eight values
     extern __shared__ __align__(16) uint4 s_ring[];               // [kDepth][2 kPieces][threads]
-    __shared__ __align__(16) float2 s_turns[2][kTokens * HD / 2];  // [tokens][rot / 2], of this group and the next
-    const int tid = threadIdx.x, lane = tid & 31, j = lane % kItems, mine = lane / kItems;
-    const int rot_items = p.rot / 16, half = p.rot / 2, stride = (int)gridDim.x * kTokens;
+    __shared__ __align__(16) float2 s_turns[2][kAll * HD / 2];  // [tokens][rot / 2], of this group and the next
+    const int tid = threadIdx.x, lane = tid & 31, j = lane % kItems, mine = (tid >> 5) / kWarps * kTokens + lane / kItems;
+    const int rot_items = p.rot / 16, half = p.rot / 2, stride = (int)gridDim.x * kAll;
     constexpr bool kWide = sizeof(T) == 4;
     constexpr int kApart = kWide ? 16 : 4;  // between a lane's first four values and its next
     const int g = j < rot_items ? j : rot_items + j, far = j < rot_items ? half : (HD - p.rot) / 2;
     const int at = kWide ? (g >> 2) * 32 + (g & 3) * 4 : g * 8;
     const bool turned = j < rot_items;
     // this warp's heads: of the queries, then of the keys, then of the values
-    const int step = kRopeWarps * (int)gridDim.y, warp = (int)blockIdx.y * kRopeWarps + (tid >> 5);
+    const int step = kWarps * (int)gridDim.y, warp = (int)blockIdx.y * kWarps + (tid >> 5) % kWarps;
     const int all = p.n_q_heads + 2 * p.n_kv_heads, v_first = p.n_q_heads + p.n_kv_heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t ring = smem_u32(s_ring + tid);
-    int ahead_tok = (int)blockIdx.x * kTokens + mine, ahead = warp, ahead_place = 0;
+    int ahead_tok = (int)blockIdx.x * kAll + mine, ahead = warp, ahead_place = 0;
     auto fetch = [&] {
         if (ahead_tok < p.n_tok && ahead < all) {
             const T* x = ahead < p.n_q_heads ? static_cast<const T*>(p.q) + (int64_t)ahead_tok * p.q_stride + ahead * HD
@@ -185,18 +187,24 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) paged_rope_kerne
         frequency = __ldg(p.turns + pair);
         if (axis >= 0 && axis < p.n_axes) positions = p.positions + (int64_t)axis * p.n_tok;
     }
-    int32_t next_pos = 0;
+    int32_t next_pos[SUBS];
     int64_t next_slot = -1;
     auto indexes = [&](int tok0) {
-        next_pos = positions && tok0 + pair_tok < p.n_tok ? __ldg(positions + tok0 + pair_tok) : 0;
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u) {
+            const int tok = tok0 + u * kTokens + pair_tok;
+            next_pos[u] = positions && tok < p.n_tok ? __ldg(positions + tok) : 0;
+        }
         next_slot = tok0 + mine < p.n_tok ? __ldg(p.slots + tok0 + mine) : -1;
     };
-    indexes((int)blockIdx.x * kTokens);
+    indexes((int)blockIdx.x * kAll);
     int buffer = 0, place = 0;
-    for (int tok0 = (int)blockIdx.x * kTokens; tok0 < p.n_tok; tok0 += stride, buffer ^= 1) {
+    for (int tok0 = (int)blockIdx.x * kAll; tok0 < p.n_tok; tok0 += stride, buffer ^= 1) {
         const int64_t slot = next_slot;
         const bool there = slot >= 0 && slot < p.n_slots;
-        if (pair < half) s_turns[buffer][pair_tok * half + pair] = cos_sin((uint64_t)(int64_t)next_pos * frequency);
+#pragma unroll
+        for (int u = 0; u < SUBS; ++u)
+            if (pair < half) s_turns[buffer][(u * kTokens + pair_tok) * half + pair] = cos_sin((uint64_t)(int64_t)next_pos[u] * frequency);
         if (tok0 + stride < p.n_tok) indexes(tok0 + stride);
         __syncthreads();  // (the other buffer's readers have passed the barrier before)
         Turns<PAIRS> turns;
@@ -249,25 +257,36 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) paged_rope_kerne
     cp_async_wait<0>();
 }
 
-template <typename T, int HD>
-int launch_rope(const RopeParams& p, bool pairs, cudaStream_t s) {
-    constexpr int kTokens = 32 / (HD / 16);
+template <typename T, int HD, bool PAIRS, int SUBS>
+int launch_rope(const RopeParams& p, cudaStream_t s) {
+    constexpr int kTokens = 32 / (HD / 16) * SUBS, kWarps = kRopeWarps / SUBS;
     const int64_t groups = ((int64_t)p.n_tok + kTokens - 1) / kTokens, full = 152 * kRopeBlocks<T>;
     // as many blocks as the GPU holds; few tokens: their heads over more blocks, a head a warp at last
-    const int64_t most = (p.n_q_heads + 2 * p.n_kv_heads + kRopeWarps - 1) / kRopeWarps, share = full / groups;
+    const int64_t most = (p.n_q_heads + 2 * p.n_kv_heads + kWarps - 1) / kWarps, share = full / groups;
     const unsigned gy = (unsigned)(share < 1 ? 1 : share < most ? share : most);
     const unsigned gx = (unsigned)(groups < full ? groups : full);
     constexpr int smem = kRopeDepth<T> * (int)sizeof(T) * kRopeThreads * 16;
-    static SmemOptIn opt[2];
-    const int rc = pairs ? opt[1].ensure(paged_rope_kernel<T, HD, true>, smem) : opt[0].ensure(paged_rope_kernel<T, HD, false>, smem);
+    static SmemOptIn opt;
+    const int rc = opt.ensure(paged_rope_kernel<T, HD, PAIRS, SUBS>, smem);
     if (rc != KVQ8_OK) return rc;
-    const dim3 grid(gx, gy);
-    if (pairs) return launch_dependent(paged_rope_kernel<T, HD, true>, grid, kRopeThreads, smem, s, p);
-    return launch_dependent(paged_rope_kernel<T, HD, false>, grid, kRopeThreads, smem, s, p);
+    return launch_dependent(paged_rope_kernel<T, HD, PAIRS, SUBS>, dim3(gx, gy), kRopeThreads, smem, s, p);
+}
+template <typename T, int HD, bool PAIRS>
+int launch_rope(const RopeParams& p, cudaStream_t s) {
+    constexpr int kTokens = 32 / (HD / 16);
+    const int64_t full = 152 * kRopeBlocks<T>;
+    // A block's heads, a head a warp at a time, and half as much again for the sines and the barrier, as often as the blocks come round.
+    auto rounds = [&](int subs) {
+        const int64_t groups = (p.n_tok + kTokens * subs - 1) / (kTokens * subs), warps = kRopeWarps / subs;
+        return (groups + full - 1) / full * (2 * ((p.n_q_heads + 2 * p.n_kv_heads + warps - 1) / warps) + 3);
+    };
+    return p.n_tok > full * kTokens && rounds(2) < rounds(1) ? launch_rope<T, HD, PAIRS, 2>(p, s)
+                                                             : launch_rope<T, HD, PAIRS, 1>(p, s);
 }
 template <typename T>
 int launch_rope(const RopeParams& p, int head_dim, bool pairs, cudaStream_t s) {
-    return head_dim == 128 ? launch_rope<T, 128>(p, pairs, s) : launch_rope<T, 256>(p, pairs, s);
+    if (head_dim == 128) return pairs ? launch_rope<T, 128, true>(p, s) : launch_rope<T, 128, false>(p, s);
+    return pairs ? launch_rope<T, 256, true>(p, s) : launch_rope<T, 256, false>(p, s);
 }
 
 }  // namespace

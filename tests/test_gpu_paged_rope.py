@@ -199,3 +199,12 @@ def test_a_captured_call_and_another_stream(lib):
         other = kvq8_paged_append_rope(*x, cache, slots, pos, turns, stream=stream)
         side.synchronize()
         assert torch.equal(other, out) and torch.equal(cache.k_codes, codes)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("n,hq,hkv,hd,rot", [(1901, 8, 2, 128, 64), (1999, 1, 1, 128, 128), (1001, 12, 1, 256, 192), (923, 2, 1, 256, 256)])
+def test_many_tokens_of_few_heads(lib, dtype, pairs, n, hq, hkv, hd, rot):
+    """Blocks that take two groups of tokens, and come round with a part of one."""
+    _case(n, n, hq, hkv, hd, dtype, rot, pairs, axes=2, axis_of=np.arange(rot // 2) % 2, skip=True)
+    _case(n + 1, n + 6, hq, hkv, hd, dtype, rot, pairs, far=10 ** 6, in_place=True, fused=True)
