@@ -101,34 +101,38 @@ constexpr uint32_t kLowestWord<__nv_bfloat16> = 0xff80ff80u;
 // How a warp reads 256 consecutive values of a row, eight a lane, -inf outside the row.
 //   VEC: eight consecutive ones a load; the row starts on their size and holds whole groups of them.
 //   Rows of odd length in 16 bits: the two 16-byte pieces around a lane's eight, and where among those they start (`shift`, of the row
-//     alone) comes to a funnel shift a word; 320 rows of 106299 bf16 values 24.9 us (by selections 26; 106304 values 20.7).
-//   Of fp32: a value a load, neighbours to neighbouring lanes (100 rows of 106299: 13.9 us; by three pieces and selections 17.6).
-template <typename T, bool VEC>
+//     alone) comes to a funnel shift a word; 320 rows of 106299 bf16 values 22.6 us (by selections 26; 106304 values 20.7).
+//   SPREAD, of fp32 and where rows are read as wholes: a value a load, neighbours to neighbouring lanes (100 fp32 rows of 106299: 13.9 us;
+//     by three pieces and selections 17.6.  4000 bf16 rows of 1001 as wholes: 11.6; by pieces 16.9; 2048 of 8001 27.4; by pieces 24.5).
+template <typename T, bool VEC, bool SPREAD = sizeof(T) == 4 && !VEC>
 struct Tile {
-    static constexpr bool kSpread = sizeof(T) == 4 && !VEC;
+    static constexpr bool kSpread = SPREAD;
     // the place of value e of a lane, in the 256 from `at` on
     static __device__ __forceinline__ int place(int at, int lane, int e) { return kSpread ? at + e * 32 + lane : at + lane * 8 + e; }
 
-    // 16 bits, odd: pieces of eight values
+    // 16 bits, odd: pieces of eight values, each from its own size's boundary on
+    static __device__ __forceinline__ bool whole(int from, int vocab) { return from >= 0 && from + 8 <= vocab; }
     static __device__ __forceinline__ void pieces(uint32_t (&w)[8], const T* row, int from, int vocab) {
 #pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint4 r = make_uint4(kLowestWord<T>, kLowestWord<T>, kLowestWord<T>, kLowestWord<T>);
+            if (whole(from + 8 * k, vocab)) r = __ldg(reinterpret_cast<const uint4*>(row + from + 8 * k));
+            w[4 * k] = r.x, w[4 * k + 1] = r.y, w[4 * k + 2] = r.z, w[4 * k + 3] = r.w;
+        }
+    }
+    // the row's first and last piece
+    static __device__ __forceinline__ void ends(uint32_t (&w)[8], const T* row, int from, int vocab) {
+#pragma unroll
         for (int k = 0; k < 2; ++k, from += 8) {
-            if (from >= 0 && from + 8 <= vocab) {
-                const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + from));
-                w[4 * k] = r.x, w[4 * k + 1] = r.y, w[4 * k + 2] = r.z, w[4 * k + 3] = r.w;
-            } else {  // the row's first and last piece
+            if (from <= -8 || from >= vocab || whole(from, vocab)) continue;
+            uint32_t v[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[4 * k + i] = kLowestWord<T>;
-                if (from > -8 && from < vocab) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (from + i >= 0 && from + i < vocab) {
-                            const uint32_t bits = *reinterpret_cast<const uint16_t*>(row + from + i);
-                            uint32_t& to = w[4 * k + i / 2];
-                            to = i & 1 ? (to & 0xffffu) | bits << 16 : (to & 0xffff0000u) | bits;
-                        }
-                }
+            for (int i = 0; i < 8; ++i) {
+                v[i] = kLowestWord<T> & 0xffffu;
+                if (from + i >= 0 && from + i < vocab) v[i] = *reinterpret_cast<const uint16_t*>(row + from + i);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 * k + i] = v[2 * i] | v[2 * i + 1] << 16;
         }
     }
     // N times 256 values, from at[u] on
@@ -140,7 +144,7 @@ struct Tile {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int i = place(at[u], lane, e);
-                    x[u].put(e, i < vocab ? __ldg(row + i) : -INFINITY);
+                    x[u].put(e, i < vocab ? __ldg(row + i) : static_cast<T>(-INFINITY));
                 }
         } else if constexpr (VEC) {
 #pragma unroll
@@ -158,6 +162,8 @@ struct Tile {
             uint32_t w[N][8];
 #pragma unroll
             for (int u = 0; u < N; ++u) pieces(w[u], row, at[u] + lane * 8 - shift, vocab);
+#pragma unroll
+            for (int u = 0; u < N; ++u) ends(w[u], row, at[u] + lane * 8 - shift, vocab);
             auto take = [&](auto words) {  // one branch for all, as the shift is the warp's
 #pragma unroll
                 for (int u = 0; u < N; ++u)
@@ -822,6 +828,7 @@ __device__ __noinline__ int search_slowly(RowSearch& s, const T* x, int vocab, f
 template <typename T, bool VEC, bool SCANNED>
 __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_constant__ SelectParams p) {
     constexpr int kPerGroup = kGroup<T> / 256;
+    using Rows = Tile<T, VEC, !VEC && (sizeof(T) == 4 || !SCANNED)>;
     extern __shared__ __align__(16) unsigned char s_lists[];
     __shared__ RowBlock s_all;
     __shared__ PlaceBounds s_places;
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
             int at[kLoads];
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) at[u] = chunk * kChunk + u * 256;
-            Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
+            Rows::load(v8, x, at, p.vocab, lane);
         };
         const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
         int ended = p.ended ? __ldg(p.ended + row) : -1;
@@ -949,7 +956,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
                     else
                         at[u] = i * 256;
                 }
-                if (SCANNED || p.n_chunks > 1) Tile<T, VEC>::load(v8, x, at, p.vocab, lane);
+                if (SCANNED || p.n_chunks > 1) Rows::load(v8, x, at, p.vocab, lane);
                 uint32_t hit = 0;
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
@@ -964,7 +971,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
                     int from = at[0];
 #pragma unroll
                     for (int u = 1; u < kLoads; ++u) from = i >= u * 8 ? at[u] : from;
-                    if (place < kRowList) s.place[place] = (uint32_t)Tile<T, VEC>::place(from, lane, i & 7);
+                    if (place < kRowList) s.place[place] = (uint32_t)Rows::place(from, lane, i & 7);
                 }
             }
             __syncwarp();
