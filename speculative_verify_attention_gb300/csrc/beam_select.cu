@@ -103,7 +103,7 @@ constexpr uint32_t kLowestWord<__nv_bfloat16> = 0xff80ff80u;
 //   Rows of odd length in 16 bits: the two 16-byte pieces around a lane's eight, and where among those they start (`shift`, of the row
 //     alone) comes to a funnel shift a word; 320 rows of 106299 bf16 values 22.6 us (by selections 26; 106304 values 20.7).
 //   SPREAD, of fp32 and where rows are read as wholes: a value a load, neighbours to neighbouring lanes (100 fp32 rows of 106299: 13.9 us;
-//     by three pieces and selections 17.6.  4000 bf16 rows of 1001 as wholes: 11.6; by pieces 16.9; 2048 of 8001 27.4; by pieces 24.5).
+//     by three pieces and selections 17.6.  4000 bf16 rows of 1001 as wholes 11.8 us, by pieces 16.9).
 template <typename T, bool VEC, bool SPREAD = sizeof(T) == 4 && !VEC>
 struct Tile {
     static constexpr bool kSpread = SPREAD;
@@ -753,23 +753,32 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
     }
 }
 
-// A block per request and a warp per row; what needs 64-bit arithmetic is done for all rows together, a thread each.
+// A block per request and a warp per row.  64-bit arithmetic is slow: behind the scan, where the rows of a block come to it at once, it is
+// done for all of them together, a thread each (912 rows of 32000 24.4 us, a warp each 28.7); rows that are read as wholes do it by
+// themselves (2048 rows of 8000 15.9 us, together 18.6).
 //   SCANNED: after beam_scan_kernel, where there are so many rows that blocks for each would queue.
 //   Else in one launch, for small vocabularies: the row is read (and a second time from L1, if it is more than the lanes hold at once).
 // The bound is the n_out-th best of 32, 64 or 128 shares, which the lanes have of the groups or of the row.
-// 4000 rows of 1000 bf16 values, 16 of each 250 requests: 10.5 us in one launch (304 by beam_pick_kernel); one row 4.0 (25.7).  2048 rows
-// of 32000, 8 of each 256: 36.6 (60.1).
+// 4000 rows of 1000 bf16 values, 16 of each 250 requests: 11.3 us in one launch (304 by beam_pick_kernel); one row 3.6 (25.7).  2048 rows
+// of 32000, 8 of each 256: 35.8 (60.1).
 constexpr int kRowWarps = 16;
 constexpr int kRowList = 384;   // candidates of a row
+template <bool SCANNED>
 struct alignas(16) RowSearch {  // (read 16 bytes at a time)
-    uint64_t key[kRowList];
+    uint64_t key[kRowList];     // first the candidates' places, in its second half
     uint64_t best[kMaxOut];
     int32_t share[128];
-    uint32_t place[kRowList];
+    int n, pad[3];              // candidates
+    uint32_t group[SCANNED ? kRowList : 4];
 };
-static_assert(sizeof(RowSearch) % 16 == 0 && offsetof(RowSearch, share) % 16 == 0 && offsetof(Search, top) % 16 == 0);
+static_assert(sizeof(RowSearch<true>) % 16 == 0 && offsetof(RowSearch<true>, share) % 16 == 0 && offsetof(Search, top) % 16 == 0);
 static_assert(kRowList >= kMaxOut + 256);
+template <bool SCANNED>
 struct RowBlock {
+    int counts[kMaxWindowRows];
+};
+template <>
+struct RowBlock<true> {
     unsigned long long sum[kMaxWindowRows];  // of exponentials, in units of 2^-32
     double base[kMaxWindowRows];
     float top[kMaxWindowRows], e[kMaxWindowRows], score[kMaxWindowRows], weight[kMaxWindowRows];
@@ -778,7 +787,8 @@ struct RowBlock {
 };
 
 // The best n_out of a warp's n keys, in order.
-__device__ __forceinline__ void rank_row(RowSearch& s, int n, int n_out, int lane) {
+template <typename S>
+__device__ __forceinline__ void rank_row(S& s, int n, int n_out, int lane) {
     for (int i = lane; i < n; i += 32) {
         const uint64_t key = s.key[i];
         int rank = 0;
@@ -790,8 +800,8 @@ __device__ __forceinline__ void rank_row(RowSearch& s, int n, int n_out, int lan
 
 // A row of which more values reach `least` than the list holds (many equal ones): those above the list's worst, a full list cut back to
 // its best n_out.
-template <typename T>
-__device__ __noinline__ int search_slowly(RowSearch& s, const T* x, int vocab, float least, int n_out, int lane) {
+template <typename S, typename T>
+__device__ __noinline__ int search_slowly(S& s, const T* x, int vocab, float least, int n_out, int lane) {
     int n = 0;
     uint64_t above = 0;
     auto cut = [&] {
@@ -830,7 +840,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
     constexpr int kPerGroup = kGroup<T> / 256;
     using Rows = Tile<T, VEC, !VEC && (sizeof(T) == 4 || !SCANNED)>;
     extern __shared__ __align__(16) unsigned char s_lists[];
-    __shared__ RowBlock s_all;
+    __shared__ RowBlock<SCANNED> s_all;
     __shared__ PlaceBounds s_places;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5, b = blockIdx.x, n_out = p.n_out;
     const LogTable logs(lane);
@@ -839,10 +849,17 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Lists lists(s_lists, kMaxWindowRows, n_out);
     unsigned char* behind = s_lists + lists_bytes(1, n_out);
-    RowSearch& s = reinterpret_cast<RowSearch*>(behind + placed_bytes(n_out))[warp];
+    RowSearch<SCANNED>& s = reinterpret_cast<RowSearch<SCANNED>*>(behind + placed_bytes(n_out))[warp];
     int first, rows;
     if (!rows_of(p, b, first, rows)) rows = 0;
     const int32_t lowest = ordered(-INFINITY);
+    // one continuation: of a row at its end itself, else by its key
+    auto list = [&](int at, uint64_t key, int ended, double base, float weight) {
+        const double total = ended >= 0 ? base : (double)key_value(key) + base;
+        lists.order[at] = ordered(p.weights ? total * (double)weight : total);
+        lists.total[at] = (float)total;
+        lists.token[at] = ended >= 0 ? ended : (int32_t)key_place(key);
+    };
     for (int mine = warp; mine < rows; mine += warps) {
         const int row = first + mine;
         const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
@@ -860,6 +877,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
         float top = 0.0f, e = 0.0f;
         unsigned long long sum = 0;
         int count = ended >= 0;
+        double base = (double)score;
         if (ended == -1) {
             const float* gm = p.group_max + (int64_t)row * p.n_groups;
             int32_t most[4] = {lowest, lowest, lowest, lowest};
@@ -889,9 +907,11 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
                 bad = !(part.s < INFINITY);
                 sum = bad ? 0 : __float2ull_rn(part.s * 0x1p32f);  // exact: part.s is 0, or about 0.7 at least
             }
+            if (!SCANNED) base -= norm_of(top, e, logs.log2_of(sum));
             int32_t reach = 0x7fffffff;
             auto rank = [&](auto n) {  // n shares a lane
                 __syncwarp();
+                if (lane == 0) s.n = 0;
 #pragma unroll
                 for (int u = 0; u < n.value; ++u) s.share[u * 32 + lane] = most[u];
                 __syncwarp();
@@ -919,22 +939,11 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
             }
             const int32_t bound = max(__reduce_min_sync(0xffffffffu, reach), lowest + 1);
             const float least = from_ordered(bound);
-            int n = 0;
-            // lanes with `here` more entries each: where a lane's begin
-            auto begin = [&](int here) {
-                int upto = here;
-#pragma unroll
-                for (int o = 1; o < 32; o *= 2) {
-                    const int below = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += below;
-                }
-                const int at = n + upto - here;
-                n += __shfl_sync(0xffffffffu, upto, 31);
-                return at;
-            };
-            uint32_t* groups = reinterpret_cast<uint32_t*>(s.key);
+            uint32_t* groups = s.group;
+            uint32_t* places = reinterpret_cast<uint32_t*>(s.key) + kRowList;
             int tiles = p.n_chunks * kLoads;
             if (SCANNED) {
+                int n = 0;
                 for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
                     const bool hit = g0 + lane < p.n_groups && ordered(__ldg(gm + g0 + lane)) >= bound;
                     const uint32_t who = __ballot_sync(0xffffffffu, hit);
@@ -944,7 +953,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
                 }
                 __syncwarp();
                 tiles = n <= kRowList ? n * kPerGroup : 0;
-                n = n <= kRowList ? 0 : kRowList + 1;
+                if (n > kRowList && lane == 0) s.n = n;
             }
             for (int t = 0; t < tiles; t += kLoads) {
                 int at[kLoads];
@@ -960,65 +969,73 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
                 uint32_t hit = 0;
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
+                    if (!(largest(v8[u]) >= least)) continue;
                     float v[8];
                     v8[u].floats(v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) hit |= (v[i] >= least ? 1u : 0u) << (u * 8 + i);
                 }
-                if (!__any_sync(0xffffffffu, hit)) continue;
-                for (int place = begin(__popc(hit)); hit; hit &= hit - 1, ++place) {
+                if (hit == 0) continue;
+                for (int place = atomicAdd(&s.n, __popc(hit)); hit; hit &= hit - 1, ++place) {
                     const int i = __ffs(hit) - 1;
                     int from = at[0];
 #pragma unroll
                     for (int u = 1; u < kLoads; ++u) from = i >= u * 8 ? at[u] : from;
-                    if (place < kRowList) s.place[place] = (uint32_t)Rows::place(from, lane, i & 7);
+                    if (place < kRowList) places[place] = (uint32_t)Rows::place(from, lane, i & 7);
                 }
             }
             __syncwarp();
+            const int n = s.n;
             if (n <= kRowList) {
-                for (int i = lane; i < n; i += 32) {
-                    const uint32_t place = s.place[i];
-                    s.key[i] = key_of(ordered(to_float(x[place])), place);
+                // (the keys of 32 reach no further into the places than those that have been read)
+                for (int i0 = 0; i0 < n; i0 += 32) {
+                    const int i = i0 + lane;
+                    const uint32_t place = i < n ? places[i] : 0u;
+                    __syncwarp();
+                    if (i < n) s.key[i] = key_of(ordered(to_float(x[place])), place);
+                    __syncwarp();
                 }
-                __syncwarp();
                 rank_row(s, n, n_out, lane);
                 count = min(n, n_out);
             } else {
                 count = search_slowly(s, x, p.vocab, least, n_out, lane);
             }
             if (bad || sum == 0) count = 0;
-            for (int k = lane; k < count; k += 32) lists.order[mine * n_out + k] = (int64_t)s.best[k];
-            __syncwarp();
+        }
+        for (int k = lane; k < count; k += 32) {
+            if (SCANNED)
+                lists.order[mine * n_out + k] = (int64_t)s.best[k];
+            else
+                list(mine * n_out + k, s.best[k], ended, base, weight);
         }
         if (lane == 0) {
-            s_all.sum[mine] = sum;
-            s_all.top[mine] = top;
-            s_all.e[mine] = e;
-            s_all.score[mine] = score;
-            s_all.weight[mine] = weight;
-            s_all.ended[mine] = ended;
             s_all.counts[mine] = count;
+            if constexpr (SCANNED) {
+                s_all.sum[mine] = sum;
+                s_all.top[mine] = top;
+                s_all.e[mine] = e;
+                s_all.score[mine] = score;
+                s_all.weight[mine] = weight;
+                s_all.ended[mine] = ended;
+            }
         }
+        __syncwarp();
     }
     __syncthreads();
-    for (int r0 = warp * 32; r0 < rows; r0 += warps * 32) {
-        const int r = min(r0 + lane, rows - 1);
-        const double log2_sum = logs.log2_of(s_all.sum[r]);
-        const double base = (double)s_all.score[r] - (s_all.ended[r] == -1 ? norm_of(s_all.top[r], s_all.e[r], log2_sum) : 0.0);
-        if (r0 + lane < rows) s_all.base[r] = base;
+    if constexpr (SCANNED) {
+        for (int r0 = warp * 32; r0 < rows; r0 += warps * 32) {
+            const int r = min(r0 + lane, rows - 1);
+            const double log2_sum = logs.log2_of(s_all.sum[r]);
+            const double base = (double)s_all.score[r] - (s_all.ended[r] == -1 ? norm_of(s_all.top[r], s_all.e[r], log2_sum) : 0.0);
+            if (r0 + lane < rows) s_all.base[r] = base;
+        }
+        __syncthreads();
+        for (int c = tid; c < rows * n_out; c += (int)blockDim.x) {
+            const int r = c / n_out;
+            if (c - r * n_out < s_all.counts[r]) list(c, (uint64_t)lists.order[c], s_all.ended[r], s_all.base[r], s_all.weight[r]);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int c = tid; c < rows * n_out; c += (int)blockDim.x) {
-        const int r = c / n_out;
-        if (c - r * n_out >= s_all.counts[r]) continue;
-        const int ended = s_all.ended[r];
-        const uint64_t key = (uint64_t)lists.order[c];
-        const double total = ended >= 0 ? s_all.base[r] : (double)key_value(key) + s_all.base[r];
-        lists.order[c] = ordered(p.weights ? total * (double)s_all.weight[r] : total);
-        lists.total[c] = (float)total;
-        lists.token[c] = ended >= 0 ? ended : (int32_t)key_place(key);
-    }
-    __syncthreads();
     const int64_t to = (int64_t)b * n_out;
     if (rows) place_all(p, lists, s_all.counts, s_places, reinterpret_cast<Placed*>(behind), first, rows, 0, 1, to);
     fill_rest(p, s_all.counts, rows, to);
@@ -1066,25 +1083,25 @@ constexpr int kSomeRows = 152 * 2, kManyRows = 152 * 5;
 constexpr int kFewOut = 32;
 template <typename T, bool VEC>
 int launch_select(const SelectParams& p, cudaStream_t s) {
-    auto rows_kernel = [&](auto kernel, SmemOptIn& opt) {
+    auto rows_kernel = [&](auto kernel, SmemOptIn& opt, int row_bytes) {
         int warps = 1;  // a row each, by the mean of the requests' rows
         while (warps < kRowWarps && (int64_t)warps * p.n_seqs < p.n_rows) warps *= 2;
-        const int opted = opt.ensure(kernel, lists_bytes(1, kMaxOut) + placed_bytes(kMaxOut) + kRowWarps * (int)sizeof(RowSearch));
+        const int opted = opt.ensure(kernel, lists_bytes(1, kMaxOut) + placed_bytes(kMaxOut) + kRowWarps * row_bytes);
         if (opted != KVQ8_OK) return opted;
         return launch_dependent(kernel, (unsigned)p.n_seqs, 32u * (unsigned)warps,
-                                lists_bytes(1, p.n_out) + placed_bytes(p.n_out) + warps * (int)sizeof(RowSearch), s, p);
+                                lists_bytes(1, p.n_out) + placed_bytes(p.n_out) + warps * row_bytes, s, p);
     };
     const bool few_out = p.n_out <= kFewOut, few_groups = 4 * p.n_groups < 5 * p.n_out;
     if (p.vocab <= kSmallVocab || (few_out && (p.vocab <= kMediumVocab ? p.n_rows > kSomeRows : p.n_rows > kManyRows && few_groups))) {
         static SmemOptIn opt;
-        return rows_kernel(beam_rows_kernel<T, VEC, false>, opt);
+        return rows_kernel(beam_rows_kernel<T, VEC, false>, opt, (int)sizeof(RowSearch<false>));
     }
     const dim3 grid((unsigned)(p.n_parts / kScanWarps), (unsigned)p.n_rows);
     const int rc = launch_dependent(beam_scan_kernel<T, VEC>, grid, kScanThreads, 0, s, p);
     if (rc != KVQ8_OK) return rc;
     if (p.n_rows > kManyRows && few_out) {
         static SmemOptIn opt;
-        return rows_kernel(beam_rows_kernel<T, VEC, true>, opt);
+        return rows_kernel(beam_rows_kernel<T, VEC, true>, opt, (int)sizeof(RowSearch<true>));
     }
     // A block a row, by the mean of the requests' rows.  Clusters of 16 where the GPU holds all of them at once: 12 requests of 32 beams, 64
     // of each, over 106304 bf16 logits 48.2 us (of 8: 72.8); 24 of 16 beams 39.3 us (of 8: 35.1).
