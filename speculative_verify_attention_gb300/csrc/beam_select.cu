@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
             Rows::load(v8, x, at, p.vocab, lane);
         };
         const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
-        int ended = p.ended ? __ldg(p.ended + row) : -1;
+        int ended = p.ended ? max(__ldg(p.ended + row), -1) : -1;  // any value below zero: the row goes on
         if (!SCANNED) load(0);
         if (!(fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY)) ended = -2;
         float top = 0.0f, e = 0.0f;
