@@ -770,7 +770,10 @@ class KVPagedCacheQ8:
         self._planes = {"k_codes": k_codes, "k_scales": k_scales, "v_codes": v_codes, "v_scales": v_scales}
         self._struct = struct = kvq8_paged_cache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(),
                                         n_kv_heads, head_dim, page_size, n_pages)
-        self._at = ctypes.addressof(struct)
+        # The native calls read the struct at its address while other threads may replace a plane, which makes a new one: each keeps
+        # this pair, and by it the planes, until it has returned.
+        struct.planes = (k_codes, k_scales, v_codes, v_scales)
+        self._handle = (ctypes.addressof(struct), struct)
 
     def _plane(name: str):
         # the C struct is kept, so a plane that is replaced has to reach it; one of another shape, type or device raises
@@ -832,7 +835,8 @@ def kvq8_paged_append(k: torch.Tensor, v: torch.Tensor, cache: KVPagedCacheQ8, s
 def kvq8_paged_read(cache: KVPagedCacheQ8, slots: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stream=None) -> None:
     """Write the values of int64 slots [n_tok] into k and v [n_tok][n_kv_heads][head_dim] (fp32, fp16 or bf16; tokens
     and heads may be strided, so a KVCacheF16's planes can be given as k.transpose(0, 1)[:n_tok])."""
-    st = _native().paged_read(cache._at, cache._index, slots, k, v, _launch_on(cache._index, stream))
+    at, _held = cache._handle
+    st = _native().paged_read(at, cache._index, slots, k, v, _launch_on(cache._index, stream))
     if st is None:
         n = slots.shape[0]
         if k.dtype is not v.dtype or k.dtype not in _DTYPE:
@@ -1058,7 +1062,8 @@ def kvq8_paged_copy(cache: KVPagedCacheQ8, src_pages: torch.Tensor, dst_pages: t
                     stream=None) -> None:
     """Copy the first rows (int32 [n]; None: all) of pages src_pages to pages dst_pages (int32 [n]; -1: nothing), K and V."""
     dev = cache._index
-    st = _native().paged_copy(cache._at, dev, src_pages, dst_pages, rows, _launch_on(dev, stream))
+    at, _held = cache._handle
+    st = _native().paged_copy(at, dev, src_pages, dst_pages, rows, _launch_on(dev, stream))
     if st is None:
         i32, shape = torch.int32, tuple(src_pages.shape[:1])
         _refuse(dev, (src_pages, "src_pages", i32, shape), (dst_pages, "dst_pages", i32, shape),
@@ -1071,7 +1076,8 @@ def kvq8_paged_compact(cache: KVPagedCacheQ8, page_table: torch.Tensor, lens: to
     """Move the kept rows of every request's window (kept int64 [n], bit j = place j) together to its first places; page_table int32
     [n][max_pages], lens int32 [n], row_starts int32 [n + 1].  lens_out int32 [n]: the lengths afterwards."""
     dev = cache._index
-    st = _native().paged_compact(cache._at, dev, page_table, lens, row_starts, kept, lens_out, _launch_on(dev, stream))
+    at, _held = cache._handle
+    st = _native().paged_compact(at, dev, page_table, lens, row_starts, kept, lens_out, _launch_on(dev, stream))
     if st is None:
         if page_table.dim() != 2:
             raise ValueError("page_table must be [n][max_pages]")
@@ -1109,7 +1115,8 @@ def kvq8_paged_append_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ca
     raw = _launch_on(dev, stream)
     if q_out is None:
         q_out = _empty(q.shape, q.dtype, q.device, stream)
-    st = calls.paged_append_rope(cache._at, dev, q, k, v, slots, positions, turns, axis_of, bool(pairs), q_out, raw)
+    at, _held = cache._handle
+    st = calls.paged_append_rope(at, dev, q, k, v, slots, positions, turns, axis_of, bool(pairs), q_out, raw)
     if st is None:
         heads, dim = cache.n_kv_heads, cache.head_dim
         if q.dim() != 3 or q.dtype not in _DTYPE or q.get_device() != dev or q.shape[2] != dim:
