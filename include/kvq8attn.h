@@ -668,7 +668,8 @@ size_t kvq8_paged_fork_workspace_bytes(int n_seqs, int n_children, int n_pages);
  * noticed; the results then are no better, but nothing outside the arrays is touched.
  * kvq8_paged_tables takes pages for growing sequences as before (a fresh page's share is 0, and a sequence grows only in pages of its
  * own).  It gives pages back whoever shares them: sequences with shared pages are cut short and ended by this call.
- * Errors: INVALID_ARG (outputs over the sequences' inputs as well), UNSUPPORTED (n_seqs or n_children > 4096, page_size, n_pages > 2^30, max_pages
+ * Errors: INVALID_ARG (outputs over inputs or one another as well, but for the two that may be updated in place; free_ring counts as an
+ * output), UNSUPPORTED (n_seqs or n_children > 4096, page_size, n_pages > 2^30, max_pages
  * > 2^24), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  One launch for small tables, else three.
  */
 int kvq8_paged_fork(const int32_t* parents, int n_children, const int32_t* lens, const int32_t* held, int n_seqs,

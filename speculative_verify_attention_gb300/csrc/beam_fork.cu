@@ -582,15 +582,23 @@ extern "C" int kvq8_paged_fork(const int32_t* parents, int n_children, const int
         if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
     for (const void* q : out)
         if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
-    // the sequences' state is read while the children's is written
-    const size_t old = (size_t)n_seqs * 4, kids = (size_t)n_children * 4;
-    if (ranges_meet(page_table, old * max_pages, page_table_out, kids * max_pages)) return KVQ8_ERR_INVALID_ARG;
-    for (const void* o : {(const void*)lens_out, (const void*)held_out, (const void*)copy_src, (const void*)copy_dst, (const void*)copy_rows})
-        if (ranges_meet(lens, old, o, kids) || ranges_meet(held, old, o, kids) || ranges_meet(parents, kids, o, kids))
-            return KVQ8_ERR_INVALID_ARG;
-    if ((shares != shares_out && ranges_meet(shares, (size_t)n_pages * 4, shares_out, (size_t)n_pages * 4)) ||
-        (ring_state != ring_out && ranges_meet(ring_state, 8, ring_out, 8)))
-        return KVQ8_ERR_INVALID_ARG;
+    // the sequences' state is read while the children's is written, and what one kernel writes the next one indexes by
+    struct Array {
+        const void* at;
+        size_t bytes;
+    };
+    const size_t old = (size_t)n_seqs * 4, kids = (size_t)n_children * 4, pool = (size_t)n_pages * 4;
+    const Array reads[] = {{parents, kids}, {lens, old}, {held, old}, {page_table, old * max_pages}, {shares, pool}, {ring_state, 8}};
+    const Array writes[] = {{free_ring, pool}, {page_table_out, kids * max_pages}, {lens_out, kids}, {held_out, kids}, {shares_out, pool},
+                            {ring_out, 8}, {copy_src, kids}, {copy_dst, kids}, {copy_rows, kids}, {status, 4}};
+    for (const Array& w : writes) {
+        for (const Array& r : reads) {
+            const bool itself = w.at == r.at && ((r.at == shares && w.at == shares_out) || (r.at == ring_state && w.at == ring_out));
+            if (!itself && ranges_meet(r.at, r.bytes, w.at, w.bytes)) return KVQ8_ERR_INVALID_ARG;
+        }
+        for (const Array* o = writes; o != &w; ++o)
+            if (ranges_meet(o->at, o->bytes, w.at, w.bytes)) return KVQ8_ERR_INVALID_ARG;
+    }
     if (!workspace || workspace_bytes < kvq8_paged_fork_workspace_bytes(n_seqs, n_children, n_pages)) return KVQ8_ERR_WORKSPACE;
     if (!aligned16(workspace)) return KVQ8_ERR_MISALIGNED;
     PagedFork p = {parents, lens, held, page_table, shares, ring_state, free_ring, page_table_out, lens_out, held_out, shares_out,

@@ -1,0 +1,41 @@
+"""Outputs over inputs, or over one another: refused by status before any launch, without a GPU."""
+import pytest
+
+from .test_beam_refusals import FORK, INVALID, WORKSPACE, A, _call
+
+# bytes of each array as tests/test_beam_refusals.py has the call: 4 children of 3 sequences, tables of 5 pages, a pool of 9
+READ = dict(parents=16, lens=12, held=12, page_table=60, shares=36, ring_state=8)
+WRITTEN = dict(free_ring=36, page_table_out=80, lens_out=16, held_out=16, shares_out=36, ring_out=8, copy_src=16, copy_dst=16, copy_rows=16,
+               status=4)
+IN_PLACE = {("shares", "shares_out"), ("ring_state", "ring_out")}
+
+
+def _refused(name, over, at):
+    assert _call("kvq8_paged_fork", FORK, {name: FORK[over] + at}) == INVALID, (name, over, at)
+
+
+@pytest.mark.parametrize("name", WRITTEN)
+def test_fork_writes_over_nothing_that_it_reads(name):
+    for over, size in READ.items():
+        for at in (0, 4, size - 4, 4 - WRITTEN[name]):
+            if at == 0 and (over, name) in IN_PLACE:
+                continue
+            _refused(name, over, at)
+
+
+@pytest.mark.parametrize("name", WRITTEN)
+def test_fork_has_no_two_outputs_in_one_place(name):
+    for over, size in WRITTEN.items():
+        for at in (0, size - 4, 4 - WRITTEN[name]):
+            if over != name:
+                _refused(name, over, at)
+
+
+def test_fork_takes_arrays_side_by_side_and_in_place():
+    """Behind one another in one buffer, and shares and the ring's state updated in place: what is refused then is the workspace."""
+    at, but = A, {}
+    for name, size in {**READ, **WRITTEN}.items():
+        but[name] = at
+        at += size
+    assert _call("kvq8_paged_fork", FORK, {**but, "workspace": None}) == WORKSPACE
+    assert _call("kvq8_paged_fork", FORK, {**but, "shares_out": but["shares"], "ring_out": but["ring_state"], "workspace": None}) == WORKSPACE
