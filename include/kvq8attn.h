@@ -693,7 +693,7 @@ int kvq8_paged_copy(const kvq8_paged_cache* kv, const int32_t* src_pages, const 
  *   page_table, lens, row_starts as in attn_verify_paged_q8: request b's window of T <= 64 rows are its last T tokens
  *   kept     : uint64 [n_seqs], bit j = place j of the window is kept (bits from T on are ignored; a row's window_mask word is
  *              its path)
- *   lens_out : int32 [n_seqs] or null, not lens: lens - T + rows kept
+ *   lens_out : int32 [n_seqs] or null: lens - T + rows kept; over lens or another input it is refused
  * Places behind the kept ones hold what they held or a moved row's old copy.  Rows from or to a page outside [0, n_pages) do not move.
  * A malformed request (T outside [0, 64], T > lens, lens > max_pages * page_size) is left as it is.  The pages of a window belong
  * to one request.

@@ -153,8 +153,11 @@ extern "C" int kvq8_paged_compact(const kvq8_paged_cache* kv, const int32_t* pag
     for (const int32_t* q : {page_table, lens, row_starts, (const int32_t*)lens_out})
         if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
     if (!aligned_to(kept, 8)) return KVQ8_ERR_MISALIGNED;
-    // blocks read the lengths while one writes the new ones
-    if (ranges_meet(lens, (size_t)n_seqs * 4, lens_out, (size_t)n_seqs * 4)) return KVQ8_ERR_INVALID_ARG;
+    // blocks read these while one writes the new lengths
+    const size_t lens_bytes = (size_t)n_seqs * 4;
+    if (ranges_meet(lens, lens_bytes, lens_out, lens_bytes) || ranges_meet(row_starts, lens_bytes + 4, lens_out, lens_bytes) ||
+        ranges_meet(kept, 2 * lens_bytes, lens_out, lens_bytes) || ranges_meet(page_table, lens_bytes * max_pages, lens_out, lens_bytes))
+        return KVQ8_ERR_INVALID_ARG;
     const int smem = kMaxWindowRows * (kv->head_dim + kv->head_dim / 16);
     return launch_dependent(paged_compact_kernel, dim3((unsigned)n_seqs, 2u * (unsigned)kv->n_kv_heads), kMoveThreads, smem,
                             (cudaStream_t)stream, paged_move(kv), Compact{page_table, lens, row_starts, kept, lens_out, n_seqs, max_pages});

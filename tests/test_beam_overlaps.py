@@ -1,7 +1,7 @@
 """Outputs over inputs, or over one another: refused by status before any launch, without a GPU."""
 import pytest
 
-from .test_beam_refusals import FORK, INVALID, WORKSPACE, A, _call
+from .test_beam_refusals import COMPACT, FORK, INVALID, WORKSPACE, A, _call
 
 # bytes of each array as tests/test_beam_refusals.py has the call: 4 children of 3 sequences, tables of 5 pages, a pool of 9
 READ = dict(parents=16, lens=12, held=12, page_table=60, shares=36, ring_state=8)
@@ -39,3 +39,10 @@ def test_fork_takes_arrays_side_by_side_and_in_place():
         at += size
     assert _call("kvq8_paged_fork", FORK, {**but, "workspace": None}) == WORKSPACE
     assert _call("kvq8_paged_fork", FORK, {**but, "shares_out": but["shares"], "ring_out": but["ring_state"], "workspace": None}) == WORKSPACE
+
+
+@pytest.mark.parametrize("over,size", [("lens", 12), ("row_starts", 16), ("kept", 24), ("page_table", 48)])
+def test_compact_writes_over_nothing_that_it_reads(over, size):
+    apart = dict(COMPACT, page_table=A, lens=2 * A, row_starts=3 * A, kept=4 * A, lens_out=5 * A)
+    for at in (0, 4, size - 4, -8):
+        assert _call("kvq8_paged_compact", apart, {"lens_out": apart[over] + at}) == INVALID, (over, at)
