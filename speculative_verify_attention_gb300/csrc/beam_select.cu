@@ -864,15 +864,15 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
         const int row = first + mine;
         const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.stride;
         Eight<T> v8[kLoads];
-        auto load = [&](int chunk) {
+        auto load = [&](int chunk, int vocab) {
             int at[kLoads];
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) at[u] = chunk * kChunk + u * 256;
-            Rows::load(v8, x, at, p.vocab, lane);
+            Rows::load(v8, x, at, vocab, lane);
         };
         const float score = p.scores ? __ldg(p.scores + row) : 0.0f, weight = p.weights ? __ldg(p.weights + row) : 1.0f;
         int ended = p.ended ? max(__ldg(p.ended + row), -1) : -1;  // any value below zero: the row goes on
-        if (!SCANNED) load(0);
+        if (!SCANNED) load(0, ended < 0 ? p.vocab : 0);  // of a row at its end no value (a branch instead: 97 registers, 12.0 -> 16.8 us)
         if (!(fabsf(score) < INFINITY && weight > 0.0f && weight < INFINITY)) ended = -2;
         float top = 0.0f, e = 0.0f;
         unsigned long long sum = 0;
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
                     }
                     add_to(part, v8, fmaxf(warp_max(m), part.m));
                     if (++chunk == p.n_chunks) break;
-                    load(chunk);
+                    load(chunk, p.vocab);
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) part.s += __shfl_xor_sync(0xffffffffu, part.s, o);

@@ -39,3 +39,28 @@ def test_all_below_zero_go_on(lib, dtype, vocab, requests, n_out):
     few = min(requests, 20)                                          # the definition, of some
     check_selection(x[:4 * few].float().cpu().numpy(), starts[:few + 1], n_out, [t[:few] for t in got],
                     scores.cpu().numpy()[:4 * few], None, ended[:4 * few])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,requests,n_out", [(5, 3, 6), (1001, 5, 6), (2048, 3, 64), (9001, 90, 12), (32504, 200, 9), (20003, 4, 5)])
+def test_logits_of_rows_at_their_end_count_for_nothing(lib, dtype, vocab, requests, n_out):
+    """Whatever they hold, the outputs are the same bits; requests whose rows are all at their end among them."""
+    from speculative_verify_attention_gb300 import beam_select
+    rng = np.random.default_rng(vocab)
+    starts = starts_of([4] * requests)
+    n = int(starts[-1])
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(vocab + 1)
+    x = torch.randn((n, vocab), generator=gen, device="cuda").mul_(3.0).to(dtype)
+    ended = np.where(rng.random(n) < 0.5, 3, -1)
+    ended[4:8] = vocab - 1
+    at_end = torch.from_numpy(ended >= 0).cuda()
+    scores = torch.from_numpy((-20 - 3 * rng.random(n)).astype(np.float32)).cuda()
+    first = None
+    for held in (0.0, float("nan"), float("inf"), -float("inf"), torch.finfo(dtype).max):
+        x[at_end] = held
+        got = beam_select(x, i32(starts), n_out, scores=scores, ended=i32(ended))
+        first = first or got
+        for a, b in zip(got, first):
+            assert torch.equal(a, b), held
+    assert first[1][1, :4].tolist() == [vocab - 1] * 4 and torch.all(first[0][1, 4:] == -1)
