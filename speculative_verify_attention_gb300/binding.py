@@ -79,7 +79,7 @@ def library_path() -> str:
 
 def load_library():
     """Load the in-tree library (built by ``build.build()``); raises if it is missing."""
-    global _lib, _calls
+    global _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -183,8 +183,6 @@ def load_library():
         lib.kvq8_device_error.restype = i32
         lib.kvq8_status_str.argtypes = [i32]
         lib.kvq8_status_str.restype = ctypes.c_char_p
-        from . import _calls as calls  # linked to the library
-        _calls = calls
         _lib = lib
         return lib
 
@@ -944,8 +942,14 @@ def token_counts(tokens: torch.Tensor, token_starts: torch.Tensor, counts: torch
 # The tensors' types, shapes and devices are checked in csrc/calls.cpp; where one does not fit, _refuse says which.
 
 def _native():
+    """csrc/calls.cpp's module, loaded by the first call that needs it; raises if it is missing."""
+    global _calls
     if _calls is None:
-        load_library()
+        load_library()  # which the module is linked to
+        if not os.path.exists(_build.CALLS_PATH):
+            raise RuntimeError(f"{_build.CALLS_PATH} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        from . import _calls as calls
+        _calls = calls
     return _calls
 
 

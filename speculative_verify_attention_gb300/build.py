@@ -4,7 +4,8 @@ Every .cu file under csrc/ is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a -O3 -lineinfo`` and linked into one shared
 library next to this file.  csrc/calls.cpp, the binding's argument checks of the calls that stand in steps
 of a few microseconds, is compiled beside them with the host compiler against torch's headers, and linked
-to that library.  No CMake, no torch extension machinery.
+to that library.  No CMake, no torch extension machinery.  The C library is linked first and needs neither
+torch nor Python; where torch is not installed it is all that is built.
 """
 from __future__ import annotations
 
@@ -46,11 +47,26 @@ def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [CALLS_SOURCE, os.path.join(INCLUDE, "kvq8attn.h")]
 
 
+def _torch_dir():
+    """Where torch is installed, or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
+    paths = [LIB_PATH] + ([CALLS_PATH] if _torch_dir() else [])
+    if not all(os.path.exists(p) for p in paths):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
+    t = min(os.path.getmtime(p) for p in paths)
     return any(os.path.getmtime(p) > t for p in _deps())
+
+
+def _link(path: str, compiler: list, rest: list) -> None:
+    tmp = path + f".{os.getpid()}.tmp"
+    r = subprocess.run([*compiler, "-shared", "-o", tmp, *rest], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -73,7 +89,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         return obj
 
     calls_obj = os.path.join(BUILD_DIR, "calls.cpp.o")
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_dir = _torch_dir()
 
     def compile_calls():
         include = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -84,22 +100,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"the host compiler failed for {CALLS_SOURCE}:\n{r.stdout}\n{r.stderr}")
 
     with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        calls = ex.submit(compile_calls)
+        calls = ex.submit(compile_calls) if torch_dir else None
         objs = list(ex.map(compile_one, srcs))
-        calls.result()
-    tmp = LIB_PATH + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    tmp = CALLS_PATH + f".{os.getpid()}.tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, calls_obj, f"-L{HERE}", "-lkvq8attn", f"-L{os.path.join(torch_dir, 'lib')}",
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS_PATH)
+        # the C library first: it needs nothing of torch or Python
+        _link(LIB_PATH, [nvcc, *ARCH], [*objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"])
+        if calls:
+            calls.result()
+    if torch_dir:
+        _link(CALLS_PATH, [os.environ.get("CXX", "g++")], [calls_obj, f"-L{HERE}", "-lkvq8attn", f"-L{os.path.join(torch_dir, 'lib')}",
+                                                            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    else:
+        sys.stderr.write("torch is not installed: the C library alone was built\n")
     return LIB_PATH
 
 
