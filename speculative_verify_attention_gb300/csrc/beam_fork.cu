@@ -333,7 +333,7 @@ __device__ __forceinline__ bool fork_plan(const PagedFork& p, int* sm, int* s_wa
             p.copy_dst[i] = fresh;
             p.copy_rows[i] = take ? len & (page - 1) : 0;
             p.lens_out[i] = len;
-            p.held_out[i] = (len + page - 1) >> p.page_shift;
+            p.held_out[i] = ((len - 1) >> p.page_shift) + 1;  // (rounded up first, a length may pass 31 bits)
         }
     }
     const int status = bad ? 2 : takes > count ? 1 : 0;

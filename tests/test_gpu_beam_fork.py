@@ -266,3 +266,15 @@ def test_counts_that_start_anywhere(lib, vocab, first):
     assert int(status) == want[2] == 0 and np.array_equal(out.cpu().numpy(), want[0])
     whole[first:first + states * vocab] = want[1].reshape(-1)
     assert np.array_equal(on.cpu().numpy(), whole)
+
+
+@pytest.mark.parametrize("length", [2 ** 31 - 1, 2 ** 31 - 1023, 2 ** 31 - 1024])
+def test_lengths_at_the_end_of_their_type(lib, length):
+    """Rounded up to pages such a length passes 31 bits.  Two million entries of a table, all but the first and last of no page."""
+    width = 2 ** 21
+    table = np.full((1, width), -3, np.int32)
+    table[0, [0, (length - 1) // 1024]] = 4, 6
+    ring = np.array([1, 2, 3, 5, 7, 0, -9, -9], np.int32)
+    s = (np.array([length]), np.array([width]), 1024, table, np.zeros(8, np.int32), ring, np.array([0, 6]))
+    want = _pages([0, 0], s)
+    assert want[2].tolist() == [-(-length // 1024)] * 2 and want[-1] == 0
