@@ -4,7 +4,8 @@
 // Pair i of a rotated row turns by positions[axis_of[i]] * f_i:  (a, b) -> (a cos - b sin, b cos + a sin).  A frequency is given
 // in turns a position as a 64-bit fraction, so position times frequency, modulo 2^64, is the angle's fraction of a turn whatever
 // the position: no rounding but the frequency's own, 2^-64 of a turn a position.  Its two upper bits are the quarter, and what is
-// left, within an eighth of a turn of zero, goes through sincospif.
+// left, within an eighth of a turn of zero, goes through sincospif: cut to 2^-34 of a turn, and rounded to fp32, half a step of which
+// is 2^-28 of a turn at most.
 //
 // A block works out the sines and cosines of its tokens, two or four, once for all of its heads.  A thread has sixteen values of a
 // row, eight and their partners eight, the same ones of several heads: its eight sines and cosines stay in its registers.  What it
