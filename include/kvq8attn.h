@@ -607,9 +607,10 @@ size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs, int n_out)
  *   parents, tokens, totals : int32, int32, fp32 [n_seqs][n_out], best first: row, token and total of each; where a request has
  *             fewer, -1, -1 and -inf
  *   workspace : beam_select_workspace_bytes(...) bytes, 16-byte aligned; calls that may overlap need one each
- * total = scores[r] + (x - log sum exp x) over the row's logits x: the sum to about 2e-7 of itself, nearly the same for all rows
- * (they differ by some 1e-8), the rest in 64 bits, totals rounded to fp32 at the end.  Continuations are ordered by weight * total in
- * 64 bits, equal ones of different rows by row, those of a row by logit, then by token (-0 equals 0).
+ * total = scores[r] + (x - log sum exp x) over the row's logits x: the sum in 32 bits, its log off by less than 3e-6 + 2e-13 vocab (3e-7 at
+ * most as measured) whatever the logits' size, the rest in 64 bits, totals rounded to fp32 at the end.  Continuations are ordered by
+ * weight * total in 64 bits; of different rows' ones that are nearer to each other than the sums are exact either may come first.  Equal
+ * ones of different rows are ordered by row, those of a row by logit, then by token (-0 equals 0).
  * A logit of -inf is no continuation.  A row with a NaN or +inf among its logits, a score that is not finite or a weight that is
  * not positive and finite has none.  Requests without rows, with more than 64 or outside [0, n_rows) get -1; rows of no request are
  * not read for any.  The same call gives the same bits.
