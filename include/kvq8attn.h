@@ -478,7 +478,8 @@ int kvq8_paged_tables(const int32_t* lens, const int32_t* n_new, const int32_t* 
  *   slots  : int64 [n_tok], device; a token whose slot lies outside [0, n_pages * page_size) is
  *            skipped.  No two tokens of a call may have the same slot: its contents would be a
  *            mixture of theirs.
- * The bytes are those of kvq8_append for the same values (in fp32).  The planes are written through.
+ * The bytes are those of kvq8_append for the same values (in fp32), also of values that are not finite: a NaN has code -127 beside
+ * numbers, and 32 of them the scale NaN.  The planes are written through.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size), MISALIGNED (16 bytes; slots 8).
  */
 int kvq8_paged_append(const void* k, const void* v, int dtype, int n_tok, int64_t k_stride, int64_t v_stride,
