@@ -982,6 +982,8 @@ def beam_select(logits: torch.Tensor, row_starts: torch.Tensor, n_out: int, scor
     dev, calls = logits.get_device(), _native()
     raw = _launch_on(dev, stream)
     if parents is None or tokens is None or totals is None or workspace is None:
+        if logits.dim() != 2 or row_starts.dim() != 1 or row_starts.shape[0] < 1 or n_out < 0:
+            raise ValueError("logits must be [n_rows][V], row_starts [n + 1], and n_out 1 or more")
         shape, on = (row_starts.shape[0] - 1, int(n_out)), logits.device
         parents = _empty(shape, torch.int32, on, stream) if parents is None else parents
         tokens = _empty(shape, torch.int32, on, stream) if tokens is None else tokens
@@ -991,6 +993,8 @@ def beam_select(logits: torch.Tensor, row_starts: torch.Tensor, n_out: int, scor
     if st is None:
         if logits.dim() != 2 or logits.dtype not in _DTYPE or logits.stride(1) != 1 and logits.shape[1] > 1:
             raise ValueError("logits must be [n_rows][V] of float32, float16 or bfloat16 with contiguous rows")
+        if row_starts.dim() != 1:
+            raise ValueError("row_starts must be [n + 1]")
         rows, n, i32, f32 = logits.shape[0], row_starts.shape[0] - 1, torch.int32, torch.float32
         _refuse(dev, (row_starts, "row_starts", i32, (n + 1,)),
                 *[(t, name, ty, (rows,)) for t, name, ty in ((scores, "scores", f32), (weights, "weights", f32), (ended, "ended", i32))

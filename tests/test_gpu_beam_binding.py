@@ -61,3 +61,17 @@ def test_outputs_and_workspaces_that_are_left_out(lib):
     out = kv.kvq8_paged_append_rope(q, q[:, :2], q[:, 2:], cache, torch.arange(3, device="cuda"), _z(3), _z(32, dtype=I64), pairs=True)
     assert torch.equal(out, q)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("but", [dict(logits=(4, 5, 10)), dict(logits=(50,)), dict(logits=()), dict(row_starts=(1, 3)), dict(row_starts=(0,)), dict(row_starts=()),
+                                 dict(n_out=-3)])
+@pytest.mark.parametrize("with_outputs", [False, True])
+def test_select_names_sizes_that_it_does_not_take(lib, but, with_outputs):
+    """Of wrong rank, empty, or fewer than nothing wanted: the binding's own error, whether it makes the outputs or is given them."""
+    import speculative_verify_attention_gb300 as kv
+    args = dict(logits=_z(4, 50, dtype=torch.float32), row_starts=_z(3), n_out=5)
+    args.update({k: _z(*v, dtype=args[k].dtype) if isinstance(v, tuple) else v for k, v in but.items()})
+    if with_outputs:
+        args.update(parents=_z(2, 5), tokens=_z(2, 5), totals=_z(2, 5, dtype=torch.float32), workspace=_z(1 << 16, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        kv.beam_select(**args)
