@@ -615,7 +615,7 @@ size_t beam_select_workspace_bytes(int n_rows, int vocab, int n_seqs, int n_out)
  * A logit of -inf is no continuation.  A row with a NaN or +inf among its logits, a score that is not finite or a weight that is
  * not positive and finite has none.  Requests without rows, with more than 64 or outside [0, n_rows) get -1; rows of no request are
  * not read for any.  The same call gives the same bits.
- * Errors: INVALID_ARG (an output over row_starts, scores, weights or ended as well), UNSUPPORTED (n_rows > 65535, vocab > 2^30,
+ * Errors: INVALID_ARG (an output over an input, the workspace or another output as well), UNSUPPORTED (n_rows > 65535, vocab > 2^30,
  * n_seqs > 4096, n_out > 64), WORKSPACE, MISALIGNED (element size; workspace 16).  One launch for up to 2048 values, and for some hundreds of
  * rows of up to some ten thousand; else two.
  */

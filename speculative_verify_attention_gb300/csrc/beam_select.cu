@@ -1155,17 +1155,22 @@ extern "C" int beam_select(const void* logits, int dtype, int64_t logits_stride,
     if (n_rows == 0) return KVQ8_ERR_INVALID_ARG;
     if (!logits || !row_starts || !parents || !tokens || !totals || logits_stride < vocab) return KVQ8_ERR_INVALID_ARG;
     if (!select_shape(n_rows, vocab, n_seqs, n_out)) return KVQ8_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < beam_select_workspace_bytes(n_rows, vocab, n_seqs, n_out)) return KVQ8_ERR_WORKSPACE;
+    const size_t need = beam_select_workspace_bytes(n_rows, vocab, n_seqs, n_out);
+    if (!workspace || workspace_bytes < need) return KVQ8_ERR_WORKSPACE;
     if (!aligned_to(logits, esz) || !aligned16(workspace)) return KVQ8_ERR_MISALIGNED;
     for (const void* q : {(const void*)row_starts, (const void*)scores, (const void*)weights, (const void*)ended,
                           (const void*)parents, (const void*)tokens, (const void*)totals})
         if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
     // (a request's outputs are written while others' inputs are still read)
-    for (const void* out : {(const void*)parents, (const void*)tokens, (const void*)totals}) {
-        const size_t bytes = (size_t)n_seqs * n_out * 4;
-        if (ranges_meet(out, bytes, row_starts, ((size_t)n_seqs + 1) * 4)) return KVQ8_ERR_INVALID_ARG;
-        for (const void* in : {(const void*)scores, (const void*)weights, (const void*)ended})
-            if (in && ranges_meet(out, bytes, in, (size_t)n_rows * 4)) return KVQ8_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)n_seqs * n_out * 4, rows = (size_t)n_rows * 4;
+    const void* const outs[] = {parents, tokens, totals};
+    for (int i = 0; i < 3; ++i) {
+        if (ranges_meet(outs[i], bytes, row_starts, ((size_t)n_seqs + 1) * 4) || ranges_meet(outs[i], bytes, scores, rows) ||
+            ranges_meet(outs[i], bytes, weights, rows) || ranges_meet(outs[i], bytes, ended, rows) || ranges_meet(outs[i], bytes, workspace, need) ||
+            range_meets_rows(outs[i], bytes, logits, (int64_t)(vocab * esz), logits_stride * (int64_t)esz, n_rows))
+            return KVQ8_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (ranges_meet(outs[i], bytes, outs[j], bytes)) return KVQ8_ERR_INVALID_ARG;
     }
     SelectParams p = {};
     p.logits = logits, p.stride = logits_stride, p.row_starts = row_starts, p.scores = scores, p.weights = weights;

@@ -48,6 +48,14 @@ inline bool ranges_meet(const void* a, size_t a_len, const void* b, size_t b_len
     return a && b && x < y + b_len && y < x + a_len;
 }
 
+// Whether an array of bytes shares one with any of n rows of row_len bytes, row_step apart (no less than row_len).
+inline bool range_meets_rows(const void* a, size_t bytes, const void* rows, int64_t row_len, int64_t row_step, int64_t n) {
+    if (!a || !rows || n < 1) return false;
+    const int64_t from = (int64_t)(reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(rows)), to = from + (int64_t)bytes;
+    const int64_t i = from < row_len ? 0 : (from - row_len) / row_step + 1;  // the first row that ends behind the array's start
+    return i < n && i * row_step < to;
+}
+
 // Whether any of n rows of a_len bytes, a_step apart, shares a byte with any of n rows of b_len bytes, b_step apart (a step is
 // no less than its length).  Rows that lie between the other's are no overlap.
 inline bool rows_meet(uintptr_t a, int64_t a_len, int64_t a_step, uintptr_t b, int64_t b_len, int64_t b_step, int n) {

@@ -1,7 +1,7 @@
 """Outputs over inputs, or over one another: refused by status before any launch, without a GPU."""
 import pytest
 
-from .test_beam_refusals import COMPACT, FORK, INVALID, WORKSPACE, A, _call
+from .test_beam_refusals import COMPACT, FORK, INVALID, SELECT, WORKSPACE, A, _call
 
 # bytes of each array as tests/test_beam_refusals.py has the call: 4 children of 3 sequences, tables of 5 pages, a pool of 9
 READ = dict(parents=16, lens=12, held=12, page_table=60, shares=36, ring_state=8)
@@ -46,3 +46,17 @@ def test_compact_writes_over_nothing_that_it_reads(over, size):
     apart = dict(COMPACT, page_table=A, lens=2 * A, row_starts=3 * A, kept=4 * A, lens_out=5 * A)
     for at in (0, 4, size - 4, -8):
         assert _call("kvq8_paged_compact", apart, {"lens_out": apart[over] + at}) == INVALID, (over, at)
+
+
+@pytest.mark.parametrize("name", ["parents", "tokens", "totals"])
+def test_select_writes_over_nothing_at_all(name):
+    """Logits of 4 rows of 1000 values, 1100 apart: over their first, last or any row, the workspace, another output."""
+    apart = dict(SELECT, logits=A, logits_stride=1100, row_starts=2 * A, scores=3 * A, weights=4 * A, ended=5 * A, parents=6 * A, tokens=7 * A,
+                 totals=8 * A, workspace=9 * A)
+    for at in (-36, 0, 3996, 4400 - 36, 4400, 2 * 4400 + 2000, 3 * 4400 - 36, 3 * 4400 + 3996):
+        assert _call("beam_select", apart, {name: A + at}) == INVALID, at
+    for at in (-36, 0, 16):
+        assert _call("beam_select", apart, {name: apart["workspace"] + at}) == INVALID, at
+    for other in {"parents", "tokens", "totals"} - {name}:
+        for at in (-36, 0, 36):
+            assert _call("beam_select", apart, {name: apart[other] + at}) == INVALID, (other, at)
