@@ -638,7 +638,8 @@ size_t token_counts_fork_workspace_bytes(int n_children);
  * numbers in the lowest rows that no first child keeps.  So every row of `counts` belongs to one of the call's sequences or to
  * nobody: a row of a sequence that is not in the call would be written over.  With a nonzero status no row changes and every
  * state_of_out is -1 (in place: the rows are then known to the caller alone).  (token_counts then adds the children's tokens.)
- * Errors: INVALID_ARG (state_of_out over parents or part of state_of as well), UNSUPPORTED (n_children or n_seqs > 4096, n_states > 65536,
+ * Errors: INVALID_ARG (an output, counts among them, over an input, the workspace or another output as well, but for state_of_out that is
+ * state_of), UNSUPPORTED (n_children or n_seqs > 4096, n_states > 65536,
  * vocab > 2^30), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  Two launches.
  */
 int token_counts_fork(const int32_t* parents, int n_children, const int32_t* state_of, int n_seqs, uint32_t* counts,

@@ -538,6 +538,19 @@ extern "C" int token_counts_fork(const int32_t* parents, int n_children, const i
     for (const void* q : {(const void*)parents, (const void*)state_of, (const void*)counts, (const void*)state_of_out, (const void*)status})
         if (!aligned_to(q, 4)) return KVQ8_ERR_MISALIGNED;
     if (!aligned16(workspace)) return KVQ8_ERR_MISALIGNED;
+    // rows are copied by what the plan has written; one of them or the status over it would be followed
+    const size_t need = token_counts_fork_workspace_bytes(n_children), all = (size_t)n_states * vocab * 4;
+    const struct {
+        const void* at;
+        size_t bytes;
+    } reads[] = {{parents, kids}, {state_of == state_of_out ? nullptr : state_of, old}},
+      writes[] = {{counts, all}, {state_of_out, kids}, {status, 4}, {workspace, need}};
+    for (const auto& w : writes) {
+        for (const auto& r : reads)
+            if (ranges_meet(r.at, r.bytes, w.at, w.bytes)) return KVQ8_ERR_INVALID_ARG;
+        for (const auto* o = writes; o != &w; ++o)
+            if (ranges_meet(o->at, o->bytes, w.at, w.bytes)) return KVQ8_ERR_INVALID_ARG;
+    }
     const CountsFork p = {parents, state_of, state_of_out, counts, status, static_cast<int2*>(workspace), n_children, n_seqs, n_states, vocab};
     const int smem = (3 * n_seqs + 2 * ((n_states + 31) / 32)) * 4;
     static SmemOptIn opt;

@@ -1,7 +1,7 @@
 """Outputs over inputs, or over one another: refused by status before any launch, without a GPU."""
 import pytest
 
-from .test_beam_refusals import COMPACT, FORK, INVALID, SELECT, WORKSPACE, A, _call
+from .test_beam_refusals import COMPACT, COUNTS, FORK, INVALID, SELECT, WORKSPACE, A, _call
 
 # bytes of each array as tests/test_beam_refusals.py has the call: 4 children of 3 sequences, tables of 5 pages, a pool of 9
 READ = dict(parents=16, lens=12, held=12, page_table=60, shares=36, ring_state=8)
@@ -60,3 +60,21 @@ def test_select_writes_over_nothing_at_all(name):
     for other in {"parents", "tokens", "totals"} - {name}:
         for at in (-36, 0, 36):
             assert _call("beam_select", apart, {name: apart[other] + at}) == INVALID, (other, at)
+
+
+@pytest.mark.parametrize("name,size", [("counts", 2000), ("state_of_out", 16), ("status", 4), ("workspace", 32)])
+def test_counts_fork_writes_over_nothing_that_it_reads(name, size):
+    """4 children of 3 sequences, 5 rows of 100 counts; state_of_out in place of state_of, with status over it."""
+    sizes = dict(parents=16, state_of=12, counts=2000, state_of_out=16, status=4, workspace=32)
+    apart = {**COUNTS, **{k: (i + 1) * A for i, k in enumerate(sizes)}}
+    for over in sizes:
+        for at in (0, 16 if name == "workspace" else 4, sizes[over] - 4, 4 - size):
+            there = apart[over] + at
+            if over == name or not there < apart[over] + sizes[over] or (over, name, at) == ("state_of", "state_of_out", 0):
+                continue
+            if name == "workspace":
+                there -= there % 16
+            if there + size > apart[over]:
+                assert _call("token_counts_fork", apart, {name: there}) == INVALID, (over, at)
+    if name == "status":
+        assert _call("token_counts_fork", apart, {"state_of_out": apart["state_of"], name: apart["state_of"] + 8}) == INVALID
