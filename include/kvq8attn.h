@@ -717,7 +717,7 @@ int kvq8_paged_compact(const kvq8_paged_cache* kv, const int32_t* page_table, in
  *   pairs    : 0: pair i is dims i and i + rot_dim / 2; else 2 i and 2 i + 1.  (a, b) becomes (a cos - b sin, b cos + a sin)
  *   slots    : int64 [n_tok] as for kvq8_paged_append; a token whose slot lies outside the cache is left alone, its row of q_out too
  *   q_out    : as q, out_stride elements between tokens; may be q itself (equal strides).  Rows of it that share bytes with rows of
- *              q in any other way, or of k or v, are refused
+ *              q in any other way, or of k or v, or with positions, turns, axis_of or slots, are refused
  * Angles are exact modulo a turn to about 2^-28 of it at any position (an int32), their sines and cosines fp32 (3e-7), products and sums fp32; q_out
  * is rounded once, and the rotated keys are quantised from fp32, as kvq8_append would, without a rounding in between.
  * Errors: INVALID_ARG, UNSUPPORTED (the cache, rot_dim, n_axes > 4, n_q_heads > 65536), MISALIGNED (16 bytes; slots and turns 8,

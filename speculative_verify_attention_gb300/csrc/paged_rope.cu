@@ -321,6 +321,14 @@ extern "C" int kvq8_paged_append_rope(const void* q, const void* k, const void* 
     for (int64_t st : {q_stride, k_stride, v_stride, out_stride})
         if (st * esz % 16) return KVQ8_ERR_MISALIGNED;
     if (!aligned_to(positions, 4) || !aligned_to(axis_of, 4) || !aligned_to(turns, 8) || !aligned_to(slots, 8)) return KVQ8_ERR_MISALIGNED;
+    // what says where a later token goes and how far it turns is read while earlier ones' queries are written
+    const size_t tok = (size_t)n_tok, half = (size_t)rot_dim / 2;
+    const struct {
+        const void* at;
+        size_t bytes;
+    } reads[] = {{positions, tok * n_axes * 4}, {turns, half * 8}, {axis_of, half * 4}, {slots, tok * 8}};
+    for (const auto& r : reads)
+        if (range_meets_rows(r.at, r.bytes, q_out, q_row * esz, out_stride * esz, n_tok)) return KVQ8_ERR_INVALID_ARG;
     RopeParams p = {q, k, v, q_out, q_stride, k_stride, v_stride, out_stride, positions, turns, axis_of, slots,
                     {const_cast<int8_t*>(kv->k_codes), const_cast<int8_t*>(kv->v_codes)},
                     {const_cast<uint16_t*>(kv->k_scales), const_cast<uint16_t*>(kv->v_scales)},

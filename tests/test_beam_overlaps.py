@@ -1,7 +1,7 @@
 """Outputs over inputs, or over one another: refused by status before any launch, without a GPU."""
 import pytest
 
-from .test_beam_refusals import COMPACT, COUNTS, FORK, INVALID, SELECT, WORKSPACE, A, _call
+from .test_beam_refusals import COMPACT, COUNTS, FORK, INVALID, ROPE, SELECT, WORKSPACE, A, _call
 
 # bytes of each array as tests/test_beam_refusals.py has the call: 4 children of 3 sequences, tables of 5 pages, a pool of 9
 READ = dict(parents=16, lens=12, held=12, page_table=60, shares=36, ring_state=8)
@@ -78,3 +78,12 @@ def test_counts_fork_writes_over_nothing_that_it_reads(name, size):
                 assert _call("token_counts_fork", apart, {name: there}) == INVALID, (over, at)
     if name == "status":
         assert _call("token_counts_fork", apart, {"state_of_out": apart["state_of"], name: apart["state_of"] + 8}) == INVALID
+
+
+@pytest.mark.parametrize("name,size", [("positions", 48), ("turns", 512), ("axis_of", 256), ("slots", 48)])
+def test_rope_turns_no_queries_over_what_says_how(name, size):
+    """6 tokens on 2 axes, 128 dims turned; rows of q_out of 2048 bytes, as they are and 2400 apart."""
+    apart = dict(ROPE, q=A, k=2 * A, v=3 * A, q_out=4 * A, positions=5 * A, turns=6 * A, axis_of=7 * A, slots=8 * A)
+    for stride in (1024, 1200):
+        for at in (8 - size, 0, 2040, 2 * stride * 5, 2 * stride * 5 + 2040):
+            assert _call("kvq8_paged_append_rope", apart, {"out_stride": stride, name: apart["q_out"] + at}) == INVALID, at
