@@ -590,7 +590,7 @@ int token_counts(const int32_t* tokens, const int32_t* token_starts, int n_lists
  *   token_counts_fork and kvq8_paged_fork let the beams' counts and pages follow, and kvq8_paged_copy copies, in every layer's
  *   cache, the pages that could not be shared; kvq8_paged_compact moves the accepted path of a tree together.
  * A sequence is what has a row of a page table: a request, or one of its beams.  Like the calls above these neither
- * synchronise nor read a length on the host, and can be captured into graphs.
+ * synchronise nor read a length on the host, and can be captured into graphs; and what they read must not be written while they run.
  */
 
 /* Bytes of workspace beam_select needs (0: unsupported sizes). */
@@ -639,8 +639,8 @@ size_t token_counts_fork_workspace_bytes(int n_children);
  * nobody: a row of a sequence that is not in the call would be written over.  With a nonzero status no row changes and every
  * state_of_out is -1 (in place: the rows are then known to the caller alone).  (token_counts then adds the children's tokens.)
  * Errors: INVALID_ARG (an output, counts among them, over an input, the workspace or another output as well, but for state_of_out that is
- * state_of), UNSUPPORTED (n_children or n_seqs > 4096, n_states > 65536,
- * vocab > 2^30), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  Two launches.
+ * state_of), UNSUPPORTED (n_children or n_seqs > 4096, n_states > 65536, vocab > 2^30), WORKSPACE, MISALIGNED (4 bytes; workspace 16).
+ * Two launches.
  */
 int token_counts_fork(const int32_t* parents, int n_children, const int32_t* state_of, int n_seqs, uint32_t* counts,
                       int n_states, int vocab, int32_t* state_of_out, int32_t* status, void* workspace,
@@ -673,8 +673,8 @@ size_t kvq8_paged_fork_workspace_bytes(int n_seqs, int n_children, int n_pages);
  * kvq8_paged_tables takes pages for growing sequences as before (a fresh page's share is 0, and a sequence grows only in pages of its
  * own).  It gives pages back whoever shares them: sequences with shared pages are cut short and ended by this call.
  * Errors: INVALID_ARG (outputs over inputs or one another as well, but for the two that may be updated in place; free_ring counts as an
- * output), UNSUPPORTED (n_seqs or n_children > 4096, page_size, n_pages > 2^30, max_pages
- * > 2^24), WORKSPACE, MISALIGNED (4 bytes; workspace 16).  One launch for small tables, else three.
+ * output), UNSUPPORTED (n_seqs or n_children > 4096, page_size, n_pages > 2^30, max_pages > 2^24), WORKSPACE, MISALIGNED (4 bytes;
+ * workspace 16).  One launch for small tables, else three.
  */
 int kvq8_paged_fork(const int32_t* parents, int n_children, const int32_t* lens, const int32_t* held, int n_seqs,
                     int page_size, const int32_t* page_table, int max_pages, const int32_t* shares, int32_t* free_ring,

@@ -101,8 +101,8 @@ constexpr uint32_t kLowestWord<__nv_bfloat16> = 0xff80ff80u;
 // How a warp reads 256 consecutive values of a row, eight a lane, -inf outside the row.
 //   VEC: eight consecutive ones a load; the row starts on their size and holds whole groups of them.
 //   Rows of odd length in 16 bits: the two 16-byte pieces around a lane's eight, and where among those they start (`shift`, of the row
-//     alone) comes to a funnel shift a word; 320 rows of 106299 bf16 values 22.6 us (by selections 26; 106304 values 20.7).
-//   SPREAD, of fp32 and where rows are read as wholes: a value a load, neighbours to neighbouring lanes (100 fp32 rows of 106299: 13.9 us;
+//     alone) comes to a funnel shift a word; 320 rows of 106299 bf16 values 22.5 us (by selections 26; 106304 values 19.4).
+//   SPREAD, of fp32 and where rows are read as wholes: a value a load, neighbours to neighbouring lanes (100 fp32 rows of 106299: 13.6 us;
 //     by three pieces and selections 17.6.  4000 bf16 rows of 1001 as wholes 11.8 us, by pieces 16.9).
 template <typename T, bool VEC, bool SPREAD = sizeof(T) == 4 && !VEC>
 struct Tile {
@@ -764,8 +764,8 @@ __global__ void __launch_bounds__(kPickThreads, 3) beam_pick_kernel(const __grid
 //   SCANNED: after beam_scan_kernel, where there are so many rows that blocks for each would queue.
 //   Else in one launch, for small vocabularies: the row is read (and a second time from L1, if it is more than the lanes hold at once).
 // The bound is the n_out-th best of 32, 64 or 128 shares, which the lanes have of the groups or of the row.
-// 4000 rows of 1000 bf16 values, 16 of each 250 requests: 11.3 us in one launch (304 by beam_pick_kernel); one row 3.6 (25.7).  2048 rows
-// of 32000, 8 of each 256: 35.8 (60.1).
+// 4000 rows of 1000 bf16 values, 16 of each 250 requests: 12.1 us in one launch (68 by beam_pick_kernel); one row 3.5 (6.0).  2048 rows
+// of 32000, 8 of each 256: 36 (62).  (Logits that no call has read before; of those in L2 4000 rows of 1000 take 11.5 us.)
 constexpr int kRowWarps = 16;
 constexpr int kRowList = 384;   // candidates of a row
 template <bool SCANNED>
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) beam_rows_kernel(const __grid_
 }
 
 // What the sizes give: chunks, groups and parts of a row.  A warp takes two chunks of 16-bit values where there are many (320 rows of
-// 248320: the call 34.1 us, 35.5 with one, 34.1 with four; 96 rows 17.2 and 17.3), else one (160 rows of fp32: 30.9 us, 31.2 with two).
+// 248320: the call 33.4 us, 34.8 with one, 33.2 with four; 96 rows 16.5 and 16.8), else one (160 rows of fp32: 29.9 us, 30.2 with two).
 void plan(SelectParams& p, size_t value_bytes) {
     p.n_chunks = (p.vocab + kChunk - 1) / kChunk;
     p.n_groups = p.n_chunks * (int)value_bytes;
@@ -1074,14 +1074,20 @@ bool select_shape(int n_rows, int vocab, int n_seqs, int n_out) {
 }
 
 // A warp per row (beam_rows_kernel) or a block per row (beam_pick_kernel)?  bf16, beams of 8 (of 4 where there is one request), n_out 8
-// (4), us; a row read as a whole / a warp per row after the scan / a block per row after it:
-//   rows    vocab 1000       vocab 4096       vocab 8000           vocab 32000          vocab 106304
-//   4       4.5 /  - / 6.9   7.3 /  - / 8.0   10.5 / 8.0 / 7.2     27.4 / 8.4 / 7.1
-//   304     5.5 /  - / 8.0   9.1 /  - / 8.6   13.3 / 14.9 / 12.7   34.4 / 17.8 / 10.9     - / 27.4 / 19.0
-//   608     5.7 /  - / 14.1  9.2 /  - / 14.7  13.4 / 15.7 / 20.4   43.6 / 22.2 / 21.4     - / 37.3 / 34.6
-//   2048    7.2 /  - / 39.0  13.4 / - / 39.9  21.1 / 20.6 / 52.1   71.3 / 36.6 / 60.1     - / 81.6 / 102.6
-// Of 32 continuations 1024 rows, 16 of each request, 15 / - / 33 at 4096, 59 / 39 / 57 at 32000; of 64 (32 rows of each) a block is faster
-// from 2048 values on: 36 us for 41 at 4096, 103 for 152 at 106304.
+// (4), us, twenty calls in a graph, each on logits that have left L2; a row read as a whole / a warp per row after the scan / a block per
+// row after it:
+//   rows    vocab 1000         vocab 4096         vocab 8000         vocab 32000        vocab 106304
+//   4       4.1 / 25 / 6.4     6.3 / 7.4 / 7.7    9.7 / 7.3 / 6.9    28 / 8.0 / 6.9     - / 8.8 / 7.0
+//   304     5.7 / 37 / 8.0     8.8 / 15 / 8.8     14.5 / 15 / 13.2   42 / 17 / 12.2     - / 26 / 18.9
+//   608     5.8 / 33 / 14.0    9.5 / 16 / 16.0    14.9 / 16 / 22.4   42 / 21.1 / 21.8   - / 36.7 / 34.6
+//   912     5.8 / 36 / 19.9    10.0 / 17 / 22.7   15.1 / 17 / 28.7   42 / 24.4 / 31.0   - / 46.4 / 50.3
+//   2048    7.2 / 46 / 39.6    12.0 / 20 / 43.5   17.3 / 21 / 54.1   62 / 36.0 / 61.7   - / 80.7 / 103.7
+// Of 32 continuations 1024 rows, 16 of each request, 16.3 / - / 35 at 4096, 53 / 38.5 / 57.7 at 32000, - / 69.8 / 74.7 at 106304.
+// The rule goes by the rows alone, and there are sizes where it takes the slower side.  With a warp per row a request has one block, so
+// few requests of many beams leave multiprocessors idle; of 32 continuations: 24 requests of 32 beams 39 / - / 34.7 at 8000, 100 / 53.8 /
+// 55.9 at 32000, - / 90.7 / 63.2 at 106304; 12 of 64 77 / - / 42.2, 200 / 94 / 61.7, - / 151 / 69.8; 5 of 64 72.6 / - / 40.3 at 8000.  And
+// of 64 continuations, which always go to a block per row above kSmallVocab, 64 requests of 32 beams took 41.4 / - / 72.9 at 4096 and
+// - / 179 / 185 at 106304; 4 rows of 4096 values 6.3 as wholes and 7.7 as the rule has it.
 constexpr int kSmallVocab = 2048;    // rows of no more are read as a whole,
 constexpr int kMediumVocab = 10240;  // and of no more where there are more than kSomeRows of them
 constexpr int kSomeRows = 152 * 2, kManyRows = 152 * 5;
@@ -1109,7 +1115,8 @@ int launch_select(const SelectParams& p, cudaStream_t s) {
         return rows_kernel(beam_rows_kernel<T, VEC, true>, opt, (int)sizeof(RowSearch<true>));
     }
     // A block a row, by the mean of the requests' rows.  Clusters of 16 where the GPU holds all of them at once: 12 requests of 32 beams, 64
-    // of each, over 106304 bf16 logits 48.2 us (of 8: 72.8); 24 of 16 beams 39.3 us (of 8: 35.1).
+    // of each, over 106304 bf16 logits 48.6 us (of 8: 72.6), 19 of 16 beams, 16 of each, 22.4 (26.7); 24 of 16 beams, 16 of each, 32.9 us (of
+    // 8: 28.9).
     int cluster = 1;
     while (cluster < 8 && (int64_t)cluster * p.n_seqs < p.n_rows) cluster *= 2;
     if ((int64_t)p.n_seqs * 8 < p.n_rows && p.n_seqs * 16 <= kSomeRows) cluster = 16;
